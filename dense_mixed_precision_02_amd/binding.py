@@ -14,12 +14,22 @@ GEMM_OUT_F32, GEMM_OUT_F16, GEMM_OUT_BF16, GEMM_OUT_I32, GEMM_OUT_F64 = 0, 1, 2,
 GEMM_OK = 0
 
 EXPORTED_SYMBOLS = ("gemm_create", "gemm_run", "gemm_run_ex", "gemm_run_noalloc", "gemm_prune24",
-                    "gemm_run_sparse24", "gemm_destroy", "gemm_status_string", "gemm_plan")
+                    "gemm_run_sparse24", "gemm_run_grouped", "gemm_run_grouped_wgrad", "gemm_quant8",
+                    "gemm_run_scaled8", "gemm_destroy", "gemm_status_string", "gemm_plan")
+GEMM_OFFSETS_I32 = 16
+GEMM_E4M3, GEMM_E5M2 = 0, 1
 GEMM_ERR_SCRATCH = 5
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
 _lib = None
 _lock = threading.Lock()
+
+
+class Q8Operand(ctypes.Structure):
+    """gemm_q8_t: an 8-bit operand of gemm_run_scaled8."""
+    _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("ld", ctypes.c_int64),
+                ("scale_row", ctypes.c_int64), ("scale_k", ctypes.c_int64), ("group", ctypes.c_int64),
+                ("scale_group", ctypes.c_int64), ("type", ctypes.c_int)]
 
 
 class GemmError(RuntimeError):
@@ -64,6 +74,17 @@ def load_library():
         lib.gemm_run_sparse24.restype = ctypes.c_int
         lib.gemm_run_sparse24.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64,
                                           ctypes.c_int, ctypes.c_uint, i64, vp]
+        cf, ci, cu = ctypes.c_float, ctypes.c_int, ctypes.c_uint
+        lib.gemm_run_grouped.restype = ci
+        lib.gemm_run_grouped.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, i64, ci,
+                                         cu, cf, cf, ci, ci, vp]
+        lib.gemm_run_grouped_wgrad.restype = ci
+        lib.gemm_run_grouped_wgrad.argtypes = lib.gemm_run_grouped.argtypes
+        lib.gemm_quant8.restype = ci
+        lib.gemm_quant8.argtypes = [vp, vp, i64, i64, i64, ci, cu, i64, ci, ci, vp, vp, vp]
+        lib.gemm_run_scaled8.restype = ci
+        lib.gemm_run_scaled8.argtypes = [vp, ctypes.POINTER(Q8Operand), ctypes.POINTER(Q8Operand), vp, vp,
+                                         vp, i64, i64, i64, i64, i64, cu, cf, cf, ci, ci, vp]
         lib.gemm_plan.restype = ctypes.c_int
         lib.gemm_plan.argtypes = [vp, i64, i64, i64, i64, i64, i64, ctypes.c_int, ctypes.c_uint,
                                   i64, ctypes.c_char_p, ctypes.c_size_t]
@@ -147,6 +168,31 @@ class Handle:
         """Raw-pointer call of gemm_run_sparse24; returns the status code."""
         return load_library().gemm_run_sparse24(self.ptr, Ac, meta, B, C, D, M, N, K, ldb, ldc,
                                                 dtype, flags, batch, stream)
+
+    def run_grouped(self, A, B, C, D, offsets, groups, M, N, K, lda, ldb, ldc, dtype, flags=0, alpha=1.0,
+                    beta=0.0, c_type=GEMM_OUT_F32, d_type=GEMM_OUT_F32, stream=0) -> int:
+        """Raw-pointer call of gemm_run_grouped; returns the status code."""
+        return load_library().gemm_run_grouped(self.ptr, A, B, C, D, offsets, groups, M, N, K, lda, ldb,
+                                               ldc, dtype, flags, alpha, beta, c_type, d_type, stream)
+
+    def run_grouped_wgrad(self, X, Y, C, D, offsets, groups, M, N, K, ldx, ldy, ldc, dtype, flags=0,
+                          alpha=1.0, beta=0.0, c_type=GEMM_OUT_F32, d_type=GEMM_OUT_F32, stream=0) -> int:
+        """Raw-pointer call of gemm_run_grouped_wgrad; returns the status code."""
+        return load_library().gemm_run_grouped_wgrad(self.ptr, X, Y, C, D, offsets, groups, M, N, K, ldx,
+                                                     ldy, ldc, dtype, flags, alpha, beta, c_type, d_type,
+                                                     stream)
+
+    def quant8(self, X, M, K, ldx, x_type, flags, batch, block, q_type, Q, scale, stream=0) -> int:
+        """Raw-pointer call of gemm_quant8; returns the status code."""
+        return load_library().gemm_quant8(self.ptr, X, M, K, ldx, x_type, flags, batch, block, q_type, Q,
+                                          scale, stream)
+
+    def run_scaled8(self, A: Q8Operand, B: Q8Operand, C, D, offsets, groups, M, N, K, ldc, flags=0,
+                    alpha=1.0, beta=0.0, c_type=GEMM_OUT_F32, d_type=GEMM_OUT_F32, stream=0) -> int:
+        """Raw-pointer call of gemm_run_scaled8; returns the status code."""
+        return load_library().gemm_run_scaled8(self.ptr, ctypes.byref(A), ctypes.byref(B), C, D, offsets,
+                                               groups, M, N, K, ldc, flags, alpha, beta, c_type, d_type,
+                                               stream)
 
     def run_ex(self, *args, **kw) -> None:
         """Like status_ex() but raises on a non-zero status."""
@@ -371,4 +417,233 @@ def gemm_sparse24(sp: Sparse24, B, C=None, out=None, handle: Handle | None = Non
                             torch.cuda.current_stream(B.device).cuda_stream)
     if rc != GEMM_OK:
         raise GemmError(rc, "gemm_run_sparse24")
+    return out
+
+
+def _check_offsets(offsets, device):
+    """(groups, flag) of the row offsets of a grouped product."""
+    import torch
+    if offsets.dtype not in (torch.int32, torch.int64):
+        raise TypeError("offsets must be int32 or int64")
+    if offsets.dim() != 1 or offsets.shape[0] < 1 or offsets.device != device:
+        raise ValueError("offsets must be a vector of groups + 1 row numbers on the operands' GPU")
+    if offsets.shape[0] > 1 and offsets.stride(0) != 1:
+        raise ValueError("offsets must be contiguous")
+    return offsets.shape[0] - 1, GEMM_OFFSETS_I32 if offsets.dtype == torch.int32 else 0
+
+
+def _output(C, out, shape, out_dtype, beta, device, name):
+    """(C's address, C's code, D, D's code, ldc, beta) of a grouped product with outputs `shape`."""
+    import torch
+    rows, n = shape[-2], shape[-1]
+    for X, what in ((C, "C"), (out, "out")):
+        if X is None:
+            continue
+        if X.device != device or tuple(X.shape) != shape:
+            raise ValueError(f"{what} must be a tensor of shape {name} on the operands' GPU")
+        if _out_code(X.dtype) not in (GEMM_OUT_F32, GEMM_OUT_F16, GEMM_OUT_BF16):
+            raise TypeError(f"{what} must be float32, float16 or bfloat16")
+        if (n > 1 and X.stride(-1) != 1) or (rows > 1 and X.stride(-2) < n):
+            raise ValueError(f"{what} must be row-major with a row stride of at least N")
+    like = C if C is not None else out
+    ldc = max(like.stride(-2) if like is not None and rows > 1 else n, n, 1)
+    if out is None:
+        dtype = out_dtype if out_dtype is not None else torch.float32
+        if _out_code(dtype) not in (GEMM_OUT_F32, GEMM_OUT_F16, GEMM_OUT_BF16):
+            raise TypeError("out dtype must be float32, float16 or bfloat16")
+        strides = (rows * ldc, ldc, 1) if len(shape) == 3 else (ldc, 1)
+        out = torch.empty_strided(shape, strides, dtype=dtype, device=device)
+    for X, what in ((C, "C"), (out, "out")):
+        if X is None:
+            continue
+        if (rows > 1 and X.stride(-2) != ldc) or \
+                (len(shape) == 3 and shape[0] > 1 and X.stride(0) != rows * ldc):
+            raise ValueError("C and out must have the same row stride, and contiguous groups")
+    if C is None:
+        beta = 0.0
+    return (C.data_ptr() if C is not None else 0, _out_code(C.dtype) if C is not None else GEMM_OUT_F32,
+            out, _out_code(out.dtype), ldc, float(beta))
+
+
+def _sixteen_bit(A, B, what):
+    import torch
+    dt = {torch.float16: GEMM_F16, torch.bfloat16: GEMM_BF16}.get(A.dtype)
+    if dt is None or B.dtype != A.dtype:
+        raise TypeError(f"{what} must both be float16 or bfloat16")
+    if not A.is_cuda or B.device != A.device:
+        raise ValueError(f"{what} must be on the same GPU")
+    return dt
+
+
+def _rows_of(X, name):
+    """Leading dimension of a row-major matrix."""
+    if X.dim() != 2 or (X.shape[1] > 1 and X.stride(1) != 1) or \
+            (X.shape[0] > 1 and X.stride(0) < X.shape[1]):
+        raise ValueError(f"{name} must be a row-major matrix")
+    return max(X.stride(0) if X.shape[0] > 1 else X.shape[1], X.shape[1], 1)
+
+
+def gemm_grouped(A, B, offsets, C=None, out=None, alpha: float = 1.0, beta: float = 1.0, out_dtype=None,
+                 handle: Handle | None = None):
+    """D[i] = alpha * A[i] @ B[g] + beta * C[i] for the rows i of every group g, on the
+    current stream: the experts' products of rows sorted by expert.
+
+    A: (T, K) float16 / bfloat16, row-major;  B: (groups, K, N) of the same dtype,
+    contiguous (row-major), or a contiguous (groups, N, K) tensor's transpose(1, 2)
+    (column-major);  offsets: groups + 1 ascending row numbers, int32 or int64, on the
+    GPU: group g owns the rows offsets[g] .. offsets[g+1] - 1;  C: (T, N) float32 /
+    float16 / bfloat16 row-major, or None (beta = 0).  D (T, N) has ``out_dtype``
+    (default float32), a new tensor unless ``out`` is given (``out`` may be C when the
+    dtypes agree).  Rows that no group owns are left as they are in ``out`` (in a new
+    tensor they are undefined).
+
+    The input gradient of Y = gemm_grouped(A, W, offsets) is
+    gemm_grouped(dY, W.transpose(1, 2), offsets); the weight gradient is
+    gemm_grouped_wgrad(A, dY, offsets)."""
+    import torch
+    dt = _sixteen_bit(A, B, "A and B")
+    if B.dim() != 3 or A.dim() != 2 or B.shape[1] != A.shape[1]:
+        raise ValueError("A must be (T, K) and B (groups, K, N)")
+    groups, flags = _check_offsets(offsets, A.device)
+    (T, K), N = A.shape, B.shape[2]
+    if B.shape[0] != groups:
+        raise ValueError("offsets must hold one number more than B has groups")
+    lda = _rows_of(A, "A")
+    b_col, ldb = _operand_layout(B, K, N, "B")
+    if groups > 1 and K > 0 and N > 0 and B.stride(0) != (N if b_col else K) * ldb:
+        raise ValueError("B's groups must be contiguous")
+    c, c_code, out, d_code, ldc, beta = _output(C, out, (T, N), out_dtype, beta, A.device, "(T, N)")
+    with torch.cuda.device(A.device):
+        h = handle if handle is not None else default_handle()
+        rc = h.run_grouped(A.data_ptr(), B.data_ptr(), c, out.data_ptr(), offsets.data_ptr(), groups, T, N,
+                           K, lda, ldb, ldc, dt, flags | (GEMM_B_COLMAJOR if b_col else 0), float(alpha),
+                           beta, c_code, d_code, torch.cuda.current_stream(A.device).cuda_stream)
+    if rc != GEMM_OK:
+        raise GemmError(rc, "gemm_run_grouped")
+    return out
+
+
+def gemm_grouped_wgrad(X, Y, offsets, C=None, out=None, alpha: float = 1.0, beta: float = 1.0,
+                       out_dtype=None, handle: Handle | None = None):
+    """D[g] = alpha * X_g^T @ Y_g + beta * C[g] for every group g, X_g and Y_g the group's
+    rows (see gemm_grouped), on the current stream: the experts' weight gradients.
+
+    X: (T, M), Y: (T, N), float16 / bfloat16, row-major;  C: (groups, M, N) float32 /
+    float16 / bfloat16 with contiguous groups, or None (beta = 0).  D has ``out_dtype``
+    (default float32), a new tensor unless ``out`` is given (``out`` may be C when the
+    dtypes agree).  An empty group's D is beta * C (zero without C).  Rows that no group
+    owns are not read."""
+    import torch
+    dt = _sixteen_bit(X, Y, "X and Y")
+    ldx, ldy = _rows_of(X, "X"), _rows_of(Y, "Y")
+    if Y.shape[0] != X.shape[0]:
+        raise ValueError("X and Y must have the same rows")
+    groups, flags = _check_offsets(offsets, X.device)
+    (T, M), N = X.shape, Y.shape[1]
+    c, c_code, out, d_code, ldc, beta = _output(C, out, (groups, M, N), out_dtype, beta, X.device,
+                                                "(groups, M, N)")
+    with torch.cuda.device(X.device):
+        h = handle if handle is not None else default_handle()
+        rc = h.run_grouped_wgrad(X.data_ptr(), Y.data_ptr(), c, out.data_ptr(), offsets.data_ptr(), groups,
+                                 M, N, T, ldx, ldy, ldc, dt, flags, float(alpha), beta, c_code, d_code,
+                                 torch.cuda.current_stream(X.device).cuda_stream)
+    if rc != GEMM_OK:
+        raise GemmError(rc, "gemm_run_grouped_wgrad")
+    return out
+
+
+class Scaled8:
+    """An 8-bit operand of gemm_scaled8: ``q`` ((groups,) rows, Kp), float8_e4m3fn or
+    float8_e5m2, K-contiguous rows of Kp = 16 * ceil(K / 16) values, zeros past K; and
+    ``scale`` ((groups,) ceil(rows / block), ceil(K / 128)) float32 of any strides: the
+    value stands for q times the scale of its block of ``block`` rows by 128 k.  Made
+    by quant8, or from tensors that are there."""
+
+    def __init__(self, q, scale, block: int = 1, K: int | None = None):
+        import torch
+        self.type = {torch.float8_e4m3fn: GEMM_E4M3, torch.float8_e5m2: GEMM_E5M2}.get(q.dtype)
+        if self.type is None or scale.dtype != torch.float32:
+            raise TypeError("q must be float8_e4m3fn or float8_e5m2, and scale float32")
+        if block not in (1, 128):
+            raise ValueError("block must be 1 or 128")
+        K = q.shape[-1] if K is None else K
+        kp = -(-K // 16) * 16
+        if q.dim() not in (2, 3) or q.shape[-1] != kp:
+            raise ValueError("q must be ((groups,) rows, 16 * ceil(K / 16))")
+        rows = q.shape[-2]
+        if tuple(scale.shape) != (*q.shape[:-2], -(-rows // block), -(-K // 128)):
+            raise ValueError("scale must be ((groups,) ceil(rows / block), ceil(K / 128))")
+        if scale.device != q.device or not q.is_cuda:
+            raise ValueError("q and scale must be on the same GPU")
+        if q.numel() and (q.stride(-1) != 1 or (rows > 1 and (q.stride(-2) < kp or q.stride(-2) % 16)) or
+                          (q.dim() == 3 and q.shape[0] > 1 and q.stride(0) % 16) or q.data_ptr() % 16):
+            raise ValueError("q's rows must be contiguous and begin at multiples of 16 bytes")
+        self.q, self.scale, self.block, self.K, self.rows = q, scale, block, K, rows
+        self.groups = q.shape[0] if q.dim() == 3 else None
+        self.operand = Q8Operand(q.data_ptr(), scale.data_ptr(), q.stride(-2) if rows > 1 and kp else kp,
+                                 scale.stride(-2), scale.stride(-1), q.stride(0) if q.dim() == 3 else 0,
+                                 scale.stride(0) if q.dim() == 3 else 0, self.type)
+
+
+def quant8(X, block: int = 1, dtype=None, handle: Handle | None = None) -> Scaled8:
+    """Quantize X ((batch,) M, K; float32, float16 or bfloat16; row-major or a transposed
+    view) to 8-bit floats (``dtype``: torch.float8_e4m3fn, the default, or float8_e5m2)
+    with a scale for every block of 128 consecutive k of one row (block = 1: activations)
+    or of 128 rows (block = 128: weights), on the current stream.  The result is
+    K-contiguous whatever X's layout: the operand B of gemm_scaled8 for weights stored
+    (K, N) is quant8(W.t(), block=128)."""
+    import torch
+    dtype = torch.float8_e4m3fn if dtype is None else dtype
+    code = {torch.float8_e4m3fn: GEMM_E4M3, torch.float8_e5m2: GEMM_E5M2}.get(dtype)
+    x_code = _out_code(X.dtype)
+    if code is None or x_code not in (GEMM_OUT_F32, GEMM_OUT_F16, GEMM_OUT_BF16):
+        raise TypeError("X must be float32, float16 or bfloat16, and dtype float8_e4m3fn or float8_e5m2")
+    if X.dim() not in (2, 3) or not X.is_cuda:
+        raise ValueError("X must be a 2-D or 3-D GPU tensor")
+    if block not in (1, 128):
+        raise ValueError("block must be 1 or 128")
+    M, K = X.shape[-2], X.shape[-1]
+    lead = X.shape[:-2]
+    batch = X.shape[0] if lead else 1
+    col, ldx = _operand_layout(X, M, K, "X")
+    if batch > 1 and X.numel() and X.stride(0) != (K if col else M) * ldx:
+        raise ValueError("batched X must have a contiguous batch stride")
+    kb, mb = -(-K // 128), -(-M // block)
+    q = torch.empty((*lead, M, -(-K // 16) * 16), dtype=dtype, device=X.device)
+    scale = torch.empty((*lead, kb, mb), dtype=torch.float32, device=X.device)
+    with torch.cuda.device(X.device):
+        h = handle if handle is not None else default_handle()
+        rc = h.quant8(X.data_ptr(), M, K, ldx, x_code, GEMM_A_COLMAJOR if col else 0, batch, block, code,
+                      q.data_ptr(), scale.data_ptr(), torch.cuda.current_stream(X.device).cuda_stream)
+    if rc != GEMM_OK:
+        raise GemmError(rc, "gemm_quant8")
+    return Scaled8(q, scale.transpose(-1, -2), block, K)
+
+
+def gemm_scaled8(A: Scaled8, B: Scaled8, offsets=None, C=None, out=None, alpha: float = 1.0,
+                 beta: float = 1.0, out_dtype=None, handle: Handle | None = None):
+    """D = alpha * (A @ B^T) + beta * C of 8-bit operands with block scales, on the current
+    stream.  A: (T, K) with blocks of one row;  B: (N, K) with blocks of 128 rows (the N
+    columns of a K x N matrix as rows);  formats may differ.  With ``offsets`` (see
+    gemm_grouped) B is (groups, N, K) and the rows of group g meet B[g].  C, ``out`` and
+    ``out_dtype`` (default float32) as in gemm_grouped."""
+    import torch
+    if A.block != 1 or B.block != 128:
+        raise ValueError("A must have blocks of one row and B blocks of 128 rows")
+    if A.groups is not None or A.K != B.K or B.q.device != A.q.device:
+        raise ValueError("A must be (T, K) and B ((groups,) N, K) on the same GPU")
+    device = A.q.device
+    groups, flags = (1, 0) if offsets is None else _check_offsets(offsets, device)
+    if (offsets is None) != (B.groups is None) or (offsets is not None and B.groups != groups):
+        raise ValueError("a grouped B needs offsets that hold one number more than it has groups")
+    T, N = A.rows, B.rows
+    c, c_code, out, d_code, ldc, beta = _output(C, out, (T, N), out_dtype, beta, device, "(T, N)")
+    with torch.cuda.device(device):
+        h = handle if handle is not None else default_handle()
+        rc = h.run_scaled8(A.operand, B.operand, c, out.data_ptr(),
+                           offsets.data_ptr() if offsets is not None else 0, groups, T, N, A.K, ldc, flags,
+                           float(alpha), beta, c_code, d_code,
+                           torch.cuda.current_stream(device).cuda_stream)
+    if rc != GEMM_OK:
+        raise GemmError(rc, "gemm_run_scaled8")
     return out

@@ -4,9 +4,10 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
-SOURCES = [os.path.join(_HERE, "csrc", "gemm_api.hip")]
+SOURCES = [os.path.join(_HERE, "csrc", "gemm_api.hip"), os.path.join(_HERE, "csrc", "ragged_api.hip")]
 OUT = os.path.join(_HERE, "libdmp_gemm.so")
 # The race-check variant: every pipeline step waits for its copies and meets
 # every wave; its results must equal the library's bit for bit.
@@ -19,27 +20,39 @@ HIPCC_FLAGS = [
 ]
 
 
-def _compile(out: str, extra: list) -> subprocess.Popen:
+def _run(args: list) -> subprocess.Popen:
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
-    cmd = [hipcc, *HIPCC_FLAGS, *extra, "-o", out + ".tmp", *SOURCES]
-    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)
+    return subprocess.Popen([hipcc, *args], stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)
+
+
+def _finish(jobs: list, verbose: bool) -> None:
+    failed = []
+    for name, proc in jobs:
+        _, err = proc.communicate()
+        if proc.returncode != 0:
+            failed.append(name)
+        if proc.returncode != 0 or verbose:
+            sys.stderr.write(err)
+    if failed:
+        raise RuntimeError("hipcc failed for " + ", ".join(failed))
 
 
 def build(verbose: bool = False) -> str:
-    """Builds the library and its race-check variant (in parallel); returns the library's path."""
-    jobs = [(OUT, _compile(OUT, [])), (OUT_SYNC, _compile(OUT_SYNC, ["-DDMP_EXTRA_SYNC"]))]
-    failed = []
-    for out, proc in jobs:
-        _, err = proc.communicate()
-        if proc.returncode != 0:
-            sys.stderr.write(err)
-            failed.append(os.path.basename(out))
-            continue
-        if verbose:
-            sys.stderr.write(err)
+    """Builds the library and its race-check variant, every source of both in
+    parallel; returns the library's path."""
+    compile_flags = [f for f in HIPCC_FLAGS if f != "-shared"]
+    with tempfile.TemporaryDirectory() as tmp:
+        libs = []
+        jobs = []
+        for out, extra in ((OUT, []), (OUT_SYNC, ["-DDMP_EXTRA_SYNC"])):
+            objs = [os.path.join(tmp, os.path.basename(out) + os.path.basename(s) + ".o") for s in SOURCES]
+            libs.append((out, objs))
+            jobs += [(s, _run([*compile_flags, *extra, "-c", "-o", o, s])) for s, o in zip(SOURCES, objs)]
+        _finish(jobs, verbose)
+        _finish([(out, _run(["--offload-arch=gfx950", "-shared", "-fPIC", "-o", out + ".tmp", *objs]))
+                 for out, objs in libs], verbose)
+    for out in (OUT, OUT_SYNC):
         os.replace(out + ".tmp", out)
-    if failed:
-        raise RuntimeError("hipcc failed for " + ", ".join(failed))
     return OUT
 
 

@@ -12,6 +12,7 @@
 #include "../../include/dmp_gemm.h"
 #include "aux_kernels.hpp"
 #include "dgemm.hpp"
+#include "handle.hpp"
 #include "sparse_gemm.hpp"
 #include "tile_gemm.hpp"
 #include "tile16_gemm.hpp"
@@ -20,13 +21,6 @@
 
 using namespace dmp;
 using namespace dmp::plan;
-
-struct gemm_handle {
-    int device = 0;
-    int num_cus = 0;
-    void *ws = nullptr;   // split-K partials or the transposed int8 B, grown on demand
-    size_t ws_bytes = 0;
-};
 
 namespace {
 

@@ -1,0 +1,145 @@
+// ragged_api.hip -- the entry points of the products over ragged groups, the
+// 8-bit quantization and the 8-bit block-scaled products (declared in
+// include/dmp_gemm.h): argument checks, kernel choice and launches.
+#include <hip/hip_runtime.h>
+
+#include "../../include/dmp_gemm.h"
+#include "handle.hpp"
+#include "quant8.hpp"
+#include "ragged.hpp"
+#include "ragged_plan.hpp"
+
+using namespace dmp;
+using namespace dmp::plan;
+
+namespace {
+
+EpiParams out_stage(float alpha, float beta, int c_type, int d_type) {
+    EpiParams ep;
+    ep.alpha = alpha;
+    ep.beta = beta;
+    ep.c_type = c_type;
+    ep.d_type = d_type;
+    ep.use_c = beta != 0.0f;
+    return ep;
+}
+
+int launched() { return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_HIP; }
+
+template <class DT, bool AK, bool BKC, int MODE>
+int launch_any(const RaggedArgs &a, hipStream_t s) {
+    // row tiles: at most one more for each group than the rows fill
+    const int64_t row_tiles = MODE == RAGGED_WGRAD ? (int64_t)a.groups * a.tiles_m : cdiv(a.M, 64) + a.groups;
+    const int64_t grid = row_tiles * a.tiles_n;
+    if (grid > 0x7fffffff) return GEMM_ERR_INVALID_ARG;
+    hipLaunchKernelGGL((ragged_any<DT, AK, BKC, MODE>), dim3((unsigned)grid), dim3(256), 0, s, a);
+    return launched();
+}
+
+template <int XT, int FMT>
+int launch_quant8(const Quant8Args &a, bool col, int block, int64_t grid, hipStream_t s) {
+    const dim3 g((unsigned)grid), blk(256);
+    if (!col && block == 1) hipLaunchKernelGGL((quant8_rows<XT, FMT>), g, blk, 0, s, a);
+    else if (!col) hipLaunchKernelGGL((quant8_tile<XT, FMT, false, true>), g, blk, 0, s, a);
+    else if (block == 1) hipLaunchKernelGGL((quant8_tile<XT, FMT, true, false>), g, blk, 0, s, a);
+    else hipLaunchKernelGGL((quant8_tile<XT, FMT, true, true>), g, blk, 0, s, a);
+    return launched();
+}
+
+}  // namespace
+
+extern "C" {
+
+int gemm_run_grouped(gemm_handle_t h, const void *A, const void *B, const void *C, void *D,
+                     const void *offsets, int64_t groups, int64_t M, int64_t N, int64_t K, int64_t lda,
+                     int64_t ldb, int64_t ldc, int dtype, unsigned flags, float alpha, float beta,
+                     int c_type, int d_type, void *stream) {
+    const EpiParams ep = out_stage(alpha, beta, c_type, d_type);
+    const int rc = validate_grouped(h, A, B, C, D, offsets, groups, M, N, K, lda, ldb, ldc, dtype, flags, ep);
+    if (rc != GEMM_OK || M == 0 || N == 0 || groups == 0) return rc;
+    const bool bc = flags & GEMM_B_COLMAJOR;
+    RaggedArgs a{};
+    a.A = A; a.B = B; a.C = C; a.D = D; a.offsets = offsets;
+    a.M = M; a.N = N; a.K = K; a.lda = lda; a.ldb = ldb; a.ldc = ldc;
+    a.sB = K == 0 ? 0 : (bc ? N : K) * ldb;
+    a.groups = (int)groups;
+    a.off32 = (flags & GEMM_OFFSETS_I32) != 0;
+    a.tiles_n = (int)cdiv(N, 64);
+    a.ep = ep;
+    hipStream_t s = (hipStream_t)stream;
+    if (dtype == GEMM_F16)
+        return bc ? launch_any<F16, true, true, RAGGED_ROWS>(a, s) : launch_any<F16, true, false, RAGGED_ROWS>(a, s);
+    return bc ? launch_any<BF16, true, true, RAGGED_ROWS>(a, s) : launch_any<BF16, true, false, RAGGED_ROWS>(a, s);
+}
+
+int gemm_run_grouped_wgrad(gemm_handle_t h, const void *X, const void *Y, const void *C, void *D,
+                           const void *offsets, int64_t groups, int64_t M, int64_t N, int64_t K,
+                           int64_t ldx, int64_t ldy, int64_t ldc, int dtype, unsigned flags, float alpha,
+                           float beta, int c_type, int d_type, void *stream) {
+    const EpiParams ep = out_stage(alpha, beta, c_type, d_type);
+    const int rc = validate_wgrad(h, X, Y, C, D, offsets, groups, M, N, K, ldx, ldy, ldc, dtype, flags, ep);
+    if (rc != GEMM_OK || M == 0 || N == 0 || groups == 0) return rc;
+    RaggedArgs a{};
+    a.A = X; a.B = Y; a.C = C; a.D = D; a.offsets = offsets;
+    a.M = M; a.N = N; a.K = K; a.lda = ldx; a.ldb = ldy; a.ldc = ldc;
+    a.sC = M * ldc;
+    a.groups = (int)groups;
+    a.off32 = (flags & GEMM_OFFSETS_I32) != 0;
+    a.tiles_m = (int)cdiv(M, 64);
+    a.tiles_n = (int)cdiv(N, 64);
+    a.ep = ep;
+    hipStream_t s = (hipStream_t)stream;
+    return dtype == GEMM_F16 ? launch_any<F16, false, false, RAGGED_WGRAD>(a, s)
+                             : launch_any<BF16, false, false, RAGGED_WGRAD>(a, s);
+}
+
+int gemm_quant8(gemm_handle_t h, const void *X, int64_t M, int64_t K, int64_t ldx, int x_type,
+                unsigned flags, int64_t batch, int block, int q_type, void *Q, float *scale, void *stream) {
+    const int rc = validate_quant8(h, X, M, K, ldx, x_type, flags, batch, block, q_type, Q, scale);
+    if (rc != GEMM_OK || M == 0 || K == 0 || batch == 0) return rc;
+    const bool col = flags & GEMM_A_COLMAJOR;
+    Quant8Args a{};
+    a.X = X; a.Q = (uint8_t *)Q; a.scale = scale;
+    a.M = M; a.K = K; a.ldx = ldx; a.Kp = k16(K); a.sX = (col ? K : M) * ldx;
+    a.KB = (int)cdiv(K, 128);
+    a.MB = cdiv(M, block);
+    const bool rows = !col && block == 1;
+    a.tiles_m = cdiv(M, rows ? QUANT_ROWS : 128);
+    a.batch = (int)batch;
+    const __int128 g = (__int128)batch * a.tiles_m * (rows ? cdiv(a.KB, 8) : a.KB);
+    if (g > 0x7fffffff) return GEMM_ERR_INVALID_ARG;
+    const int64_t grid = (int64_t)g;
+    hipStream_t s = (hipStream_t)stream;
+    const bool e4 = q_type == GEMM_E4M3;
+    if (x_type == GEMM_OUT_F32)
+        return e4 ? launch_quant8<OUT_F32, 0>(a, col, block, grid, s) : launch_quant8<OUT_F32, 1>(a, col, block, grid, s);
+    if (x_type == GEMM_OUT_F16)
+        return e4 ? launch_quant8<OUT_F16, 0>(a, col, block, grid, s) : launch_quant8<OUT_F16, 1>(a, col, block, grid, s);
+    return e4 ? launch_quant8<OUT_BF16, 0>(a, col, block, grid, s) : launch_quant8<OUT_BF16, 1>(a, col, block, grid, s);
+}
+
+int gemm_run_scaled8(gemm_handle_t h, const gemm_q8_t *A, const gemm_q8_t *B, const void *C, void *D,
+                     const void *offsets, int64_t groups, int64_t M, int64_t N, int64_t K, int64_t ldc,
+                     unsigned flags, float alpha, float beta, int c_type, int d_type, void *stream) {
+    const EpiParams ep = out_stage(alpha, beta, c_type, d_type);
+    const int rc = validate_scaled8(h, A, B, C, D, offsets, groups, M, N, K, ldc, flags, ep);
+    if (rc != GEMM_OK || M == 0 || N == 0 || groups == 0) return rc;
+    RaggedArgs a{};
+    a.A = A->q; a.B = B->q; a.C = C; a.D = D; a.offsets = offsets;
+    a.sa = A->scale; a.sb = B->scale;
+    a.M = M; a.N = N; a.K = k16(K);
+    a.lda = A->ld; a.ldb = B->ld; a.ldc = ldc;
+    a.sB = groups > 1 ? B->group : 0;
+    a.sa_row = A->scale_row; a.sa_k = A->scale_k;
+    a.sb_col = B->scale_row; a.sb_k = B->scale_k; a.sb_group = groups > 1 ? B->scale_group : 0;
+    a.groups = (int)groups;
+    a.off32 = (flags & GEMM_OFFSETS_I32) != 0;
+    a.tiles_n = (int)cdiv(N, 64);
+    a.ep = ep;
+    hipStream_t s = (hipStream_t)stream;
+    const bool a4 = A->type == GEMM_E4M3, b4 = B->type == GEMM_E4M3;
+    if (a4) return b4 ? launch_any<F8<0, 0>, true, true, RAGGED_SCALED>(a, s) : launch_any<F8<0, 1>, true, true, RAGGED_SCALED>(a, s);
+    return b4 ? launch_any<F8<1, 0>, true, true, RAGGED_SCALED>(a, s) : launch_any<F8<1, 1>, true, true, RAGGED_SCALED>(a, s);
+}
+
+}  // extern "C"

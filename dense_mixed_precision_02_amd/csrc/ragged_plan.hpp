@@ -1,0 +1,131 @@
+// ragged_plan.hpp -- host-side argument checks and kernel choice of the
+// products over ragged groups, the 8-bit block-scaled products and the 8-bit
+// quantization (plain C++: no HIP types).
+#pragma once
+#include "plan.hpp"
+
+namespace dmp {
+namespace plan {
+
+constexpr unsigned GROUPED_FLAGS = GEMM_B_COLMAJOR | GEMM_OFFSETS_I32;
+constexpr int64_t SIZE_MAX_1 = (1ll << 31) - 1024, LD_MAX = 1ll << 48, GROUPS_MAX = 1ll << 20;
+
+inline bool float_out(int t) { return t == GEMM_OUT_F32 || t == GEMM_OUT_F16 || t == GEMM_OUT_BF16; }
+
+// The output stage's types and pointers (D, and C where it is read).
+inline int check_outputs(const void *C, const void *D, const EpiParams &ep) {
+    if (!D || (ep.use_c && !C)) return GEMM_ERR_INVALID_ARG;
+    if (C == D && ep.use_c && ep.c_type != ep.d_type) return GEMM_ERR_INVALID_ARG;
+    if ((ep.use_c && (uintptr_t)C % (uintptr_t)out_bytes(ep.c_type)) ||
+        (uintptr_t)D % (uintptr_t)out_bytes(ep.d_type))
+        return GEMM_ERR_INVALID_ARG;
+    return GEMM_OK;
+}
+
+inline int check_sizes(gemm_handle_t h, int64_t groups, int64_t M, int64_t N, int64_t K,
+                       int64_t ldc, const EpiParams &ep) {
+    if (!h || M < 0 || N < 0 || K < 0 || groups < 0 || groups > GROUPS_MAX) return GEMM_ERR_INVALID_ARG;
+    if (M > SIZE_MAX_1 || N > SIZE_MAX_1 || K > SIZE_MAX_1) return GEMM_ERR_INVALID_ARG;
+    if (ldc < std::max<int64_t>(1, N) || ldc > LD_MAX) return GEMM_ERR_INVALID_ARG;
+    if (!float_out(ep.c_type) || !float_out(ep.d_type)) return GEMM_ERR_INVALID_ARG;
+    return GEMM_OK;
+}
+
+inline bool offsets_ok(const void *offsets, unsigned flags) {
+    return offsets && (uintptr_t)offsets % ((flags & GEMM_OFFSETS_I32) ? 4 : 8) == 0;
+}
+
+// D[i] = alpha A[i] B_g + beta C[i]: A M x K row-major, B_g K x N or N x K, D M x N.
+inline int validate_grouped(gemm_handle_t h, const void *A, const void *B, const void *C, const void *D,
+                            const void *offsets, int64_t groups, int64_t M, int64_t N, int64_t K,
+                            int64_t lda, int64_t ldb, int64_t ldc, int dtype, unsigned flags,
+                            const EpiParams &ep) {
+    int rc = check_sizes(h, groups, M, N, K, ldc, ep);
+    if (rc != GEMM_OK) return rc;
+    if (dtype != GEMM_F16 && dtype != GEMM_BF16) return GEMM_ERR_INVALID_ARG;
+    if (flags & ~GROUPED_FLAGS) return GEMM_ERR_INVALID_ARG;
+    const bool bc = flags & GEMM_B_COLMAJOR;
+    if (K > 0 && (lda < K || lda > LD_MAX || ldb < std::max<int64_t>(1, bc ? K : N) || ldb > LD_MAX))
+        return GEMM_ERR_INVALID_ARG;
+    if (M == 0 || N == 0 || groups == 0) return GEMM_OK;
+    if (!extent_ok(1, M, ldc, N)) return GEMM_ERR_INVALID_ARG;
+    if (K > 0 && (!extent_ok(1, M, lda, K) || !extent_ok(groups, bc ? N : K, ldb, bc ? K : N)))
+        return GEMM_ERR_INVALID_ARG;
+    if (!offsets_ok(offsets, flags)) return GEMM_ERR_INVALID_ARG;
+    if (K > 0 && (!A || !B || (uintptr_t)A % 2 || (uintptr_t)B % 2)) return GEMM_ERR_INVALID_ARG;
+    return check_outputs(C, D, ep);
+}
+
+// D_g = alpha X_g^T Y_g + beta C_g: X K x M and Y K x N row-major, D_g M x N.
+inline int validate_wgrad(gemm_handle_t h, const void *X, const void *Y, const void *C, const void *D,
+                          const void *offsets, int64_t groups, int64_t M, int64_t N, int64_t K,
+                          int64_t ldx, int64_t ldy, int64_t ldc, int dtype, unsigned flags,
+                          const EpiParams &ep) {
+    int rc = check_sizes(h, groups, M, N, K, ldc, ep);
+    if (rc != GEMM_OK) return rc;
+    if (dtype != GEMM_F16 && dtype != GEMM_BF16) return GEMM_ERR_INVALID_ARG;
+    if (flags & ~(unsigned)GEMM_OFFSETS_I32) return GEMM_ERR_INVALID_ARG;
+    if (K > 0 && (ldx < std::max<int64_t>(1, M) || ldx > LD_MAX || ldy < std::max<int64_t>(1, N) || ldy > LD_MAX))
+        return GEMM_ERR_INVALID_ARG;
+    if (M == 0 || N == 0 || groups == 0) return GEMM_OK;
+    if (!extent_ok(groups, M, ldc, N)) return GEMM_ERR_INVALID_ARG;
+    if (K > 0 && (!extent_ok(1, K, ldx, M) || !extent_ok(1, K, ldy, N))) return GEMM_ERR_INVALID_ARG;
+    if (!offsets_ok(offsets, flags)) return GEMM_ERR_INVALID_ARG;
+    if (K > 0 && (!X || !Y || (uintptr_t)X % 2 || (uintptr_t)Y % 2)) return GEMM_ERR_INVALID_ARG;
+    return check_outputs(C, D, ep);
+}
+
+inline int64_t k16(int64_t K) { return cdiv(K, 16) * 16; }
+
+inline bool q8_operand_ok(const gemm_q8_t &o, int64_t K, int64_t groups, int64_t rows, int64_t blocks) {
+    if (o.type != GEMM_E4M3 && o.type != GEMM_E5M2) return false;
+    if (!o.q || !aligned16(o.q) || !o.scale || (uintptr_t)o.scale % 4) return false;
+    if (o.ld < k16(K) || o.ld % 16 || o.ld > LD_MAX) return false;
+    if (o.scale_row < 0 || o.scale_k < 0 || o.scale_row > LD_MAX || o.scale_k > LD_MAX) return false;
+    if (groups > 1 && (o.group < 0 || o.group % 16 || o.group > LD_MAX || o.scale_group < 0 ||
+                       o.scale_group > LD_MAX))
+        return false;
+    const __int128 lim = (__int128)1 << 48;
+    return (__int128)(groups - 1) * (groups > 1 ? o.group : 0) + (__int128)rows * o.ld <= lim &&
+           (__int128)(groups - 1) * (groups > 1 ? o.scale_group : 0) + (__int128)blocks * o.scale_row +
+                   (__int128)cdiv(K, 128) * o.scale_k <= lim &&
+           256 * o.ld < (1ll << 31) - (1ll << 22);  // offsets inside a tile fit 31 bits
+}
+
+inline int validate_scaled8(gemm_handle_t h, const gemm_q8_t *A, const gemm_q8_t *B, const void *C,
+                            const void *D, const void *offsets, int64_t groups, int64_t M, int64_t N,
+                            int64_t K, int64_t ldc, unsigned flags, const EpiParams &ep) {
+    int rc = check_sizes(h, groups, M, N, K, ldc, ep);
+    if (rc != GEMM_OK) return rc;
+    if (flags & ~(unsigned)GEMM_OFFSETS_I32) return GEMM_ERR_INVALID_ARG;
+    if (!offsets && groups != 1) return GEMM_ERR_INVALID_ARG;
+    if (!A || !B) return GEMM_ERR_INVALID_ARG;
+    if (M == 0 || N == 0 || groups == 0) return GEMM_OK;
+    if (!extent_ok(1, M, ldc, N)) return GEMM_ERR_INVALID_ARG;
+    if (offsets && !offsets_ok(offsets, flags)) return GEMM_ERR_INVALID_ARG;
+    if (K > 0 && (!q8_operand_ok(*A, K, 1, M, M) || !q8_operand_ok(*B, K, groups, N, cdiv(N, 128))))
+        return GEMM_ERR_INVALID_ARG;
+    return check_outputs(C, D, ep);
+}
+
+inline int validate_quant8(gemm_handle_t h, const void *X, int64_t M, int64_t K, int64_t ldx, int x_type,
+                           unsigned flags, int64_t batch, int block, int q_type, const void *Q,
+                           const void *scale) {
+    if (!h || M < 0 || K < 0 || batch < 0 || batch > (1ll << 30) || M > SIZE_MAX_1 || K > SIZE_MAX_1)
+        return GEMM_ERR_INVALID_ARG;
+    if (!float_out(x_type) || (flags & ~(unsigned)GEMM_A_COLMAJOR)) return GEMM_ERR_INVALID_ARG;
+    if ((block != 1 && block != 128) || (q_type != GEMM_E4M3 && q_type != GEMM_E5M2))
+        return GEMM_ERR_INVALID_ARG;
+    if (M == 0 || K == 0 || batch == 0) return GEMM_OK;
+    const bool col = flags & GEMM_A_COLMAJOR;
+    if (ldx < (col ? M : K) || ldx > LD_MAX) return GEMM_ERR_INVALID_ARG;
+    if (!extent_ok(batch, col ? K : M, ldx, col ? M : K) || !extent_ok(batch, M, k16(K), k16(K)))
+        return GEMM_ERR_INVALID_ARG;
+    if (!X || !Q || !scale || (uintptr_t)X % (uintptr_t)out_bytes(x_type) || !aligned16(Q) ||
+        (uintptr_t)scale % 4)
+        return GEMM_ERR_INVALID_ARG;
+    return GEMM_OK;
+}
+
+}  // namespace plan
+}  // namespace dmp

@@ -234,6 +234,121 @@ int gemm_run_noalloc(gemm_handle_t h, const void *A, const void *B, const void *
                      int dtype, unsigned flags, int64_t batch, float alpha, float beta,
                      int c_type, int d_type, void *stream);
 
+/*
+ * Products over ragged groups of rows (mixture-of-experts layers).  The rows
+ * (tokens) are sorted by group (expert); `offsets`, in device memory, holds
+ * groups + 1 ascending row numbers, and group g owns the rows offsets[g] ..
+ * offsets[g+1]-1.  A group may be empty, and rows before offsets[0] or from
+ * offsets[groups] on belong to none.  The offsets are int64_t, or int32_t with
+ * GEMM_OFFSETS_I32, aligned to their size.  The host never reads them: nothing
+ * waits for the device, and a captured graph follows the offsets that are there
+ * at replay.  Values outside 0 .. the number of rows count as the nearest end,
+ * and where they do not ascend the results are unspecified, but no access
+ * leaves the operands.
+ *
+ * These calls need no workspace.  groups is at most 2^20; the limits on sizes,
+ * leading dimensions and extents are those of gemm_run.  M, N or groups == 0
+ * enqueues nothing; K == 0 gives D = cvt(beta * C).
+ */
+enum { GEMM_OFFSETS_I32 = 16u };
+
+/*
+ * D[i] = cvt_D(alpha * A[i] * B_g + beta * C[i]) for every row i of every group
+ * g, in gemm_run_ex's arithmetic and within gemm_run's error bound.  A: M x K
+ * row-major, M rows in all; B_g: K x N row-major, or column-major with
+ * GEMM_B_COLMAJOR (each B_g begins (K or N) * ldb elements after the one
+ * before); C and D: M x N row-major with a common ldc.  dtype: GEMM_F16 or
+ * GEMM_BF16; c_type, d_type, alpha, beta and aliasing as in gemm_run_ex.  Rows
+ * of D that no group owns are left as they were.  flags: GEMM_B_COLMAJOR and
+ * GEMM_OFFSETS_I32.
+ *
+ * With the other layout of the same B this is the input gradient of a layer:
+ * for Y = A W_g with W_g K x N row-major, dA = dY W_g^T is the product with B =
+ * W read as an N x K column-major matrix.
+ */
+int gemm_run_grouped(gemm_handle_t h, const void *A, const void *B, const void *C, void *D,
+                     const void *offsets, int64_t groups, int64_t M, int64_t N, int64_t K,
+                     int64_t lda, int64_t ldb, int64_t ldc, int dtype, unsigned flags, float alpha,
+                     float beta, int c_type, int d_type, void *stream);
+
+/*
+ * The weight gradients: D_g = cvt_D(alpha * X_g^T * Y_g + beta * C_g) for every
+ * group g, where X_g and Y_g are the group's rows of X (K x M, row-major) and Y
+ * (K x N, row-major), K rows in all.  C_g and D_g: M x N row-major with a
+ * common ldc, each beginning M * ldc elements after the one before.  An empty
+ * group's D_g is cvt(beta * C_g).  Rows that no group owns are not read.
+ * flags: GEMM_OFFSETS_I32.  Types, alpha, beta, aliasing and error bound (with
+ * the group's rows as K) as above.
+ */
+int gemm_run_grouped_wgrad(gemm_handle_t h, const void *X, const void *Y, const void *C, void *D,
+                           const void *offsets, int64_t groups, int64_t M, int64_t N, int64_t K,
+                           int64_t ldx, int64_t ldy, int64_t ldc, int dtype, unsigned flags,
+                           float alpha, float beta, int c_type, int d_type, void *stream);
+
+/* 8-bit float formats (OCP): e4m3 (largest value 448, no infinity) and e5m2 (57344). */
+typedef enum { GEMM_E4M3 = 0, GEMM_E5M2 = 1 } gemm_f8_t;
+
+/*
+ * Quantize X (batch x M x K; x_type GEMM_OUT_F32, _F16 or _BF16; row-major, or
+ * column-major with GEMM_A_COLMAJOR; batch entries (M or K) * ldx elements
+ * apart) to 8-bit floats with a scale for each block of 128 consecutive k of
+ * one row (block == 1) or of 128 rows (block == 128; the last row block and the
+ * last k-block may be shorter).  With top the format's largest value and
+ * a = max(the block's largest magnitude, 2^-100), in fp32 arithmetic:
+ *
+ *     scale = a / top,   q = round8(x * (top / a))   (to nearest even)
+ *
+ * so that x is about q * scale.  A block with an infinity or a NaN has the
+ * scale NaN and zeros for q.  Output, always K-contiguous:
+ *   Q:     batch x M x Kp bytes, Kp = 16 * ceil(K / 16), zeros past K; 16-byte
+ *          aligned;
+ *   scale: batch x ceil(K / 128) x ceil(M / block) floats.
+ * K == 0 enqueues nothing.  X needs element alignment.
+ */
+int gemm_quant8(gemm_handle_t h, const void *X, int64_t M, int64_t K, int64_t ldx, int x_type,
+                unsigned flags, int64_t batch, int block, int q_type, void *Q, float *scale,
+                void *stream);
+
+/*
+ * An 8-bit operand: `rows` rows of K-contiguous 8-bit floats, and its factors.
+ * q is 16-byte aligned, ld (bytes) a multiple of 16, and every row's bytes from
+ * K to the next multiple of 16 are zero.  The factor of row block r and k-block
+ * kb is scale[r * scale_row + kb * scale_k].  group and scale_group: bytes and
+ * floats from one group's operand to the next (read for B when groups > 1;
+ * group a multiple of 16).  256 * ld is below 2^31 - 2^22.  For gemm_quant8's
+ * output: ld = Kp, scale_row = 1, scale_k = ceil(M / block), group = M * Kp,
+ * scale_group = ceil(K / 128) * scale_k.
+ */
+typedef struct {
+    const void *q;
+    const float *scale;
+    int64_t ld;
+    int64_t scale_row, scale_k;
+    int64_t group, scale_group;
+    int type; /* gemm_f8_t */
+} gemm_q8_t;
+
+/*
+ * The product of 8-bit operands with a factor for each block of 128: with a the
+ * values of A (M rows, blocks of one row) and b those of B (the N columns of a
+ * K x N matrix as N rows, blocks of 128 rows),
+ *
+ *   acc[i][j] = sum over k-blocks kb of (sA[i][kb] * sB[j / 128][kb]) *
+ *                                       sum over k in kb of a[i][k] * b[j][k]
+ *   D[i][j]   = cvt_D(alpha * acc[i][j] + beta * C[i][j])
+ *
+ * The inner sums and acc are held in fp32, and each block enters acc by one
+ * fused multiply-add.  Per element |D - D_exact| <= 4*(K + 128)*2^-24 * S with
+ * S the same sum over magnitudes, plus the output stage's rounding.  With offsets the
+ * rows are grouped as above and row i of group g meets B_g; with offsets NULL
+ * (groups == 1) all M rows meet one B.  A and B may be of either format.
+ * flags: GEMM_OFFSETS_I32.  Everything else as in gemm_run_grouped.
+ */
+int gemm_run_scaled8(gemm_handle_t h, const gemm_q8_t *A, const gemm_q8_t *B, const void *C,
+                     void *D, const void *offsets, int64_t groups, int64_t M, int64_t N, int64_t K,
+                     int64_t ldc, unsigned flags, float alpha, float beta, int c_type, int d_type,
+                     void *stream);
+
 /* Release the handle's workspace (after synchronising its device) and the handle. */
 int gemm_destroy(gemm_handle_t h);
 

@@ -1,0 +1,344 @@
+"""Products over ragged groups of rows (gemm_grouped, gemm_grouped_wgrad) on the
+GPU against a plain 64-bit computation on the CPU.
+
+Tolerance per element, from the arithmetic alone: the header's accumulation bound
+4 K 2^-24 S (S: the sum of the products' magnitudes) times |alpha|, three fp32
+roundings of the output stage (alpha * acc, beta * c, their sum), and half a step
+of the output type."""
+import numpy as np
+import pytest
+
+from gpu_util import log
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def dmp():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import dense_mixed_precision_02_amd as dmp
+    return dmp
+
+
+def normal(seed, *shape, dtype):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn(*shape, generator=g).to(dtype)
+
+
+def offsets_of(counts, head=0):
+    return torch.tensor([head] + [int(x) for x in head + np.cumsum(counts)], dtype=torch.int64)
+
+
+def bound(S, k, alpha, acc, beta, c, ref, out_dtype):
+    """See the module's text; k is the number of products in a sum (a scalar or per row)."""
+    u = 2.0 ** -24
+    stage = u * (abs(alpha) * acc.abs() + (beta * c).abs() + 2 * ref.abs()) * 1.01
+    # half a step of the output type, and half its smallest subnormal
+    step = torch.finfo(out_dtype).eps / 2 * ref.abs() * 1.01 + \
+        {torch.float16: 2.0 ** -25, torch.bfloat16: 2.0 ** -134, torch.float32: 2.0 ** -150}[out_dtype]
+    return 4.0 * k * u * abs(alpha) * S * 1.01 + stage + step
+
+
+def check(got, ref, tol, what):
+    got = got.double().cpu()
+    assert torch.isfinite(got).all(), what
+    bad = (got - ref).abs() > tol
+    assert not bad.any(), f"{what}: {int(bad.sum())} over the bound, worst " \
+        f"{float(((got - ref).abs() / tol.clamp_min(1e-300)).max()):.3g}"
+
+
+def grouped_reference(A, B, off, alpha, beta, C):
+    A, B = A.double(), B.double()
+    T, N = A.shape[0], B.shape[2]
+    acc, S = torch.zeros(T, N, dtype=torch.float64), torch.zeros(T, N, dtype=torch.float64)
+    owned = torch.zeros(T, dtype=torch.bool)
+    for g in range(len(off) - 1):
+        lo, hi = int(off[g]), int(off[g + 1])
+        acc[lo:hi] = A[lo:hi] @ B[g]
+        S[lo:hi] = A[lo:hi].abs() @ B[g].abs()
+        owned[lo:hi] = True
+    c = C.double() if C is not None else torch.zeros(T, N, dtype=torch.float64)
+    return acc, S, alpha * acc + beta * c, c, owned
+
+
+# dtype, counts, head, tail, K, N, b_col, out, alpha, beta
+GROUPED = [
+    ("f16", [1], 0, 0, 1, 1, True, "f32", 1.0, 0.0),
+    ("bf16", [1], 0, 0, 64, 64, False, "bf16", 1.0, 0.0),
+    ("bf16", [0, 0, 3], 0, 0, 72, 40, True, "f32", 1.0, 0.0),
+    ("f16", [5, 0, 64, 65, 1, 0], 3, 9, 136, 200, True, "f32", 0.5, 2.0),
+    ("f16", [5, 0, 64, 65, 1, 0], 3, 9, 136, 200, False, "f16", 0.5, 2.0),
+    ("bf16", [17, 31, 0, 129], 0, 5, 99, 33, True, "f32", 1.0, 1.0),
+    ("bf16", [17, 31, 0, 129], 2, 0, 99, 33, False, "bf16", 1.0, 1.0),
+    ("bf16", [1] * 70 + [0] * 63 + [3, 2], 0, 0, 64, 72, True, "bf16", 1.0, 0.0),
+    ("f16", [0] * 128 + [7], 1, 1, 64, 72, False, "f32", 1.0, 0.0),
+    ("bf16", [300, 0, 511, 260], 0, 0, 512, 520, True, "bf16", 1.0, 0.0),
+    ("f16", [300, 0, 511, 260], 0, 7, 520, 264, False, "f32", 1.0, 1.0),
+    ("bf16", [1029, 513], 0, 0, 1032, 1024, True, "f32", 1.0, 0.0),
+    ("bf16", [2, 1, 0, 5, 16, 17], 0, 0, 2048, 512, True, "bf16", 1.0, 0.0),
+    ("f16", [33, 1, 8, 40], 0, 0, 1000, 264, True, "f32", 1.0, 1.0),
+    ("f16", [2, 0, 12], 0, 1, 4096, 130, False, "f16", 1.0, 0.0),
+]
+
+
+@pytest.mark.parametrize("case", GROUPED, ids=lambda c: f"{c[0]}-g{len(c[1])}-{c[4]}x{c[5]}-{'col' if c[6] else 'row'}")
+def test_grouped(dmp, case):
+    dt, counts, head, tail, K, N, b_col, out, alpha, beta = case
+    T, G = head + sum(counts) + tail, len(counts)
+    log(f"[grouped] {case}")
+    off = offsets_of(counts, head)
+    A = normal(1, T, K, dtype=DT[dt])
+    B = normal(2, G, N, K, dtype=DT[dt]).transpose(1, 2) if b_col else normal(2, G, K, N, dtype=DT[dt])
+    C = normal(3, T, N, dtype=DT[out]) if beta else None
+    acc, S, ref, c, owned = grouped_reference(A, B, off, alpha, beta, C)
+    D = torch.full((T, N), 7.0, dtype=DT[out], device="cuda")
+    r = dmp.gemm_grouped(A.cuda(), B.cuda(), off.cuda(), C.cuda() if beta else None, out=D, alpha=alpha, beta=beta)
+    assert r is D
+    torch.cuda.synchronize()
+    assert torch.equal(D[~owned.cuda()].cpu(), torch.full((int((~owned).sum()), N), 7.0, dtype=DT[out]))
+    tol = bound(S, K, alpha, acc, beta, c, ref, DT[out])
+    check(D[owned.cuda()], ref[owned], tol[owned], "grouped")
+    # int32 offsets, and a new output in the default type
+    D2 = dmp.gemm_grouped(A.cuda(), B.cuda(), off.int().cuda(), alpha=alpha)
+    assert D2.dtype == torch.float32
+    if beta == 0 and out == "f32":
+        assert torch.equal(D2[owned.cuda()], D[owned.cuda()])
+
+
+WGRAD = [
+    ("f16", [1], 0, 0, 1, 1, "f32", 1.0, 0.0),
+    ("bf16", [0, 1, 0], 0, 0, 8, 16, "bf16", 1.0, 0.0),
+    ("bf16", [63, 0, 64, 65, 200], 3, 9, 72, 136, "f32", 0.5, 2.0),
+    ("f16", [63, 0, 64, 65, 200], 3, 9, 33, 47, "f16", 1.0, 1.0),
+    ("f16", [5, 300, 1], 0, 3, 264, 520, "f32", 1.0, 1.0),
+    ("bf16", [1029, 130], 0, 0, 512, 256, "bf16", 1.0, 0.0),
+    ("bf16", [3] * 70, 1, 0, 16, 24, "f32", 1.0, 0.0),
+    ("f16", [0, 0], 4, 0, 64, 64, "f32", 1.0, 1.0),
+    ("f16", [0, 0], 4, 0, 64, 64, "f32", 1.0, 0.0),
+]
+
+
+@pytest.mark.parametrize("case", WGRAD, ids=lambda c: f"{c[0]}-g{len(c[1])}-{c[4]}x{c[5]}")
+def test_wgrad(dmp, case):
+    dt, counts, head, tail, M, N, out, alpha, beta = case
+    T, G = head + sum(counts) + tail, len(counts)
+    log(f"[wgrad] {case}")
+    off = offsets_of(counts, head)
+    X, Y = normal(4, T, M, dtype=DT[dt]), normal(5, T, N, dtype=DT[dt])
+    X[:head], Y[T - tail:] = float("nan"), float("inf")  # rows of no group are not read
+    C = normal(6, G, M, N, dtype=DT[out]) if beta else None
+    acc, S = torch.zeros(G, M, N, dtype=torch.float64), torch.zeros(G, M, N, dtype=torch.float64)
+    for g in range(G):
+        lo, hi = int(off[g]), int(off[g + 1])
+        x, y = X[lo:hi].double(), Y[lo:hi].double()
+        acc[g], S[g] = x.t() @ y, x.abs().t() @ y.abs()
+    c = C.double() if beta else torch.zeros_like(acc)
+    ref = alpha * acc + beta * c
+    D = dmp.gemm_grouped_wgrad(X.cuda(), Y.cuda(), off.cuda(), C.cuda() if beta else None, alpha=alpha,
+                               beta=beta, out_dtype=DT[out])
+    k = torch.tensor([max(1, n) for n in counts], dtype=torch.float64)[:, None, None]
+    check(D, ref, bound(S, k, alpha, acc, beta, c, ref, DT[out]), "wgrad")
+    if beta:  # in place
+        Cg = C.cuda()
+        assert dmp.gemm_grouped_wgrad(X.cuda(), Y.cuda(), off.int().cuda(), Cg, out=Cg, alpha=alpha, beta=beta) is Cg
+        assert torch.equal(Cg, D)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("K,N,b_col", [(256, 512, True), (264, 136, False), (77, 50, True), (1024, 768, True)])
+def test_small_integers_are_exact(dmp, dt, K, N, b_col):
+    """Products of small integers, every sum below 2^24: no rounding anywhere."""
+    counts = [0, 300, 1, 64, 2, 17]
+    T, off = sum(counts), offsets_of(counts)
+    g = torch.Generator().manual_seed(7)
+    A = torch.randint(-2, 3, (T, K), generator=g).to(DT[dt])
+    B = torch.randint(-2, 3, (len(counts), N, K) if b_col else (len(counts), K, N), generator=g).to(DT[dt])
+    B = B.transpose(1, 2) if b_col else B
+    Y = torch.randint(-2, 3, (T, N), generator=g).to(DT[dt])
+    ref = grouped_reference(A, B, off, 1.0, 0.0, None)[0]
+    D = dmp.gemm_grouped(A.cuda(), B.cuda(), off.cuda())
+    assert torch.equal(D.double().cpu(), ref)
+    W = dmp.gemm_grouped_wgrad(A.cuda(), Y.cuda(), off.cuda())
+    want = torch.stack([A[int(a):int(b)].double().t() @ Y[int(a):int(b)].double() for a, b in zip(off[:-1], off[1:])])
+    assert torch.equal(W.double().cpu(), want)
+
+
+def test_strided_operands_and_padding_stay(dmp):
+    """Leading dimensions larger than the rows; the columns past N of a padded output
+    stay, and a misaligned base address is served."""
+    counts = [40, 0, 25]
+    T, K, N, off = 65, 48, 56, offsets_of(counts)
+    for shift in (0, 1):
+        buf = normal(8, T * 80 + shift, dtype=torch.float16).cuda()
+        A = buf[shift:].view(T, 80)[:, :K]
+        B = normal(9, 3, K, N, dtype=torch.float16)
+        acc, S, ref, c, _ = grouped_reference(A.cpu(), B, off, 1.0, 0.0, None)
+        D = torch.full((T, 64), 7.0, device="cuda")
+        dmp.gemm_grouped(A, B.cuda(), off.cuda(), out=D[:, :N])
+        check(D[:, :N], ref, bound(S, K, 1.0, acc, 0.0, c, ref, torch.float32), f"strided, shift {shift}")
+        assert (D[:, N:] == 7.0).all()
+
+
+def test_one_group_is_the_dense_product(dmp):
+    """A single group that owns every row: gemm's product, to its bound."""
+    A, B = normal(10, 200, 128, dtype=torch.bfloat16).cuda(), normal(11, 1, 128, 192, dtype=torch.bfloat16).cuda()
+    off = torch.tensor([0, 200], device="cuda")
+    d, e = dmp.gemm_grouped(A, B, off).double(), dmp.gemm(A, B[0]).double()
+    S = A.double().abs().cpu() @ B[0].double().abs().cpu()
+    assert ((d - e).cpu().abs() <= 2 * 4 * 128 * 2.0 ** -24 * S).all()
+
+
+def test_k0_and_empty_sizes(dmp):
+    off = torch.tensor([0, 2, 3], device="cuda")
+    A, B = torch.empty(3, 0, dtype=torch.float16, device="cuda"), torch.empty(2, 0, 8, dtype=torch.float16, device="cuda")
+    C = torch.arange(24.0, device="cuda").view(3, 8)
+    assert torch.equal(dmp.gemm_grouped(A, B, off, C, beta=0.5), 0.5 * C)
+    e = torch.empty(0, 16, dtype=torch.float16, device="cuda")
+    z = torch.zeros(3, dtype=torch.int64, device="cuda")
+    assert dmp.gemm_grouped(e, torch.ones(2, 16, 8, dtype=torch.float16, device="cuda"), z).shape == (0, 8)
+    assert torch.equal(dmp.gemm_grouped_wgrad(e, e, z), torch.zeros(2, 16, 16, device="cuda"))
+    assert dmp.gemm_grouped(torch.ones(4, 16, dtype=torch.float16, device="cuda"),
+                            torch.empty(0, 16, 8, dtype=torch.float16, device="cuda"), z[:1]).shape == (4, 8)
+
+
+def test_offsets_out_of_range_touch_nothing_outside(dmp):
+    """The kernels bring every offset into 0 .. T: guards around the output stay."""
+    T, K, N, G = 100, 64, 72, 4
+    A, B = normal(12, T, K, dtype=torch.bfloat16).cuda(), normal(13, G, K, N, dtype=torch.bfloat16).cuda()
+    for off in ([-5, 20, 1 << 40, 90, 300], [90, 10, 50, 0, 100], [1 << 33] * 5, [-1] * 5):
+        buf = torch.full((T + 200, N), 7.0, device="cuda")
+        dmp.gemm_grouped(A, B, torch.tensor(off, device="cuda"), out=buf[100:100 + T])
+        w = torch.full((G + 2, K, N), 7.0, device="cuda")
+        dmp.gemm_grouped_wgrad(A, A.new_ones(T, N), torch.tensor(off, device="cuda"), out=w[1:1 + G])
+        torch.cuda.synchronize()
+        assert (buf[:100] == 7.0).all() and (buf[100 + T:] == 7.0).all()
+        assert (w[0] == 7.0).all() and (w[-1] == 7.0).all()
+        assert torch.isfinite(w).all()
+
+
+def test_not_finite_values_stay_in_their_rows(dmp):
+    """A NaN in a row of A reaches that row of D alone, also next to a group's border."""
+    counts = [70, 58]
+    A, B = normal(14, 128, 64, dtype=torch.float16), normal(15, 2, 64, 64, dtype=torch.float16)
+    clean = dmp.gemm_grouped(A.cuda(), B.cuda(), offsets_of(counts).cuda())
+    A[69, 5], A[70, 6] = float("nan"), float("inf")
+    D = dmp.gemm_grouped(A.cuda(), B.cuda(), offsets_of(counts).cuda())
+    assert torch.isnan(D[69]).all() and not torch.isfinite(D[70]).any()
+    keep = [i for i in range(128) if i not in (69, 70)]
+    assert torch.equal(D[keep], clean[keep])
+
+
+def test_same_result_every_time_and_on_another_stream(dmp):
+    counts = [300, 0, 77, 1]
+    A, B = normal(16, 378, 256, dtype=torch.bfloat16).cuda(), normal(17, 4, 256, 264, dtype=torch.bfloat16).cuda()
+    Y, off = normal(18, 378, 264, dtype=torch.bfloat16).cuda(), offsets_of(counts).cuda()
+    D, W = dmp.gemm_grouped(A, B, off), dmp.gemm_grouped_wgrad(A, Y, off)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        D2, W2 = dmp.gemm_grouped(A, B, off), dmp.gemm_grouped_wgrad(A, Y, off)
+    s.synchronize()
+    assert torch.equal(D, D2) and torch.equal(W, W2)
+
+
+def test_captured_graph_follows_the_offsets(dmp):
+    """A forward product, its input gradient and weight gradient in one graph, replayed
+    with eager work between and then on other offsets and inputs."""
+    T, K, N, G = 260, 128, 136, 5
+    A, dY = normal(19, T, K, dtype=torch.bfloat16).cuda(), normal(20, T, N, dtype=torch.bfloat16).cuda()
+    B = normal(21, G, K, N, dtype=torch.bfloat16).cuda()
+    off = offsets_of([100, 0, 60, 99, 1]).cuda()
+    outs = [torch.zeros(T, N, device="cuda"), torch.zeros(T, K, device="cuda"), torch.zeros(G, K, N, device="cuda")]
+
+    def step(o):
+        dmp.gemm_grouped(A, B, off, out=o[0])
+        dmp.gemm_grouped(dY, B.transpose(1, 2), off, out=o[1])
+        dmp.gemm_grouped_wgrad(A, dY, off, out=o[2])
+
+    want = [torch.zeros_like(o) for o in outs]
+    step(want)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step(outs)  # a handle of this stream is there before the capture
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        step(outs)
+    for r in range(3):
+        for o in outs:
+            o.zero_()
+        dmp.gemm(A, B[0])
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want)), f"replay {r}"
+    off.copy_(offsets_of([3, 57, 0, 0, 200]))
+    A.copy_(normal(22, T, K, dtype=torch.bfloat16))
+    step(want)
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_expert_layer_gradients_against_differences(dmp):
+    """A two-layer expert block, Y = relu(X W1_g) W2_g, its gradients by the library's
+    products against central differences of the same loss in 64 bits, along a random
+    direction v for each of X, W1 and W2.  One bf16 rounding (half a step, 2^-8
+    relative) lies on every term's path (of the hidden values, or of their gradient),
+    so the quotient may be off by 2^-8 times the sum of the terms' magnitudes; the fp32
+    sums over at most 128 values add 4 * 128 * 2^-24 twice of the sums over all the
+    factors' magnitudes, below 1e-4 of them (which also covers the quotient's own
+    64-bit rounding).  The step is far below the smallest hidden value, so none
+    crosses zero."""
+    counts, K, H = [37, 0, 64, 27], 64, 96
+    T, G, off = sum(counts), len(counts), offsets_of(counts)
+    X = normal(23, T, K, dtype=torch.bfloat16)
+    W1 = (normal(24, G, K, H, dtype=torch.float32) / 8).to(torch.bfloat16)
+    W2 = (normal(25, G, H, K, dtype=torch.float32) / 10).to(torch.bfloat16)
+    R = normal(26, T, K, dtype=torch.bfloat16)  # loss = sum(R * Y)
+    c = [t.cuda() for t in (X, W1, W2, R, off)]
+    h = dmp.gemm_grouped(c[0], c[1], c[4], out_dtype=torch.bfloat16)
+    a = h.clamp_min(0)
+    dW2 = dmp.gemm_grouped_wgrad(a, c[3], c[4])
+    da = dmp.gemm_grouped(c[3], c[2].transpose(1, 2), c[4], out_dtype=torch.bfloat16)
+    dh = torch.where(h > 0, da, torch.zeros_like(da))
+    dW1 = dmp.gemm_grouped_wgrad(c[0], dh, c[4])
+    dX = dmp.gemm_grouped(dh, c[1].transpose(1, 2), c[4])
+
+    x, w1, w2, r = X.double(), W1.double(), W2.double(), R.double()
+    rows = [slice(int(off[g]), int(off[g + 1])) for g in range(G)]
+
+    def each(f):  # one result per group, joined along the rows
+        return torch.cat([f(g, s) for g, s in enumerate(rows)])
+
+    def loss(x, w1, w2):
+        return (r * each(lambda g, s: (x[s] @ w1[g]).clamp_min(0) @ w2[g])).sum()
+
+    hid = each(lambda g, s: x[s] @ w1[g])
+    eps = 1e-7
+    ad, dhd = a.double().cpu().abs(), dh.double().cpu().abs()
+    big_dh = each(lambda g, s: r[s].abs() @ w2[g].abs().t())
+    big_a = each(lambda g, s: x[s].abs() @ w1[g].abs())
+    for i, (grad, base) in enumerate([(dX, x), (dW1, w1), (dW2, w2)]):
+        v = normal(30 + i, *base.shape, dtype=torch.float64)
+        assert float(hid.abs().min()) > 100 * eps
+        args = [x, w1, w2]
+        args[i] = base + eps * v
+        up = loss(*args)
+        args[i] = base - eps * v
+        quotient = float((up - loss(*args)) / (2 * eps))
+
+        def size(d, hidden):  # sum of the magnitudes of <gradient, v>'s terms
+            if i == 0:
+                return float((each(lambda g, s: d[s] @ w1[g].abs().t()) * v.abs()).sum())
+            left, right = (x.abs(), d) if i == 1 else (hidden, r.abs())
+            return float(sum((left[s].t() @ right[s] * v[g].abs()).sum() for g, s in enumerate(rows)))
+
+        tol = 1.01 * 2.0 ** -8 * size(dhd, ad) + 1e-4 * size(big_dh, big_a)
+        assert abs(float((grad.double().cpu() * v).sum()) - quotient) <= tol, i
