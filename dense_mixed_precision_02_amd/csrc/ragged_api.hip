@@ -8,6 +8,7 @@
 #include "quant8.hpp"
 #include "ragged.hpp"
 #include "ragged_plan.hpp"
+#include "ragged_tile.hpp"
 
 using namespace dmp;
 using namespace dmp::plan;
@@ -34,6 +35,25 @@ int launch_any(const RaggedArgs &a, hipStream_t s) {
     if (grid > 0x7fffffff) return GEMM_ERR_INVALID_ARG;
     hipLaunchKernelGGL((ragged_any<DT, AK, BKC, MODE>), dim3((unsigned)grid), dim3(256), 0, s, a);
     return launched();
+}
+
+template <class DT, int E, bool AK, bool BKC, int MODE>
+int launch_tile(RaggedArgs a, hipStream_t s) {
+    a.tiles_m = MODE == RAGGED_WGRAD ? (int)cdiv(a.M, E) : 0;
+    a.tiles_n = (int)cdiv(a.N, E);
+    // row tiles: at most one more for each group than the rows fill
+    const int64_t grid = MODE == RAGGED_WGRAD ? (int64_t)a.groups * a.tiles_m * a.tiles_n
+                                              : (cdiv(a.M, E) + a.groups) * a.tiles_n;
+    if (grid > 0x7fffffff) return GEMM_ERR_INVALID_ARG;
+    hipLaunchKernelGGL((ragged_tile<DT, E, E, AK, BKC, MODE>), dim3((unsigned)grid), dim3(256), 0, s, a);
+    return launched();
+}
+
+template <class DT, bool AK, bool BKC, int MODE>
+int launch_cfg(int cfg, const RaggedArgs &a, hipStream_t s) {
+    if (cfg == CFG_L) return launch_tile<DT, 256, AK, BKC, MODE>(a, s);
+    if (cfg == CFG_M) return launch_tile<DT, 128, AK, BKC, MODE>(a, s);
+    return launch_any<DT, AK, BKC, MODE>(a, s);
 }
 
 template <int XT, int FMT>
@@ -67,9 +87,12 @@ int gemm_run_grouped(gemm_handle_t h, const void *A, const void *B, const void *
     a.tiles_n = (int)cdiv(N, 64);
     a.ep = ep;
     hipStream_t s = (hipStream_t)stream;
+    const int cfg = grouped_cfg(h->num_cus, A, B, groups, M, N, K, lda, ldb, bc);
     if (dtype == GEMM_F16)
-        return bc ? launch_any<F16, true, true, RAGGED_ROWS>(a, s) : launch_any<F16, true, false, RAGGED_ROWS>(a, s);
-    return bc ? launch_any<BF16, true, true, RAGGED_ROWS>(a, s) : launch_any<BF16, true, false, RAGGED_ROWS>(a, s);
+        return bc ? launch_cfg<F16, true, true, RAGGED_ROWS>(cfg, a, s)
+                  : launch_cfg<F16, true, false, RAGGED_ROWS>(cfg, a, s);
+    return bc ? launch_cfg<BF16, true, true, RAGGED_ROWS>(cfg, a, s)
+              : launch_cfg<BF16, true, false, RAGGED_ROWS>(cfg, a, s);
 }
 
 int gemm_run_grouped_wgrad(gemm_handle_t h, const void *X, const void *Y, const void *C, void *D,
@@ -89,8 +112,9 @@ int gemm_run_grouped_wgrad(gemm_handle_t h, const void *X, const void *Y, const 
     a.tiles_n = (int)cdiv(N, 64);
     a.ep = ep;
     hipStream_t s = (hipStream_t)stream;
-    return dtype == GEMM_F16 ? launch_any<F16, false, false, RAGGED_WGRAD>(a, s)
-                             : launch_any<BF16, false, false, RAGGED_WGRAD>(a, s);
+    const int cfg = wgrad_cfg(h->num_cus, X, Y, groups, M, N, K, ldx, ldy);
+    return dtype == GEMM_F16 ? launch_cfg<F16, false, false, RAGGED_WGRAD>(cfg, a, s)
+                             : launch_cfg<BF16, false, false, RAGGED_WGRAD>(cfg, a, s);
 }
 
 int gemm_quant8(gemm_handle_t h, const void *X, int64_t M, int64_t K, int64_t ldx, int x_type,

@@ -127,5 +127,27 @@ inline int validate_quant8(gemm_handle_t h, const void *X, int64_t M, int64_t K,
     return GEMM_OK;
 }
 
+// ---------------------------------------------------------------------------
+// Which kernel.  The host knows the rows in all and the number of groups, not
+// how the rows are spread; the rules go by the mean.
+// ---------------------------------------------------------------------------
+
+// Grouped rows: 16-byte granules need aligned operands, whole granules along
+// the contiguous extents and 31-bit offsets inside a tile.
+inline int grouped_cfg(int num_cus, const void *A, const void *B, int64_t groups, int64_t M, int64_t N,
+                       int64_t K, int64_t lda, int64_t ldb, bool b_col) {
+    if (K == 0 || !granule_ok(A, B, M, N, K, lda, ldb, GEMM_F16, false, b_col, true)) return CFG_GENERIC;
+    const int64_t tiles = (cdiv(M, 256) + groups / 2) * cdiv(N, 256);
+    if (M / groups >= 192 && tiles >= num_cus) return CFG_L;
+    return CFG_M;
+}
+
+inline int wgrad_cfg(int num_cus, const void *X, const void *Y, int64_t groups, int64_t M, int64_t N,
+                     int64_t K, int64_t ldx, int64_t ldy) {
+    if (K == 0 || !granule_ok(X, Y, M, N, K, ldx, ldy, GEMM_F16, true, false, true)) return CFG_GENERIC;
+    if (groups * cdiv(M, 256) * cdiv(N, 256) >= num_cus) return CFG_L;
+    return CFG_M;
+}
+
 }  // namespace plan
 }  // namespace dmp
