@@ -292,33 +292,12 @@ __global__ __launch_bounds__(256) void ragged_any(const RaggedArgs p) {
             for (int j = 0; j < TN; ++j)
                 fb[j][s] = frag16<DT, typename LB::Op, BN, BKC>(lb, wn * 32 + j * 16, s, lane);
         }
-        if constexpr (MODE == RAGGED_SCALED) {
-            const float sb = p.sb[at.group * p.sb_group + (at.col0 >> 7) * p.sb_col + kt * p.sb_k];
 #pragma unroll
-            for (int i = 0; i < TM; ++i) {
-                floatx4 s;
+        for (int s = 0; s < 2; ++s)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int r = wm * 32 + i * 16 + 4 * (lane >> 4) + q;
-                    s[q] = r < at.rows ? p.sa[(at.row0 + r) * p.sa_row + kt * p.sa_k] * sb : 0.0f;
-                }
+            for (int i = 0; i < TM; ++i)
 #pragma unroll
-                for (int j = 0; j < TN; ++j) {
-                    const intx8 a = __builtin_shufflevector(fa[i][0], fa[i][1], 0, 1, 2, 3, 4, 5, 6, 7);
-                    const intx8 b = __builtin_shufflevector(fb[j][0], fb[j][1], 0, 1, 2, 3, 4, 5, 6, 7);
-                    const floatx4 part = DT::mma(a, b, floatx4{0, 0, 0, 0});
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) acc[i][j][q] = __builtin_fmaf(s[q], part[q], acc[i][j][q]);
-                }
-            }
-        } else {
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int i = 0; i < TM; ++i)
-#pragma unroll
-                    for (int j = 0; j < TN; ++j) acc[i][j] = mma16<DT>(fa[i][s], fb[j][s], acc[i][j]);
-        }
+                for (int j = 0; j < TN; ++j) acc[i][j] = mma16<DT>(fa[i][s], fb[j][s], acc[i][j]);
         if (kt + 1 < nkt) put((kt + 1) & 1);
         __syncthreads();
     }

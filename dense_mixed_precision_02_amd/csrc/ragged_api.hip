@@ -9,6 +9,7 @@
 #include "ragged.hpp"
 #include "ragged_plan.hpp"
 #include "ragged_tile.hpp"
+#include "scaled_tile.hpp"
 
 using namespace dmp;
 using namespace dmp::plan;
@@ -54,6 +55,25 @@ int launch_cfg(int cfg, const RaggedArgs &a, hipStream_t s) {
     if (cfg == CFG_L) return launch_tile<DT, 256, AK, BKC, MODE>(a, s);
     if (cfg == CFG_M) return launch_tile<DT, 128, AK, BKC, MODE>(a, s);
     return launch_any<DT, AK, BKC, MODE>(a, s);
+}
+
+template <int FA, int FB, int BM, int BN, int WM, int WN, bool EXACT>
+int launch_scaled_tile(RaggedArgs a, hipStream_t s) {
+    a.tiles_n = (int)cdiv(a.N, BN);
+    const int64_t grid = (cdiv(a.M, BM) + a.groups) * a.tiles_n;
+    if (grid > 0x7fffffff) return GEMM_ERR_INVALID_ARG;
+    hipLaunchKernelGGL((scaled_tile<FA, FB, BM, BN, WM, WN, EXACT>), dim3((unsigned)grid), dim3(WM * WN * 64), 0, s, a);
+    return launched();
+}
+
+template <int FA, int FB>
+int launch_scaled(int cfg, const RaggedArgs &a, hipStream_t s) {
+    const bool exact = a.ep.d_type == OUT_F32;
+    if (cfg == CFG_L)
+        return exact ? launch_scaled_tile<FA, FB, 256, 128, 4, 2, true>(a, s)
+                     : launch_scaled_tile<FA, FB, 256, 256, 2, 4, false>(a, s);
+    return exact ? launch_scaled_tile<FA, FB, 128, 128, 2, 2, true>(a, s)
+                 : launch_scaled_tile<FA, FB, 128, 128, 2, 2, false>(a, s);
 }
 
 template <int XT, int FMT>
@@ -161,9 +181,10 @@ int gemm_run_scaled8(gemm_handle_t h, const gemm_q8_t *A, const gemm_q8_t *B, co
     a.tiles_n = (int)cdiv(N, 64);
     a.ep = ep;
     hipStream_t s = (hipStream_t)stream;
+    const int cfg = scaled_cfg(h->num_cus, groups, M, N);
     const bool a4 = A->type == GEMM_E4M3, b4 = B->type == GEMM_E4M3;
-    if (a4) return b4 ? launch_any<F8<0, 0>, true, true, RAGGED_SCALED>(a, s) : launch_any<F8<0, 1>, true, true, RAGGED_SCALED>(a, s);
-    return b4 ? launch_any<F8<1, 0>, true, true, RAGGED_SCALED>(a, s) : launch_any<F8<1, 1>, true, true, RAGGED_SCALED>(a, s);
+    if (a4) return b4 ? launch_scaled<0, 0>(cfg, a, s) : launch_scaled<0, 1>(cfg, a, s);
+    return b4 ? launch_scaled<1, 0>(cfg, a, s) : launch_scaled<1, 1>(cfg, a, s);
 }
 
 }  // extern "C"

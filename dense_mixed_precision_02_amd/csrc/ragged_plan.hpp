@@ -149,5 +149,10 @@ inline int wgrad_cfg(int num_cus, const void *X, const void *Y, int64_t groups, 
     return CFG_M;
 }
 
+inline int scaled_cfg(int num_cus, int64_t groups, int64_t M, int64_t N) {
+    const int64_t tiles = (cdiv(M, 256) + groups / 2) * cdiv(N, 256);
+    return M / groups >= 192 && tiles >= num_cus ? CFG_L : CFG_M;
+}
+
 }  // namespace plan
 }  // namespace dmp

@@ -1,0 +1,217 @@
+// scaled_tile.hpp -- 8-bit block-scaled products on BM x BN tiles.
+//
+// A k-tile is 128 bytes: one k-block of the scales.  Both operands are
+// K-contiguous and come straight to LDS, double buffered.  The factors of the
+// k-tile, sA[row] * sB[column block] for every row and 128-column block of the
+// tile, are formed once by the workgroup and put beside the operands, so a wave
+// reads four of them with one LDS read for each 16 x 16 block of rows.  Every
+// 16 x 16 block's sum over the k-block starts from zero and enters the
+// accumulator by four fused multiply-adds.  So the accumulators are in the
+// ordinary registers (vector instructions cannot write the accumulation
+// registers), which limits a wave to a 128 x 64 part of the tile: two waves to
+// a SIMD, one's multiply-adds running beside the other's matrix instructions.
+//
+// Two ways to the k-block's sum:
+//  * the 8-bit matrix instruction on 128 k.  Within every 8 consecutive k it
+//    aligns the products to the largest and drops what lies 13 bits below
+//    (found by feeding it pairs of powers of two), an error of about 1.5e-5 of
+//    a sum of random terms.  It is used where D has 16 bits, whose own rounding
+//    is 2e-3 (bf16) or 2.4e-4 (fp16) of each value.
+//  * EXACT, where D is fp32: the bytes are widened to bf16, which holds every
+//    e4m3 and e5m2 value, and the bf16 instruction (half the rate) sums exact
+//    products in fp32.
+#pragma once
+#include "ragged_tile.hpp"
+
+namespace dmp {
+
+// Bytes 8 h .. 8 h + 7 of a granule as eight bf16 values (exact).
+template <int FMT>
+__device__ static inline intx4 widen8(const intx4 &v, int h) {
+    intx4 r;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        const uint32_t x = (uint32_t)v[2 * h + w];
+        if constexpr (FMT == 0) {
+            r[2 * w] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, 1.0f, false));
+            r[2 * w + 1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, 1.0f, true));
+        } else {
+            r[2 * w] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(x, 1.0f, false));
+            r[2 * w + 1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(x, 1.0f, true));
+        }
+    }
+    return r;
+}
+
+template <int FA, int FB, int BM, int BN, int WM, int WN, bool EXACT>
+__global__ __launch_bounds__(WM *WN * 64, 2) void scaled_tile(const RaggedArgs p) {
+    using DT = F8<FA, FB>;
+    constexpr int NW = WM * WN, WTM = BM / WM, WTN = BN / WN;
+    constexpr int TM = WTM / 16, TN = WTN / 16, KT = 128;
+    static_assert(128 % WTN == 0, "a wave's columns lie in one block of B's scales");
+    using OpA = Operand<DT, BM, NW, true>;
+    using OpB = Operand<DT, BN, NW, true>;
+    constexpr int NB = BN / 128, ITEMS = BM * NB;
+    static_assert(ITEMS <= NW * 64, "a factor to a thread");
+    __shared__ __attribute__((aligned(1024))) char lds_a0[OpA::BYTES];
+    __shared__ __attribute__((aligned(1024))) char lds_b0[OpB::BYTES];
+    __shared__ __attribute__((aligned(1024))) char lds_a1[OpA::BYTES];
+    __shared__ __attribute__((aligned(1024))) char lds_b1[OpB::BYTES];
+    __shared__ __attribute__((aligned(16))) float sc0[ITEMS], sc1[ITEMS];
+    DMP_LDS char *LA[2] = {(DMP_LDS char *)lds_a0, (DMP_LDS char *)lds_a1};
+    DMP_LDS char *LB[2] = {(DMP_LDS char *)lds_b0, (DMP_LDS char *)lds_b1};
+    DMP_LDS float *SC[2] = {(DMP_LDS float *)sc0, (DMP_LDS float *)sc1};
+
+    const int lane = lane_id(), wave = wave_id(), tid = threadIdx.x;
+    const int wm = wave / WN, wn = wave % WN;
+    const int total = (int)p.M;
+
+    GroupWalk<BM> count, walk;
+    count.load(p, total, lane);
+    walk = count;
+    const int64_t tiles = (int64_t)count.all(p, total, lane) * p.tiles_n;
+    if ((int64_t)blockIdx.x >= tiles) return;
+    const int t = xcd_remap(blockIdx.x, (int)tiles);
+    int g, r0, r1, tile0, tm, tn;
+    if (!walk.find(p, total, lane, t / p.tiles_n, g, r0, r1, tile0)) return;
+    grouped_order(t - tile0 * p.tiles_n, (r1 - r0 - 1) / BM + 1, p.tiles_n, tm, tn);
+    const TileAt at = tile_at<DT, true, true, RAGGED_SCALED, BM, BN>(p, g, r0, r1, tm, tn);
+
+    const int kspan = (int)at.k, nkt = (kspan + KT - 1) / KT;
+    OpA opa;
+    OpB opb;
+    opa.init(wave, lane, p.lda, 0, at.rows);
+    opb.init(wave, lane, p.ldb, 0, at.cols);
+    auto copy = [&](int kt, int buf) {
+        const int64_t k0 = (int64_t)kt * KT;
+        const int kleft = min(kspan - kt * KT, KT);
+        const __amdgpu_buffer_rsrc_t ra = make_rsrc(OpA::tile_base(at.A, p.lda, 0, k0));
+        const __amdgpu_buffer_rsrc_t rb = make_rsrc(OpB::tile_base(at.B, p.ldb, 0, k0));
+#pragma unroll
+        for (int c = 0; c < OpA::CPW; ++c) opa.issue(ra, LA[buf], wave, c, kleft, at.rows);
+#pragma unroll
+        for (int c = 0; c < OpB::CPW; ++c) opb.issue(rb, LB[buf], wave, c, kleft, at.cols);
+    };
+    // this thread's factor: row srow of the tile, column block snb
+    const int srow = tid % BM, snb = tid / BM;
+    const bool has = tid < ITEMS && srow < at.rows && 128 * snb < at.cols;
+    const float *sa = p.sa + (at.row0 + srow) * p.sa_row;
+    const float *sb = p.sb + g * p.sb_group + ((at.col0 >> 7) + snb) * p.sb_col;
+    float va = 0.0f, vb = 0.0f;
+    auto fetch = [&](int kt) {
+        if (has) {
+            va = sa[kt * p.sa_k];
+            vb = sb[kt * p.sb_k];
+        }
+    };
+    auto put = [&](int buf) {
+        if (tid < ITEMS) SC[buf][snb * BM + srow] = va * vb;
+    };
+
+    floatx4 acc[TM][TN] = {};
+    const int nb = (wn * WTN) >> 7;
+    // One k-tile: row blocks i in turn.  While the matrix instructions of row
+    // block i run, the sums of row block i - 1 enter the accumulators and the
+    // fragment and factors of i + 1 are read.  The scheduling barriers keep this
+    // order; without them the compiler draws all row blocks' reads together and
+    // spills.
+    auto compute = [&](int buf) {
+        // frag16's place for rows that begin at a multiple of 16: the swizzle then
+        // depends on the lane alone, and a row block is an immediate offset
+        const int own = (lane & 15) * 128, sw = swz(lane & 15), gr = 2 * (lane >> 4);
+        const int off[2] = {own + ((gr ^ sw) << 4), own + (((gr + 1) ^ sw) << 4)};
+        const DMP_LDS char *la[2], *lb[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            la[h] = LA[buf] + wm * WTM * 128 + off[h];
+            lb[h] = LB[buf] + wn * WTN * 128 + off[h];
+        }
+        auto frag = [&](const DMP_LDS char *l, int blk) { return *(const DMP_LDS intx4 *)(l + blk * 2048); };
+        const DMP_LDS float *sc = SC[buf] + nb * BM + wm * WTM + 4 * (lane >> 4);
+        intx4 b[TN][EXACT ? 4 : 2];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            const intx4 lo = frag(lb[0], j), hi = frag(lb[1], j);
+            if constexpr (EXACT) {
+                b[j][0] = widen8<FB>(lo, 0); b[j][1] = widen8<FB>(lo, 1);
+                b[j][2] = widen8<FB>(hi, 0); b[j][3] = widen8<FB>(hi, 1);
+            } else {
+                b[j][0] = lo; b[j][1] = hi;
+            }
+        }
+        intx4 lo[2], hi[2];
+        floatx4 s[3], part[2][TN];
+        auto read = [&](int i) {
+            lo[i & 1] = frag(la[0], i);
+            hi[i & 1] = frag(la[1], i);
+            s[i % 3] = *(const DMP_LDS floatx4 *)(sc + i * 16);
+        };
+        auto add = [&](int i, int j) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                acc[i][j][q] = __builtin_fmaf(s[i % 3][q], part[i & 1][j][q], acc[i][j][q]);
+            asm volatile("" : "+v"(acc[i][j]));  // here, not sunk to where the sum is next used
+        };
+        read(0);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            if (i + 1 < TM) read(i + 1);
+            intx4 a[4];
+            if constexpr (EXACT) {
+                a[0] = widen8<FA>(lo[i & 1], 0); a[1] = widen8<FA>(lo[i & 1], 1);
+                a[2] = widen8<FA>(hi[i & 1], 0); a[3] = widen8<FA>(hi[i & 1], 1);
+            }
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                floatx4 c = {0, 0, 0, 0};
+                if constexpr (EXACT) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) c = mma16<BF16>(a[q], b[j][q], c);
+                } else {
+                    const intx8 a8 = __builtin_shufflevector(lo[i & 1], hi[i & 1], 0, 1, 2, 3, 4, 5, 6, 7);
+                    const intx8 b8 = __builtin_shufflevector(b[j][0], b[j][1], 0, 1, 2, 3, 4, 5, 6, 7);
+                    c = DT::mma(a8, b8, c);
+                }
+                part[i & 1][j] = c;
+                if (i > 0) add(i - 1, j);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < TN; ++j) add(TM - 1, j);
+    };
+    if (nkt > 0) {
+        copy(0, 0);
+        fetch(0);
+        put(0);
+        wait_vmcnt<0>();
+    }
+    __syncthreads();
+    auto ktile = [&](int kt, int cur) {
+        const bool more = kt + 1 < nkt;
+        if (more) {
+            copy(kt + 1, cur ^ 1);
+            fetch(kt + 1);
+        }
+        compute(cur);
+        if (more) put(cur ^ 1);
+        wait_vmcnt<0>();
+        __syncthreads();
+    };
+    for (int kt = 0; kt < nkt; kt += 2) {
+        ktile(kt, 0);
+        if (kt + 1 < nkt) ktile(kt + 1, 1);
+    }
+    // each wave's slab in one of the operand buffers, as many as fit each
+    constexpr int SLAB = 32 * (WTN + 4) * 4, INA = OpA::BYTES / SLAB, INB = OpB::BYTES / SLAB;
+    static_assert(2 * (INA + INB) >= NW, "slabs must fit");
+    const int w2 = wave % (INA + INB), half = wave / (INA + INB);
+    DMP_LDS char *slab = w2 < INA ? (half ? LA[1] : LA[0]) + w2 * SLAB
+                                  : (half ? LB[1] : LB[0]) + (w2 - INA) * SLAB;
+    const int64_t first = at.row0 * p.ldc + at.col0;
+    store_wave_tile<WTM, WTN>((DMP_LDS float *)slab, p.ep, (const char *)p.C + first * out_size(p.ep.c_type),
+                              (char *)p.D + first * out_size(p.ep.d_type), p.ldc, at.rows, at.cols, wm * WTM,
+                              wn * WTN, lane, [&](int i, int j) { return acc[i][j]; });
+}
+
+}  // namespace dmp
