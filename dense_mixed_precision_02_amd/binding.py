@@ -260,11 +260,16 @@ def _operand_layout(X, rows: int, cols: int, name: str):
     raise ValueError(f"{name} must be row-major or column-major in its last two dims")
 
 
+_OUT_CODES: dict = {}
+
+
 def _out_code(dtype):
-    import torch
-    return {torch.float32: GEMM_OUT_F32, torch.float16: GEMM_OUT_F16,
-            torch.bfloat16: GEMM_OUT_BF16, torch.int32: GEMM_OUT_I32,
-            torch.float64: GEMM_OUT_F64}.get(dtype)
+    if not _OUT_CODES:
+        import torch
+        _OUT_CODES.update({torch.float32: GEMM_OUT_F32, torch.float16: GEMM_OUT_F16,
+                           torch.bfloat16: GEMM_OUT_BF16, torch.int32: GEMM_OUT_I32,
+                           torch.float64: GEMM_OUT_F64})
+    return _OUT_CODES.get(dtype)
 
 
 def gemm(A, B, C=None, out=None, alpha: float = 1.0, beta: float = 1.0, out_dtype=None,
@@ -420,54 +425,73 @@ def gemm_sparse24(sp: Sparse24, B, C=None, out=None, handle: Handle | None = Non
     return out
 
 
+def _on(device, handle, call):
+    """call(handle, stream) with `device` current: `handle`, or the default one of the
+    device's current stream, and that stream."""
+    import torch
+    index = device.index
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return _on(device, handle, call)
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if handle is None:
+        handles = getattr(_tls, "handles", None)
+        handle = handles.get((index, stream)) if handles else None
+        if handle is None:
+            handle = default_handle()
+    return call(handle, stream)
+
+
+_FLOAT_OUT = (GEMM_OUT_F32, GEMM_OUT_F16, GEMM_OUT_BF16)
+
+
 def _check_offsets(offsets, device):
     """(groups, flag) of the row offsets of a grouped product."""
     import torch
     if offsets.dtype not in (torch.int32, torch.int64):
         raise TypeError("offsets must be int32 or int64")
-    if offsets.dim() != 1 or offsets.shape[0] < 1 or offsets.device != device:
+    n = offsets.shape[0] if offsets.dim() == 1 else 0
+    if n < 1 or offsets.device != device:
         raise ValueError("offsets must be a vector of groups + 1 row numbers on the operands' GPU")
-    if offsets.shape[0] > 1 and offsets.stride(0) != 1:
+    if n > 1 and offsets.stride(0) != 1:
         raise ValueError("offsets must be contiguous")
-    return offsets.shape[0] - 1, GEMM_OFFSETS_I32 if offsets.dtype == torch.int32 else 0
+    return n - 1, GEMM_OFFSETS_I32 if offsets.dtype == torch.int32 else 0
 
 
 def _output(C, out, shape, out_dtype, beta, device, name):
     """(C's address, C's code, D, D's code, ldc, beta) of a grouped product with outputs `shape`."""
     import torch
     rows, n = shape[-2], shape[-1]
+    ldc = None  # the row stride that C and out share, where rows have one
     for X, what in ((C, "C"), (out, "out")):
         if X is None:
             continue
-        if X.device != device or tuple(X.shape) != shape:
+        if X.device != device or X.shape != shape:
             raise ValueError(f"{what} must be a tensor of shape {name} on the operands' GPU")
-        if _out_code(X.dtype) not in (GEMM_OUT_F32, GEMM_OUT_F16, GEMM_OUT_BF16):
+        if _out_code(X.dtype) not in _FLOAT_OUT:
             raise TypeError(f"{what} must be float32, float16 or bfloat16")
-        if (n > 1 and X.stride(-1) != 1) or (rows > 1 and X.stride(-2) < n):
+        strides = X.stride()
+        if (n > 1 and strides[-1] != 1) or (rows > 1 and strides[-2] < n):
             raise ValueError(f"{what} must be row-major with a row stride of at least N")
-    like = C if C is not None else out
-    ldc = max(like.stride(-2) if like is not None and rows > 1 else n, n, 1)
+        ld = max(strides[-2] if rows > 1 else n, 1)
+        if (ldc is not None and ld != ldc) or (len(shape) == 3 and shape[0] > 1 and strides[0] != rows * ld):
+            raise ValueError("C and out must have the same row stride, and contiguous groups")
+        ldc = ld
+    if ldc is None:
+        ldc = max(n, 1)
     if out is None:
         dtype = out_dtype if out_dtype is not None else torch.float32
-        if _out_code(dtype) not in (GEMM_OUT_F32, GEMM_OUT_F16, GEMM_OUT_BF16):
+        if _out_code(dtype) not in _FLOAT_OUT:
             raise TypeError("out dtype must be float32, float16 or bfloat16")
-        strides = (rows * ldc, ldc, 1) if len(shape) == 3 else (ldc, 1)
-        out = torch.empty_strided(shape, strides, dtype=dtype, device=device)
-    for X, what in ((C, "C"), (out, "out")):
-        if X is None:
-            continue
-        if (rows > 1 and X.stride(-2) != ldc) or \
-                (len(shape) == 3 and shape[0] > 1 and X.stride(0) != rows * ldc):
-            raise ValueError("C and out must have the same row stride, and contiguous groups")
+        out = torch.empty_strided(shape, (rows * ldc, ldc, 1) if len(shape) == 3 else (ldc, 1), dtype=dtype,
+                                  device=device)
     if C is None:
-        beta = 0.0
-    return (C.data_ptr() if C is not None else 0, _out_code(C.dtype) if C is not None else GEMM_OUT_F32,
-            out, _out_code(out.dtype), ldc, float(beta))
+        return 0, GEMM_OUT_F32, out, _out_code(out.dtype), ldc, 0.0
+    return C.data_ptr(), _out_code(C.dtype), out, _out_code(out.dtype), ldc, float(beta)
 
 
 def _sixteen_bit(A, B, what):
-    import torch
-    dt = {torch.float16: GEMM_F16, torch.bfloat16: GEMM_BF16}.get(A.dtype)
+    dt = {GEMM_OUT_F16: GEMM_F16, GEMM_OUT_BF16: GEMM_BF16}.get(_out_code(A.dtype))
     if dt is None or B.dtype != A.dtype:
         raise TypeError(f"{what} must both be float16 or bfloat16")
     if not A.is_cuda or B.device != A.device:
@@ -477,10 +501,11 @@ def _sixteen_bit(A, B, what):
 
 def _rows_of(X, name):
     """Leading dimension of a row-major matrix."""
-    if X.dim() != 2 or (X.shape[1] > 1 and X.stride(1) != 1) or \
-            (X.shape[0] > 1 and X.stride(0) < X.shape[1]):
+    rows, cols = X.shape if X.dim() == 2 else (-1, -1)
+    s = X.stride()
+    if rows < 0 or (cols > 1 and s[1] != 1) or (rows > 1 and s[0] < cols):
         raise ValueError(f"{name} must be a row-major matrix")
-    return max(X.stride(0) if X.shape[0] > 1 else X.shape[1], X.shape[1], 1)
+    return max(s[0] if rows > 1 else cols, 1)
 
 
 def gemm_grouped(A, B, offsets, C=None, out=None, alpha: float = 1.0, beta: float = 1.0, out_dtype=None,
@@ -500,7 +525,6 @@ def gemm_grouped(A, B, offsets, C=None, out=None, alpha: float = 1.0, beta: floa
     The input gradient of Y = gemm_grouped(A, W, offsets) is
     gemm_grouped(dY, W.transpose(1, 2), offsets); the weight gradient is
     gemm_grouped_wgrad(A, dY, offsets)."""
-    import torch
     dt = _sixteen_bit(A, B, "A and B")
     if B.dim() != 3 or A.dim() != 2 or B.shape[1] != A.shape[1]:
         raise ValueError("A must be (T, K) and B (groups, K, N)")
@@ -513,11 +537,9 @@ def gemm_grouped(A, B, offsets, C=None, out=None, alpha: float = 1.0, beta: floa
     if groups > 1 and K > 0 and N > 0 and B.stride(0) != (N if b_col else K) * ldb:
         raise ValueError("B's groups must be contiguous")
     c, c_code, out, d_code, ldc, beta = _output(C, out, (T, N), out_dtype, beta, A.device, "(T, N)")
-    with torch.cuda.device(A.device):
-        h = handle if handle is not None else default_handle()
-        rc = h.run_grouped(A.data_ptr(), B.data_ptr(), c, out.data_ptr(), offsets.data_ptr(), groups, T, N,
-                           K, lda, ldb, ldc, dt, flags | (GEMM_B_COLMAJOR if b_col else 0), float(alpha),
-                           beta, c_code, d_code, torch.cuda.current_stream(A.device).cuda_stream)
+    rc = _on(A.device, handle, lambda h, stream: h.run_grouped(
+        A.data_ptr(), B.data_ptr(), c, out.data_ptr(), offsets.data_ptr(), groups, T, N, K, lda, ldb, ldc, dt,
+        flags | (GEMM_B_COLMAJOR if b_col else 0), alpha, beta, c_code, d_code, stream))
     if rc != GEMM_OK:
         raise GemmError(rc, "gemm_run_grouped")
     return out
@@ -533,7 +555,6 @@ def gemm_grouped_wgrad(X, Y, offsets, C=None, out=None, alpha: float = 1.0, beta
     (default float32), a new tensor unless ``out`` is given (``out`` may be C when the
     dtypes agree).  An empty group's D is beta * C (zero without C).  Rows that no group
     owns are not read."""
-    import torch
     dt = _sixteen_bit(X, Y, "X and Y")
     ldx, ldy = _rows_of(X, "X"), _rows_of(Y, "Y")
     if Y.shape[0] != X.shape[0]:
@@ -542,14 +563,22 @@ def gemm_grouped_wgrad(X, Y, offsets, C=None, out=None, alpha: float = 1.0, beta
     (T, M), N = X.shape, Y.shape[1]
     c, c_code, out, d_code, ldc, beta = _output(C, out, (groups, M, N), out_dtype, beta, X.device,
                                                 "(groups, M, N)")
-    with torch.cuda.device(X.device):
-        h = handle if handle is not None else default_handle()
-        rc = h.run_grouped_wgrad(X.data_ptr(), Y.data_ptr(), c, out.data_ptr(), offsets.data_ptr(), groups,
-                                 M, N, T, ldx, ldy, ldc, dt, flags, float(alpha), beta, c_code, d_code,
-                                 torch.cuda.current_stream(X.device).cuda_stream)
+    rc = _on(X.device, handle, lambda h, stream: h.run_grouped_wgrad(
+        X.data_ptr(), Y.data_ptr(), c, out.data_ptr(), offsets.data_ptr(), groups, M, N, T, ldx, ldy, ldc, dt,
+        flags, alpha, beta, c_code, d_code, stream))
     if rc != GEMM_OK:
         raise GemmError(rc, "gemm_run_grouped_wgrad")
     return out
+
+
+_F8_CODES: dict = {}
+
+
+def _f8_code(dtype):
+    if not _F8_CODES:
+        import torch
+        _F8_CODES.update({torch.float8_e4m3fn: GEMM_E4M3, torch.float8_e5m2: GEMM_E5M2})
+    return _F8_CODES.get(dtype)
 
 
 class Scaled8:
@@ -560,29 +589,35 @@ class Scaled8:
     by quant8, or from tensors that are there."""
 
     def __init__(self, q, scale, block: int = 1, K: int | None = None):
-        import torch
-        self.type = {torch.float8_e4m3fn: GEMM_E4M3, torch.float8_e5m2: GEMM_E5M2}.get(q.dtype)
-        if self.type is None or scale.dtype != torch.float32:
+        self.type = _f8_code(q.dtype)
+        if self.type is None or _out_code(scale.dtype) != GEMM_OUT_F32:
             raise TypeError("q must be float8_e4m3fn or float8_e5m2, and scale float32")
-        if block not in (1, 128):
+        if block != 1 and block != 128:
             raise ValueError("block must be 1 or 128")
-        K = q.shape[-1] if K is None else K
+        shape, dims = q.shape, q.dim()
+        K = shape[-1] if K is None else K
         kp = -(-K // 16) * 16
-        if q.dim() not in (2, 3) or q.shape[-1] != kp:
+        if dims not in (2, 3) or shape[-1] != kp:
             raise ValueError("q must be ((groups,) rows, 16 * ceil(K / 16))")
-        rows = q.shape[-2]
-        if tuple(scale.shape) != (*q.shape[:-2], -(-rows // block), -(-K // 128)):
+        rows = shape[-2]
+        groups = shape[0] if dims == 3 else None
+        blocks = (-(-rows // block), -(-K // 128))
+        if scale.shape != (blocks if groups is None else (groups, *blocks)):
             raise ValueError("scale must be ((groups,) ceil(rows / block), ceil(K / 128))")
         if scale.device != q.device or not q.is_cuda:
             raise ValueError("q and scale must be on the same GPU")
-        if q.numel() and (q.stride(-1) != 1 or (rows > 1 and (q.stride(-2) < kp or q.stride(-2) % 16)) or
-                          (q.dim() == 3 and q.shape[0] > 1 and q.stride(0) % 16) or q.data_ptr() % 16):
+        s, t, at = q.stride(), scale.stride(), q.data_ptr()
+        if q.numel() and (s[-1] != 1 or (rows > 1 and (s[-2] < kp or s[-2] % 16)) or
+                          (dims == 3 and groups > 1 and s[0] % 16) or at % 16):
             raise ValueError("q's rows must be contiguous and begin at multiples of 16 bytes")
-        self.q, self.scale, self.block, self.K, self.rows = q, scale, block, K, rows
-        self.groups = q.shape[0] if q.dim() == 3 else None
-        self.operand = Q8Operand(q.data_ptr(), scale.data_ptr(), q.stride(-2) if rows > 1 and kp else kp,
-                                 scale.stride(-2), scale.stride(-1), q.stride(0) if q.dim() == 3 else 0,
-                                 scale.stride(0) if q.dim() == 3 else 0, self.type)
+        self._set(q, scale, block, K, rows, groups, at, s[-2] if rows > 1 and kp else kp,
+                  s[0] if dims == 3 else 0)
+
+    def _set(self, q, scale, block, K, rows, groups, at, ld, group):
+        t = scale.stride()
+        self.q, self.scale, self.block, self.K, self.rows, self.groups = q, scale, block, K, rows, groups
+        self.operand = Q8Operand(at, scale.data_ptr(), ld, t[-2], t[-1], group, t[0] if groups is not None else 0,
+                                 self.type)
 
 
 def quant8(X, block: int = 1, dtype=None, handle: Handle | None = None) -> Scaled8:
@@ -594,9 +629,9 @@ def quant8(X, block: int = 1, dtype=None, handle: Handle | None = None) -> Scale
     (K, N) is quant8(W.t(), block=128)."""
     import torch
     dtype = torch.float8_e4m3fn if dtype is None else dtype
-    code = {torch.float8_e4m3fn: GEMM_E4M3, torch.float8_e5m2: GEMM_E5M2}.get(dtype)
+    code = _f8_code(dtype)
     x_code = _out_code(X.dtype)
-    if code is None or x_code not in (GEMM_OUT_F32, GEMM_OUT_F16, GEMM_OUT_BF16):
+    if code is None or x_code not in _FLOAT_OUT:
         raise TypeError("X must be float32, float16 or bfloat16, and dtype float8_e4m3fn or float8_e5m2")
     if X.dim() not in (2, 3) or not X.is_cuda:
         raise ValueError("X must be a 2-D or 3-D GPU tensor")
@@ -609,15 +644,19 @@ def quant8(X, block: int = 1, dtype=None, handle: Handle | None = None) -> Scale
     if batch > 1 and X.numel() and X.stride(0) != (K if col else M) * ldx:
         raise ValueError("batched X must have a contiguous batch stride")
     kb, mb = -(-K // 128), -(-M // block)
-    q = torch.empty((*lead, M, -(-K // 16) * 16), dtype=dtype, device=X.device)
+    kp = -(-K // 16) * 16
+    q = torch.empty((*lead, M, kp), dtype=dtype, device=X.device)
     scale = torch.empty((*lead, kb, mb), dtype=torch.float32, device=X.device)
-    with torch.cuda.device(X.device):
-        h = handle if handle is not None else default_handle()
-        rc = h.quant8(X.data_ptr(), M, K, ldx, x_code, GEMM_A_COLMAJOR if col else 0, batch, block, code,
-                      q.data_ptr(), scale.data_ptr(), torch.cuda.current_stream(X.device).cuda_stream)
+    at = q.data_ptr()
+    rc = _on(X.device, handle, lambda h, stream: h.quant8(
+        X.data_ptr(), M, K, ldx, x_code, GEMM_A_COLMAJOR if col else 0, batch, block, code, at, scale.data_ptr(),
+        stream))
     if rc != GEMM_OK:
         raise GemmError(rc, "gemm_quant8")
-    return Scaled8(q, scale.transpose(-1, -2), block, K)
+    r = Scaled8.__new__(Scaled8)  # what the constructor would check holds
+    r.type = code
+    r._set(q, scale.transpose(-1, -2), block, K, M, batch if lead else None, at, kp, M * kp)
+    return r
 
 
 def gemm_scaled8(A: Scaled8, B: Scaled8, offsets=None, C=None, out=None, alpha: float = 1.0,
@@ -627,7 +666,6 @@ def gemm_scaled8(A: Scaled8, B: Scaled8, offsets=None, C=None, out=None, alpha: 
     columns of a K x N matrix as rows);  formats may differ.  With ``offsets`` (see
     gemm_grouped) B is (groups, N, K) and the rows of group g meet B[g].  C, ``out`` and
     ``out_dtype`` (default float32) as in gemm_grouped."""
-    import torch
     if A.block != 1 or B.block != 128:
         raise ValueError("A must have blocks of one row and B blocks of 128 rows")
     if A.groups is not None or A.K != B.K or B.q.device != A.q.device:
@@ -638,12 +676,9 @@ def gemm_scaled8(A: Scaled8, B: Scaled8, offsets=None, C=None, out=None, alpha: 
         raise ValueError("a grouped B needs offsets that hold one number more than it has groups")
     T, N = A.rows, B.rows
     c, c_code, out, d_code, ldc, beta = _output(C, out, (T, N), out_dtype, beta, device, "(T, N)")
-    with torch.cuda.device(device):
-        h = handle if handle is not None else default_handle()
-        rc = h.run_scaled8(A.operand, B.operand, c, out.data_ptr(),
-                           offsets.data_ptr() if offsets is not None else 0, groups, T, N, A.K, ldc, flags,
-                           float(alpha), beta, c_code, d_code,
-                           torch.cuda.current_stream(device).cuda_stream)
+    rc = _on(device, handle, lambda h, stream: h.run_scaled8(
+        A.operand, B.operand, c, out.data_ptr(), offsets.data_ptr() if offsets is not None else 0, groups, T, N,
+        A.K, ldc, flags, alpha, beta, c_code, d_code, stream))
     if rc != GEMM_OK:
         raise GemmError(rc, "gemm_run_scaled8")
     return out

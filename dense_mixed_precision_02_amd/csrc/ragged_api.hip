@@ -10,6 +10,7 @@
 #include "ragged_plan.hpp"
 #include "ragged_tile.hpp"
 #include "scaled_tile.hpp"
+#include "skinny.hpp"
 
 using namespace dmp;
 using namespace dmp::plan;
@@ -50,10 +51,24 @@ int launch_tile(RaggedArgs a, hipStream_t s) {
     return launched();
 }
 
+// 16-bit operands: FA, FB unused.
+template <class DT, int MODE, int TN, int NW, int FA, int FB>
+int launch_skinny(RaggedArgs a, hipStream_t s) {
+    a.tiles_n = (int)cdiv(a.N, 16 * TN);
+    const int64_t grid = (int64_t)a.groups * a.tiles_n;
+    if (grid > 0x7fffffff) return GEMM_ERR_INVALID_ARG;
+    hipLaunchKernelGGL((skinny<DT, MODE, TN, NW, FA, FB>), dim3((unsigned)grid), dim3(NW * 64), 0, s, a);
+    return launched();
+}
+
 template <class DT, bool AK, bool BKC, int MODE>
 int launch_cfg(int cfg, const RaggedArgs &a, hipStream_t s) {
     if (cfg == CFG_L) return launch_tile<DT, 256, AK, BKC, MODE>(a, s);
     if (cfg == CFG_M) return launch_tile<DT, 128, AK, BKC, MODE>(a, s);
+    if constexpr (MODE == RAGGED_ROWS && BKC) {
+        if (cfg == CFG_SKINNY) return launch_skinny<DT, MODE, 1, 4, 0, 0>(a, s);
+        if (cfg == CFG_SKINNY4) return launch_skinny<DT, MODE, 4, 4, 0, 0>(a, s);
+    }
     return launch_any<DT, AK, BKC, MODE>(a, s);
 }
 
@@ -68,6 +83,8 @@ int launch_scaled_tile(RaggedArgs a, hipStream_t s) {
 
 template <int FA, int FB>
 int launch_scaled(int cfg, const RaggedArgs &a, hipStream_t s) {
+    if (cfg == CFG_SKINNY) return launch_skinny<F8<FA, FB>, RAGGED_SCALED, 1, 4, FA, FB>(a, s);
+    if (cfg == CFG_SKINNY4) return launch_skinny<F8<FA, FB>, RAGGED_SCALED, 4, 4, FA, FB>(a, s);
     const bool exact = a.ep.d_type == OUT_F32;
     if (cfg == CFG_L)
         return exact ? launch_scaled_tile<FA, FB, 256, 128, 4, 2, true>(a, s)

@@ -132,11 +132,14 @@ inline int validate_quant8(gemm_handle_t h, const void *X, int64_t M, int64_t K,
 // how the rows are spread; the rules go by the mean.
 // ---------------------------------------------------------------------------
 
+enum { CFG_SKINNY = 16, CFG_SKINNY4 = 17 };  // 16 and 64 columns to a workgroup
+
 // Grouped rows: 16-byte granules need aligned operands, whole granules along
 // the contiguous extents and 31-bit offsets inside a tile.
 inline int grouped_cfg(int num_cus, const void *A, const void *B, int64_t groups, int64_t M, int64_t N,
                        int64_t K, int64_t lda, int64_t ldb, bool b_col) {
     if (K == 0 || !granule_ok(A, B, M, N, K, lda, ldb, GEMM_F16, false, b_col, true)) return CFG_GENERIC;
+    if (b_col && M <= 64 * groups) return M <= 16 * groups ? CFG_SKINNY : CFG_SKINNY4;
     const int64_t tiles = (cdiv(M, 256) + groups / 2) * cdiv(N, 256);
     if (M / groups >= 192 && tiles >= num_cus) return CFG_L;
     return CFG_M;
@@ -150,6 +153,7 @@ inline int wgrad_cfg(int num_cus, const void *X, const void *Y, int64_t groups, 
 }
 
 inline int scaled_cfg(int num_cus, int64_t groups, int64_t M, int64_t N) {
+    if (M <= 64 * groups) return M <= 16 * groups ? CFG_SKINNY : CFG_SKINNY4;
     const int64_t tiles = (cdiv(M, 256) + groups / 2) * cdiv(N, 256);
     return M / groups >= 192 && tiles >= num_cus ? CFG_L : CFG_M;
 }

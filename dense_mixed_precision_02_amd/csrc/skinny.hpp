@@ -1,0 +1,160 @@
+// skinny.hpp -- products of few rows by large K-contiguous matrices (decoding).
+//
+// With a few rows to a group the time is that of reading every B_g once.  A
+// workgroup takes 16 TN columns of one group; its NW waves split K and each
+// streams its share of the columns from memory straight into matrix-instruction
+// operands (lane L: column L % 16, granules L / 16 and L / 16 + 4 of a 128-byte
+// k-tile), two stages of U k-tiles in registers, so that a stage's loads are in flight
+// while the one before is multiplied.  No LDS on the way; A's rows come the
+// same way out of the caches.  At the end the waves' sums meet in LDS and are
+// added in the order of the waves (the same result every run).  Rows go 16 or
+// 32 at a time (16-bit operands with TN = 4: 32 or 64; the widened 8-bit ones
+// would not fit the registers); a group with more reads its B again, by then
+// from the caches.
+//
+// 8-bit operands (SCALED) are widened to bf16 exactly as in scaled_tile.hpp:
+// the matrix units idle here anyway, so every D type gets exact products.
+#pragma once
+#include "scaled_tile.hpp"
+
+namespace dmp {
+
+__device__ static inline intx4 load_granule(__amdgpu_buffer_rsrc_t r, int off) {
+    return __builtin_bit_cast(intx4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+
+// One group's rows [row0, row0 + rows), rows <= 16 TM, times this workgroup's columns.
+template <class DT, int MODE, int TM, int TN, int NW, int FA, int FB>
+__device__ static inline void skinny_rows(const RaggedArgs &p, float *lds, int g, int64_t row0, int rows,
+                                          int64_t col0, int cols) {
+    constexpr int U = TM + TN <= 2 ? 4 : TM + TN <= 3 ? 2 : 1;  // k-tiles in a stage
+    constexpr int ESZ = DT::ESZ, KT = 128 / ESZ;
+    const int lane = lane_id(), wave = wave_id();
+    const int nkt = (int)((p.K + KT - 1) / KT);
+    const int per = (nkt + NW - 1) / NW, kt0 = min(wave * per, nkt), kt1 = min(kt0 + per, nkt);
+    const int kbytes = (int)(p.K * ESZ);
+    const __amdgpu_buffer_rsrc_t ra = make_rsrc((const char *)p.A + row0 * p.lda * ESZ);
+    const __amdgpu_buffer_rsrc_t rb = make_rsrc((const char *)p.B + (g * p.sB + col0 * p.ldb) * ESZ);
+    const int r16 = lane & 15, gr = (lane >> 4) * 16;  // this lane's row or column; byte of its first granule
+
+    floatx4 acc[TM][TN] = {};
+    intx4 fa[2][U][TM][2], fb[2][U][TN][2];
+    float fs[2][U][TM];  // SCALED: lane L holds the factor of row L % 16
+    float fsb[2][U];
+    auto load = [&](int st, int kt) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = (kt + u) * 128 + gr;
+            const bool in = kt + u < kt1;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int kb = k + 64 * h;
+                const bool ok = in && kb < kbytes;
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    const int c = j * 16 + r16;
+                    fb[st][u][j][h] = load_granule(rb, ok && c < cols ? c * (int)(p.ldb * ESZ) + kb : OOB_OFFSET);
+                }
+#pragma unroll
+                for (int i = 0; i < TM; ++i) {
+                    const int r = i * 16 + r16;
+                    fa[st][u][i][h] = load_granule(ra, ok && r < rows ? r * (int)(p.lda * ESZ) + kb : OOB_OFFSET);
+                }
+            }
+            if constexpr (MODE == RAGGED_SCALED) {
+#pragma unroll
+                for (int i = 0; i < TM; ++i) {
+                    const int r = i * 16 + r16;
+                    fs[st][u][i] = in && r < rows ? p.sa[(row0 + r) * p.sa_row + (kt + u) * p.sa_k] : 0.0f;
+                }
+                fsb[st][u] = in ? p.sb[g * p.sb_group + (col0 >> 7) * p.sb_col + (kt + u) * p.sb_k] : 0.0f;
+            }
+        }
+    };
+    auto multiply = [&](int st) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if constexpr (MODE == RAGGED_SCALED) {
+                intx4 b[TN][4];
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) b[j][h] = widen8<FB>(fb[st][u][j][h >> 1], h & 1);
+#pragma unroll
+                for (int i = 0; i < TM; ++i) {
+                    floatx4 s;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        s[q] = __shfl(fs[st][u][i], 4 * (lane >> 4) + q, 64) * fsb[st][u];
+#pragma unroll
+                    for (int j = 0; j < TN; ++j) {
+                        floatx4 c = {0, 0, 0, 0};
+#pragma unroll
+                        for (int h = 0; h < 4; ++h)
+                            c = mma16<BF16>(widen8<FA>(fa[st][u][i][h >> 1], h & 1), b[j][h], c);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) acc[i][j][q] = __builtin_fmaf(s[q], c[q], acc[i][j][q]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < TM; ++i)
+#pragma unroll
+                        for (int j = 0; j < TN; ++j) acc[i][j] = mma16<DT>(fa[st][u][i][h], fb[st][u][j][h], acc[i][j]);
+            }
+        }
+    };
+    if (kt0 < kt1) {
+        load(0, kt0);
+        for (int kt = kt0; kt < kt1; kt += 2 * U) {
+            load(1, kt + U);
+            multiply(0);
+            load(0, kt + 2 * U);
+            multiply(1);
+        }
+    }
+    // sums of the waves, [wave][row][column]
+    constexpr int CW = 16 * TN, SZ = 16 * TM * CW;
+    __syncthreads();  // the sums of the rows before are read
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                lds[wave * SZ + (i * 16 + 4 * (lane >> 4) + q) * CW + j * 16 + (lane & 15)] = acc[i][j][q];
+    __syncthreads();
+    for (int e = threadIdx.x; e < rows * CW; e += NW * 64) {
+        const int r = e / CW, c = e % CW;
+        if (c >= cols) continue;
+        float v = lds[e];
+        for (int w = 1; w < NW; ++w) v += lds[w * SZ + e];
+        const int64_t idx = (row0 + r) * p.ldc + col0 + c;
+        const floatx4 cv = p.ep.use_c ? load4<float>(p.C, idx, p.ep.c_type, false, 1) : floatx4{0, 0, 0, 0};
+        store4<float>(p.D, idx, finish4(floatx4{v, 0, 0, 0}, cv, p.ep), p.ep.d_type, false, 1);
+    }
+}
+
+template <class DT, int MODE, int TN, int NW, int FA, int FB>
+__global__ __launch_bounds__(NW * 64, 2) void skinny(const RaggedArgs p) {
+    constexpr int TS = TN == 1 || MODE == RAGGED_SCALED ? 1 : 2;  // passes of 16 TS and 32 TS rows
+    __shared__ float lds[NW * 32 * TS * 16 * TN];
+    const int total = (int)p.M;
+    const int g = blockIdx.x / p.tiles_n;
+    const int64_t col0 = (int64_t)(blockIdx.x - g * p.tiles_n) * 16 * TN;
+    const int cols = (int)min((int64_t)16 * TN, p.N - col0);
+    int r0 = 0, r1 = total;
+    if (p.offsets) {
+        r0 = load_offset(p, g, total);
+        r1 = load_offset(p, g + 1, total);
+    }
+    for (int r = r0; r < r1; r += 32 * TS) {
+        const int n = min(32 * TS, r1 - r);
+        if (n <= 16 * TS) skinny_rows<DT, MODE, TS, TN, NW, FA, FB>(p, lds, g, r, n, col0, cols);
+        else skinny_rows<DT, MODE, 2 * TS, TN, NW, FA, FB>(p, lds, g, r, n, col0, cols);
+    }
+}
+
+}  // namespace dmp
