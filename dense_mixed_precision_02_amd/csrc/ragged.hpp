@@ -52,13 +52,24 @@ struct RaggedArgs {
     int64_t sb_col, sb_k, sb_group;  // SCALED: the same of B's, by blocks of 128 columns
     int groups, off32;       // off32: the offsets are int32_t, else int64_t
     int tiles_m, tiles_n;    // WGRAD: both; ROWS, SCALED: tiles_n
+    int cut;                 // ragged_tile: workgroups in a round, or 0
     EpiParams ep;
 };
 
-// Row number i of the offsets, brought into 0 .. total.
+// Row number i of the offsets, brought into 0 .. total.  (In 32-bit steps: the
+// scalar unit cannot compare 64-bit values, and one vector comparison would take
+// everything that a tile derives from its rows into vector registers.)
 __device__ static inline int load_offset(const RaggedArgs &p, int i, int total) {
-    const int64_t v = p.off32 ? (int64_t)((const int32_t *)p.offsets)[i] : ((const int64_t *)p.offsets)[i];
-    return (int)(v < 0 ? 0 : v > total ? total : v);
+    int lo, hi;
+    if (p.off32) {
+        lo = ((const int32_t *)p.offsets)[i];
+        hi = lo >> 31;
+    } else {
+        const intx2 v = ((const intx2 *)p.offsets)[i];
+        lo = v[0];
+        hi = v[1];
+    }
+    return hi < 0 ? 0 : (hi > 0 || (uint32_t)lo > (uint32_t)total) ? total : lo;
 }
 
 __device__ static inline int wave_scan_add(int v, int lane) {
@@ -152,7 +163,7 @@ struct AnyOperand {
 
     // granule of this lane in chunk j: rows / mn from `base` (element (row0, k0)),
     // `rows` valid rows, `kleft` valid k
-    __device__ static intx4 load(const elem *base, int64_t ld, int wave, int lane, int j, int64_t rows,
+    __device__ static intx4 load(const elem *base, int64_t ld, int wave, int lane, int j, int rows,
                                  int kleft) {
         const int bid = (j * 4 + wave) * 8 + (lane >> 3);
         int r, k, n;  // K-contiguous: row r, k .. k + n - 1; else row r .. r + n - 1, k
@@ -166,8 +177,7 @@ struct AnyOperand {
             const int kb = bid / (R / 16), mb = bid % (R / 16);
             k = DT::ESZ == 2 ? kb * 4 + ((lane & 7) >> 1) : kb * 8 + (lane & 7);
             r = mb * 16 + (DT::ESZ == 2 ? (lane & 1) * 8 : 0);
-            const int64_t left = rows - r;
-            n = k < kleft ? (left > G ? G : (int)left) : 0;
+            n = k < kleft ? min(G, rows - r) : 0;
             q = base + (int64_t)k * ld + r;
         }
         intx4 v = {0, 0, 0, 0};
@@ -199,7 +209,7 @@ __device__ static inline floatx4 mma16(const intx4 &a, const intx4 &b, const flo
 // What a tile of the three products is: its operands' corners and valid extents.
 struct TileAt {
     const char *A, *B;       // element (first row, first k) of A, (first k, first column) of B
-    int64_t rows, cols, k;   // valid rows of A, columns of B, k
+    int rows, cols, k;       // valid rows of A, columns of B (to the operand's end), k
     int64_t row0, col0;      // in D
     int group;
 };
@@ -209,17 +219,17 @@ __device__ static inline TileAt tile_at(const RaggedArgs &p, int g, int r0, int 
     TileAt t;
     t.group = g;
     t.col0 = (int64_t)tn * BN;
-    t.cols = p.N - t.col0;
+    t.cols = (int)p.N - tn * BN;
     if constexpr (MODE == RAGGED_WGRAD) {
         t.row0 = (int64_t)tm * BM;
-        t.rows = p.M - t.row0;
+        t.rows = (int)p.M - tm * BM;
         t.k = r1 - r0;
         t.A = (const char *)p.A + ((int64_t)r0 * p.lda + t.row0) * DT::ESZ;
         t.B = (const char *)p.B + ((int64_t)r0 * p.ldb + t.col0) * DT::ESZ;
     } else {
         t.row0 = r0 + (int64_t)tm * BM;
-        t.rows = r1 - t.row0;
-        t.k = p.K;
+        t.rows = r1 - r0 - tm * BM;
+        t.k = (int)p.K;
         t.A = (const char *)p.A + t.row0 * p.lda * DT::ESZ;
         t.B = (const char *)p.B + (g * p.sB + (BKC ? t.col0 * p.ldb : t.col0)) * DT::ESZ;
     }
@@ -253,13 +263,13 @@ __global__ __launch_bounds__(256) void ragged_any(const RaggedArgs p) {
         if (!walk.find(p, total, lane, t, g, r0, r1, tile0)) return;
         at = tile_at<DT, AK, BKC, MODE, BM, BN>(p, g, r0, r1, t - tile0, blockIdx.x % p.tiles_n);
     }
-    const int nkt = (int)((at.k + KT - 1) / KT);
+    const int nkt = at.k / KT + (at.k % KT != 0);
 
     floatx4 acc[TM][TN] = {};
     intx4 ra[LA::CPW], rb[LB::CPW];
     auto fetch = [&](int kt) {
-        const int64_t k0 = (int64_t)kt * KT, left = at.k - k0;
-        const int kleft = left > KT ? KT : (int)left;
+        const int64_t k0 = (int64_t)kt * KT;
+        const int kleft = min(KT, at.k - kt * KT);
         const elem *A = (const elem *)at.A + (AK ? k0 : k0 * p.lda);
         const elem *B = (const elem *)at.B + (BKC ? k0 : k0 * p.ldb);
 #pragma unroll

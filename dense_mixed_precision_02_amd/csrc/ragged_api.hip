@@ -40,12 +40,14 @@ int launch_any(const RaggedArgs &a, hipStream_t s) {
 }
 
 template <class DT, int E, bool AK, bool BKC, int MODE>
-int launch_tile(RaggedArgs a, hipStream_t s) {
+int launch_tile(gemm_handle_t h, RaggedArgs a, hipStream_t s) {
     a.tiles_m = MODE == RAGGED_WGRAD ? (int)cdiv(a.M, E) : 0;
     a.tiles_n = (int)cdiv(a.N, E);
-    // row tiles: at most one more for each group than the rows fill
-    const int64_t grid = MODE == RAGGED_WGRAD ? (int64_t)a.groups * a.tiles_m * a.tiles_n
-                                              : (cdiv(a.M, E) + a.groups) * a.tiles_n;
+    a.cut = E == 256 ? h->num_cus : 0;  // 256 x 256 tiles: one workgroup to a CU
+    // ROWS: row tiles, at most one more for each group than the rows fill, and the
+    // cut last round.  WGRAD: every group's tiles rounded up to a multiple of 8.
+    const int64_t grid = MODE == RAGGED_WGRAD ? (int64_t)a.groups * cdiv((int64_t)a.tiles_m * a.tiles_n, 8) * 8
+                                              : (cdiv(a.M, E) + a.groups) * a.tiles_n + 2 * a.cut;
     if (grid > 0x7fffffff) return GEMM_ERR_INVALID_ARG;
     hipLaunchKernelGGL((ragged_tile<DT, E, E, AK, BKC, MODE>), dim3((unsigned)grid), dim3(256), 0, s, a);
     return launched();
@@ -62,9 +64,9 @@ int launch_skinny(RaggedArgs a, hipStream_t s) {
 }
 
 template <class DT, bool AK, bool BKC, int MODE>
-int launch_cfg(int cfg, const RaggedArgs &a, hipStream_t s) {
-    if (cfg == CFG_L) return launch_tile<DT, 256, AK, BKC, MODE>(a, s);
-    if (cfg == CFG_M) return launch_tile<DT, 128, AK, BKC, MODE>(a, s);
+int launch_cfg(gemm_handle_t h, int cfg, const RaggedArgs &a, hipStream_t s) {
+    if (cfg == CFG_L) return launch_tile<DT, 256, AK, BKC, MODE>(h, a, s);
+    if (cfg == CFG_M) return launch_tile<DT, 128, AK, BKC, MODE>(h, a, s);
     if constexpr (MODE == RAGGED_ROWS && BKC) {
         if (cfg == CFG_SKINNY) return launch_skinny<DT, MODE, 1, 4, 0, 0>(a, s);
         if (cfg == CFG_SKINNY4) return launch_skinny<DT, MODE, 4, 4, 0, 0>(a, s);
@@ -126,10 +128,10 @@ int gemm_run_grouped(gemm_handle_t h, const void *A, const void *B, const void *
     hipStream_t s = (hipStream_t)stream;
     const int cfg = grouped_cfg(h->num_cus, A, B, groups, M, N, K, lda, ldb, bc);
     if (dtype == GEMM_F16)
-        return bc ? launch_cfg<F16, true, true, RAGGED_ROWS>(cfg, a, s)
-                  : launch_cfg<F16, true, false, RAGGED_ROWS>(cfg, a, s);
-    return bc ? launch_cfg<BF16, true, true, RAGGED_ROWS>(cfg, a, s)
-              : launch_cfg<BF16, true, false, RAGGED_ROWS>(cfg, a, s);
+        return bc ? launch_cfg<F16, true, true, RAGGED_ROWS>(h, cfg, a, s)
+                  : launch_cfg<F16, true, false, RAGGED_ROWS>(h, cfg, a, s);
+    return bc ? launch_cfg<BF16, true, true, RAGGED_ROWS>(h, cfg, a, s)
+              : launch_cfg<BF16, true, false, RAGGED_ROWS>(h, cfg, a, s);
 }
 
 int gemm_run_grouped_wgrad(gemm_handle_t h, const void *X, const void *Y, const void *C, void *D,
@@ -150,8 +152,8 @@ int gemm_run_grouped_wgrad(gemm_handle_t h, const void *X, const void *Y, const 
     a.ep = ep;
     hipStream_t s = (hipStream_t)stream;
     const int cfg = wgrad_cfg(h->num_cus, X, Y, groups, M, N, K, ldx, ldy);
-    return dtype == GEMM_F16 ? launch_cfg<F16, false, false, RAGGED_WGRAD>(cfg, a, s)
-                             : launch_cfg<BF16, false, false, RAGGED_WGRAD>(cfg, a, s);
+    return dtype == GEMM_F16 ? launch_cfg<F16, false, false, RAGGED_WGRAD>(h, cfg, a, s)
+                             : launch_cfg<BF16, false, false, RAGGED_WGRAD>(h, cfg, a, s);
 }
 
 int gemm_quant8(gemm_handle_t h, const void *X, int64_t M, int64_t K, int64_t ldx, int x_type,

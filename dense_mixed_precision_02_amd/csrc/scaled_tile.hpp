@@ -77,7 +77,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void scaled_tile(const RaggedArgs p
     grouped_order(t - tile0 * p.tiles_n, (r1 - r0 - 1) / BM + 1, p.tiles_n, tm, tn);
     const TileAt at = tile_at<DT, true, true, RAGGED_SCALED, BM, BN>(p, g, r0, r1, tm, tn);
 
-    const int kspan = (int)at.k, nkt = (kspan + KT - 1) / KT;
+    const int kspan = at.k, nkt = kspan / KT + (kspan % KT != 0);
     OpA opa;
     OpB opb;
     opa.init(wave, lane, p.lda, 0, at.rows);

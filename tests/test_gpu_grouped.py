@@ -168,6 +168,42 @@ def test_small_integers_are_exact(dmp, dt, K, N, b_col):
     assert torch.equal(W.double().cpu(), want)
 
 
+@pytest.mark.parametrize("b_col", [True, False], ids=["col", "row"])
+@pytest.mark.parametrize("counts", [[1700, 0, 1501, 1200], [4400, 3, 40], [5, 4090], [4608]],
+                         ids=lambda c: "-".join(map(str, c)))
+def test_largest_tiles_small_integers(dmp, counts, b_col):
+    """Enough tiles for the 256 x 256 kernels, whole and partial last rounds, the last
+    column tile partial; exact sums, so every element must be equal."""
+    K, N, G = 200, 4000, len(counts)
+    T, off = sum(counts) + 9, offsets_of(counts, 4).cuda()
+    g = torch.Generator(device="cuda").manual_seed(8)
+    A = torch.randint(-2, 3, (T, K), generator=g, device="cuda").bfloat16()
+    B = torch.randint(-2, 3, (G, N, K) if b_col else (G, K, N), generator=g, device="cuda").bfloat16()
+    B = B.transpose(1, 2) if b_col else B
+    C = torch.randint(-9, 10, (T, N), generator=g, device="cuda").float()
+    D = torch.full((T, N), 7.0, device="cuda")
+    dmp.gemm_grouped(A, B, off, C, out=D)
+    want = torch.full((T, N), 7.0, device="cuda", dtype=torch.float64)
+    for i in range(G):
+        s = slice(int(off[i]), int(off[i + 1]))
+        want[s] = A[s].double() @ B[i].double().contiguous() + C[s].double()
+    assert torch.equal(D.double(), want)
+
+
+@pytest.mark.parametrize("counts", [[300, 0, 129, 64], [1, 700, 63, 2]], ids=lambda c: "-".join(map(str, c)))
+def test_largest_gradient_tiles_small_integers(dmp, counts):
+    M, N, G = 2000, 2048, len(counts)
+    T, off = sum(counts) + 9, offsets_of(counts, 4).cuda()
+    g = torch.Generator(device="cuda").manual_seed(9)
+    X = torch.randint(-2, 3, (T, M), generator=g, device="cuda").half()
+    Y = torch.randint(-2, 3, (T, N), generator=g, device="cuda").half()
+    C = torch.randint(-9, 10, (G, M, N), generator=g, device="cuda").float()
+    D = dmp.gemm_grouped_wgrad(X, Y, off, C)
+    for i in range(G):
+        s = slice(int(off[i]), int(off[i + 1]))
+        assert torch.equal(D[i].double(), X[s].double().t().contiguous() @ Y[s].double() + C[i].double()), i
+
+
 def test_strided_operands_and_padding_stay(dmp):
     """Leading dimensions larger than the rows; the columns past N of a padded output
     stay, and a misaligned base address is served."""

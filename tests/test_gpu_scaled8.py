@@ -207,6 +207,33 @@ def test_small_integers_are_exact(dmp, fa, fb, T, K, N):
     assert torch.equal(D.double().cpu(), values(A, K) @ values(B, K).t())
 
 
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("counts", [None, [1700, 0, 1501, 1200]], ids=["dense", "grouped"])
+def test_largest_tiles_small_integers(dmp, counts, out):
+    """Enough tiles for the largest kernels; integers whose sums stay below 2^8 (bf16) or
+    2^24 in magnitude: exact."""
+    K, N, T = 272, 4000, 4410
+    g = torch.Generator(device="cuda").manual_seed(6)
+    G = 1 if counts is None else len(counts)
+    density = 0.02 if out == "bf16" else 1.0  # about 5 products of at most 16 to a sum
+    a = torch.randint(-4, 5, (T, K), generator=g, device="cuda").float()
+    b = torch.randint(-4, 5, (G, N, K), generator=g, device="cuda").float()
+    a = a * (torch.rand(T, K, generator=g, device="cuda") < density)
+    B = dmp.Scaled8((b if counts else b[0]).to(E5), torch.full((G, 32, 3) if counts else (32, 3), 2.0, device="cuda"),
+                    block=128)
+    A = dmp.Scaled8(a.to(E4), torch.full((T, 3), 0.5, device="cuda"))
+    off = None if counts is None else offsets_of(counts, 4)
+    D = torch.full((T, N), 7.0, device="cuda").to(DT[out])
+    dmp.gemm_scaled8(A, B, off.cuda() if counts else None, out=D)
+    want = torch.full((T, N), 7.0, device="cuda", dtype=torch.float64)
+    for i in range(G):
+        s = slice(int(off[i]), int(off[i + 1])) if counts else slice(0, T)
+        want[s] = a[s].double() @ b[i].double().t().contiguous()
+    keep = want.abs() <= (256 if out == "bf16" else 1 << 24)
+    assert keep.double().mean() > 0.99
+    assert torch.equal(D.double()[keep], want[keep])
+
+
 def test_not_finite_scale_reaches_its_rows_and_columns_only(dmp):
     A, B = make8(dmp, 40, (), 200, 256, E4, 1), make8(dmp, 50, (), 300, 256, E4, 128)
     clean = dmp.gemm_scaled8(A, B)
