@@ -1,6 +1,5 @@
 // ragged.hpp -- what the products over ragged groups of rows share: arguments,
-// 8-bit float types, the search for a tile's group, and the kernel that takes
-// any size, alignment and layout.
+// 8-bit float types and the search for a tile's group.
 //
 // Rows (tokens) are sorted by group (expert); offsets[g] .. offsets[g+1] are the
 // rows of group g.  Three products use them:
@@ -52,7 +51,8 @@ struct RaggedArgs {
     int64_t sb_col, sb_k, sb_group;  // SCALED: the same of B's, by blocks of 128 columns
     int groups, off32;       // off32: the offsets are int32_t, else int64_t
     int tiles_m, tiles_n;    // WGRAD: both; ROWS, SCALED: tiles_n
-    int cut;                 // ragged_tile: workgroups in a round, or 0
+    int cut;                 // ragged_tile, ROWS: workgroups in a round, or 0
+    int run;                 // ragged_tile, WGRAD: tiles in a run (on one XCD)
     EpiParams ep;
 };
 
@@ -145,57 +145,6 @@ struct GroupWalk {
     }
 };
 
-// ---------------------------------------------------------------------------
-// Any size, alignment and layout: 64 x 64 tiles of four waves, each 32 x 32 in
-// 16 x 16 instructions.  A k-tile (128 bytes of K) comes through registers: a
-// lane loads a 16-byte granule wherever it lies (unaligned 16-byte loads are
-// allowed on global memory), element by element only where the granule crosses
-// the operand's end, and writes it to the LDS place that the direct copies of
-// the aligned kernels use.  The next k-tile's loads are in flight while this
-// one is multiplied.  A K that is not a multiple of 8 leaves no other way than
-// unaligned rows; the aligned kernels take everything else.
-// ---------------------------------------------------------------------------
-template <class DT, int R, bool KCONTIG>
-struct AnyOperand {
-    using Op = Operand<DT, R, 4, KCONTIG>;
-    using elem = typename DT::elem;
-    static constexpr int G = DT::G, CPW = Op::CPW;
-
-    // granule of this lane in chunk j: rows / mn from `base` (element (row0, k0)),
-    // `rows` valid rows, `kleft` valid k
-    __device__ static intx4 load(const elem *base, int64_t ld, int wave, int lane, int j, int rows,
-                                 int kleft) {
-        const int bid = (j * 4 + wave) * 8 + (lane >> 3);
-        int r, k, n;  // K-contiguous: row r, k .. k + n - 1; else row r .. r + n - 1, k
-        const elem *q;
-        if constexpr (KCONTIG) {
-            r = bid;
-            k = ((lane & 7) ^ swz(r)) * G;
-            n = r < rows ? kleft - k : 0;
-            q = base + r * ld + k;
-        } else {
-            const int kb = bid / (R / 16), mb = bid % (R / 16);
-            k = DT::ESZ == 2 ? kb * 4 + ((lane & 7) >> 1) : kb * 8 + (lane & 7);
-            r = mb * 16 + (DT::ESZ == 2 ? (lane & 1) * 8 : 0);
-            n = k < kleft ? min(G, rows - r) : 0;
-            q = base + (int64_t)k * ld + r;
-        }
-        intx4 v = {0, 0, 0, 0};
-        if (n >= G) {
-            __builtin_memcpy(&v, q, 16);
-        } else if (n > 0) {
-            constexpr int EPW = 4 / DT::ESZ;
-#pragma unroll
-            for (int e = 0; e < G; ++e)
-                if (e < n) v[e / EPW] |= (int)((uint32_t)q[e] << (e % EPW * 8 * DT::ESZ));
-        }
-        return v;
-    }
-    __device__ static void store(DMP_LDS char *lds, int wave, int lane, int j, const intx4 &v) {
-        *(DMP_LDS intx4 *)(lds + Op::chunk_offset(j * 4 + wave) + lane * 16) = v;
-    }
-};
-
 template <class DT>
 __device__ static inline floatx4 mma16(const intx4 &a, const intx4 &b, const floatx4 &c) {
     if constexpr (std::is_same_v<DT, F16>)
@@ -234,98 +183,6 @@ __device__ static inline TileAt tile_at(const RaggedArgs &p, int g, int r0, int 
         t.B = (const char *)p.B + (g * p.sB + (BKC ? t.col0 * p.ldb : t.col0)) * DT::ESZ;
     }
     return t;
-}
-
-template <class DT, bool AK, bool BKC, int MODE>
-__global__ __launch_bounds__(256) void ragged_any(const RaggedArgs p) {
-    constexpr int BM = 64, BN = 64, TM = 2, TN = 2;
-    constexpr int KT = 128 / DT::ESZ;
-    using LA = AnyOperand<DT, BM, AK>;
-    using LB = AnyOperand<DT, BN, BKC>;
-    using elem = typename DT::elem;
-    __shared__ __attribute__((aligned(1024))) char lds_a[2][LA::Op::BYTES];
-    __shared__ __attribute__((aligned(1024))) char lds_b[2][LB::Op::BYTES];
-    const int lane = lane_id(), wave = wave_id();
-    const int wm = wave >> 1, wn = wave & 1;
-    const int total = (int)(MODE == RAGGED_WGRAD ? p.K : p.M);
-
-    TileAt at;
-    if constexpr (MODE == RAGGED_WGRAD) {
-        const int tiles = p.tiles_m * p.tiles_n;
-        const int g = blockIdx.x / tiles, t = blockIdx.x - g * tiles;
-        const int r0 = load_offset(p, g, total), r1 = max(r0, load_offset(p, g + 1, total));
-        at = tile_at<DT, AK, BKC, MODE, BM, BN>(p, g, r0, r1, t / p.tiles_n, t % p.tiles_n);
-    } else {
-        GroupWalk<BM> walk;
-        walk.load(p, total, lane);
-        int g, r0, r1, tile0;
-        const int t = blockIdx.x / p.tiles_n;
-        if (!walk.find(p, total, lane, t, g, r0, r1, tile0)) return;
-        at = tile_at<DT, AK, BKC, MODE, BM, BN>(p, g, r0, r1, t - tile0, blockIdx.x % p.tiles_n);
-    }
-    const int nkt = at.k / KT + (at.k % KT != 0);
-
-    floatx4 acc[TM][TN] = {};
-    intx4 ra[LA::CPW], rb[LB::CPW];
-    auto fetch = [&](int kt) {
-        const int64_t k0 = (int64_t)kt * KT;
-        const int kleft = min(KT, at.k - kt * KT);
-        const elem *A = (const elem *)at.A + (AK ? k0 : k0 * p.lda);
-        const elem *B = (const elem *)at.B + (BKC ? k0 : k0 * p.ldb);
-#pragma unroll
-        for (int j = 0; j < LA::CPW; ++j) ra[j] = LA::load(A, p.lda, wave, lane, j, at.rows, kleft);
-#pragma unroll
-        for (int j = 0; j < LB::CPW; ++j) rb[j] = LB::load(B, p.ldb, wave, lane, j, at.cols, kleft);
-    };
-    auto put = [&](int buf) {
-#pragma unroll
-        for (int j = 0; j < LA::CPW; ++j) LA::store((DMP_LDS char *)lds_a[buf], wave, lane, j, ra[j]);
-#pragma unroll
-        for (int j = 0; j < LB::CPW; ++j) LB::store((DMP_LDS char *)lds_b[buf], wave, lane, j, rb[j]);
-    };
-    if (nkt > 0) {
-        fetch(0);
-        put(0);
-    }
-    __syncthreads();
-    for (int kt = 0; kt < nkt; ++kt) {
-        if (kt + 1 < nkt) fetch(kt + 1);
-        const DMP_LDS char *la = (const DMP_LDS char *)lds_a[kt & 1];
-        const DMP_LDS char *lb = (const DMP_LDS char *)lds_b[kt & 1];
-        intx4 fa[TM][2], fb[TN][2];
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-#pragma unroll
-            for (int i = 0; i < TM; ++i)
-                fa[i][s] = frag16<DT, typename LA::Op, BM, AK>(la, wm * 32 + i * 16, s, lane);
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-                fb[j][s] = frag16<DT, typename LB::Op, BN, BKC>(lb, wn * 32 + j * 16, s, lane);
-        }
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int i = 0; i < TM; ++i)
-#pragma unroll
-                for (int j = 0; j < TN; ++j) acc[i][j] = mma16<DT>(fa[i][s], fb[j][s], acc[i][j]);
-        if (kt + 1 < nkt) put((kt + 1) & 1);
-        __syncthreads();
-    }
-    const int64_t base = MODE == RAGGED_WGRAD ? at.group * p.sC : 0;
-#pragma unroll
-    for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int r = wm * 32 + i * 16 + 4 * (lane >> 4) + q, c = wn * 32 + j * 16 + (lane & 15);
-                if (r >= at.rows || c >= at.cols) continue;
-                const int64_t idx = base + (at.row0 + r) * p.ldc + at.col0 + c;
-                const floatx4 a = {acc[i][j][q], 0, 0, 0};
-                const floatx4 cv = p.ep.use_c ? load4<float>(p.C, idx, p.ep.c_type, false, 1)
-                                              : floatx4{0, 0, 0, 0};
-                store4<float>(p.D, idx, finish4(a, cv, p.ep), p.ep.d_type, false, 1);
-            }
 }
 
 }  // namespace dmp

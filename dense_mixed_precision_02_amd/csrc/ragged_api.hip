@@ -8,6 +8,7 @@
 #include "quant8.hpp"
 #include "ragged.hpp"
 #include "ragged_plan.hpp"
+#include "ragged_staged.hpp"
 #include "ragged_tile.hpp"
 #include "scaled_tile.hpp"
 #include "skinny.hpp"
@@ -29,27 +30,33 @@ EpiParams out_stage(float alpha, float beta, int c_type, int d_type) {
 
 int launched() { return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_HIP; }
 
+// One workgroup to each tile there can be.  ROWS, SCALED: row tiles, at most one
+// more for each group than the rows fill.  WGRAD: runs of tiles (my_tile), the
+// tiles that an XCD works on at a time, but few enough that every XCD gets some.
+int64_t tile_grid(gemm_handle_t h, RaggedArgs &a, int mode, int bm, int bn, int per_cu) {
+    a.tiles_n = (int)cdiv(a.N, bn);
+    if (mode != RAGGED_WGRAD) return (cdiv(a.M, bm) + a.groups) * a.tiles_n;
+    a.tiles_m = (int)cdiv(a.M, bm);
+    const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
+    a.run = (int)std::max<int64_t>(1, std::min<int64_t>(h->num_cus / 8 * per_cu, cdiv(a.groups * tiles, 8)));
+    return cdiv(a.groups * cdiv(tiles, a.run), 8) * 8 * a.run;
+}
+
 template <class DT, bool AK, bool BKC, int MODE>
-int launch_any(const RaggedArgs &a, hipStream_t s) {
-    // row tiles: at most one more for each group than the rows fill
-    const int64_t row_tiles = MODE == RAGGED_WGRAD ? (int64_t)a.groups * a.tiles_m : cdiv(a.M, 64) + a.groups;
-    const int64_t grid = row_tiles * a.tiles_n;
+int launch_tile(gemm_handle_t h, RaggedArgs a, hipStream_t s) {
+    a.cut = h->num_cus;  // 256 x 256 tiles: one workgroup to a CU
+    const int64_t grid = tile_grid(h, a, MODE, 256, 256, 1) + (MODE == RAGGED_ROWS ? 2 * a.cut : 0);
     if (grid > 0x7fffffff) return GEMM_ERR_INVALID_ARG;
-    hipLaunchKernelGGL((ragged_any<DT, AK, BKC, MODE>), dim3((unsigned)grid), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((ragged_tile<DT, 256, 256, AK, BKC, MODE>), dim3((unsigned)grid), dim3(256), 0, s, a);
     return launched();
 }
 
-template <class DT, int E, bool AK, bool BKC, int MODE>
-int launch_tile(gemm_handle_t h, RaggedArgs a, hipStream_t s) {
-    a.tiles_m = MODE == RAGGED_WGRAD ? (int)cdiv(a.M, E) : 0;
-    a.tiles_n = (int)cdiv(a.N, E);
-    a.cut = E == 256 ? h->num_cus : 0;  // 256 x 256 tiles: one workgroup to a CU
-    // ROWS: row tiles, at most one more for each group than the rows fill, and the
-    // cut last round.  WGRAD: every group's tiles rounded up to a multiple of 8.
-    const int64_t grid = MODE == RAGGED_WGRAD ? (int64_t)a.groups * cdiv((int64_t)a.tiles_m * a.tiles_n, 8) * 8
-                                              : (cdiv(a.M, E) + a.groups) * a.tiles_n + 2 * a.cut;
+template <class DT, bool AK, bool BKC, int MODE, bool FAST>
+int launch_staged(gemm_handle_t h, RaggedArgs a, hipStream_t s) {
+    const int64_t grid = tile_grid(h, a, MODE, 128, 128, 2);
     if (grid > 0x7fffffff) return GEMM_ERR_INVALID_ARG;
-    hipLaunchKernelGGL((ragged_tile<DT, E, E, AK, BKC, MODE>), dim3((unsigned)grid), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((ragged_staged<DT, 128, 128, AK, BKC, MODE, FAST, FAST ? 4 : 2>), dim3((unsigned)grid),
+                       dim3(256), 0, s, a);
     return launched();
 }
 
@@ -65,34 +72,33 @@ int launch_skinny(RaggedArgs a, hipStream_t s) {
 
 template <class DT, bool AK, bool BKC, int MODE>
 int launch_cfg(gemm_handle_t h, int cfg, const RaggedArgs &a, hipStream_t s) {
-    if (cfg == CFG_L) return launch_tile<DT, 256, AK, BKC, MODE>(h, a, s);
-    if (cfg == CFG_M) return launch_tile<DT, 128, AK, BKC, MODE>(h, a, s);
+    if (cfg == CFG_L) return launch_tile<DT, AK, BKC, MODE>(h, a, s);
+    if (cfg == CFG_M) return launch_staged<DT, AK, BKC, MODE, true>(h, a, s);
     if constexpr (MODE == RAGGED_ROWS && BKC) {
         if (cfg == CFG_SKINNY) return launch_skinny<DT, MODE, 1, 4, 0, 0>(a, s);
         if (cfg == CFG_SKINNY4) return launch_skinny<DT, MODE, 4, 4, 0, 0>(a, s);
     }
-    return launch_any<DT, AK, BKC, MODE>(a, s);
+    return launch_staged<DT, AK, BKC, MODE, false>(h, a, s);
 }
 
 template <int FA, int FB, int BM, int BN, int WM, int WN, bool EXACT>
-int launch_scaled_tile(RaggedArgs a, hipStream_t s) {
-    a.tiles_n = (int)cdiv(a.N, BN);
-    const int64_t grid = (cdiv(a.M, BM) + a.groups) * a.tiles_n;
+int launch_scaled_tile(gemm_handle_t h, RaggedArgs a, hipStream_t s) {
+    const int64_t grid = tile_grid(h, a, RAGGED_SCALED, BM, BN, 1);
     if (grid > 0x7fffffff) return GEMM_ERR_INVALID_ARG;
     hipLaunchKernelGGL((scaled_tile<FA, FB, BM, BN, WM, WN, EXACT>), dim3((unsigned)grid), dim3(WM * WN * 64), 0, s, a);
     return launched();
 }
 
 template <int FA, int FB>
-int launch_scaled(int cfg, const RaggedArgs &a, hipStream_t s) {
+int launch_scaled(gemm_handle_t h, int cfg, const RaggedArgs &a, hipStream_t s) {
     if (cfg == CFG_SKINNY) return launch_skinny<F8<FA, FB>, RAGGED_SCALED, 1, 4, FA, FB>(a, s);
     if (cfg == CFG_SKINNY4) return launch_skinny<F8<FA, FB>, RAGGED_SCALED, 4, 4, FA, FB>(a, s);
     const bool exact = a.ep.d_type == OUT_F32;
     if (cfg == CFG_L)
-        return exact ? launch_scaled_tile<FA, FB, 256, 128, 4, 2, true>(a, s)
-                     : launch_scaled_tile<FA, FB, 256, 256, 2, 4, false>(a, s);
-    return exact ? launch_scaled_tile<FA, FB, 128, 128, 2, 2, true>(a, s)
-                 : launch_scaled_tile<FA, FB, 128, 128, 2, 2, false>(a, s);
+        return exact ? launch_scaled_tile<FA, FB, 256, 128, 4, 2, true>(h, a, s)
+                     : launch_scaled_tile<FA, FB, 256, 256, 2, 4, false>(h, a, s);
+    return exact ? launch_scaled_tile<FA, FB, 128, 128, 2, 2, true>(h, a, s)
+                 : launch_scaled_tile<FA, FB, 128, 128, 2, 2, false>(h, a, s);
 }
 
 template <int XT, int FMT>
@@ -123,7 +129,6 @@ int gemm_run_grouped(gemm_handle_t h, const void *A, const void *B, const void *
     a.sB = K == 0 ? 0 : (bc ? N : K) * ldb;
     a.groups = (int)groups;
     a.off32 = (flags & GEMM_OFFSETS_I32) != 0;
-    a.tiles_n = (int)cdiv(N, 64);
     a.ep = ep;
     hipStream_t s = (hipStream_t)stream;
     const int cfg = grouped_cfg(h->num_cus, A, B, groups, M, N, K, lda, ldb, bc);
@@ -147,8 +152,6 @@ int gemm_run_grouped_wgrad(gemm_handle_t h, const void *X, const void *Y, const 
     a.sC = M * ldc;
     a.groups = (int)groups;
     a.off32 = (flags & GEMM_OFFSETS_I32) != 0;
-    a.tiles_m = (int)cdiv(M, 64);
-    a.tiles_n = (int)cdiv(N, 64);
     a.ep = ep;
     hipStream_t s = (hipStream_t)stream;
     const int cfg = wgrad_cfg(h->num_cus, X, Y, groups, M, N, K, ldx, ldy);
@@ -197,13 +200,12 @@ int gemm_run_scaled8(gemm_handle_t h, const gemm_q8_t *A, const gemm_q8_t *B, co
     a.sb_col = B->scale_row; a.sb_k = B->scale_k; a.sb_group = groups > 1 ? B->scale_group : 0;
     a.groups = (int)groups;
     a.off32 = (flags & GEMM_OFFSETS_I32) != 0;
-    a.tiles_n = (int)cdiv(N, 64);
     a.ep = ep;
     hipStream_t s = (hipStream_t)stream;
     const int cfg = scaled_cfg(h->num_cus, groups, M, N);
     const bool a4 = A->type == GEMM_E4M3, b4 = B->type == GEMM_E4M3;
-    if (a4) return b4 ? launch_scaled<0, 0>(cfg, a, s) : launch_scaled<0, 1>(cfg, a, s);
-    return b4 ? launch_scaled<1, 0>(cfg, a, s) : launch_scaled<1, 1>(cfg, a, s);
+    if (a4) return b4 ? launch_scaled<0, 0>(h, cfg, a, s) : launch_scaled<0, 1>(h, cfg, a, s);
+    return b4 ? launch_scaled<1, 0>(h, cfg, a, s) : launch_scaled<1, 1>(h, cfg, a, s);
 }
 
 }  // extern "C"

@@ -148,7 +148,9 @@ inline int grouped_cfg(int num_cus, const void *A, const void *B, int64_t groups
 inline int wgrad_cfg(int num_cus, const void *X, const void *Y, int64_t groups, int64_t M, int64_t N,
                      int64_t K, int64_t ldx, int64_t ldy) {
     if (K == 0 || !granule_ok(X, Y, M, N, K, ldx, ldy, GEMM_F16, true, false, true)) return CFG_GENERIC;
-    if (groups * cdiv(M, 256) * cdiv(N, 256) >= num_cus) return CFG_L;
+    const int64_t t256 = cdiv(M, 256) * cdiv(N, 256);
+    const double useful = (double)M * (double)N / ((double)t256 * 65536.0);
+    if (groups * t256 >= num_cus && useful >= 0.75 && K / groups >= 256) return CFG_L;
     return CFG_M;
 }
 

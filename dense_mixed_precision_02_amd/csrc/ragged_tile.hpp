@@ -4,13 +4,13 @@
 // instructions with the accumulators tied in place, 128-byte k-tiles copied
 // straight to LDS, double buffered, fragments read between the instructions.
 //
-// K-contiguous operands are copied straight to LDS.  An MN-contiguous one (B
-// row-major, and both of the weight gradients') is turned on its way: a thread
-// loads 8 k of 8 rows as eight vectors, packs the pairs of neighbouring k with
-// byte permutes and writes K-contiguous granules, so that LDS and the K loop are
-// the same for every layout.  tile16_gemm reads such an operand with transposing
-// LDS reads instead, in one piece behind the barrier, with no matrix instruction
-// beside them (the compiler makes each wait for every copy in flight).
+// The K loop and the reading of MN-contiguous operands (B row-major, and both of
+// the weight gradients') are tile16_gemm's.  Two other ways for the latter were
+// built: turning 8 x 8 blocks in registers between the load and LDS (872 against
+// 1214 TFLOP/s on 8 x 2048 x 4096 x 4096 with a row-major B: the loads of eight
+// rows to an instruction take longer than the transposing reads), and copies
+// written as assembly so that the compiler would not hold the transposing reads
+// back (not kept).
 //
 // Which tile.  ROWS: a workgroup finds its tile's group by a scan of the
 // offsets.  The tiles past the last full round of the device's workgroups are
@@ -18,7 +18,8 @@
 // workgroup works on while the others idle costs the whole launch its time.
 // WGRAD: the outputs are common to all groups, so the grid is known, but a
 // tile's time is its group's rows: groups are taken longest first, and each
-// group's tiles are spread over all XCDs.
+// group's tiles are spread over the XCDs in runs (2048 x 4096 gradients of 16384
+// rows, unevenly over 8 groups: 315 us with each group on one XCD, 264 so).
 //
 // Edges: a group's last row tile is usually partial, so rows are bounded by
 // predicates on whole vectors instead of a slow path for the whole slab.
@@ -142,88 +143,6 @@ __device__ static inline void store_wave_tile(DMP_LDS float *slab, const EpiPara
 // s have thing s * N / NS behind it?
 __device__ static constexpr bool slot_has(int s, int N, int NS) { return (s + 1) * N / NS != s * N / NS; }
 
-// A K-contiguous operand's copies to LDS: Operand::issue's places and bounds.
-template <class DT, int R>
-struct Copied {
-    using Op = Operand<DT, R, 4, true>;
-    static constexpr int FETCHES = Op::CPW, PUTS = 0;
-    Op op;
-    const char *base;
-    int wave, rows, kleft;
-    __amdgpu_buffer_rsrc_t rs;
-    __device__ void init(const char *X, int wave_, int lane, int64_t ld, int rows_) {
-        op.init(wave_, lane, ld, 0, rows_);
-        base = X;
-        wave = wave_;
-        rows = rows_;
-    }
-    // For k-tile kt, of which kleft values remain (none: not positive).
-    __device__ void aim(int64_t, int kt, int kleft_) {
-        rs = make_rsrc(base + (int64_t)kt * 128);
-        kleft = kleft_;
-    }
-    __device__ void fetch(DMP_LDS char *lds, int c) const { op.issue(rs, lds, wave, c, kleft, rows); }
-    __device__ void put(DMP_LDS char *, int) const {}
-};
-
-// An MN-contiguous 16-bit operand, turned.  Thread: k 8 kb .. 8 kb + 7 of rows
-// PER rb .. PER rb + PER - 1; kb = lane % 8, so that eight lanes write the eight
-// granules of a row (no bank conflicts), and rb = lane / 8 counts on, so that a
-// load takes runs of 8 PER neighbouring elements (128 bytes for R = 256).  The
-// loads (fetch) stay in registers from step 1 of a k-tile to step 0 of the next,
-// where they are turned and written (put), one granule at a time.
-template <class DT, int R>
-struct Turned {
-    using Op = Operand<DT, R, 4, true>;  // the LDS layout
-    static_assert(DT::ESZ == 2 && (R == 256 || R == 128), "8 k of 8 or 4 rows to a thread");
-    static constexpr int PER = R / 32, W = PER / 2, FETCHES = 8, PUTS = PER;
-    const char *base;
-    int off, kb8, pitch, kleft;  // off: this thread's first element, or out of range; pitch: bytes from k to k
-    uint32_t at;                 // its first granule in LDS
-    int in[8][W];
-    __amdgpu_buffer_rsrc_t rs;
-    __device__ void init(const char *X, int wave, int lane, int64_t ld, int rows) {
-        const int rb = wave * 8 + (lane >> 3), row = rb * PER;
-        base = X;
-        kb8 = (lane & 7) * 8;
-        pitch = (int)ld * 2;
-        off = row < rows ? kb8 * pitch + row * 2 : OOB_OFFSET;
-        at = row * 128 + (((lane & 7) ^ swz(row)) << 4);
-    }
-    __device__ void aim(int64_t ld, int kt, int kleft_) {
-        rs = make_rsrc(base + (int64_t)kt * Op::KT * ld * 2);
-        kleft = kleft_;
-    }
-    __device__ void fetch(DMP_LDS char *, int e) {
-        const int v = kb8 < kleft - e ? off : OOB_OFFSET;
-        if constexpr (W == 4) {
-            const intx4 x = __builtin_bit_cast(intx4, __builtin_amdgcn_raw_buffer_load_b128(rs, v, e * pitch, 0));
-#pragma unroll
-            for (int w = 0; w < 4; ++w) in[e][w] = x[w];
-        } else {
-            const intx2 x = __builtin_bit_cast(intx2, __builtin_amdgcn_raw_buffer_load_b64(rs, v, e * pitch, 0));
-            in[e][0] = x[0];
-            in[e][1] = x[1];
-        }
-    }
-    // Row r of the block: swz xors the low three bits of the row, which count r,
-    // into the granule's place.
-    __device__ void put(DMP_LDS char *lds, int r) const {
-        intx4 v;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-            v[c] = __builtin_amdgcn_perm(in[2 * c + 1][r / 2], in[2 * c][r / 2], r % 2 ? 0x07060302u : 0x05040100u);
-        *(DMP_LDS intx4 *)(lds + (at ^ (r << 4)) + r * 128) = v;
-    }
-};
-
-// frag16 (tile16_gemm.hpp) of row block r of a wave, l being the wave's first: the
-// lane's place once, the row block and the step as constants beside it.
-__device__ static inline intx4 frag_at(const DMP_LDS char *l, int r, int s, int lane) {
-    const int row = lane & 15, grp = lane >> 4;
-    return *(const DMP_LDS intx4 *)(l + row * 128 + (((2 * grp + s) ^ swz(row)) << 4) + r * 2048);
-}
-
 // One tile of BM x BN on four waves; the LDS arrays hold at least its panels.
 template <class DT, int BM, int BN, bool AK, bool BKC>
 struct Tile16 {
@@ -231,11 +150,10 @@ struct Tile16 {
     static constexpr int WTM = BM / WM, WTN = BN / WN;
     static constexpr int TM = WTM / 16, TN = WTN / 16, NI = TM * TN;
     static constexpr int KT = 128 / DT::ESZ;
-    using SrcA = std::conditional_t<AK, Copied<DT, BM>, Turned<DT, BM>>;
-    using SrcB = std::conditional_t<BKC, Copied<DT, BN>, Turned<DT, BN>>;
-    using OpA = typename SrcA::Op;
-    using OpB = typename SrcB::Op;
-    static constexpr int NC = SrcA::FETCHES + SrcB::FETCHES, NP = SrcA::PUTS + SrcB::PUTS;
+    // padding of the MN-contiguous panels: see tile16_gemm
+    using OpA = Operand<DT, BM, NW, AK, AK ? 0 : 32>;
+    using OpB = Operand<DT, BN, NW, BKC, BKC ? 0 : 32>;
+    static constexpr int NC = OpA::CPW + OpB::CPW;
 
     __device__ static inline void run(const RaggedArgs &p, const TileAt &at, int64_t first, DMP_LDS char *a0,
                                       DMP_LDS char *b0, DMP_LDS char *a1, DMP_LDS char *b1) {
@@ -244,10 +162,10 @@ struct Tile16 {
         const int lane = lane_id(), wave = wave_id();
         const int wm = wave / WN, wn = wave % WN;
         const int kspan = at.k, nkt = kspan / KT + (kspan % KT != 0);
-        SrcA ca;
-        SrcB cb;
-        ca.init(at.A, wave, lane, p.lda, at.rows);
-        cb.init(at.B, wave, lane, p.ldb, at.cols);
+        OpA opa;
+        OpB opb;
+        opa.init(wave, lane, p.lda, 0, at.rows);
+        opb.init(wave, lane, p.ldb, 0, at.cols);
         floatx4 acc[TM][TN];
 #pragma unroll
         for (int i = 0; i < TM; ++i)
@@ -259,71 +177,81 @@ struct Tile16 {
 #pragma unroll
                 for (int j = 0; j < TN; ++j) asm volatile("" : "+a"(acc[i][j]));
         };
-        // fetch c (A's, then B's) of the k-tile that `aim` named; k-tiles past the end
-        // are zeros and touch no memory
-        auto aim = [&](int kt) {
-            ca.aim(p.lda, kt, min(kspan - kt * KT, KT));
-            cb.aim(p.ldb, kt, min(kspan - kt * KT, KT));
+        // copy c (A's chunks, then B's) of k-tile kt; k-tiles past the end are zeros and touch no memory
+        auto copy = [&](int kt, int buf, int c) {
+            const int kleft = min(kspan - kt * KT, KT);
+            if (c < OpA::CPW)
+                opa.issue(make_rsrc(OpA::tile_base(at.A, p.lda, 0, (int64_t)kt * KT)), LA[buf], wave, c, kleft, at.rows);
+            else
+                opb.issue(make_rsrc(OpB::tile_base(at.B, p.ldb, 0, (int64_t)kt * KT)), LB[buf], wave, c - OpA::CPW,
+                          kleft, at.cols);
         };
-        auto fetch = [&](int buf, int c) {
-            if (c < SrcA::FETCHES) ca.fetch(LA[buf], c);
-            else cb.fetch(LB[buf], c - SrcA::FETCHES);
+        auto fragA = [&](int buf, int i, int s) {
+            return frag16<DT, OpA, BM, AK>(LA[buf], wm * WTM + i * 16, s, lane);
         };
-        auto put = [&](int buf, int c) {
-            if (c < SrcA::PUTS) ca.put(LA[buf], c);
-            else cb.put(LB[buf], c - SrcA::PUTS);
+        auto fragB = [&](int buf, int j, int s) {
+            return frag16<DT, OpB, BN, BKC>(LB[buf], wn * WTN + j * 16, s, lane);
         };
-        // fragments: the next step's are read while this one's are multiplied
-        intx4 fa[2][TM], fb[2][TN];
-        // fragment r (A's, then B's) of step s of the k-tile in buf
-        auto read = [&](int buf, int s, int r) {
-            if (r < TM) fa[s][r] = frag_at(LA[buf] + wm * WTM * 128, r, s, lane);
-            else fb[s][r - TM] = frag_at(LB[buf] + wn * WTN * 128, r - TM, s, lane);
+        // fragment sets: as in tile16_gemm
+        constexpr int NSA = AK ? 2 : 4, NSB = BKC ? 2 : 4;
+        intx4 fa[NSA][TM], fb[NSB][TN];
+        auto seta = [](int buf, int s) { return AK ? s : 2 * buf + s; };
+        auto setb = [](int buf, int s) { return BKC ? s : 2 * buf + s; };
+        auto read_mn = [&](int buf) {
+            if constexpr (!AK) {
+#pragma unroll
+                for (int s2 = 0; s2 < 2; ++s2)
+#pragma unroll
+                    for (int i = 0; i < TM; ++i) fa[seta(buf, s2)][i] = fragA(buf, i, s2);
+            }
+            if constexpr (!BKC) {
+#pragma unroll
+                for (int s2 = 0; s2 < 2; ++s2)
+#pragma unroll
+                    for (int j = 0; j < TN; ++j) fb[setb(buf, s2)][j] = fragB(buf, j, s2);
+            }
         };
-        // Per k-tile kt in buffer cur, step 0: the step-1 fragments are read, and in the
-        // second half k-tile kt + 1, on its way in registers where an operand is turned,
-        // is written to the other buffer.  Then every copy has landed and the waves meet.
-        // Step 1: the next k-tile's step-0 fragments are read, and k-tile kt + 2 is
-        // fetched (to buffer cur, or to registers).
+        // fragment r (A's, then B's) of step s of the k-tile in buf, where it is read between instructions
+        auto read_one = [&](int buf, int s, int r) {
+            if (r < TM) {
+                if constexpr (AK) fa[seta(buf, s)][r] = fragA(buf, r, s);
+            } else {
+                if constexpr (BKC) fb[setb(buf, s)][r - TM] = fragB(buf, r - TM, s);
+            }
+        };
         auto ktile = [&](int kt, int cur) {
 #pragma unroll
             for (int i = 0; i < TM; ++i)
 #pragma unroll
                 for (int j = 0; j < TN; ++j) {
-                    Mma16<DT>::run(acc[i][j], fa[0][i], fb[0][j]);
-                    const int q = i * TN + j, h = q - NI / 2;
-                    if (slot_has(q, TM + TN, NI)) read(cur, 1, q * (TM + TN) / NI);
-                    if constexpr (NP > 0) {
-                        if (h >= 0 && slot_has(h, NP, NI / 2)) put(cur ^ 1, h * NP / (NI / 2));
-                    }
+                    Mma16<DT>::run(acc[i][j], fa[seta(cur, 0)][i], fb[setb(cur, 0)][j]);
+                    const int q = i * TN + j;
+                    if (slot_has(q, TM + TN, NI)) read_one(cur, 1, q * (TM + TN) / NI);
                 }
             wait_vmcnt<0>();
             __syncthreads();
+            read_mn(cur ^ 1);
 #pragma unroll
             for (int i = 0; i < TM; ++i)
 #pragma unroll
                 for (int j = 0; j < TN; ++j) {
-                    Mma16<DT>::run(acc[i][j], fa[1][i], fb[1][j]);
+                    Mma16<DT>::run(acc[i][j], fa[seta(cur, 1)][i], fb[setb(cur, 1)][j]);
                     const int q = i * TN + j;
-                    if (q == 0) aim(kt + 2);
-                    if (slot_has(q, NC, NI)) fetch(cur, q * NC / NI);
-                    if (slot_has(q, TM + TN, NI)) read(cur ^ 1, 0, q * (TM + TN) / NI);
+                    if (slot_has(q, NC, NI)) copy(kt + 2, cur, q * NC / NI);
+                    if (slot_has(q, TM + TN, NI)) read_one(cur ^ 1, 0, q * (TM + TN) / NI);
                 }
             step_sync();
         };
         if (nkt > 0) {
-            aim(0);
 #pragma unroll
-            for (int c = 0; c < NC; ++c) fetch(0, c);
-#pragma unroll
-            for (int c = 0; c < NP; ++c) put(0, c);
+            for (int c = 0; c < NC; ++c) copy(0, 0, c);
             wait_vmcnt<0>();
             __syncthreads();
+            read_mn(0);
 #pragma unroll
-            for (int r = 0; r < TM + TN; ++r) read(0, 0, r);
-            aim(1);
+            for (int r = 0; r < TM + TN; ++r) read_one(0, 0, r);
 #pragma unroll
-            for (int c = 0; c < NC; ++c) fetch(1, c);
+            for (int c = 0; c < NC; ++c) copy(1, 1, c);
             pin_acc();
             asm volatile("s_nop 7" ::);
             // two k-tiles to a trip so that each buffer is named statically; an
@@ -356,6 +284,42 @@ __device__ static inline int longest_first(const RaggedArgs &p, int q, int total
     return __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)__ballot(lane < p.groups && rank == q)) - 1);
 }
 
+// This workgroup's tile (false: it has none).  One tile to a workgroup; the grid
+// is the most tiles there can be.
+template <class DT, bool AK, bool BKC, int MODE, int BM, int BN>
+__device__ static inline bool my_tile(const RaggedArgs &p, int lane, TileAt &at) {
+    const int total = (int)(MODE == RAGGED_WGRAD ? p.K : p.M);
+    if constexpr (MODE == RAGGED_WGRAD) {
+        // Workgroup i runs on XCD i % 8 and is the (i / 8)-th there.  Every group's
+        // tiles are cut into runs of p.run, as many as one XCD works on at a time (they
+        // share panels through its L2); the runs, longest groups first, are dealt out
+        // to the XCDs to and fro, so that no XCD gets a long group alone.
+        const int tiles = p.tiles_m * p.tiles_n, runs = (tiles + p.run - 1) / p.run;
+        const int seq = blockIdx.x / 8, s = seq / p.run, xcd = blockIdx.x % 8;
+        const int r = 8 * s + (s % 2 ? 7 - xcd : xcd), q = r / runs;
+        const int t = (r - q * runs) * p.run + seq - s * p.run;
+        if (q >= p.groups || t >= tiles) return false;
+        const int g = p.groups <= 64 ? longest_first(p, q, total, lane) : q;
+        int tm, tn;
+        grouped_order(t, p.tiles_m, p.tiles_n, tm, tn);
+        const int r0 = __builtin_amdgcn_readfirstlane(load_offset(p, g, total));
+        const int r1 = max(r0, __builtin_amdgcn_readfirstlane(load_offset(p, g + 1, total)));
+        at = tile_at<DT, AK, BKC, MODE, BM, BN>(p, g, r0, r1, tm, tn);
+    } else {
+        GroupWalk<BM> count, walk;
+        count.load(p, total, lane);
+        walk = count;
+        const int64_t tiles = (int64_t)count.all(p, total, lane) * p.tiles_n;
+        if ((int64_t)blockIdx.x >= tiles) return false;
+        const int t = xcd_remap(blockIdx.x, (int)tiles);
+        int g, r0, r1, tile0, tm, tn;
+        if (!walk.find(p, total, lane, t / p.tiles_n, g, r0, r1, tile0)) return false;
+        grouped_order(t - tile0 * p.tiles_n, (r1 - r0 - 1) / BM + 1, p.tiles_n, tm, tn);
+        at = tile_at<DT, AK, BKC, MODE, BM, BN>(p, g, r0, r1, tm, tn);
+    }
+    return true;
+}
+
 template <class DT, int BM, int BN, bool AK, bool BKC, int MODE>
 __global__ __launch_bounds__(256) void ragged_tile(const RaggedArgs p) {
     using T = Tile16<DT, BM, BN, AK, BKC>;
@@ -364,26 +328,13 @@ __global__ __launch_bounds__(256) void ragged_tile(const RaggedArgs p) {
     __shared__ __attribute__((aligned(1024))) char lds_a1[T::OpA::BYTES];
     __shared__ __attribute__((aligned(1024))) char lds_b1[T::OpB::BYTES];
     const int lane = lane_id();
-    const int total = (int)(MODE == RAGGED_WGRAD ? p.K : p.M);
-
     if constexpr (MODE == RAGGED_WGRAD) {
-        // Workgroup i runs on XCD i % 8 and is the (i / 8)-th there.  Every group's
-        // tiles (rounded up to a multiple of 8) are dealt out in eight runs, one to
-        // each XCD, so that no XCD gets a long group alone.
-        const int tiles = p.tiles_m * p.tiles_n, per = (tiles + 7) / 8;
-        const int seq = blockIdx.x / 8, q = seq / per;
-        const int t = (blockIdx.x % 8) * per + seq - q * per;
-        if (t >= tiles) return;
-        const int g = BM == 256 && p.groups <= 64 ? longest_first(p, q, total, lane) : q;
-        const int r0 = __builtin_amdgcn_readfirstlane(load_offset(p, g, total));
-        const int r1 = max(r0, __builtin_amdgcn_readfirstlane(load_offset(p, g + 1, total)));
-        int tm, tn;
-        grouped_order(t, p.tiles_m, p.tiles_n, tm, tn);
-        const TileAt at = tile_at<DT, AK, BKC, MODE, BM, BN>(p, g, r0, r1, tm, tn);
+        TileAt at;
+        if (!my_tile<DT, AK, BKC, MODE, BM, BN>(p, lane, at)) return;
         T::run(p, at, at.group * p.sC + at.row0 * p.ldc + at.col0, (DMP_LDS char *)lds_a0, (DMP_LDS char *)lds_b0,
                (DMP_LDS char *)lds_a1, (DMP_LDS char *)lds_b1);
     } else {
-        // the grid is the most row tiles there can be; the ones past the last leave
+        const int total = (int)p.M;
         GroupWalk<BM> count, walk;
         count.load(p, total, lane);
         walk = count;

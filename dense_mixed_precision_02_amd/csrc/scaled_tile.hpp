@@ -64,18 +64,8 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void scaled_tile(const RaggedArgs p
 
     const int lane = lane_id(), wave = wave_id(), tid = threadIdx.x;
     const int wm = wave / WN, wn = wave % WN;
-    const int total = (int)p.M;
-
-    GroupWalk<BM> count, walk;
-    count.load(p, total, lane);
-    walk = count;
-    const int64_t tiles = (int64_t)count.all(p, total, lane) * p.tiles_n;
-    if ((int64_t)blockIdx.x >= tiles) return;
-    const int t = xcd_remap(blockIdx.x, (int)tiles);
-    int g, r0, r1, tile0, tm, tn;
-    if (!walk.find(p, total, lane, t / p.tiles_n, g, r0, r1, tile0)) return;
-    grouped_order(t - tile0 * p.tiles_n, (r1 - r0 - 1) / BM + 1, p.tiles_n, tm, tn);
-    const TileAt at = tile_at<DT, true, true, RAGGED_SCALED, BM, BN>(p, g, r0, r1, tm, tn);
+    TileAt at;
+    if (!my_tile<DT, true, true, RAGGED_SCALED, BM, BN>(p, lane, at)) return;
 
     const int kspan = at.k, nkt = kspan / KT + (kspan % KT != 0);
     OpA opa;
@@ -96,7 +86,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void scaled_tile(const RaggedArgs p
     const int srow = tid % BM, snb = tid / BM;
     const bool has = tid < ITEMS && srow < at.rows && 128 * snb < at.cols;
     const float *sa = p.sa + (at.row0 + srow) * p.sa_row;
-    const float *sb = p.sb + g * p.sb_group + ((at.col0 >> 7) + snb) * p.sb_col;
+    const float *sb = p.sb + at.group * p.sb_group + ((at.col0 >> 7) + snb) * p.sb_col;
     float va = 0.0f, vb = 0.0f;
     auto fetch = [&](int kt) {
         if (has) {
