@@ -51,12 +51,12 @@ int launch_tile(gemm_handle_t h, RaggedArgs a, hipStream_t s) {
     return launched();
 }
 
-template <class DT, bool AK, bool BKC, int MODE, bool FAST>
+template <class DT, int BM, int BN, int WM, int WN, bool AK, bool BKC, int MODE, bool FAST>
 int launch_staged(gemm_handle_t h, RaggedArgs a, hipStream_t s) {
-    const int64_t grid = tile_grid(h, a, MODE, 128, 128, 2);
+    const int64_t grid = tile_grid(h, a, MODE, BM, BN, 8 / (WM * WN));
     if (grid > 0x7fffffff) return GEMM_ERR_INVALID_ARG;
-    hipLaunchKernelGGL((ragged_staged<DT, 128, 128, AK, BKC, MODE, FAST, FAST ? 4 : 2>), dim3((unsigned)grid),
-                       dim3(256), 0, s, a);
+    hipLaunchKernelGGL((ragged_staged<DT, BM, BN, WM, WN, AK, BKC, MODE, FAST>), dim3((unsigned)grid),
+                       dim3(WM * WN * 64), 0, s, a);
     return launched();
 }
 
@@ -73,12 +73,16 @@ int launch_skinny(RaggedArgs a, hipStream_t s) {
 template <class DT, bool AK, bool BKC, int MODE>
 int launch_cfg(gemm_handle_t h, int cfg, const RaggedArgs &a, hipStream_t s) {
     if (cfg == CFG_L) return launch_tile<DT, AK, BKC, MODE>(h, a, s);
-    if (cfg == CFG_M) return launch_staged<DT, AK, BKC, MODE, true>(h, a, s);
+    if constexpr (MODE == RAGGED_ROWS) {
+        if (cfg == CFG_M) return launch_staged<DT, 128, 128, 2, 2, AK, BKC, MODE, true>(h, a, s);
+    } else {
+        if (cfg == CFG_S) return launch_staged<DT, 64, 128, 1, 4, AK, BKC, MODE, true>(h, a, s);
+    }
     if constexpr (MODE == RAGGED_ROWS && BKC) {
         if (cfg == CFG_SKINNY) return launch_skinny<DT, MODE, 1, 4, 0, 0>(a, s);
         if (cfg == CFG_SKINNY4) return launch_skinny<DT, MODE, 4, 4, 0, 0>(a, s);
     }
-    return launch_staged<DT, AK, BKC, MODE, false>(h, a, s);
+    return launch_staged<DT, 64, 128, 1, 4, AK, BKC, MODE, false>(h, a, s);
 }
 
 template <int FA, int FB, int BM, int BN, int WM, int WN, bool EXACT>

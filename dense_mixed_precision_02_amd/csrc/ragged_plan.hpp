@@ -140,18 +140,24 @@ inline int grouped_cfg(int num_cus, const void *A, const void *B, int64_t groups
                        int64_t K, int64_t lda, int64_t ldb, bool b_col) {
     if (K == 0 || !granule_ok(A, B, M, N, K, lda, ldb, GEMM_F16, false, b_col, true)) return CFG_GENERIC;
     if (b_col && M <= 64 * groups) return M <= 16 * groups ? CFG_SKINNY : CFG_SKINNY4;
+    // 256 x 256 tiles where the mean group fills most of one and they occupy half the
+    // device (us, 256 x 256 against 128 x 128 tiles: 8 groups, 2048 rows, 4096 x 4096:
+    // 116 / 126; 32 groups, 8192 rows, 2048 x 1024: 72 / 79; but 5003 rows: 70 / 55, and
+    // 4 groups, 1024 rows, 4096 x 4096: 119 / 77)
     const int64_t tiles = (cdiv(M, 256) + groups / 2) * cdiv(N, 256);
-    if (M / groups >= 192 && tiles >= num_cus) return CFG_L;
-    return CFG_M;
+    return M / groups >= 192 && 2 * tiles >= num_cus ? CFG_L : CFG_M;
 }
 
+// Weight gradients: 256 x 256 tiles where they fill the device and lie mostly
+// inside the outputs, else 64 x 128 ones (us, 256 x 256 / 128 x 128 / 64 x 128: 8
+// groups, 4096 rows, 1024 x 1024: 54 / 40 / 31; 24 groups, 3000 rows, 520 x 1032:
+// 65 / 38 / 36; 1024 x 1024: 35 / 38 / 37).
 inline int wgrad_cfg(int num_cus, const void *X, const void *Y, int64_t groups, int64_t M, int64_t N,
                      int64_t K, int64_t ldx, int64_t ldy) {
     if (K == 0 || !granule_ok(X, Y, M, N, K, ldx, ldy, GEMM_F16, true, false, true)) return CFG_GENERIC;
     const int64_t t256 = cdiv(M, 256) * cdiv(N, 256);
     const double useful = (double)M * (double)N / ((double)t256 * 65536.0);
-    if (groups * t256 >= num_cus && useful >= 0.75 && K / groups >= 256) return CFG_L;
-    return CFG_M;
+    return groups * t256 >= num_cus && useful >= 0.75 ? CFG_L : CFG_S;
 }
 
 inline int scaled_cfg(int num_cus, int64_t groups, int64_t M, int64_t N) {

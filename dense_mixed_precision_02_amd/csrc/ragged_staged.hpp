@@ -2,13 +2,12 @@
 // through registers: for groups of middling size, and for every size, alignment
 // and layout.
 //
-// A k-tile (128 bytes of K) comes from memory into registers, DEPTH k-tiles
-// ahead, and goes to one of two LDS buffers just before its turn.  With groups of
-// a hundred rows a k-tile's instructions take a few hundred cycles and the loads
-// some thousands, so the time goes with the bytes in flight.  Registers hold
-// more of them than LDS: at 128 x 128, two workgroups to a CU and four k-tiles
-// each, 256 KB, where ragged_tile.hpp's direct copies have one k-tile each, 64 KB.
-// Half of the tiles' LDS traffic is the price.
+// A k-tile (128 bytes of K) comes from memory into registers, two k-tiles ahead,
+// and goes to one of two LDS buffers just before its turn.  With groups of a
+// hundred rows a k-tile's instructions take a few hundred cycles and its loads
+// some thousands, so the time goes with the bytes in flight, and registers add to
+// what LDS holds (ragged_tile.hpp's direct copies have one k-tile on its way).
+// Four k-tiles ahead measured the same as two.
 //
 // LDS layouts and fragment reads are tile_gemm.hpp's and frag16's; without direct
 // copies in flight the compiler lets the transposing reads run freely.
@@ -24,9 +23,9 @@ namespace dmp {
 
 // This lane's granules of one k-tile of an operand: chunks j = 0 .. CPW - 1, in the
 // places of Operand::issue.
-template <class DT, int R, bool KCONTIG, bool FAST>
+template <class DT, int R, int NW, bool KCONTIG, bool FAST>
 struct Staged {
-    using Op = Operand<DT, R, 4, KCONTIG>;
+    using Op = Operand<DT, R, NW, KCONTIG>;
     using elem = typename DT::elem;
     static constexpr int G = DT::G, CPW = Op::CPW, KT = Op::KT;
     Op op;
@@ -47,7 +46,7 @@ struct Staged {
             const __amdgpu_buffer_rsrc_t rs = make_rsrc(q);
 #pragma unroll
             for (int j = 0; j < CPW; ++j) {
-                const bool ok = KCONTIG ? op.row_or_k + 32 * j < rows && op.fixed < kleft
+                const bool ok = KCONTIG ? op.row_or_k + 8 * NW * j < rows && op.fixed < kleft
                                         : op.fixed < rows && op.row_or_k + Op::KSTEP * j < kleft;
                 v[j] = __builtin_bit_cast(
                     intx4, __builtin_amdgcn_raw_buffer_load_b128(rs, ok ? op.off0 + j * op.step : OOB_OFFSET, 0, 0));
@@ -56,7 +55,7 @@ struct Staged {
             constexpr int EPW = 4 / DT::ESZ;
 #pragma unroll
             for (int j = 0; j < CPW; ++j) {
-                const int r = KCONTIG ? op.row_or_k + 32 * j : op.fixed;
+                const int r = KCONTIG ? op.row_or_k + 8 * NW * j : op.fixed;
                 const int k = KCONTIG ? op.fixed : op.row_or_k + Op::KSTEP * j;
                 const int n = KCONTIG ? (r < rows ? kleft - k : 0) : (k < kleft ? rows - r : 0);
                 const elem *e = (const elem *)q + (KCONTIG ? r * ld + k : k * ld + r);
@@ -73,16 +72,16 @@ struct Staged {
     }
     __device__ void put(DMP_LDS char *lds, int lane, const intx4 (&v)[CPW]) const {
 #pragma unroll
-        for (int j = 0; j < CPW; ++j) *(DMP_LDS intx4 *)(lds + Op::chunk_offset(j * 4 + wave) + lane * 16) = v[j];
+        for (int j = 0; j < CPW; ++j) *(DMP_LDS intx4 *)(lds + Op::chunk_offset(j * NW + wave) + lane * 16) = v[j];
     }
 };
 
-template <class DT, int BM, int BN, bool AK, bool BKC, int MODE, bool FAST, int DEPTH>
-__global__ __launch_bounds__(256, 2) void ragged_staged(const RaggedArgs p) {
-    constexpr int WN = 2, WTM = BM / 2, WTN = BN / 2, TM = WTM / 16, TN = WTN / 16, KT = 128 / DT::ESZ;
-    static_assert(DEPTH % 2 == 0, "a trip of DEPTH k-tiles ends on the buffer it began on");
-    using SA = Staged<DT, BM, AK, FAST>;
-    using SB = Staged<DT, BN, BKC, FAST>;
+template <class DT, int BM, int BN, int WM, int WN, bool AK, bool BKC, int MODE, bool FAST>
+__global__ __launch_bounds__(WM *WN * 64, 2) void ragged_staged(const RaggedArgs p) {
+    constexpr int NW = WM * WN, WTM = BM / WM, WTN = BN / WN, TM = WTM / 16, TN = WTN / 16, KT = 128 / DT::ESZ;
+    constexpr int DEPTH = 2;
+    using SA = Staged<DT, BM, NW, AK, FAST>;
+    using SB = Staged<DT, BN, NW, BKC, FAST>;
     __shared__ __attribute__((aligned(1024))) char lds_a[2][SA::Op::BYTES];
     __shared__ __attribute__((aligned(1024))) char lds_b[2][SB::Op::BYTES];
     const int lane = lane_id(), wave = wave_id();
@@ -107,45 +106,59 @@ __global__ __launch_bounds__(256, 2) void ragged_staged(const RaggedArgs p) {
     };
     auto multiply = [&](int buf) {
         const DMP_LDS char *la = (const DMP_LDS char *)lds_a[buf], *lb = (const DMP_LDS char *)lds_b[buf];
+        // all of the k-tile's fragments first: the reads' latency is met once
+        intx4 fa[2][TM], fb[2][TN];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            intx4 fa[TM], fb[TN];
 #pragma unroll
-            for (int i = 0; i < TM; ++i) fa[i] = frag16<DT, typename SA::Op, BM, AK>(la, wm * WTM + i * 16, s, lane);
+            for (int i = 0; i < TM; ++i) fa[s][i] = frag16<DT, typename SA::Op, BM, AK>(la, wm * WTM + i * 16, s, lane);
 #pragma unroll
-            for (int j = 0; j < TN; ++j) fb[j] = frag16<DT, typename SB::Op, BN, BKC>(lb, wn * WTN + j * 16, s, lane);
+            for (int j = 0; j < TN; ++j) fb[s][j] = frag16<DT, typename SB::Op, BN, BKC>(lb, wn * WTN + j * 16, s, lane);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
 #pragma unroll
             for (int i = 0; i < TM; ++i)
 #pragma unroll
-                for (int j = 0; j < TN; ++j) acc[i][j] = mma16<DT>(fa[i], fb[j], acc[i][j]);
-        }
+                for (int j = 0; j < TN; ++j) acc[i][j] = mma16<DT>(fa[s][i], fb[s][j], acc[i][j]);
     };
+    const int64_t first = (MODE == RAGGED_WGRAD ? at.group * p.sC : 0) + at.row0 * p.ldc + at.col0;
     if (nkt > 0) {
-        // (k-tiles past the end: a branch that every lane takes or none, so that short
-        // sums do not load zeros)
+        // K-tiles past the end are fetched too (out of range: zeros, no memory is
+        // touched), so that on every path the same number of loads is in flight: behind
+        // a branch the compiler would wait for all of them at each turn.
 #pragma unroll
-        for (int s = 0; s < DEPTH; ++s)
-            if (s < nkt) fetch(s, s);
+        for (int s = 0; s < DEPTH; ++s) fetch(s, s);
         put(0, 0);
         barrier_vmcnt<63>();
-        for (int kt = 0; kt < nkt; kt += DEPTH) {
+        bool done = nkt == 1;
+        for (int kt = 0; !done; kt += DEPTH) {
 #pragma unroll
             for (int s = 0; s < DEPTH; ++s) {
                 // k-tile kt + s is in LDS buffer s % 2, the next DEPTH - 1 are on their way
-                if (kt + s < nkt) {
-                    if (kt + s + DEPTH < nkt) fetch(kt + s + DEPTH, s);
-                    multiply(s % 2);
-                    if (kt + s + 1 < nkt) put((s + 1) % DEPTH, (s + 1) % 2);
-                    barrier_vmcnt<63>();
+                fetch(kt + s + DEPTH, s);
+                asm volatile("" ::: "memory");  // issued here, not sunk to where it is needed
+                __builtin_amdgcn_sched_barrier(0);
+                multiply(s % 2);
+                put((s + 1) % DEPTH, (s + 1) % 2);
+                barrier_vmcnt<63>();
+                if (kt + s + 2 >= nkt) {
+                    done = true;
+                    break;
                 }
             }
         }
+        multiply((nkt - 1) % 2);
     }
     __syncthreads();
-    constexpr int SLAB = 32 * (WTN + 4) * 4;
-    static_assert(2 * SLAB <= 2 * SA::Op::BYTES && 2 * SLAB <= 2 * SB::Op::BYTES, "slabs must fit");
-    DMP_LDS char *slab = wave < 2 ? (DMP_LDS char *)&lds_a[0][0] + wave * SLAB : (DMP_LDS char *)&lds_b[0][0] + (wave - 2) * SLAB;
-    const int64_t first = (MODE == RAGGED_WGRAD ? at.group * p.sC : 0) + at.row0 * p.ldc + at.col0;
+    // each wave's slab in one of the operands' buffers, as many as fit A's
+    constexpr int SLAB = 32 * (WTN + 4) * 4, INA = 2 * SA::Op::BYTES / SLAB;
+    static_assert((NW - INA) * SLAB <= 2 * SB::Op::BYTES, "slabs must fit");
+    DMP_LDS char *slab = wave < INA ? (DMP_LDS char *)&lds_a[0][0] + wave * SLAB
+                                    : (DMP_LDS char *)&lds_b[0][0] + (wave - INA) * SLAB;
+    // (C is read here, not ahead of the last k-tiles: fetching it into registers early
+    // made no case faster and 520 x 1032 gradients slower, 36 -> 43 us)
     store_wave_tile<WTM, WTN>((DMP_LDS float *)slab, p.ep, (const char *)p.C + first * out_size(p.ep.c_type),
                               (char *)p.D + first * out_size(p.ep.d_type), p.ldc, at.rows, at.cols, wm * WTM,
                               wn * WTN, lane, [&](int i, int j) { return acc[i][j]; });
