@@ -25,22 +25,21 @@
 
 namespace dmp {
 
-// Bytes 8 h .. 8 h + 7 of a granule as eight bf16 values (exact).
+// Bytes 8 h + 2 w and the next of a granule as two bf16 values (exact).
+template <int FMT>
+__device__ static inline int widen2(const intx4 &v, int h, int w) {
+    const uint32_t x = (uint32_t)v[2 * h + w / 2];
+    if constexpr (FMT == 0)
+        return __builtin_bit_cast(int, w % 2 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, 1.0f, true)
+                                             : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, 1.0f, false));
+    else
+        return __builtin_bit_cast(int, w % 2 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(x, 1.0f, true)
+                                             : __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(x, 1.0f, false));
+}
+// Bytes 8 h .. 8 h + 7 as eight.
 template <int FMT>
 __device__ static inline intx4 widen8(const intx4 &v, int h) {
-    intx4 r;
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-        const uint32_t x = (uint32_t)v[2 * h + w];
-        if constexpr (FMT == 0) {
-            r[2 * w] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, 1.0f, false));
-            r[2 * w + 1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, 1.0f, true));
-        } else {
-            r[2 * w] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(x, 1.0f, false));
-            r[2 * w + 1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(x, 1.0f, true));
-        }
-    }
-    return r;
+    return intx4{widen2<FMT>(v, h, 0), widen2<FMT>(v, h, 1), widen2<FMT>(v, h, 2), widen2<FMT>(v, h, 3)};
 }
 
 template <int FA, int FB, int BM, int BN, int WM, int WN, bool EXACT>
@@ -72,15 +71,13 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void scaled_tile(const RaggedArgs p
     OpB opb;
     opa.init(wave, lane, p.lda, 0, at.rows);
     opb.init(wave, lane, p.ldb, 0, at.cols);
-    auto copy = [&](int kt, int buf) {
+    // copy c (A's chunks, then B's) of k-tile kt; past the end: zeros, no memory is touched
+    constexpr int NC = OpA::CPW + OpB::CPW;
+    auto copy = [&](int kt, int buf, int c) {
         const int64_t k0 = (int64_t)kt * KT;
         const int kleft = min(kspan - kt * KT, KT);
-        const __amdgpu_buffer_rsrc_t ra = make_rsrc(OpA::tile_base(at.A, p.lda, 0, k0));
-        const __amdgpu_buffer_rsrc_t rb = make_rsrc(OpB::tile_base(at.B, p.ldb, 0, k0));
-#pragma unroll
-        for (int c = 0; c < OpA::CPW; ++c) opa.issue(ra, LA[buf], wave, c, kleft, at.rows);
-#pragma unroll
-        for (int c = 0; c < OpB::CPW; ++c) opb.issue(rb, LB[buf], wave, c, kleft, at.cols);
+        if (c < OpA::CPW) opa.issue(make_rsrc(OpA::tile_base(at.A, p.lda, 0, k0)), LA[buf], wave, c, kleft, at.rows);
+        else opb.issue(make_rsrc(OpB::tile_base(at.B, p.ldb, 0, k0)), LB[buf], wave, c - OpA::CPW, kleft, at.cols);
     };
     // this thread's factor: row srow of the tile, column block snb
     const int srow = tid % BM, snb = tid / BM;
@@ -89,7 +86,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void scaled_tile(const RaggedArgs p
     const float *sb = p.sb + at.group * p.sb_group + ((at.col0 >> 7) + snb) * p.sb_col;
     float va = 0.0f, vb = 0.0f;
     auto fetch = [&](int kt) {
-        if (has) {
+        if (has && kt < nkt) {
             va = sa[kt * p.sa_k];
             vb = sb[kt * p.sb_k];
         }
@@ -100,12 +97,13 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void scaled_tile(const RaggedArgs p
 
     floatx4 acc[TM][TN] = {};
     const int nb = (wn * WTN) >> 7;
-    // One k-tile: row blocks i in turn.  While the matrix instructions of row
+    // One k-tile, kt in LDS buffer buf: row blocks i in turn, and in the first half of
+    // them the next k-tile's copies.  While the matrix instructions of row
     // block i run, the sums of row block i - 1 enter the accumulators and the
     // fragment and factors of i + 1 are read.  The scheduling barriers keep this
     // order; without them the compiler draws all row blocks' reads together and
     // spills.
-    auto compute = [&](int buf) {
+    auto compute = [&](int kt, int buf) {
         // frag16's place for rows that begin at a multiple of 16: the swizzle then
         // depends on the lane alone, and a row block is an immediate offset
         const int own = (lane & 15) * 128, sw = swz(lane & 15), gr = 2 * (lane >> 4);
@@ -119,72 +117,81 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void scaled_tile(const RaggedArgs p
         auto frag = [&](const DMP_LDS char *l, int blk) { return *(const DMP_LDS intx4 *)(l + blk * 2048); };
         const DMP_LDS float *sc = SC[buf] + nb * BM + wm * WTM + 4 * (lane >> 4);
         intx4 b[TN][EXACT ? 4 : 2];
-#pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            const intx4 lo = frag(lb[0], j), hi = frag(lb[1], j);
-            if constexpr (EXACT) {
-                b[j][0] = widen8<FB>(lo, 0); b[j][1] = widen8<FB>(lo, 1);
-                b[j][2] = widen8<FB>(hi, 0); b[j][3] = widen8<FB>(hi, 1);
-            } else {
-                b[j][0] = lo; b[j][1] = hi;
-            }
-        }
         intx4 lo[2], hi[2];
-        floatx4 s[3], part[2][TN];
+        floatx4 s[4], part[2][TN];
+        intx4 a[EXACT ? 2 : 1][4];  // EXACT: A's row blocks, widened one ahead
         auto read = [&](int i) {
             lo[i & 1] = frag(la[0], i);
             hi[i & 1] = frag(la[1], i);
-            s[i % 3] = *(const DMP_LDS floatx4 *)(sc + i * 16);
+            s[i % 4] = *(const DMP_LDS floatx4 *)(sc + i * 16);
         };
         auto add = [&](int i, int j) {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                acc[i][j][q] = __builtin_fmaf(s[i % 3][q], part[i & 1][j][q], acc[i][j][q]);
+                acc[i][j][q] = __builtin_fmaf(s[i % 4][q], part[i & 1][j][q], acc[i][j][q]);
             asm volatile("" : "+v"(acc[i][j]));  // here, not sunk to where the sum is next used
         };
         read(0);
 #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            if (i + 1 < TM) read(i + 1);
-            intx4 a[4];
+        for (int j = 0; j < TN; ++j) {
+            const intx4 l = frag(lb[0], j), h = frag(lb[1], j);
             if constexpr (EXACT) {
-                a[0] = widen8<FA>(lo[i & 1], 0); a[1] = widen8<FA>(lo[i & 1], 1);
-                a[2] = widen8<FA>(hi[i & 1], 0); a[3] = widen8<FA>(hi[i & 1], 1);
+                b[j][0] = widen8<FB>(l, 0); b[j][1] = widen8<FB>(l, 1);
+                b[j][2] = widen8<FB>(h, 0); b[j][3] = widen8<FB>(h, 1);
+            } else {
+                b[j][0] = l; b[j][1] = h;
             }
+        }
+        if constexpr (EXACT) {
 #pragma unroll
-            for (int j = 0; j < TN; ++j) {
-                floatx4 c = {0, 0, 0, 0};
-                if constexpr (EXACT) {
+            for (int q = 0; q < 4; ++q) a[0][q] = widen8<FA>(q < 2 ? lo[0] : hi[0], q & 1);
+            read(1);
+        }
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) c = mma16<BF16>(a[q], b[j][q], c);
-                } else {
-                    const intx8 a8 = __builtin_shufflevector(lo[i & 1], hi[i & 1], 0, 1, 2, 3, 4, 5, 6, 7);
+        for (int i = 0; i < TM; ++i) {
+            if (i + 1 + EXACT < TM) read(i + 1 + EXACT);
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+                if (c * (TM / 2) / NC == i) copy(kt + 1, buf ^ 1, c);
+            if constexpr (EXACT) {
+                // four instructions to a sum, those of the TN sums in turn: each waits for
+                // the one before it of its own sum
+                static_assert(TN == 4, "a pair of bytes of the next row block to each instruction");
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int j = 0; j < TN; ++j) {
+                        part[i & 1][j] = mma16<BF16>(a[i & 1][q], b[j][q], q == 0 ? floatx4{0, 0, 0, 0} : part[i & 1][j]);
+                        if (i + 1 < TM) a[(i + 1) & 1][q][j] = widen2<FA>(q < 2 ? lo[(i + 1) & 1] : hi[(i + 1) & 1], q & 1, j);
+                        if (i > 0 && q == 3) add(i - 1, j);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+            } else {
+                const intx8 a8 = __builtin_shufflevector(lo[i & 1], hi[i & 1], 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
                     const intx8 b8 = __builtin_shufflevector(b[j][0], b[j][1], 0, 1, 2, 3, 4, 5, 6, 7);
-                    c = DT::mma(a8, b8, c);
+                    part[i & 1][j] = DT::mma(a8, b8, floatx4{0, 0, 0, 0});
+                    if (i > 0) add(i - 1, j);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-                part[i & 1][j] = c;
-                if (i > 0) add(i - 1, j);
-                __builtin_amdgcn_sched_barrier(0);
             }
         }
 #pragma unroll
         for (int j = 0; j < TN; ++j) add(TM - 1, j);
     };
     if (nkt > 0) {
-        copy(0, 0);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) copy(0, 0, c);
         fetch(0);
         put(0);
         wait_vmcnt<0>();
     }
     __syncthreads();
     auto ktile = [&](int kt, int cur) {
-        const bool more = kt + 1 < nkt;
-        if (more) {
-            copy(kt + 1, cur ^ 1);
-            fetch(kt + 1);
-        }
-        compute(cur);
-        if (more) put(cur ^ 1);
+        fetch(kt + 1);
+        compute(kt, cur);
+        put(cur ^ 1);
         wait_vmcnt<0>();
         __syncthreads();
     };
