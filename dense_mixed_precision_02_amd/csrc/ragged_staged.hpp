@@ -140,8 +140,10 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void ragged_staged(const RaggedArgs
                 fetch(kt + s + DEPTH, s);
                 asm volatile("" ::: "memory");  // issued here, not sunk to where it is needed
                 __builtin_amdgcn_sched_barrier(0);
+                step_sync();
                 multiply(s % 2);
                 put((s + 1) % DEPTH, (s + 1) % 2);
+                step_sync();
                 barrier_vmcnt<63>();
                 if (kt + s + 2 >= nkt) {
                     done = true;

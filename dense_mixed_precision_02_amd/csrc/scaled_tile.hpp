@@ -153,6 +153,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void scaled_tile(const RaggedArgs p
 #pragma unroll
             for (int c = 0; c < NC; ++c)
                 if (c * (TM / 2) / NC == i) copy(kt + 1, buf ^ 1, c);
+            step_sync();
             if constexpr (EXACT) {
                 // four instructions to a sum, those of the TN sums in turn: each waits for
                 // the one before it of its own sum
