@@ -70,6 +70,16 @@ int launch_skinny(RaggedArgs a, hipStream_t s) {
     return launched();
 }
 
+// N-contiguous B, 16-bit operands.
+template <class DT, int NW>
+int launch_skinny_n(RaggedArgs a, hipStream_t s) {
+    a.tiles_n = (int)cdiv(a.N, 128);
+    const int64_t grid = (int64_t)a.groups * a.tiles_n;
+    if (grid > 0x7fffffff) return GEMM_ERR_INVALID_ARG;
+    hipLaunchKernelGGL((skinny_n<DT, NW>), dim3((unsigned)grid), dim3(NW * 64), 0, s, a);
+    return launched();
+}
+
 template <class DT, bool AK, bool BKC, int MODE>
 int launch_cfg(gemm_handle_t h, int cfg, const RaggedArgs &a, hipStream_t s) {
     if (cfg == CFG_L) return launch_tile<DT, AK, BKC, MODE>(h, a, s);
@@ -79,8 +89,11 @@ int launch_cfg(gemm_handle_t h, int cfg, const RaggedArgs &a, hipStream_t s) {
         if (cfg == CFG_S) return launch_staged<DT, 64, 128, 1, 4, AK, BKC, MODE, true>(h, a, s);
     }
     if constexpr (MODE == RAGGED_ROWS && BKC) {
-        if (cfg == CFG_SKINNY) return launch_skinny<DT, MODE, 1, 4, 0, 0>(a, s);
-        if (cfg == CFG_SKINNY4) return launch_skinny<DT, MODE, 4, 4, 0, 0>(a, s);
+        if (cfg == CFG_SKINNY1) return launch_skinny<DT, MODE, 1, 4, 0, 0>(a, s);
+        if (cfg == CFG_SKINNY2) return launch_skinny<DT, MODE, 2, 4, 0, 0>(a, s);
+    }
+    if constexpr (MODE == RAGGED_ROWS && !BKC) {
+        if (cfg == CFG_SKINNY_N) return launch_skinny_n<DT, 4>(a, s);
     }
     return launch_staged<DT, 64, 128, 1, 4, AK, BKC, MODE, false>(h, a, s);
 }
@@ -95,7 +108,8 @@ int launch_scaled_tile(gemm_handle_t h, RaggedArgs a, hipStream_t s) {
 
 template <int FA, int FB>
 int launch_scaled(gemm_handle_t h, int cfg, const RaggedArgs &a, hipStream_t s) {
-    if (cfg == CFG_SKINNY) return launch_skinny<F8<FA, FB>, RAGGED_SCALED, 1, 4, FA, FB>(a, s);
+    if (cfg == CFG_SKINNY1) return launch_skinny<F8<FA, FB>, RAGGED_SCALED, 1, 4, FA, FB>(a, s);
+    if (cfg == CFG_SKINNY2) return launch_skinny<F8<FA, FB>, RAGGED_SCALED, 2, 4, FA, FB>(a, s);
     if (cfg == CFG_SKINNY4) return launch_skinny<F8<FA, FB>, RAGGED_SCALED, 4, 4, FA, FB>(a, s);
     const bool exact = a.ep.d_type == OUT_F32;
     if (cfg == CFG_L)

@@ -132,14 +132,38 @@ inline int validate_quant8(gemm_handle_t h, const void *X, int64_t M, int64_t K,
 // how the rows are spread; the rules go by the mean.
 // ---------------------------------------------------------------------------
 
-enum { CFG_SKINNY = 16, CFG_SKINNY4 = 17 };  // 16 and 64 columns to a workgroup
+// K-contiguous B with 16, 32 and 64 columns to a workgroup; N-contiguous B.
+enum { CFG_SKINNY1 = 16, CFG_SKINNY2 = 17, CFG_SKINNY4 = 18, CFG_SKINNY_N = 19 };
+
+// Few rows to a group, K-contiguous B: the widest columns whose workgroups fill the
+// device (us with 16 / 32 / 64 columns; 16 bits: 64 groups of one row, 1024 x 4096:
+// 151 / 93 / 98, 2048 x 2048: 97 / 95 / 102; one group of 16 rows, 8192 x 4096: 17 /
+// 26 / 40; 8 bits: 64 groups of one row, 1024 x 4096: 124 / 68 / 46; 16 groups of 32
+// rows, 4096 x 512: 15.7 / 12.5 / 15.7).  64 columns of 16 bits never gained much.
+// A few 16-bit rows and a long K take 16 columns: the rows are cheap to read again
+// and smaller pieces spread evener (64 groups, 4096 x 1024, 64 rows on half of the
+// groups: 53 / 58; on all: 92 / 93; but 8 groups of 16 rows, 4096 x 4096: 62 / 52).
+inline int skinny_cfg(int num_cus, int64_t groups, int64_t M, int64_t N, int64_t K, bool eight_bits) {
+    if (eight_bits && groups * cdiv(N, 64) >= num_cus) return CFG_SKINNY4;
+    if (!eight_bits && M <= 4 * groups && K >= 4096) return CFG_SKINNY1;
+    return groups * cdiv(N, 32) >= num_cus ? CFG_SKINNY2 : CFG_SKINNY1;
+}
 
 // Grouped rows: 16-byte granules need aligned operands, whole granules along
 // the contiguous extents and 31-bit offsets inside a tile.
 inline int grouped_cfg(int num_cus, const void *A, const void *B, int64_t groups, int64_t M, int64_t N,
                        int64_t K, int64_t lda, int64_t ldb, bool b_col) {
     if (K == 0 || !granule_ok(A, B, M, N, K, lda, ldb, GEMM_F16, false, b_col, true)) return CFG_GENERIC;
-    if (b_col && M <= 64 * groups) return M <= 16 * groups ? CFG_SKINNY : CFG_SKINNY4;
+    // Few rows to a group: kernels that stream B into registers, as long as they need
+    // not pass over it often or the tiles would leave most of the device idle (us,
+    // streamed against 128 x 128 tiles; B column-major: 64 groups of one row, 4096 x
+    // 1024: 93 / 108, 8 groups of 64 rows, 1024 x 1024: 11 / 16, 4096 x 4096: 92 / 51;
+    // row-major: 8 groups of one row, 4096 x 4096: 40 / 53, of 32 rows: 45 / 53, of 64
+    // rows: 85 / 54, 16 groups of 64 rows, 4096 x 512: 45 / 53)
+    const int64_t t128 = groups * cdiv(N, 128);
+    if (b_col && (M <= 16 * groups || (M <= 64 * groups && 2 * t128 <= num_cus)))
+        return skinny_cfg(num_cus, groups, M, N, K, false);
+    if (!b_col && (M <= 32 * groups || (M <= 64 * groups && 4 * t128 <= num_cus))) return CFG_SKINNY_N;
     // 256 x 256 tiles where the mean group fills most of one and they occupy half the
     // device (us, 256 x 256 against 128 x 128 tiles: 8 groups, 2048 rows, 4096 x 4096:
     // 116 / 126; 32 groups, 8192 rows, 2048 x 1024: 72 / 79; but 5003 rows: 70 / 55, and
@@ -161,7 +185,13 @@ inline int wgrad_cfg(int num_cus, const void *X, const void *Y, int64_t groups, 
 }
 
 inline int scaled_cfg(int num_cus, int64_t groups, int64_t M, int64_t N) {
-    if (M <= 64 * groups) return M <= 16 * groups ? CFG_SKINNY : CFG_SKINNY4;
+    // as for 16 bits (us, streamed against 128 x 128 tiles: 8 groups of 16 rows, 4096 x
+    // 4096: 25 / 27, of 32 rows: 31 / 27; 8 groups of 64 rows, 2048 x 1024: 12.5 / 14.7;
+    // 16 such groups: 21 / 17)
+    if (M <= 16 * groups || (M <= 64 * groups && 4 * groups * cdiv(N, 128) <= num_cus))
+        return skinny_cfg(num_cus, groups, M, N, 0, true);
+    // 256 x 256 (fp32 results: 256 x 128) tiles where the mean group fills most of one
+    // and they fill the device
     const int64_t tiles = (cdiv(M, 256) + groups / 2) * cdiv(N, 256);
     return M / groups >= 192 && tiles >= num_cus ? CFG_L : CFG_M;
 }

@@ -83,6 +83,13 @@ GROUPED = [
     ("bf16", [2, 1, 0, 5, 16, 17], 0, 0, 2048, 512, True, "bf16", 1.0, 0.0),
     ("f16", [33, 1, 8, 40], 0, 0, 1000, 264, True, "f32", 1.0, 1.0),
     ("f16", [2, 0, 12], 0, 1, 4096, 130, False, "f16", 1.0, 0.0),
+    # few rows to a group: 32 columns to a workgroup, groups with more rows than one pass takes
+    ("f16", [3, 0, 40, 70, 33] * 12, 0, 0, 1000, 200, True, "f32", 0.5, 1.0),
+    # the same with N-contiguous B
+    ("bf16", [2, 1, 0, 5, 16, 17], 0, 0, 512, 264, False, "bf16", 1.0, 0.0),
+    ("f16", [40, 70, 0, 33], 3, 5, 1000, 200, False, "f32", 0.5, 2.0),
+    ("bf16", [1, 0, 1], 0, 0, 8, 8, False, "f32", 1.0, 0.0),
+    ("f16", [129, 1, 0, 0, 2], 0, 1, 2056, 136, False, "f16", 1.0, 1.0),
 ]
 
 

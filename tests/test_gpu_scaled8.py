@@ -165,6 +165,8 @@ SCALED = [
     ([1, 0, 2], 256, 128, E4, E4, "f32", 1.0, 0.0), ([64, 0, 65, 1, 200], 400, 264, E5, E4, "bf16", 1.0, 1.0),
     ([300, 257, 0, 511], 512, 384, E4, E4, "f32", 1.0, 0.0), ([1] * 70 + [0, 5], 144, 72, E4, E4, "f32", 1.0, 0.0),
     ([17, 40, 3], 2064, 200, E4, E5, "f32", 1.0, 0.0),
+    # few rows to a group, 32 and 64 columns to a workgroup, one group with many
+    ([1, 2, 0, 5] * 25, 272, 72, E4, E4, "bf16", 1.0, 1.0), ([70] + [0] * 150 + [1] * 50, 272, 72, E5, E4, "f32", 1.0, 0.0),
 ]
 
 
