@@ -191,7 +191,9 @@ inline int scaled_cfg(int num_cus, int64_t groups, int64_t M, int64_t N) {
     if (M <= 16 * groups || (M <= 64 * groups && 4 * groups * cdiv(N, 128) <= num_cus))
         return skinny_cfg(num_cus, groups, M, N, 0, true);
     // 256 x 256 (fp32 results: 256 x 128) tiles where the mean group fills most of one
-    // and they fill the device
+    // and they fill the device (us, large / 128 x 128 tiles, 16-bit results: 8 groups, 4096
+    // rows, 4096 x 4096: 64 / 78, 16 groups, 8000 rows, 2064 x 4096: 81 / 102; but 8 groups,
+    // 2048 rows, 4096 x 4096: 50 / 42; fp32 results: 123 / 123, 146 / 141 and 64 / 66)
     const int64_t tiles = (cdiv(M, 256) + groups / 2) * cdiv(N, 256);
     return M / groups >= 192 && tiles >= num_cus ? CFG_L : CFG_M;
 }
