@@ -111,9 +111,10 @@ template <int XT, int FMT>
 __global__ __launch_bounds__(256) void quant8_rows(const Quant8Args p) {
     __shared__ float sc[8][QUANT_ROWS];
     const int kgroups = (p.KB + 7) / 8;
-    const int kg = blockIdx.x % kgroups;
-    const int64_t rest = blockIdx.x / kgroups;
+    const int id = workgroup_id(), kg = id % kgroups;
+    const int64_t rest = id / kgroups;
     const int64_t b = rest / p.tiles_m, m0 = (rest % p.tiles_m) * QUANT_ROWS;
+    if (b >= p.batch) return;
     const int lane = lane_id(), wave = wave_id();
     const int64_t k = (int64_t)kg * 1024 + lane * 16;
     const int64_t left = p.K - k;
@@ -163,9 +164,10 @@ __global__ __launch_bounds__(256) void quant8_tile(const Quant8Args p) {
     constexpr int PITCH = 33;  // words to an LDS row: 8 lanes that write one word of rows 16 apart meet two banks
     __shared__ uint32_t am[128];
     __shared__ uint32_t q[COL ? 128 * PITCH : 1];
-    const int kb = blockIdx.x % p.KB;
-    const int64_t rest = blockIdx.x / p.KB;
+    const int id = workgroup_id(), kb = id % p.KB;
+    const int64_t rest = id / p.KB;
     const int64_t b = rest / p.tiles_m, i0 = (rest % p.tiles_m) * 128;
+    if (b >= p.batch) return;
     const int64_t k0 = (int64_t)kb * 128;
     const int tid = threadIdx.x, piece = tid & 7, line = tid >> 3;  // 32 lines
     const int rows = (int)min((int64_t)128, p.M - i0), ks = (int)min((int64_t)128, p.K - k0);

@@ -16,6 +16,7 @@
 // scans for each 64 groups).
 #pragma once
 #include "common.hpp"
+#include "ragged_plan.hpp"
 #include "tile16_gemm.hpp"
 
 namespace dmp {
@@ -38,6 +39,9 @@ template <int FA, int FB> struct F8 {
         return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, FA, FB, 0, 0, 0, 0);
     }
 };
+
+// This workgroup's number in a grid of plan::grid_shape.
+__device__ static inline int workgroup_id() { return (int)(blockIdx.y << plan::GRID_ROW_BITS | blockIdx.x); }
 
 struct RaggedArgs {
     const void *A, *B, *C;

@@ -28,7 +28,13 @@ EpiParams out_stage(float alpha, float beta, int c_type, int d_type) {
     return ep;
 }
 
-int launched() { return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_HIP; }
+template <class Args>
+int launch(void (*kernel)(Args), int64_t workgroups, int threads, hipStream_t s, const Args &a) {
+    GridShape g;
+    if (!grid_shape(workgroups, g)) return GEMM_ERR_INVALID_ARG;  // beyond one launch's grid
+    hipLaunchKernelGGL(kernel, dim3(g.x, g.y), dim3((unsigned)threads), 0, s, a);
+    return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
+}
 
 // One workgroup to each tile there can be.  ROWS, SCALED: row tiles, at most one
 // more for each group than the rows fill.  WGRAD: runs of tiles (my_tile), the
@@ -46,38 +52,27 @@ template <class DT, bool AK, bool BKC, int MODE>
 int launch_tile(gemm_handle_t h, RaggedArgs a, hipStream_t s) {
     a.cut = h->num_cus;  // 256 x 256 tiles: one workgroup to a CU
     const int64_t grid = tile_grid(h, a, MODE, 256, 256, 1) + (MODE == RAGGED_ROWS ? 2 * a.cut : 0);
-    if (grid > 0x7fffffff) return GEMM_ERR_INVALID_ARG;
-    hipLaunchKernelGGL((ragged_tile<DT, 256, 256, AK, BKC, MODE>), dim3((unsigned)grid), dim3(256), 0, s, a);
-    return launched();
+    return launch(ragged_tile<DT, 256, 256, AK, BKC, MODE>, grid, 256, s, a);
 }
 
 template <class DT, int BM, int BN, int WM, int WN, bool AK, bool BKC, int MODE, bool FAST>
 int launch_staged(gemm_handle_t h, RaggedArgs a, hipStream_t s) {
     const int64_t grid = tile_grid(h, a, MODE, BM, BN, 8 / (WM * WN));
-    if (grid > 0x7fffffff) return GEMM_ERR_INVALID_ARG;
-    hipLaunchKernelGGL((ragged_staged<DT, BM, BN, WM, WN, AK, BKC, MODE, FAST>), dim3((unsigned)grid),
-                       dim3(WM * WN * 64), 0, s, a);
-    return launched();
+    return launch(ragged_staged<DT, BM, BN, WM, WN, AK, BKC, MODE, FAST>, grid, WM * WN * 64, s, a);
 }
 
 // 16-bit operands: FA, FB unused.
 template <class DT, int MODE, int TN, int NW, int FA, int FB>
 int launch_skinny(RaggedArgs a, hipStream_t s) {
     a.tiles_n = (int)cdiv(a.N, 16 * TN);
-    const int64_t grid = (int64_t)a.groups * a.tiles_n;
-    if (grid > 0x7fffffff) return GEMM_ERR_INVALID_ARG;
-    hipLaunchKernelGGL((skinny<DT, MODE, TN, NW, FA, FB>), dim3((unsigned)grid), dim3(NW * 64), 0, s, a);
-    return launched();
+    return launch(skinny<DT, MODE, TN, NW, FA, FB>, (int64_t)a.groups * a.tiles_n, NW * 64, s, a);
 }
 
 // N-contiguous B, 16-bit operands.
 template <class DT, int NW>
 int launch_skinny_n(RaggedArgs a, hipStream_t s) {
     a.tiles_n = (int)cdiv(a.N, 128);
-    const int64_t grid = (int64_t)a.groups * a.tiles_n;
-    if (grid > 0x7fffffff) return GEMM_ERR_INVALID_ARG;
-    hipLaunchKernelGGL((skinny_n<DT, NW>), dim3((unsigned)grid), dim3(NW * 64), 0, s, a);
-    return launched();
+    return launch(skinny_n<DT, NW>, (int64_t)a.groups * a.tiles_n, NW * 64, s, a);
 }
 
 template <class DT, bool AK, bool BKC, int MODE>
@@ -101,9 +96,7 @@ int launch_cfg(gemm_handle_t h, int cfg, const RaggedArgs &a, hipStream_t s) {
 template <int FA, int FB, int BM, int BN, int WM, int WN, bool EXACT>
 int launch_scaled_tile(gemm_handle_t h, RaggedArgs a, hipStream_t s) {
     const int64_t grid = tile_grid(h, a, RAGGED_SCALED, BM, BN, 1);
-    if (grid > 0x7fffffff) return GEMM_ERR_INVALID_ARG;
-    hipLaunchKernelGGL((scaled_tile<FA, FB, BM, BN, WM, WN, EXACT>), dim3((unsigned)grid), dim3(WM * WN * 64), 0, s, a);
-    return launched();
+    return launch(scaled_tile<FA, FB, BM, BN, WM, WN, EXACT>, grid, WM * WN * 64, s, a);
 }
 
 template <int FA, int FB>
@@ -121,12 +114,10 @@ int launch_scaled(gemm_handle_t h, int cfg, const RaggedArgs &a, hipStream_t s) 
 
 template <int XT, int FMT>
 int launch_quant8(const Quant8Args &a, bool col, int block, int64_t grid, hipStream_t s) {
-    const dim3 g((unsigned)grid), blk(256);
-    if (!col && block == 1) hipLaunchKernelGGL((quant8_rows<XT, FMT>), g, blk, 0, s, a);
-    else if (!col) hipLaunchKernelGGL((quant8_tile<XT, FMT, false, true>), g, blk, 0, s, a);
-    else if (block == 1) hipLaunchKernelGGL((quant8_tile<XT, FMT, true, false>), g, blk, 0, s, a);
-    else hipLaunchKernelGGL((quant8_tile<XT, FMT, true, true>), g, blk, 0, s, a);
-    return launched();
+    if (!col && block == 1) return launch(quant8_rows<XT, FMT>, grid, 256, s, a);
+    if (!col) return launch(quant8_tile<XT, FMT, false, true>, grid, 256, s, a);
+    if (block == 1) return launch(quant8_tile<XT, FMT, true, false>, grid, 256, s, a);
+    return launch(quant8_tile<XT, FMT, true, true>, grid, 256, s, a);
 }
 
 }  // namespace

@@ -10,6 +10,22 @@ namespace plan {
 constexpr unsigned GROUPED_FLAGS = GEMM_B_COLMAJOR | GEMM_OFFSETS_I32;
 constexpr int64_t SIZE_MAX_1 = (1ll << 31) - 1024, LD_MAX = 1ll << 48, GROUPS_MAX = 1ll << 20;
 
+// A grid's shape.  A launch takes fewer than 2^32 threads along x, so a grid has rows
+// of 2^22 workgroups (of up to 512 threads); workgroup i is the (i % 2^22)-th of row
+// i / 2^22 (workgroup_id()).  A last row that is not full ends in workgroups past the
+// count, which the kernels let return.
+constexpr int GRID_ROW_BITS = 22;
+struct GridShape {
+    unsigned x, y;
+};
+inline bool grid_shape(int64_t workgroups, GridShape &g) {
+    if (workgroups < 1 || workgroups > 0x7fffffff) return false;
+    const int64_t row = 1ll << GRID_ROW_BITS;
+    g.x = (unsigned)std::min(workgroups, row);
+    g.y = (unsigned)cdiv(workgroups, row);
+    return true;
+}
+
 inline bool float_out(int t) { return t == GEMM_OUT_F32 || t == GEMM_OUT_F16 || t == GEMM_OUT_BF16; }
 
 // The output stage's types and pointers (D, and C where it is read).

@@ -294,14 +294,14 @@ __device__ static inline int longest_first(const RaggedArgs &p, int q, int total
 // is the most tiles there can be.
 template <class DT, bool AK, bool BKC, int MODE, int BM, int BN>
 __device__ static inline bool my_tile(const RaggedArgs &p, int lane, TileAt &at) {
-    const int total = (int)(MODE == RAGGED_WGRAD ? p.K : p.M);
+    const int total = (int)(MODE == RAGGED_WGRAD ? p.K : p.M), id = workgroup_id();
     if constexpr (MODE == RAGGED_WGRAD) {
         // Workgroup i runs on XCD i % 8 and is the (i / 8)-th there.  Every group's
         // tiles are cut into runs of p.run, as many as one XCD works on at a time (they
         // share panels through its L2); the runs, longest groups first, are dealt out
         // to the XCDs to and fro, so that no XCD gets a long group alone.
         const int tiles = p.tiles_m * p.tiles_n, runs = (tiles + p.run - 1) / p.run;
-        const int seq = blockIdx.x / 8, s = seq / p.run, xcd = blockIdx.x % 8;
+        const int seq = id / 8, s = seq / p.run, xcd = id % 8;
         const int r = 8 * s + (s % 2 ? 7 - xcd : xcd), q = r / runs;
         const int t = (r - q * runs) * p.run + seq - s * p.run;
         if (q >= p.groups || t >= tiles) return false;
@@ -316,8 +316,8 @@ __device__ static inline bool my_tile(const RaggedArgs &p, int lane, TileAt &at)
         count.load(p, total, lane);
         walk = count;
         const int64_t tiles = (int64_t)count.all(p, total, lane) * p.tiles_n;
-        if ((int64_t)blockIdx.x >= tiles) return false;
-        const int t = xcd_remap(blockIdx.x, (int)tiles);
+        if (id >= tiles) return false;
+        const int t = xcd_remap(id, (int)tiles);
         int g, r0, r1, tile0, tm, tn;
         if (!walk.find(p, total, lane, t / p.tiles_n, g, r0, r1, tile0)) return false;
         grouped_order(t - tile0 * p.tiles_n, (r1 - r0 - 1) / BM + 1, p.tiles_n, tm, tn);
@@ -340,7 +340,7 @@ __global__ __launch_bounds__(256) void ragged_tile(const RaggedArgs p) {
         T::run(p, at, at.group * p.sC + at.row0 * p.ldc + at.col0, (DMP_LDS char *)lds_a0, (DMP_LDS char *)lds_b0,
                (DMP_LDS char *)lds_a1, (DMP_LDS char *)lds_b1);
     } else {
-        const int total = (int)p.M;
+        const int total = (int)p.M, id = workgroup_id();
         GroupWalk<BM> count, walk;
         count.load(p, total, lane);
         walk = count;
@@ -352,16 +352,16 @@ __global__ __launch_bounds__(256) void ragged_tile(const RaggedArgs p) {
             if (2 * last <= p.cut) whole -= last;
         }
         const int parts = whole + 4 * ((int)tiles - whole);
-        if ((int)blockIdx.x >= parts) return;
-        const bool cut = (int)blockIdx.x >= whole;
-        const int i = cut ? whole + ((int)blockIdx.x - whole) / 4 : xcd_remap(blockIdx.x, whole);
+        if (id >= parts) return;
+        const bool cut = id >= whole;
+        const int i = cut ? whole + (id - whole) / 4 : xcd_remap(id, whole);
         int g, r0, r1, tile0;
         if (!walk.find(p, total, lane, i / p.tiles_n, g, r0, r1, tile0)) return;
         int tm, tn;
         grouped_order(i - tile0 * p.tiles_n, (r1 - r0 - 1) / BM + 1, p.tiles_n, tm, tn);
         if constexpr (BM == 256) {
             if (cut) {
-                const int part = ((int)blockIdx.x - whole) % 4;
+                const int part = (id - whole) % 4;
                 const TileAt at = tile_at<DT, AK, BKC, MODE, BM / 2, BN / 2>(p, g, r0, r1, 2 * tm + part / 2, 2 * tn + part % 2);
                 if (at.rows <= 0 || at.cols <= 0) return;
                 Tile16<DT, BM / 2, BN / 2, AK, BKC>::run(p, at, at.row0 * p.ldc + at.col0, (DMP_LDS char *)lds_a0,

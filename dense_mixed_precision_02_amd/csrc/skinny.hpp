@@ -221,9 +221,10 @@ template <class DT, int MODE, int TN, int NW, int FA, int FB>
 __global__ __launch_bounds__(NW * 64, 2) void skinny(const RaggedArgs p) {
     constexpr int TS = TN == 1 || MODE == RAGGED_SCALED ? 1 : 2;  // passes of 16 TS and 32 TS rows
     __shared__ float lds[NW * 32 * TS * 16 * TN];
-    const int total = (int)p.M;
-    const int g = blockIdx.x / p.tiles_n;
-    const int64_t col0 = (int64_t)(blockIdx.x - g * p.tiles_n) * 16 * TN;
+    const int total = (int)p.M, id = workgroup_id();
+    const int g = id / p.tiles_n;
+    if (g >= p.groups) return;
+    const int64_t col0 = (int64_t)(id - g * p.tiles_n) * 16 * TN;
     const int cols = (int)min((int64_t)16 * TN, p.N - col0);
     int r0 = 0, r1 = total;
     if (p.offsets) {
@@ -241,9 +242,10 @@ __global__ __launch_bounds__(NW * 64, 2) void skinny(const RaggedArgs p) {
 template <class DT, int NW>
 __global__ __launch_bounds__(NW * 64, 8 / NW) void skinny_n(const RaggedArgs p) {
     __shared__ __attribute__((aligned(16))) float lds[NW * 32 * 128];
-    const int total = (int)p.M;
-    const int g = blockIdx.x / p.tiles_n;
-    const int64_t col0 = (int64_t)(blockIdx.x - g * p.tiles_n) * 128;
+    const int total = (int)p.M, id = workgroup_id();
+    const int g = id / p.tiles_n;
+    if (g >= p.groups) return;
+    const int64_t col0 = (int64_t)(id - g * p.tiles_n) * 128;
     const int cols = (int)min((int64_t)128, p.N - col0);
     const int r0 = load_offset(p, g, total), r1 = load_offset(p, g + 1, total);
     for (int r = r0; r < r1; r += 32) {

@@ -247,8 +247,10 @@ int gemm_run_noalloc(gemm_handle_t h, const void *A, const void *B, const void *
  * leaves the operands.
  *
  * These calls need no workspace.  groups is at most 2^20; the limits on sizes,
- * leading dimensions and extents are those of gemm_run.  M, N or groups == 0
- * enqueues nothing; K == 0 gives D = cvt(beta * C).
+ * leading dimensions and extents are those of gemm_run.  A call (also one of
+ * gemm_quant8 or gemm_run_scaled8) that would take 2^31 workgroups or more is
+ * refused with GEMM_ERR_INVALID_ARG.  M, N or groups == 0 enqueues nothing;
+ * K == 0 gives D = cvt(beta * C).
  */
 enum { GEMM_OFFSETS_I32 = 16u };
 
