@@ -52,6 +52,31 @@ __device__ static inline intx4 widen8(const intx4 &v, int h) {
     return intx4{widen2<FMT>(v, h, 0), widen2<FMT>(v, h, 1), widen2<FMT>(v, h, 2), widen2<FMT>(v, h, 3)};
 }
 
+// A k-block's factor sA * sB as s * 2^e.  Almost always e = 0.  Where the product of
+// two finite factors leaves the normal numbers (factors of 2^-76 each, or of 2^70),
+// though the scaled sum may well lie within them, s is the product of their
+// significands and e the sum of their exponents.
+struct Factor {
+    float s;
+    int e;
+};
+__device__ static inline bool factor_leaves(float a, float b, float product) {
+    constexpr int FINITE_NONZERO = 0x198, ZERO_SUBNORMAL_INF = 0x2f4;  // v_cmp_class masks
+    return __builtin_amdgcn_classf(product, ZERO_SUBNORMAL_INF) && __builtin_amdgcn_classf(a, FINITE_NONZERO) &&
+           __builtin_amdgcn_classf(b, FINITE_NONZERO);
+}
+__device__ static inline Factor split_factor(float a, float b) {
+    const float p = a * b;
+    if (!factor_leaves(a, b, p)) return {p, 0};
+    return {__builtin_amdgcn_frexp_mantf(a) * __builtin_amdgcn_frexp_mantf(b),
+            __builtin_amdgcn_frexp_expf(a) + __builtin_amdgcn_frexp_expf(b)};
+}
+// acc + s 2^e part; for e = 0 the same fused multiply-add as everywhere.
+__device__ static inline float add_scaled(float s, int e, float part, float acc) {
+    const float rare = acc + __builtin_amdgcn_ldexpf(s * part, e);
+    return e == 0 ? __builtin_fmaf(s, part, acc) : rare;
+}
+
 template <int FA, int FB, int BM, int BN, int WM, int WN, bool EXACT>
 __global__ __launch_bounds__(WM *WN * 64, 2) void scaled_tile(const RaggedArgs p) {
     using DT = F8<FA, FB>;
@@ -67,11 +92,15 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void scaled_tile(const RaggedArgs p
     __shared__ __attribute__((aligned(1024))) char lds_a1[OpA::BYTES];
     __shared__ __attribute__((aligned(1024))) char lds_b1[OpB::BYTES];
     __shared__ __attribute__((aligned(16))) float sc0[ITEMS], sc1[ITEMS];
+    __shared__ __attribute__((aligned(16))) int se0[ITEMS], se1[ITEMS];
+    __shared__ int again;
     DMP_LDS char *LA[2] = {(DMP_LDS char *)lds_a0, (DMP_LDS char *)lds_a1};
     DMP_LDS char *LB[2] = {(DMP_LDS char *)lds_b0, (DMP_LDS char *)lds_b1};
     DMP_LDS float *SC[2] = {(DMP_LDS float *)sc0, (DMP_LDS float *)sc1};
+    DMP_LDS int *SE[2] = {(DMP_LDS int *)se0, (DMP_LDS int *)se1};
 
-    const int lane = lane_id(), wave = wave_id(), tid = threadIdx.x;
+    int lane = lane_id(), tid = threadIdx.x;
+    const int wave = wave_id();
     const int wm = wave / WN, wn = wave % WN;
     TileAt at;
     if (!my_tile<DT, true, true, RAGGED_SCALED, BM, BN>(p, lane, at)) return;
@@ -79,8 +108,6 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void scaled_tile(const RaggedArgs p
     const int kspan = at.k, nkt = kspan / KT + (kspan % KT != 0);
     OpA opa;
     OpB opb;
-    opa.init(wave, lane, p.lda, 0, at.rows);
-    opb.init(wave, lane, p.ldb, 0, at.cols);
     // copy c (A's chunks, then B's) of k-tile kt; past the end: zeros, no memory is touched
     constexpr int NC = OpA::CPW + OpB::CPW;
     auto copy = [&](int kt, int buf, int c) {
@@ -90,10 +117,18 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void scaled_tile(const RaggedArgs p
         else opb.issue(make_rsrc(OpB::tile_base(at.B, p.ldb, 0, k0)), LB[buf], wave, c - OpA::CPW, kleft, at.cols);
     };
     // this thread's factor: row srow of the tile, column block snb
-    const int srow = tid % BM, snb = tid / BM;
-    const bool has = tid < ITEMS && srow < at.rows && 128 * snb < at.cols;
-    const float *sa = p.sa + (at.row0 + srow) * p.sa_row;
-    const float *sb = p.sb + at.group * p.sb_group + ((at.col0 >> 7) + snb) * p.sb_col;
+    int srow, snb;
+    bool has;
+    const float *sa, *sb;
+    auto place = [&]() {
+        opa.init(wave, lane, p.lda, 0, at.rows);
+        opb.init(wave, lane, p.ldb, 0, at.cols);
+        srow = tid % BM;
+        snb = tid / BM;
+        has = tid < ITEMS && srow < at.rows && 128 * snb < at.cols;
+        sa = p.sa + (at.row0 + srow) * p.sa_row;
+        sb = p.sb + at.group * p.sb_group + ((at.col0 >> 7) + snb) * p.sb_col;
+    };
     float va = 0.0f, vb = 0.0f;
     auto fetch = [&](int kt) {
         if (has && kt < nkt) {
@@ -101,11 +136,21 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void scaled_tile(const RaggedArgs p
             vb = sb[kt * p.sb_k];
         }
     };
-    auto put = [&](int buf) {
-        if (tid < ITEMS) SC[buf][snb * BM + srow] = va * vb;
+    bool leaves = false;
+    auto put = [&](auto split, int buf) {
+        if (tid >= ITEMS) return;
+        if constexpr (decltype(split)::value) {
+            const Factor f = split_factor(va, vb);
+            SC[buf][snb * BM + srow] = f.s;
+            SE[buf][snb * BM + srow] = f.e;
+        } else {
+            const float f = va * vb;
+            leaves |= factor_leaves(va, vb, f);
+            SC[buf][snb * BM + srow] = f;
+        }
     };
 
-    floatx4 acc[TM][TN] = {};
+    floatx4 acc[TM][TN];
     const int nb = (wn * WTN) >> 7;
     // One k-tile, kt in LDS buffer buf: row blocks i in turn, and in the first half of
     // them the next k-tile's copies.  While the matrix instructions of row
@@ -113,7 +158,8 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void scaled_tile(const RaggedArgs p
     // fragment and factors of i + 1 are read.  The scheduling barriers keep this
     // order; without them the compiler draws all row blocks' reads together and
     // spills.
-    auto compute = [&](int kt, int buf) {
+    auto compute = [&](auto split, int kt, int buf) {
+        constexpr bool SPLIT = decltype(split)::value;
         // frag16's place for rows that begin at a multiple of 16: the swizzle then
         // depends on the lane alone, and a row block is an immediate offset
         const int own = (lane & 15) * 128, sw = swz(lane & 15), gr = 2 * (lane >> 4);
@@ -125,7 +171,9 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void scaled_tile(const RaggedArgs p
             lb[h] = LB[buf] + wn * WTN * 128 + off[h];
         }
         auto frag = [&](const DMP_LDS char *l, int blk) { return *(const DMP_LDS intx4 *)(l + blk * 2048); };
-        const DMP_LDS float *sc = SC[buf] + nb * BM + wm * WTM + 4 * (lane >> 4);
+        const int sc_at = nb * BM + wm * WTM + 4 * (lane >> 4);
+        const DMP_LDS float *sc = SC[buf] + sc_at;
+        const DMP_LDS int *se = SE[buf] + sc_at;
         intx4 b[TN][EXACT ? 4 : 2];
         intx4 lo[2], hi[2];
         floatx4 s[4], part[2][TN];
@@ -133,12 +181,13 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void scaled_tile(const RaggedArgs p
         auto read = [&](int i) {
             lo[i & 1] = frag(la[0], i);
             hi[i & 1] = frag(la[1], i);
-            s[i % 4] = *(const DMP_LDS floatx4 *)(sc + i * 16);
+            if constexpr (!SPLIT) s[i % 4] = *(const DMP_LDS floatx4 *)(sc + i * 16);
         };
         auto add = [&](int i, int j) {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                acc[i][j][q] = __builtin_fmaf(s[i % 4][q], part[i & 1][j][q], acc[i][j][q]);
+                if constexpr (SPLIT) acc[i][j][q] = add_scaled(sc[i * 16 + q], se[i * 16 + q], part[i & 1][j][q], acc[i][j][q]);
+                else acc[i][j][q] = __builtin_fmaf(s[i % 4][q], part[i & 1][j][q], acc[i][j][q]);
             asm volatile("" : "+v"(acc[i][j]));  // here, not sunk to where the sum is next used
         };
         read(0);
@@ -191,24 +240,42 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void scaled_tile(const RaggedArgs p
 #pragma unroll
         for (int j = 0; j < TN; ++j) add(TM - 1, j);
     };
-    if (nkt > 0) {
+    auto walk = [&](auto split) {
+        place();
 #pragma unroll
-        for (int c = 0; c < NC; ++c) copy(0, 0, c);
-        fetch(0);
-        put(0);
-        wait_vmcnt<0>();
-    }
-    __syncthreads();
-    auto ktile = [&](int kt, int cur) {
-        fetch(kt + 1);
-        compute(kt, cur);
-        put(cur ^ 1);
-        wait_vmcnt<0>();
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) acc[i][j] = floatx4{0, 0, 0, 0};
+        if (nkt > 0) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) copy(0, 0, c);
+            fetch(0);
+            put(split, 0);
+            wait_vmcnt<0>();
+        }
         __syncthreads();
+        auto ktile = [&](int kt, int cur) {
+            fetch(kt + 1);
+            compute(split, kt, cur);
+            put(split, cur ^ 1);
+            wait_vmcnt<0>();
+            __syncthreads();
+        };
+        for (int kt = 0; kt < nkt; kt += 2) {
+            ktile(kt, 0);
+            if (kt + 1 < nkt) ktile(kt + 1, 1);
+        }
     };
-    for (int kt = 0; kt < nkt; kt += 2) {
-        ktile(kt, 0);
-        if (kt + 1 < nkt) ktile(kt + 1, 1);
+    // The factors' products are watched on the way; where one left the normal numbers
+    // the tile is computed once more with split factors.  (Splitting every factor would
+    // take three vector instructions for each multiply-add of the loop.)
+    if (tid == 0) again = 0;
+    walk(std::false_type{});
+    if (leaves) again = 1;
+    __syncthreads();
+    if (__builtin_expect(again, 0)) {
+        asm volatile("" : "+v"(lane), "+v"(tid));  // places are found anew, not kept in registers meanwhile
+        walk(std::true_type{});
     }
     // each wave's slab in one of the operand buffers, as many as fit each
     constexpr int SLAB = 32 * (WTN + 4) * 4, INA = OpA::BYTES / SLAB, INB = OpB::BYTES / SLAB;
@@ -219,7 +286,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void scaled_tile(const RaggedArgs p
     const int64_t first = at.row0 * p.ldc + at.col0;
     store_wave_tile<WTM, WTN>((DMP_LDS float *)slab, p.ep, (const char *)p.C + first * out_size(p.ep.c_type),
                               (char *)p.D + first * out_size(p.ep.d_type), p.ldc, at.rows, at.cols, wm * WTM,
-                              wn * WTN, lane, [&](int i, int j) { return acc[i][j]; });
+                              wn * WTN, lane_id(), [&](int i, int j) { return acc[i][j]; });
 }
 
 }  // namespace dmp

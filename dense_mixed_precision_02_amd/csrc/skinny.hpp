@@ -103,17 +103,30 @@ __device__ static inline void skinny_rows(const RaggedArgs &p, float *lds, int g
 #pragma unroll
                 for (int i = 0; i < TM; ++i) {
                     floatx4 s;
+                    bool leaves = false;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        s[q] = __shfl(fs[st][u][i], 4 * (lane >> 4) + q, 64) * fsb[st][u];
+                    for (int q = 0; q < 4; ++q) {
+                        const float sa = __shfl(fs[st][u][i], 4 * (lane >> 4) + q, 64);
+                        s[q] = sa * fsb[st][u];
+                        leaves |= factor_leaves(sa, fsb[st][u], s[q]);
+                    }
+                    const bool split = __ballot(leaves) != 0;  // see scaled_tile.hpp's Factor
 #pragma unroll
                     for (int j = 0; j < TN; ++j) {
                         floatx4 c = {0, 0, 0, 0};
 #pragma unroll
                         for (int h = 0; h < 4; ++h)
                             c = mma16<BF16>(widen8<FA>(fa[st][u][i][h >> 1], h & 1), b[j][h], c);
+                        if (split) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) acc[i][j][q] = __builtin_fmaf(s[q], c[q], acc[i][j][q]);
+                            for (int q = 0; q < 4; ++q) {
+                                const Factor f = split_factor(__shfl(fs[st][u][i], 4 * (lane >> 4) + q, 64), fsb[st][u]);
+                                acc[i][j][q] = add_scaled(f.s, f.e, c[q], acc[i][j][q]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) acc[i][j][q] = __builtin_fmaf(s[q], c[q], acc[i][j][q]);
+                        }
                     }
                 }
             } else {
