@@ -91,7 +91,8 @@ __device__ static inline void skinny_rows(const RaggedArgs &p, float *lds, int g
             }
         }
     };
-    auto multiply = [&](int st) {
+    bool leaves = false;  // SCALED: this lane's factors left the normal numbers (scaled_tile.hpp's Factor)
+    auto multiply = [&](auto split, int st) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if constexpr (MODE == RAGGED_SCALED) {
@@ -102,31 +103,31 @@ __device__ static inline void skinny_rows(const RaggedArgs &p, float *lds, int g
                     for (int h = 0; h < 4; ++h) b[j][h] = widen8<FB>(fb[st][u][j][h >> 1], h & 1);
 #pragma unroll
                 for (int i = 0; i < TM; ++i) {
+                    const float own = fs[st][u][i] * fsb[st][u];
+                    leaves |= factor_leaves(fs[st][u][i], fsb[st][u], own);
                     floatx4 s;
-                    bool leaves = false;
+                    int e[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const float sa = __shfl(fs[st][u][i], 4 * (lane >> 4) + q, 64);
-                        s[q] = sa * fsb[st][u];
-                        leaves |= factor_leaves(sa, fsb[st][u], s[q]);
+                        const int from = 4 * (lane >> 4) + q;
+                        if constexpr (decltype(split)::value) {
+                            const Factor f = split_factor(__shfl(fs[st][u][i], from, 64), fsb[st][u]);
+                            s[q] = f.s;
+                            e[q] = f.e;
+                        } else {
+                            s[q] = __shfl(own, from, 64);
+                        }
                     }
-                    const bool split = __ballot(leaves) != 0;  // see scaled_tile.hpp's Factor
 #pragma unroll
                     for (int j = 0; j < TN; ++j) {
                         floatx4 c = {0, 0, 0, 0};
 #pragma unroll
                         for (int h = 0; h < 4; ++h)
                             c = mma16<BF16>(widen8<FA>(fa[st][u][i][h >> 1], h & 1), b[j][h], c);
-                        if (split) {
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                const Factor f = split_factor(__shfl(fs[st][u][i], 4 * (lane >> 4) + q, 64), fsb[st][u]);
-                                acc[i][j][q] = add_scaled(f.s, f.e, c[q], acc[i][j][q]);
-                            }
-                        } else {
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) acc[i][j][q] = __builtin_fmaf(s[q], c[q], acc[i][j][q]);
-                        }
+                        for (int q = 0; q < 4; ++q)
+                            if constexpr (decltype(split)::value) acc[i][j][q] = add_scaled(s[q], e[q], c[q], acc[i][j][q]);
+                            else acc[i][j][q] = __builtin_fmaf(s[q], c[q], acc[i][j][q]);
                     }
                 }
             } else {
@@ -143,9 +144,21 @@ __device__ static inline void skinny_rows(const RaggedArgs &p, float *lds, int g
         load(0, kt0);
         for (int kt = kt0; kt < kt1; kt += 2 * U) {
             load(1, kt + U);
-            multiply(0);
+            multiply(std::false_type{}, 0);
             load(0, kt + 2 * U);
-            multiply(1);
+            multiply(std::false_type{}, 1);
+        }
+    }
+    if constexpr (MODE == RAGGED_SCALED) {
+        if (__builtin_expect(__ballot(leaves) != 0, 0)) {  // once more with split factors
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) acc[i][j] = floatx4{0, 0, 0, 0};
+            for (int kt = kt0; kt < kt1; kt += U) {
+                load(0, kt);
+                multiply(std::true_type{}, 0);
+            }
         }
     }
     // sums of the waves, [wave][row][column]
