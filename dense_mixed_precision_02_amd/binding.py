@@ -586,7 +586,8 @@ class Scaled8:
     float8_e5m2, K-contiguous rows of Kp = 16 * ceil(K / 16) values, zeros past K; and
     ``scale`` ((groups,) ceil(rows / block), ceil(K / 128)) float32 of any strides: the
     value stands for q times the scale of its block of ``block`` rows by 128 k.  Made
-    by quant8, or from tensors that are there."""
+    by quant8, or from tensors that are there.  Both may be changed in place or replaced;
+    a product reads what the operand holds when it is called."""
 
     def __init__(self, q, scale, block: int = 1, K: int | None = None):
         self.type = _f8_code(q.dtype)
@@ -594,7 +595,8 @@ class Scaled8:
             raise TypeError("q must be float8_e4m3fn or float8_e5m2, and scale float32")
         if block != 1 and block != 128:
             raise ValueError("block must be 1 or 128")
-        shape, dims = q.shape, q.dim()
+        shape = q.shape
+        dims = len(shape)
         K = shape[-1] if K is None else K
         kp = -(-K // 16) * 16
         if dims not in (2, 3) or shape[-1] != kp:
@@ -606,18 +608,28 @@ class Scaled8:
             raise ValueError("scale must be ((groups,) ceil(rows / block), ceil(K / 128))")
         if scale.device != q.device or not q.is_cuda:
             raise ValueError("q and scale must be on the same GPU")
-        s, t, at = q.stride(), scale.stride(), q.data_ptr()
-        if q.numel() and (s[-1] != 1 or (rows > 1 and (s[-2] < kp or s[-2] % 16)) or
+        s, at = q.stride(), q.data_ptr()
+        if 0 not in shape and (s[-1] != 1 or (rows > 1 and (s[-2] < kp or s[-2] % 16)) or
                           (dims == 3 and groups > 1 and s[0] % 16) or at % 16):
             raise ValueError("q's rows must be contiguous and begin at multiples of 16 bytes")
         self._set(q, scale, block, K, rows, groups, at, s[-2] if rows > 1 and kp else kp,
                   s[0] if dims == 3 else 0)
 
     def _set(self, q, scale, block, K, rows, groups, at, ld, group):
-        t = scale.stride()
+        t, scale_at = scale.stride(), scale.data_ptr()
         self.q, self.scale, self.block, self.K, self.rows, self.groups = q, scale, block, K, rows, groups
-        self.operand = Q8Operand(at, scale.data_ptr(), ld, t[-2], t[-1], group, t[0] if groups is not None else 0,
-                                 self.type)
+        self._operand = Q8Operand(at, scale_at, ld, t[-2], t[-1], group, t[0] if groups is not None else 0, self.type)
+        self._of = q, scale, at, scale_at, block, K
+
+    @property
+    def operand(self) -> Q8Operand:
+        """The operand as it is now: ``q`` and ``scale`` may have been replaced, or their
+        memory moved, since the structure was filled in; it is then checked and filled in anew."""
+        q, scale, at, scale_at, block, K = self._of
+        if self.q is not q or self.scale is not scale or q.data_ptr() != at or scale.data_ptr() != scale_at or \
+                self.block != block or self.K != K:
+            self.__init__(self.q, self.scale, self.block, self.K)
+        return self._operand
 
 
 def quant8(X, block: int = 1, dtype=None, handle: Handle | None = None) -> Scaled8:
@@ -666,18 +678,19 @@ def gemm_scaled8(A: Scaled8, B: Scaled8, offsets=None, C=None, out=None, alpha: 
     columns of a K x N matrix as rows);  formats may differ.  With ``offsets`` (see
     gemm_grouped) B is (groups, N, K) and the rows of group g meet B[g].  C, ``out`` and
     ``out_dtype`` (default float32) as in gemm_grouped."""
+    a, b = A.operand, B.operand
     if A.block != 1 or B.block != 128:
         raise ValueError("A must have blocks of one row and B blocks of 128 rows")
-    if A.groups is not None or A.K != B.K or B.q.device != A.q.device:
-        raise ValueError("A must be (T, K) and B ((groups,) N, K) on the same GPU")
     device = A.q.device
+    if A.groups is not None or A.K != B.K or B.q.device != device:
+        raise ValueError("A must be (T, K) and B ((groups,) N, K) on the same GPU")
     groups, flags = (1, 0) if offsets is None else _check_offsets(offsets, device)
     if (offsets is None) != (B.groups is None) or (offsets is not None and B.groups != groups):
         raise ValueError("a grouped B needs offsets that hold one number more than it has groups")
     T, N = A.rows, B.rows
     c, c_code, out, d_code, ldc, beta = _output(C, out, (T, N), out_dtype, beta, device, "(T, N)")
     rc = _on(device, handle, lambda h, stream: h.run_scaled8(
-        A.operand, B.operand, c, out.data_ptr(), offsets.data_ptr() if offsets is not None else 0, groups, T, N,
+        a, b, c, out.data_ptr(), offsets.data_ptr() if offsets is not None else 0, groups, T, N,
         A.K, ldc, flags, alpha, beta, c_code, d_code, stream))
     if rc != GEMM_OK:
         raise GemmError(rc, "gemm_run_scaled8")
