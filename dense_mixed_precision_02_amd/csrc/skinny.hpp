@@ -31,6 +31,7 @@ __device__ static inline intx4 load_granule(__amdgpu_buffer_rsrc_t r, int off) {
 template <int NW, int CW, int SZ>
 __device__ static inline void join_waves(const RaggedArgs &p, const float *lds, int64_t row0, int rows,
                                          int64_t col0, int cols) {
+    step_sync();
     __syncthreads();
     for (int e = threadIdx.x; e < rows * CW; e += NW * 64) {
         const int r = e / CW, c = e % CW;
@@ -41,6 +42,7 @@ __device__ static inline void join_waves(const RaggedArgs &p, const float *lds, 
         const floatx4 cv = p.ep.use_c ? load4<float>(p.C, idx, p.ep.c_type, false, 1) : floatx4{0, 0, 0, 0};
         store4<float>(p.D, idx, finish4(floatx4{v, 0, 0, 0}, cv, p.ep), p.ep.d_type, false, 1);
     }
+    step_sync();
 }
 
 // One group's rows [row0, row0 + rows), rows <= 16 TM, times this workgroup's columns.
@@ -163,6 +165,7 @@ __device__ static inline void skinny_rows(const RaggedArgs &p, float *lds, int g
     }
     // sums of the waves, [wave][row][column]
     constexpr int CW = 16 * TN, SZ = 16 * TM * CW;
+    step_sync();
     __syncthreads();  // the sums of the rows before are read
 #pragma unroll
     for (int i = 0; i < TM; ++i)
@@ -231,6 +234,7 @@ __device__ static inline void skinny_rows_n(const RaggedArgs &p, float *lds, int
         }
     }
     constexpr int CW = 128, SZ = 16 * TM * CW;
+    step_sync();
     __syncthreads();  // the sums of the rows before are read
 #pragma unroll
     for (int i = 0; i < TM; ++i)
