@@ -157,11 +157,17 @@ enum { CFG_SKINNY1 = 16, CFG_SKINNY2 = 17, CFG_SKINNY4 = 18, CFG_SKINNY_N = 19 }
 // 26 / 40; 8 bits: 64 groups of one row, 1024 x 4096: 124 / 68 / 46; 16 groups of 32
 // rows, 4096 x 512: 15.7 / 12.5 / 15.7).  64 columns of 16 bits never gained much.
 // A few 16-bit rows and a long K take 16 columns: the rows are cheap to read again
-// and smaller pieces spread evener (64 groups, 4096 x 1024, 64 rows on half of the
-// groups: 53 / 58; on all: 92 / 93; but 8 groups of 16 rows, 4096 x 4096: 62 / 52).
+// and smaller pieces spread evener.  Their loop takes 8 k-tiles of a wave's quarter of K
+// to a trip, so K is long where the second trip is all but full, 15 k-tiles to a wave
+// (64 groups by 1024 columns, us with 16 / 32 columns, 64 rows one to a group / on
+// 34 of the groups / 256 rows; K 3584, 14 k-tiles: 88.6 / 85.3, 50.5 / 53.2, 98.7 / 91.0;
+// 3712, 15: 92.2 / 91.2, 52.0 / 57.2, 100.0 / 96.7; 3840: 92.7 / 96.4, 53.0 / 60.6, 103.1 /
+// 103.9; 4096, 16: 92.4 / 92.8, 52.3 / 57.8, 100.6 / 98.5; 5120, 20: 126 / 133, 72.0 / 83.3,
+// 139 / 144; 8192, 32: 190 / 207, 107 / 125, 203 / 211; and on the way a third trip that
+// is mostly empty, 4608, 18: 117 / 108, 66.7 / 67.4, 129 / 116.  With 384 rows 4096 takes 106 / 102).
 inline int skinny_cfg(int num_cus, int64_t groups, int64_t M, int64_t N, int64_t K, bool eight_bits) {
     if (eight_bits && groups * cdiv(N, 64) >= num_cus) return CFG_SKINNY4;
-    if (!eight_bits && M <= 4 * groups && K >= 4096) return CFG_SKINNY1;
+    if (!eight_bits && M <= 4 * groups && cdiv(cdiv(K, 64), 4) >= 15) return CFG_SKINNY1;
     return groups * cdiv(N, 32) >= num_cus ? CFG_SKINNY2 : CFG_SKINNY1;
 }
 
