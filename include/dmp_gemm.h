@@ -344,12 +344,13 @@ typedef struct {
  * S the same sum over magnitudes, plus the output stage's rounding.  sA * sB
  * itself may lie below the normal floats or above the largest one; only where a
  * scaled block sum or acc does, it is rounded (by 2^-150 at most for each
- * k-block) or becomes infinite.  Where D has
- * 16 bits the large tiles multiply the 8-bit values as they are; that matrix
+ * k-block) or becomes infinite.  Where D is fp32, and for every D where the
+ * rows are few (up to 16 to a group, 64 where the groups' columns are few too),
+ * the values are widened to bf16 first, which is exact.  Else, where D has 16
+ * bits, the tiles multiply the 8-bit values as they are; that matrix
  * instruction keeps, of 8 products with consecutive k, what lies within 13 bits
  * of the largest, and the bound is 2^-9 * S more (about 1.5e-5 of the result's
- * norm for random values, a hundredth of bf16's rounding).  Where D is fp32 the
- * values are widened to bf16 first, which is exact.  With offsets the
+ * norm for random values, a hundredth of bf16's rounding).  With offsets the
  * rows are grouped as above and row i of group g meets B_g; with offsets NULL
  * (groups == 1) all M rows meet one B.  A and B may be of either format.
  * flags: GEMM_OFFSETS_I32.  Everything else as in gemm_run_grouped.
