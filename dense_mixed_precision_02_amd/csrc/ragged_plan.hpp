@@ -186,12 +186,15 @@ inline int grouped_cfg(int num_cus, const void *A, const void *B, int64_t groups
     if (b_col && (M <= 16 * groups || (M <= 64 * groups && 2 * t128 <= num_cus)))
         return skinny_cfg(num_cus, groups, M, N, K, false);
     if (!b_col && (M <= 32 * groups || (M <= 64 * groups && 4 * t128 <= num_cus))) return CFG_SKINNY_N;
-    // 256 x 256 tiles where the mean group fills most of one and they occupy half the
-    // device (us, 256 x 256 against 128 x 128 tiles: 8 groups, 2048 rows, 4096 x 4096:
-    // 116 / 126; 32 groups, 8192 rows, 2048 x 1024: 72 / 79; but 5003 rows: 70 / 55, and
-    // 4 groups, 1024 rows, 4096 x 4096: 119 / 77)
-    const int64_t tiles = (cdiv(M, 256) + groups / 2) * cdiv(N, 256);
-    return M / groups >= 192 && 2 * tiles >= num_cus ? CFG_L : CFG_M;
+    // 256 x 256 tiles where the mean group fills most of one and 128 x 128 ones, two to a
+    // CU, would take more than one round of the device (us, 256 x 256 / 128 x 128 tiles,
+    // column-major B, rows by chance over the groups; 8 groups by 4096 x 4096, 1536 rows, 512
+    // small tiles: 125 / 85, 2048 rows, 640: 100 / 120, 3072 rows: 106 / 150; one group, 2000
+    // rows, 512: 99 / 80, 2100 rows, 544: 88 / 114; 32 groups by 2048 x 1024, 6144 rows, 512:
+    // 70 / 47, 7168 rows, 576: 59 / 66.  By the mean: 64 groups by 1024 x 2048, of 96 rows: 73 /
+    // 59, of 192: 82 / 97, in shares that fall with the root of the rank 109 / 99)
+    const int64_t small = (cdiv(M, 128) + groups / 2) * cdiv(N, 128);
+    return M / groups >= 192 && small > 2 * (int64_t)num_cus ? CFG_L : CFG_M;
 }
 
 // Weight gradients: 256 x 256 tiles where they fill the device and lie mostly

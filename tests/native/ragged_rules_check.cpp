@@ -40,8 +40,9 @@ int main() {
         CHECK(rows(4, 505, 0, 520, col) == CFG_GENERIC);
         // 192 rows to the mean group
         CHECK(rows(32, 32 * 192, 512, 2048, col) == CFG_L && rows(32, 32 * 192 - 1, 512, 2048, col) == CFG_M);
-        // half of the device
-        CHECK(rows(4, 2048, 512, 2816, col) == CFG_M && rows(4, 2048, 512, 3328, col) == CFG_L);
+        // one round of 128 x 128 tiles, two to a CU
+        CHECK(rows(4, 2048, 512, 3584, col) == CFG_M && rows(4, 2048, 512, 3712, col) == CFG_L);
+        CHECK(rows(1, 2000, 4096, 4096, col) == CFG_M && rows(1, 2100, 4096, 4096, col) == CFG_L);
     }
     // few rows: 16 and 32 columns of a K-contiguous B
     CHECK(rows(4, 4, 512, 512, true) == CFG_SKINNY1 && rows(64, 64, 1024, 1024, true) == CFG_SKINNY2);
