@@ -631,6 +631,9 @@ class Scaled8:
             self.__init__(self.q, self.scale, self.block, self.K)
         return self._operand
 
+    def __reduce__(self):  # copies and saved operands: of the tensors, not of addresses
+        return Scaled8, (self.q, self.scale, self.block, self.K)
+
 
 def quant8(X, block: int = 1, dtype=None, handle: Handle | None = None) -> Scaled8:
     """Quantize X ((batch,) M, K; float32, float16 or bfloat16; row-major or a transposed

@@ -1,5 +1,8 @@
 """An 8-bit operand that a program keeps and changes: gemm_scaled8 reads the tensors that
 the operand holds at the call, not the addresses it was made with."""
+import copy
+import io
+
 import pytest
 
 from test_gpu_scaled8 import E4, E5, dmp  # noqa: F401
@@ -52,6 +55,20 @@ def test_memory_that_moved(dmp):  # noqa: F811
     assert B.q.data_ptr() != at and taken.numel() == size
     B.q.copy_(host)
     assert torch.equal(dmp.gemm_scaled8(A, B), want)
+
+
+def test_copies_and_saved_operands(dmp):  # noqa: F811
+    A, B, _ = operands(dmp)
+    for C in (B, dmp.quant8(B.q.float(), block=128)):
+        first = dmp.gemm_scaled8(A, C)
+        deep, shallow, file = copy.deepcopy(C), copy.copy(C), io.BytesIO()
+        torch.save(C, file)
+        file.seek(0)
+        saved = torch.load(file, weights_only=False)  # written above
+        assert deep.q.data_ptr() != C.q.data_ptr() and shallow.q is C.q
+        C.scale.mul_(2)
+        for other, factor in ((deep, 1), (saved, 1), (shallow, 2)):
+            assert torch.equal(dmp.gemm_scaled8(A, other), factor * first)
 
 
 def test_changes_that_do_not_fit_are_refused(dmp):  # noqa: F811
