@@ -152,10 +152,10 @@ inline int validate_quant8(gemm_handle_t h, const void *X, int64_t M, int64_t K,
 enum { CFG_SKINNY1 = 16, CFG_SKINNY2 = 17, CFG_SKINNY4 = 18, CFG_SKINNY_N = 19 };
 
 // Few rows to a group, K-contiguous B: the widest columns whose workgroups fill the
-// device (us with 16 / 32 / 64 columns; 16 bits: 64 groups of one row, 1024 x 4096:
-// 151 / 93 / 98, 2048 x 2048: 97 / 95 / 102; one group of 16 rows, 8192 x 4096: 17 /
-// 26 / 40; 8 bits: 64 groups of one row, 1024 x 4096: 124 / 68 / 46; 16 groups of 32
-// rows, 4096 x 512: 15.7 / 12.5 / 15.7).  64 columns of 16 bits never gained much.
+// device (us with 16 / 32 / 64 columns, weights from memory; 16 bits: 64 groups of one
+// row, 1024 x 4096: 151 / 92 / 98, 2048 x 2048: 98 / 94 / 102; 8 bits: 64 groups of one
+// row, 1024 x 4096: 143 / 78 / 56; 16 groups of 32 rows, 4096 x 512: 17 / 14.5 / 18.5; 16
+// rows, 4096 x 8192: 12.8 / 10.8 / 15.3).  64 columns of 16 bits never gained much.
 // A few 16-bit rows and a long K take 16 columns: the rows are cheap to read again
 // and smaller pieces spread evener.  Their loop takes 8 k-tiles of a wave's quarter of K
 // to a trip, so K is long where the second trip is all but full, 15 k-tiles to a wave
@@ -178,10 +178,15 @@ inline int grouped_cfg(int num_cus, const void *A, const void *B, int64_t groups
     if (K == 0 || !granule_ok(A, B, M, N, K, lda, ldb, GEMM_F16, false, b_col, true)) return CFG_GENERIC;
     // Few rows to a group: kernels that stream B into registers, as long as they need
     // not pass over it often or the tiles would leave most of the device idle (us,
-    // streamed against 128 x 128 tiles; B column-major: 64 groups of one row, 4096 x
-    // 1024: 93 / 108, 8 groups of 64 rows, 1024 x 1024: 11 / 16, 4096 x 4096: 92 / 51;
-    // row-major: 8 groups of one row, 4096 x 4096: 40 / 53, of 32 rows: 45 / 53, of 64
-    // rows: 85 / 54, 16 groups of 64 rows, 4096 x 512: 45 / 53)
+    // streamed against 128 x 128 tiles, weights from memory; B column-major: 64 groups of
+    // one row, 4096 x 1024: 92 / 110, 8 groups of 64 rows, 1024 x 1024: 11 / 18, 4096 x
+    // 4096: 100 / 65; row-major: 8 groups of one row, 4096 x 4096: 50 / 54, of 32 rows:
+    // 54 / 56, of 64 rows: 94 / 57, 16 groups of 64 rows, 4096 x 512: 58 / 55).  That goes for
+    // rows that are spread.  A workgroup takes a group's passes one after the other, so a long
+    // group sets the time, and the host cannot see it (64 groups, 1024 rows, 4096 x 1024,
+    // column- and row-major: shares that fall with the rank to the power of 0.7, longest
+    // 148: 129 / 148 and 179 / 140; of 1.5, longest 463: 227 / 105 and 380 / 100; all in one
+    // group: 364 / 51 and 592 / 55).
     const int64_t t128 = groups * cdiv(N, 128);
     if (b_col && (M <= 16 * groups || (M <= 64 * groups && 2 * t128 <= num_cus)))
         return skinny_cfg(num_cus, groups, M, N, K, false);
@@ -198,9 +203,11 @@ inline int grouped_cfg(int num_cus, const void *A, const void *B, int64_t groups
 }
 
 // Weight gradients: 256 x 256 tiles where they fill the device and lie mostly
-// inside the outputs, else 64 x 128 ones (us, 256 x 256 / 128 x 128 / 64 x 128: 8
-// groups, 4096 rows, 1024 x 1024: 54 / 40 / 31; 24 groups, 3000 rows, 520 x 1032:
-// 65 / 38 / 36; 1024 x 1024: 35 / 38 / 37).
+// inside the outputs, else 64 x 128 ones (us, 256 x 256 / 64 x 128, bf16 results: 8
+// groups of 1024 x 1024, half the device, 4096 rows: 30 / 22, 16384 rows: 62 / 60; 16 groups
+// of them, 4096 rows: 25 / 26, 16384 rows: 42 / 59; 24 groups, 3000 rows: 37 / 30, the same of
+// 520 x 1032, of which 0.55 of the tiles is useful: 43 / 23; 20 groups of 800 x 1100, 0.67,
+// 6000 rows: 59 / 59; 12 groups of 1000 x 1500, 0.95: 80 / 80).
 inline int wgrad_cfg(int num_cus, const void *X, const void *Y, int64_t groups, int64_t M, int64_t N,
                      int64_t K, int64_t ldx, int64_t ldy) {
     if (K == 0 || !granule_ok(X, Y, M, N, K, ldx, ldy, GEMM_F16, true, false, true)) return CFG_GENERIC;
@@ -210,15 +217,18 @@ inline int wgrad_cfg(int num_cus, const void *X, const void *Y, int64_t groups, 
 }
 
 inline int scaled_cfg(int num_cus, int64_t groups, int64_t M, int64_t N) {
-    // as for 16 bits (us, streamed against 128 x 128 tiles: 8 groups of 16 rows, 4096 x
-    // 4096: 25 / 27, of 32 rows: 31 / 27; 8 groups of 64 rows, 2048 x 1024: 12.5 / 14.7;
-    // 16 such groups: 21 / 17)
+    // as for 16 bits (us, streamed against 128 x 128 tiles, weights from memory: 8 groups of
+    // 16 rows, 4096 x 4096: 32 / 40, of 32 rows: 38 / 41; 8 groups of 64 rows, 2048 x 1024:
+    // 14 / 20; 16 such groups: 22 / 21; and as there a long group loses: 64 groups, 1024 rows,
+    // 4096 x 1024, longest 463: 214 / 62, all in one: 405 / 26)
     if (M <= 16 * groups || (M <= 64 * groups && 4 * groups * cdiv(N, 128) <= num_cus))
         return skinny_cfg(num_cus, groups, M, N, 0, true);
     // 256 x 256 (fp32 results: 256 x 128) tiles where the mean group fills most of one
-    // and they fill the device (us, large / 128 x 128 tiles, 16-bit results: 8 groups, 4096
-    // rows, 4096 x 4096: 64 / 78, 16 groups, 8000 rows, 2064 x 4096: 81 / 102; but 8 groups,
-    // 2048 rows, 4096 x 4096: 50 / 42; fp32 results: 123 / 123, 146 / 141 and 64 / 66)
+    // and they fill the device (us, large / 128 x 128 tiles, 4096 x 4096, 16-bit results: 8
+    // equal groups, 2048 rows: 64 / 54, 4096 rows: 75 / 92; rows by chance, 2048: 64 / 83, 3072:
+    // 65 / 84, 4096: 119 / 115; one group, 2000 rows: 57 / 42, 4096 rows: 63 / 80; 16 equal
+    // groups, 8000 rows, 2064 x 4096: 93 / 128; fp32 results: 65 / 70 and 127 / 133; 111 / 94,
+    // 116 / 119 and 168 / 149; 62 / 64 and 122 / 122; 149 / 158)
     const int64_t tiles = (cdiv(M, 256) + groups / 2) * cdiv(N, 256);
     return M / groups >= 192 && tiles >= num_cus ? CFG_L : CFG_M;
 }

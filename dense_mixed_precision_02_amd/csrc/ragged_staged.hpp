@@ -14,7 +14,8 @@
 // Measured: 32 groups, 5003 rows in all, by 2056 x 1000 row-major, fp32 results added to:
 // 76 us, 2.5 TB/s; 24 gradients of 520 x 1032 from 3001 rows, fp32 results added to: 34
 // us, 3.3 TB/s.  What bounds it is what one CU can have on its way: with one tile on
-// a CU a k-tile of 32 KB takes 0.7 us, in this kernel as in scaled_tile's.
+// a CU a k-tile of 32 KB takes 0.7 us, in this kernel as in scaled_tile's: 4096 of K take
+// 50 us whatever the rows and columns, as long as there are no more tiles than CUs.
 //
 // LDS layouts and fragment reads are tile_gemm.hpp's and frag16's; without direct
 // copies in flight the compiler lets the transposing reads run freely.
@@ -22,7 +23,10 @@
 // FAST: operands whose 16-byte granules are aligned and whole, read through
 // descriptors that turn what is out of range into zeros.  Otherwise a lane loads
 // its granule wherever it lies (unaligned 16-byte loads are allowed on global
-// memory), element by element only where it crosses the operand's end.
+// memory), element by element only where it crosses the operand's end.  (5003 rows over
+// 32 groups by 2057 x 1001: column-major 102 us, row-major 174, where 2056 x 1000 takes 64;
+// 24 gradients of 521 x 1033 from 3001 rows: 88 us against 34 for 520 x 1032; 8 groups of
+// 2048 rows by 4097 x 4097 1.6 ms.)
 #pragma once
 #include "ragged_tile.hpp"
 

@@ -6,9 +6,9 @@
 //
 // The K loop and the reading of MN-contiguous operands (B row-major, and both of
 // the weight gradients') are tile16_gemm's.  Two other ways for the latter were
-// built: turning 8 x 8 blocks in registers between the load and LDS (872 against
-// 1214 TFLOP/s on 8 x 2048 x 4096 x 4096 with a row-major B: the loads of eight
-// rows to an instruction take longer than the transposing reads), and copies
+// built: turning 8 x 8 blocks in registers between the load and LDS (872 TFLOP/s on
+// 8 groups of 2048 rows by 4096 x 4096 row-major, where this takes 1172: the loads of
+// eight rows to an instruction take longer than the transposing reads), and copies
 // written as assembly so that the compiler would not hold the transposing reads
 // back (not kept).
 //
@@ -19,13 +19,17 @@
 // WGRAD: the outputs are common to all groups, so the grid is known, but a
 // tile's time is its group's rows: groups are taken longest first, and each
 // group's tiles are spread over the XCDs in runs (2048 x 4096 gradients of 16384
-// rows, unevenly over 8 groups: 315 us with each group on one XCD, 264 so).
+// rows, unevenly over 8 groups: 366 us with each group on one XCD, 286 so; equal
+// groups: 265 and 269).
 //
-// Measured: 8 groups of 2048 rows by 4096 x 4096 (bf16, column-major B) 1214 TFLOP/s,
-// what tile16_gemm reaches on such products; bound by the power limit there and,
-// with uneven groups, by their partial row tiles and the last round of tiles (16384 rows
-// unevenly over 8 groups, 4096 x 4096: 486 us, 1.13 PFLOP/s; gradients of 2048 x 4096
-// from the same rows: 287 us, 0.96 PFLOP/s).
+// Measured (bf16): 8 groups of 2048 rows by 4096 x 4096, column-major B: 442 us, 1244
+// TFLOP/s, row-major 1172; tile16_gemm on 8 such products 1297 and 1213.  Bound by the
+// power limit there and, with uneven groups, by their partial row tiles and the last
+// round of tiles (16384 rows unevenly over 8 groups: 488 us, 1.13 PFLOP/s, row-major 519
+// us).  Gradients of 2048 x 4096 from 8 groups of 2048 rows: 269 us, 1022 TFLOP/s, where
+// tile16_gemm has 1189 on the same layouts; from 16384 uneven rows 287 us.  The matrix
+// units are busy for 40 % there, at 2.1 GHz, so the power limit does not bound them;
+// both operands' transposing reads all follow the barrier of the k-tile.
 //
 // Edges: a group's last row tile is usually partial, so rows are bounded by
 // predicates on whole vectors instead of a slow path for the whole slab.

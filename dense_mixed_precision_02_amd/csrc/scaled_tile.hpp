@@ -14,8 +14,10 @@
 // The next k-tile's copies are spread over the first half of the row blocks (all of
 // them at once: 63.8 us instead of 62 for 4096^3).
 //
-// Measured: 4096^3 e4m3 with bf16 results 62 us, 2.2 PFLOP/s; with fp32 results 16
-// groups, 8011 rows, 2064 x 4096: 171 us, 0.79 PFLOP/s.  The matrix units are
+// Measured: 4096^3 e4m3 with bf16 results 63 us, 2.2 PFLOP/s; with fp32 results 16
+// groups, 8011 rows, 2064 x 4096: 171 us, 0.79 PFLOP/s; with bf16 ones 8000 rows there,
+// equal groups 93 to 99 us, uneven ones 130: 17 k-tiles between a prologue and an epilogue, two
+// rounds of tiles.  The matrix units are
 // busy for about half of the time; the multiply-adds run beside them (two waves to a
 // SIMD: 34 cycles for an instruction and four multiply-adds, 33 without), the rest
 // is the LDS (192 KB read and 64 KB written for a k-tile of 256 x 256) and the

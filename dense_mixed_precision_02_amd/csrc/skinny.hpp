@@ -10,13 +10,16 @@
 // added in the order of the waves (the same result every run).  Rows go 16 or
 // 32 at a time (16-bit operands with TN = 2: 32 or 64; the widened 8-bit ones
 // would not fit the registers); a group with more reads its B again, by then
-// from the caches.  64 groups of one row, bf16 4096 x 1024: 92 us, 5.8 TB/s.
+// from the caches, one pass after the other (which a long group makes slow: grouped_cfg
+// has the figures).  64 groups of one row, bf16 4096 x 1024: 92 us, 5.8 TB/s.
 //
 // skinny_n does the same for N-contiguous B (16-bit operands): 92 us.
 //
 // 8-bit operands (SCALED) are widened to bf16 exactly as in scaled_tile.hpp:
 // the matrix units idle here anyway, so every D type gets exact products.
-// (64 groups of one row, 1024 x 4096: 46 us, 5.9 TB/s.)
+// (64 groups of one row, 1024 x 4096: 56 us, 4.8 TB/s.)  Whether a factor has to be taken
+// apart is noted in the loop and done after it (scaled_tile.hpp's Factor; 16 rows by 4096
+// x 8192 with warm weights 8.6 us, 8.3 without).
 #pragma once
 #include "scaled_tile.hpp"
 

@@ -250,7 +250,9 @@ int gemm_run_noalloc(gemm_handle_t h, const void *A, const void *B, const void *
  * leading dimensions and extents are those of gemm_run.  A call (also one of
  * gemm_quant8 or gemm_run_scaled8) that would take 2^31 workgroups or more is
  * refused with GEMM_ERR_INVALID_ARG.  M, N or groups == 0 enqueues nothing;
- * K == 0 gives D = cvt(beta * C).
+ * K == 0 gives D = cvt(beta * C).  The time grows with the longest group where
+ * rows are few, and, beyond a thousand groups whose products do not take the
+ * kernels for few rows, with the square of the number of groups.
  */
 enum { GEMM_OFFSETS_I32 = 16u };
 
