@@ -194,7 +194,7 @@ inline int grouped_cfg(int num_cus, const void *A, const void *B, int64_t groups
     // 256 x 256 tiles where the mean group fills most of one and 128 x 128 ones, two to a
     // CU, would take more than one round of the device (us, 256 x 256 / 128 x 128 tiles,
     // column-major B, rows by chance over the groups; 8 groups by 4096 x 4096, 1536 rows, 512
-    // small tiles: 125 / 85, 2048 rows, 640: 100 / 120, 3072 rows: 106 / 150; one group, 2000
+    // small tiles: 125 / 85, 2048 rows, 640: 100 / 120, 4096 rows: 156 / 187; one group, 2000
     // rows, 512: 99 / 80, 2100 rows, 544: 88 / 114; 32 groups by 2048 x 1024, 6144 rows, 512:
     // 70 / 47, 7168 rows, 576: 59 / 66.  By the mean: 64 groups by 1024 x 2048, of 96 rows: 73 /
     // 59, of 192: 82 / 97, in shares that fall with the root of the rank 109 / 99)
@@ -225,10 +225,10 @@ inline int scaled_cfg(int num_cus, int64_t groups, int64_t M, int64_t N) {
         return skinny_cfg(num_cus, groups, M, N, 0, true);
     // 256 x 256 (fp32 results: 256 x 128) tiles where the mean group fills most of one
     // and they fill the device (us, large / 128 x 128 tiles, 4096 x 4096, 16-bit results: 8
-    // equal groups, 2048 rows: 64 / 54, 4096 rows: 75 / 92; rows by chance, 2048: 64 / 83, 3072:
-    // 65 / 84, 4096: 119 / 115; one group, 2000 rows: 57 / 42, 4096 rows: 63 / 80; 16 equal
+    // equal groups, 2048 rows: 64 / 54, 4096 rows: 75 / 92; rows by chance, 2048: 64 / 83, 2560:
+    // 65 / 81, 4096: 119 / 115; one group, 2000 rows: 57 / 42, 4096 rows: 63 / 80; 16 equal
     // groups, 8000 rows, 2064 x 4096: 93 / 128; fp32 results: 65 / 70 and 127 / 133; 111 / 94,
-    // 116 / 119 and 168 / 149; 62 / 64 and 122 / 122; 149 / 158)
+    // 113 / 99 and 168 / 149; 62 / 64 and 122 / 122; 149 / 158)
     const int64_t tiles = (cdiv(M, 256) + groups / 2) * cdiv(N, 256);
     return M / groups >= 192 && tiles >= num_cus ? CFG_L : CFG_M;
 }

@@ -28,7 +28,7 @@
 // round of tiles (16384 rows unevenly over 8 groups: 488 us, 1.13 PFLOP/s, row-major 519
 // us).  Gradients of 2048 x 4096 from 8 groups of 2048 rows: 269 us, 1022 TFLOP/s, where
 // tile16_gemm has 1189 on the same layouts; from 16384 uneven rows 287 us.  The matrix
-// units are busy for 40 % there, at 2.1 GHz, so the power limit does not bound them;
+// units are busy for 41 % there, at 2.0 GHz, so the power limit does not bound them;
 // both operands' transposing reads all follow the barrier of the k-tile.
 //
 // Edges: a group's last row tile is usually partial, so rows are bounded by
