@@ -1,0 +1,451 @@
+"""What is measured of the router of the experts (with its balance loss), the low-rank
+adapters of many requests beside a shared projection, and the weight gradients from
+8-bit checkpoints of activations.
+
+Notation: rows (tokens) are sorted by group (an expert, an adapter's request) and
+`offsets` holds groups + 1 ascending row numbers; group g owns rows offsets[g] ..
+offsets[g+1].
+
+  route    the k experts of largest logit of each token (ties: the lower expert; a logit of -inf: not
+           available, and with fewer than k available the slots left over are -1), their weights (the
+           softmax over all experts, or over the chosen ones where they are normalized), how many
+           slots each expert got and where its rows begin, the slots sorted by expert (stable; slots
+           without an expert behind the last) and each slot's place in that order;
+           balance = E * sum over e of (count_e / slots) * (mean over tokens of p_te),
+           z = mean over tokens of logsumexp^2; masked tokens and tokens without an expert count nowhere.
+           With gradients: of sum(dw * weights) + cb * balance + cz * z in the logits, the counts held.
+  adapt    D[i] = X[i] W + scale_a (X[i] A_a) B_a + beta C[i]     a: the adapter of row i's request, if any
+           With gradients: dX = dY W^T + scale_a (dY B_a^T) A_a^T, dA_a = scale_a X_a^T dY_a B_a^T,
+           dB_a = scale_a A_a^T X_a^T dY_a.
+  save     q = round8(x / s) with s the smallest power of two for which the block's (one row, 128
+           columns) largest magnitude fits the 8-bit type
+  wgrad    D_g = X_g^T Y_g + beta C_g, X such an 8-bit checkpoint (x = q * s)
+
+The plain forms compute the same in 32 bits and round once at the end.
+"""
+import math
+import random
+
+import numpy as np
+import torch
+
+own = False
+
+_F = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32,
+      "e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
+_SIZE = {"bf16": 2, "f16": 2, "f32": 4, "e4m3": 1, "e5m2": 1}
+# largest value = 0.875 * 2^top
+_TOP = {"e4m3": 9, "e5m2": 16}
+_F16_TOP = {"e4m3": 61440.0, "e5m2": 57344.0}  # the largest that both the 8-bit type's digits and fp16 hold
+
+
+def listed():
+    return [
+        # one decoding step of a batch of 16 tokens (launch latency)
+        {"name": "route_decode", "op": "route", "dtype": "f32", "t": 16, "e": 32, "k": 4, "normalize": True, "masked": 0.0,
+         "absent": 0.0, "spread": 1.5, "train": False},
+        # a prompt of 16384 tokens over 64 experts (bound by the choice of the experts and the passes over the slots)
+        {"name": "route_prompt", "op": "route", "dtype": "bf16", "t": 16384, "e": 64, "k": 8, "normalize": True, "masked": 0.0,
+         "absent": 0.0, "spread": 1.5, "train": False},
+        # a training step's router with its gradients: padded sequences, experts that some tokens may not use
+        {"name": "route_train", "op": "route", "dtype": "bf16", "t": 16384, "e": 64, "k": 2, "normalize": False, "masked": 0.1,
+         "absent": 0.0, "spread": 1.0, "train": True},
+        # the same of many small experts, ragged sizes, tokens that may use only some of the experts
+        {"name": "route_train_ragged", "op": "route", "dtype": "f32", "t": 5003, "e": 160, "k": 6, "normalize": True,
+         "masked": 0.05, "absent": 0.5, "spread": 1.0, "train": True},
+        # one token of a small model for each of four requests (launch latency)
+        {"name": "adapt_token", "op": "adapt", "dtype": "f16", "out": "f16", "rows": 4, "tail": 0, "requests": 4, "adapters": 3,
+         "k": 512, "n": 512, "r": 8, "linear": True, "none": 0.25, "skew": 0.0, "beta": 0.0, "train": False},
+        # decoding: a token of each of 64 requests, 32 adapters (bound by reading the weights)
+        {"name": "adapt_decode", "op": "adapt", "dtype": "bf16", "out": "bf16", "rows": 64, "tail": 0, "requests": 64,
+         "adapters": 32, "k": 4096, "n": 4096, "r": 16, "linear": True, "none": 0.1, "skew": 0.0, "beta": 0.0, "train": False},
+        # prompts of nine requests in one batch (bound by the matrix units)
+        {"name": "adapt_prompts", "op": "adapt", "dtype": "bf16", "out": "bf16", "rows": 8192, "tail": 0, "requests": 9,
+         "adapters": 6, "k": 4096, "n": 4096, "r": 64, "linear": True, "none": 0.1, "skew": 0.7, "beta": 0.0, "train": False},
+        # a training step of eight adapters, each with its own rows, ragged sizes, padding rows
+        # behind them: the forward product, the input's gradient and the adapters' gradients
+        {"name": "adapt_train", "op": "adapt", "dtype": "bf16", "out": "bf16", "rows": 5003, "tail": 37, "requests": 8,
+         "adapters": 8, "k": 2056, "n": 1000, "r": 24, "linear": True, "none": 0.0, "skew": 0.5, "beta": 0.0, "train": True},
+        # a small layer's step: 256 tokens saved in 8 bits, and the weight gradient from what was saved (launch latency)
+        {"name": "checkpoint_small", "op": "wgrad", "dtype": "bf16", "out": "bf16", "q": "e4m3", "groups": 0, "rows": 256,
+         "tail": 0, "m": 512, "n": 512, "skew": 0.0, "beta": 0.0, "save": True},
+        # a layer's weight gradient over 8192 tokens (bound by the matrix units)
+        {"name": "checkpoint_layer", "op": "wgrad", "dtype": "bf16", "out": "bf16", "q": "e4m3", "groups": 0, "rows": 8192,
+         "tail": 0, "m": 4096, "n": 4096, "skew": 0.0, "beta": 0.0, "save": False},
+        # small experts, some without tokens, added up in 32 bits over micro-batches
+        {"name": "checkpoint_experts", "op": "wgrad", "dtype": "f16", "out": "f32", "q": "e4m3", "groups": 24, "rows": 3001,
+         "tail": 11, "m": 520, "n": 1032, "skew": 1.2, "beta": 1.0, "save": False},
+        # a training step over 8 experts: saved in 8 bits, the experts' weight gradients from that
+        {"name": "checkpoint_train", "op": "wgrad", "dtype": "bf16", "out": "bf16", "q": "e4m3", "groups": 8, "rows": 16384,
+         "tail": 0, "m": 2048, "n": 2048, "skew": 0.3, "beta": 0.0, "save": True},
+    ]
+
+
+def _spread(rng, lo, hi, step=1):
+    v = int(round(math.exp(rng.uniform(math.log(lo), math.log(hi))) / step)) * step
+    return min(hi, max(lo, v))
+
+
+def draw(rng):
+    op = rng.choice(["route", "adapt", "wgrad"])
+    if op == "route":
+        e = _spread(rng, 4, 256, rng.choice([1, 8]))
+        return {"op": op, "dtype": rng.choice(["bf16", "f16", "f32"]), "t": _spread(rng, 1, 16384), "e": e,
+                "k": rng.randint(1, min(8, e)), "normalize": rng.random() < 0.5, "masked": rng.choice([0.0, 0.1, 0.9]),
+                "absent": rng.choice([0.0, 0.0, 0.5]), "spread": rng.choice([0.5, 1.5, 4.0]), "train": rng.random() < 0.6}
+    step = rng.choice([1, 8, 8, 8, 64, 128])  # most widths are whole granules, some are odd
+    dtype, tail, skew = rng.choice(["bf16", "f16"]), rng.choice([0, 0, 5, 130]), rng.choice([0.0, 0.4, 1.5])
+    if op == "adapt":
+        train = rng.random() < 0.4
+        requests = _spread(rng, 1, 64)
+        adapters = requests if train else _spread(rng, 1, 32)
+        r = min(_spread(rng, 1, 128, rng.choice([1, 8, 16])), max(1, 1024 // adapters))
+        return {"op": op, "dtype": dtype, "out": dtype if train else rng.choice([dtype, "f32"]),
+                "rows": _spread(rng, 1, 2048 if train else 6000), "tail": tail, "requests": requests, "adapters": adapters,
+                "k": _spread(rng, 64, 4096, step), "n": _spread(rng, 64, 4096, step), "r": r, "linear": rng.random() < 0.6,
+                "none": 0.0 if train else rng.choice([0.0, 0.1, 0.5]), "skew": skew,
+                "beta": 0.0 if train else rng.choice([0.0, 0.0, 1.0, 0.5]), "train": train}
+    groups = _spread(rng, 1, 64)
+    m, n = _spread(rng, 64, 4096, step), _spread(rng, 64, 4096, step)
+    while groups * m * n > 1 << 25:  # no more gradients than the largest listed case has
+        groups //= 2
+    if rng.random() < 0.4:
+        groups = 0
+    return {"op": op, "dtype": dtype, "out": rng.choice([dtype, "f32"]), "q": rng.choice(["e4m3", "e4m3", "e5m2"]),
+            "groups": groups, "rows": _spread(rng, 1, 8000), "tail": tail if groups else 0, "m": m, "n": n, "skew": skew,
+            "beta": rng.choice([0.0, 0.0, 1.0, 0.5]), "save": rng.random() < 0.5}
+
+
+def _counts(rows, groups, skew):
+    """Rows of each group, largest first: shares that fall as 1 / (rank + 1)^skew."""
+    w = np.arange(1, groups + 1, dtype=np.float64) ** -skew
+    c = np.floor(rows * w / w.sum()).astype(np.int64)
+    left = rows - int(c.sum())
+    c[:left % len(c)] += 1
+    c += left // len(c)
+    return [int(x) for x in c]
+
+
+def _offsets(rows, groups, skew, seed):
+    if not groups:
+        return [0, rows]
+    c = _counts(rows, groups, skew)
+    random.Random(seed).shuffle(c)
+    return [0] + [int(x) for x in np.cumsum(c)]
+
+
+def _blocks(n):
+    return -(-n // 128)
+
+
+def prepare(case, seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    s = {"case": case}
+
+    def normal(*shape, dtype=torch.float32, scale=1.0):
+        return (torch.randn(*shape, generator=g, device="cuda", dtype=torch.float32) * scale).to(dtype)
+
+    def uniform(*shape):
+        return torch.rand(*shape, generator=g, device="cuda")
+
+    if case["op"] == "route":
+        t, e = case["t"], case["e"]
+        # logits whose experts differ in how often they are chosen
+        x = normal(t, e, scale=case["spread"]) + normal(e, scale=0.5)
+        if case["absent"]:
+            x = x.masked_fill(uniform(t, e) < case["absent"], -math.inf)
+        s["logits"] = x.to(_F[case["dtype"]])
+        s["mask"] = uniform(t) >= case["masked"] if case["masked"] else None
+        s["dw"] = normal(t, case["k"], scale=1e-2)
+        return s
+    dt = _F[case["dtype"]]
+    total = case["rows"] + case["tail"]
+    if case["op"] == "adapt":
+        k, n, r, a = case["k"], case["n"], case["r"], case["adapters"]
+        s["host_offsets"] = _offsets(case["rows"], case["requests"], case["skew"], seed)
+        s["offsets"] = torch.tensor(s["host_offsets"], device="cuda", dtype=torch.int64)
+        s["X"] = normal(total, k, dtype=dt)
+        sk, sr = 1.0 / math.sqrt(k), 0.5 / math.sqrt(r)
+        # the layout of linear layers (outputs by inputs), or inputs by outputs
+        s["W"] = normal(n, k, dtype=dt, scale=sk).t() if case["linear"] else normal(k, n, dtype=dt, scale=sk)
+        s["A"] = normal(a, r, k, dtype=dt, scale=sk).transpose(1, 2) if case["linear"] else normal(a, k, r, dtype=dt, scale=sk)
+        s["B"] = normal(a, n, r, dtype=dt, scale=sr).transpose(1, 2) if case["linear"] else normal(a, r, n, dtype=dt, scale=sr)
+        s["scale"] = torch.exp2(torch.floor(uniform(a) * 3) - 1)
+        rng = random.Random(seed)
+        ids = list(range(a)) if case["train"] else \
+            [-1 if rng.random() < case["none"] else rng.randrange(a) for _ in range(case["requests"])]
+        s["host_ids"], s["ids"] = ids, torch.tensor(ids, device="cuda", dtype=torch.int32)
+        s["C"] = normal(total, n, dtype=_F[case["out"]])
+        s["out"] = s["C"].clone()  # rows that no request owns keep what is here
+        if case["train"]:
+            s["dY"] = normal(total, n, dtype=dt, scale=0.1)
+            s["dX"] = normal(total, k, dtype=dt)
+        return s
+    m, n = case["m"], case["n"]
+    s["host_offsets"] = _offsets(case["rows"], case["groups"], case["skew"], seed)
+    s["offsets"] = torch.tensor(s["host_offsets"], device="cuda", dtype=torch.int64)
+    # activations with a spread of magnitudes from row to row
+    s["X"] = (normal(total, m) * torch.exp(normal(total, 1))).to(dt)
+    if not case["save"]:
+        s["q"], s["s"] = _save_plain(case, s.pop("X"))
+    s["Y"] = normal(total, n, dtype=dt, scale=0.1)
+    shape = (case["groups"], m, n) if case["groups"] else (m, n)
+    s["C"] = normal(*shape, dtype=_F[case["out"]])
+    return s
+
+
+def _save_plain(case, x):
+    """(8-bit values, rows of 16 * ceil(m / 16) with zeros at the end; the scales (rows, ceil(m / 128)))"""
+    rows, m = x.shape
+    kb = _blocks(m)
+    p = torch.nn.functional.pad(x.float(), (0, kb * 128 - m)).reshape(rows, kb, 128)
+    mant, e = torch.frexp(p.abs().amax(-1).clamp_min(2.0 ** -100))
+    # in 64 bits: 2^(e - top) of the least blocks lies below what exp2 in 32 bits gives exactly
+    s = torch.exp2((e - _TOP[case["q"]] + (mant > 0.875)).double()).float()
+    if case["dtype"] == "f16":
+        p = p.clamp(-_F16_TOP[case["q"]], _F16_TOP[case["q"]])
+    q = (p / s[..., None]).reshape(rows, kb * 128)[:, :-(-m // 16) * 16]
+    return q.to(_F[case["q"]]), s
+
+
+def _route_plain(case, s):
+    e, k, mask = case["e"], case["k"], s["mask"]
+    x = s["logits"].float()
+    if mask is not None:
+        x = x.masked_fill(~mask[:, None], -math.inf)
+    top = x.amax(-1, keepdim=True)
+    there = top[:, 0] > -math.inf
+    u = torch.exp(x - top.masked_fill(~there[:, None], 0.0))
+    total = u.sum(-1, keepdim=True)
+    p = u / total.masked_fill(~there[:, None], 1.0)
+    lse = (torch.log(total) + top)[:, 0].masked_fill(~there, 0.0)
+    value, experts = torch.sort(x, dim=-1, descending=True, stable=True)
+    value, experts = value[:, :k], experts[:, :k]
+    got = value > -math.inf
+    w = torch.where(got, torch.gather(p, 1, experts), 0.0)
+    if case["normalize"]:
+        w = torch.where(got, torch.exp(value - top), 0.0)
+        w = w / w.sum(-1, keepdim=True).masked_fill(~there[:, None], 1.0)
+    slot = torch.where(got, experts, e).flatten()
+    counts = torch.zeros(e + 1, device=x.device, dtype=torch.int64).scatter_add_(0, slot, torch.ones_like(slot))[:e]
+    order = torch.sort(slot, stable=True)[1]
+    place = torch.empty_like(order).scatter_(0, order, torch.arange(len(order), device=x.device))
+    n = there.sum().clamp_min(1).float()
+    share = counts / counts.sum().clamp_min(1).float()
+    out = {"experts": torch.where(got, experts, -1).int(), "weights": w, "counts": counts.int(),
+           "offsets": torch.nn.functional.pad(counts.cumsum(0), (1, 0)).int(), "order": order.int(), "place": place.int(),
+           "loss": torch.stack([e * (share * p.sum(0) / n).sum(), (lse * lse).sum() / n])}
+    if case["train"]:
+        cb, cz = _COEF
+        g = (cb * e / n) * share
+        d = p * (g - (p * g).sum(-1, keepdim=True)) + p * (2 * cz / n * lse)[:, None]
+        dw = torch.where(got, s["dw"], 0.0)
+        back = w * dw
+        if case["normalize"]:
+            d = d.scatter_add(1, experts, back - w * back.sum(-1, keepdim=True))
+        else:
+            d = d.scatter_add(1, experts, back) - p * back.sum(-1, keepdim=True)
+        out["dlogits"] = d.to(s["logits"].dtype)
+    return out
+
+
+_COEF = (1e-2, 1e-3)  # of the balance loss and of the z loss
+
+
+def _adapt_plain(case, s):
+    t, a, r = case["rows"], case["adapters"], case["r"]
+    off, ids = s["offsets"], s["ids"].long()
+    request = torch.searchsorted(off[1:].contiguous(), torch.arange(t, device=off.device), right=True)
+    one = (ids[request][:, None] == torch.arange(a, device=off.device)).float() * s["scale"]  # (t, a): the row's scale
+    x, W = s["X"][:t].float(), s["W"].float().contiguous()
+    A = s["A"].permute(1, 0, 2).float().reshape(-1, a * r)  # all adapters beside each other
+    B = s["B"].float().reshape(a * r, -1)
+    h = ((x @ A).reshape(t, a, r) * one[:, :, None]).reshape(t, a * r)
+    y = x @ W + h @ B
+    if case["beta"]:
+        y += case["beta"] * s["C"][:t].float()
+    out = {"y": torch.cat([y.to(s["out"].dtype), s["out"][t:]])}
+    if case["train"]:
+        dy = s["dY"][:t].float()
+        g = ((dy @ B.t().contiguous()).reshape(t, a, r) * one[:, :, None]).reshape(t, a * r)
+        dx = dy @ W.t().contiguous() + g @ A.t().contiguous()
+        out["dx"] = torch.cat([dx.to(s["dX"].dtype), s["dX"][t:]])
+        dt = s["X"].dtype
+        out["da"] = (x.t().contiguous() @ g).reshape(-1, a, r).transpose(0, 1).contiguous().to(dt)
+        out["db"] = (h.t().contiguous() @ dy).reshape(a, r, -1).to(dt)
+    return out
+
+
+def _wgrad_plain(case, s):
+    q, sc = _save_plain(case, s["X"]) if case["save"] else (s["q"], s["s"])
+    m, off, y = case["m"], s["host_offsets"], s["Y"].float()
+    x = q[:, :m].float() * sc.repeat_interleave(128, dim=1)[:, :m]
+    d = torch.stack([x[lo:hi].t().contiguous() @ y[lo:hi] for lo, hi in zip(off[:-1], off[1:])])
+    d = d if case["groups"] else d[0]
+    if case["beta"]:
+        d = d + case["beta"] * s["C"].float()
+    d = d.to(s["C"].dtype)
+    return {"q": q[:, :m], "s": sc, "dw": d} if case["save"] else {"dw": d}
+
+
+def run(s):
+    case = s["case"]
+    if own:
+        import dense_mixed_precision_02_amd as dmp
+        if case["op"] == "route":
+            r = dmp.route(s["logits"], case["k"], mask=s["mask"], normalize=case["normalize"])
+            out = {"experts": r.experts, "weights": r.weights, "counts": r.counts, "offsets": r.offsets, "order": r.order,
+                   "place": r.place, "loss": r.loss}
+            if case["train"]:
+                out["dlogits"] = dmp.route_grad(r, s["dw"], balance=_COEF[0], z=_COEF[1])
+            return out
+        if case["op"] == "adapt":
+            X, W, A, B, off, scale = s["X"], s["W"], s["A"], s["B"], s["offsets"], s["scale"]
+            if not case["train"]:
+                c = s["C"] if case["beta"] else None
+                return {"y": dmp.gemm_adapters(X, W, A, B, off, s["ids"], scale, c, out=s["out"], beta=case["beta"])}
+            dY, dt = s["dY"], X.dtype
+            h = torch.empty(X.shape[0], case["r"], dtype=dt, device=X.device)
+            g = torch.empty_like(h)
+            y = dmp.gemm_adapters(X, W, A, B, off, scale=scale, out=s["out"], hidden=h)
+            dx = dmp.gemm_adapters(dY, W.t(), B.transpose(1, 2), A.transpose(1, 2), off, scale=scale, out=s["dX"], hidden=g)
+            return {"y": y, "dx": dx, "da": dmp.gemm_grouped_wgrad(X, g, off, out_dtype=dt),
+                    "db": dmp.gemm_grouped_wgrad(h, dY, off, out_dtype=dt)}
+        c = s["C"] if case["beta"] else None
+        off = s["offsets"] if case["groups"] else None
+        x8 = dmp.quant8(s["X"], dtype=_F[case["q"]], pow2=True) if case["save"] else dmp.Scaled8(s["q"], s["s"], K=case["m"])
+        d = dmp.gemm_wgrad8(x8, s["Y"], off, c, beta=case["beta"], out_dtype=s["C"].dtype)
+        return {"q": x8.q[:, :case["m"]], "s": x8.scale, "dw": d} if case["save"] else {"dw": d}
+    return {"route": _route_plain, "adapt": _adapt_plain, "wgrad": _wgrad_plain}[case["op"]](case, s)
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    return {"route": _route_exact, "adapt": _adapt_exact, "wgrad": _wgrad_exact}[case["op"]](case, s)
+
+
+def _route_exact(case, s):
+    f, e, k = torch.float64, case["e"], case["k"]
+    x = s["logits"].to(f)
+    if s["mask"] is not None:
+        x[~s["mask"]] = -math.inf
+    t = x.shape[0]
+    index = torch.arange(e, device=x.device)
+    left, chosen, values = x.clone(), [], []
+    for _ in range(k):  # the largest that is left, the lowest number among equals
+        v = left.max(-1).values
+        i = torch.where((left == v[:, None]) & (v > -math.inf)[:, None], index, e).amin(-1)
+        chosen.append(i)
+        values.append(v)
+        left.scatter_(1, i.clamp_max(e - 1)[:, None], -math.inf)
+    experts, values = torch.stack(chosen, 1), torch.stack(values, 1)
+    none = experts == e
+    dead = none[:, 0]
+    lse = torch.logsumexp(x, -1).masked_fill(dead, 0.0)
+    p = torch.exp(x - lse[:, None])
+    w = torch.exp(values - lse[:, None])
+    if case["normalize"]:
+        w = torch.softmax(values.masked_fill(dead[:, None], 0.0), -1)
+    w = w.masked_fill(none, 0.0)
+    host = experts.flatten().tolist()
+    order = sorted(range(len(host)), key=host.__getitem__)
+    place = np.empty(len(host), dtype=np.int64)
+    place[order] = np.arange(len(host))
+    counts = np.bincount(host, minlength=e + 1)[:e]
+    n = max(1, t - int(dead.sum()))
+    share = torch.tensor(counts / max(1, int(counts.sum())), device=x.device, dtype=f)
+
+    def whole(v):
+        return torch.as_tensor(v, device=x.device).int()
+
+    out = {"experts": whole(experts.masked_fill(none, -1)), "weights": w, "counts": whole(counts),
+           "offsets": whole(np.concatenate([[0], np.cumsum(counts)])), "order": whole(order),
+           "place": whole(place).reshape(-1), "loss": torch.stack([(p @ share).sum() * e / n, (lse ** 2).sum() / n])}
+    if case["train"]:
+        cb, cz = _COEF
+        dp = (cb * e / n * share).expand(t, e).clone()  # the gradient in the probabilities
+        dw = s["dw"].to(f).masked_fill(none, 0.0)
+        at = experts.clamp_max(e - 1)
+        if case["normalize"]:
+            chosen_sum = torch.gather(p, 1, at).masked_fill(none, 0.0).sum(-1, keepdim=True).masked_fill(dead[:, None], 1.0)
+            dw = ((dw - (dw * w).sum(-1, keepdim=True)) / chosen_sum).masked_fill(none, 0.0)
+        dp.scatter_add_(1, at, dw)
+        d = p * (dp - (p * dp).sum(-1, keepdim=True)) + 2 * cz / n * lse[:, None] * p
+        out["dlogits"] = d.masked_fill(dead[:, None], 0.0)
+    return out
+
+
+def _adapt_exact(case, s):
+    """Request by request of the definition in 64 bits."""
+    f, t = torch.float64, case["rows"]
+    off, ids = s["host_offsets"], s["host_ids"]
+    W = s["W"].to(f).contiguous()
+    y = torch.matmul(s["X"][:t].to(f), W) + case["beta"] * s["C"][:t].to(f)
+    train = case["train"]
+    dx = torch.matmul(s["dY"][:t].to(f), W.t().contiguous()) if train else None
+    da, db = [], []
+    for i, (lo, hi) in enumerate(zip(off[:-1], off[1:])):
+        if ids[i] < 0:
+            continue
+        A, B, c = s["A"][ids[i]].to(f), s["B"][ids[i]].to(f), float(s["scale"][ids[i]])
+        x = s["X"][lo:hi].to(f)
+        y[lo:hi] += c * ((x @ A) @ B)
+        if train:
+            dy = s["dY"][lo:hi].to(f)
+            dx[lo:hi] += c * ((dy @ B.t()) @ A.t())
+            da.append(c * (x.t() @ (dy @ B.t())))
+            db.append(c * ((x @ A).t() @ dy))
+    out = {"y": torch.cat([y, s["out"][t:].to(f)])}
+    if train:
+        out.update(dx=torch.cat([dx, s["dX"][t:].to(f)]), da=torch.stack(da), db=torch.stack(db))
+    return out
+
+
+def _wgrad_exact(case, s):
+    f, m, off = torch.float64, case["m"], s["host_offsets"]
+    if case["save"]:
+        x, kb = s["X"].to(f), _blocks(m)
+        mant, low = (3, -6) if case["q"] == "e4m3" else (2, -14)
+        top = 0.875 * 2.0 ** _TOP[case["q"]]
+        sc = torch.empty(x.shape[0], kb, device="cuda", dtype=f)
+        q = torch.empty_like(x)
+        for b in range(kb):
+            part = x[:, 128 * b:128 * b + 128]
+            sc[:, b] = torch.exp2(torch.ceil(torch.log2(part.abs().amax(-1).clamp_min(2.0 ** -100) / top)))
+            if case["dtype"] == "f16":
+                part = part.clamp(-_F16_TOP[case["q"]], _F16_TOP[case["q"]])
+            v = part / sc[:, b, None]
+            # rounding to 8 bits from 64: to the nearest multiple of the value's last place, ties to even
+            place = torch.exp2(torch.floor(torch.log2(v.abs().clamp_min(2.0 ** low))) - mant)
+            q[:, 128 * b:128 * b + 128] = torch.round(v / place) * place
+    else:
+        q, sc = s["q"][:, :m].to(f), s["s"].to(f)
+    x = q * sc.repeat_interleave(128, dim=1)[:, :m]
+    d = torch.stack([torch.matmul(x[a:b].t(), s["Y"][a:b].to(f)) for a, b in zip(off[:-1], off[1:])])
+    d = (d if case["groups"] else d[0]) + case["beta"] * s["C"].to(f)
+    return {"q": q, "s": sc, "dw": d} if case["save"] else {"dw": d}
+
+
+def work(case):
+    if case["op"] == "route":
+        t, e, k = case["t"], case["e"], case["k"]
+        size = _SIZE[case["dtype"]]
+        moved = t * e * size + 16 * t * k + 8 * e
+        if case["train"]:  # logits, slots and weights again, and the gradient
+            moved += 2 * t * e * size + 12 * t * k
+        return {"bytes": moved, "flops": t * e * (12 if case["train"] else 4)}
+    if case["op"] == "adapt":
+        t, k, n, r, o = case["rows"], case["k"], case["n"], case["r"], _SIZE[case["out"]]
+        used = min(case["requests"], case["adapters"])
+        moved = 2 * (t * k + k * n + used * r * (k + n)) + o * t * n * (2 if case["beta"] else 1)
+        flops = 2 * t * (k * n + r * (k + n))
+        if case["train"]:
+            moved += 2 * (t * (k + n) + k * n + 2 * used * r * (k + n)) + 2 * t * k
+            flops = 2 * flops + 2 * t * r * (k + n)
+        return {"bytes": moved, "flops": flops}
+    t, m, n, o = case["rows"], case["m"], case["n"], _SIZE[case["out"]]
+    moved = t * m + 4 * t * _blocks(m) + 2 * t * n + o * max(1, case["groups"]) * m * n * (2 if case["beta"] else 1)
+    if case["save"]:
+        moved += 3 * t * m + 4 * t * _blocks(m)
+    return {"bytes": moved, "flops": 2 * t * m * n}
