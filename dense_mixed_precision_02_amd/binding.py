@@ -15,8 +15,9 @@ GEMM_OK = 0
 
 EXPORTED_SYMBOLS = ("gemm_create", "gemm_run", "gemm_run_ex", "gemm_run_noalloc", "gemm_prune24",
                     "gemm_run_sparse24", "gemm_run_grouped", "gemm_run_grouped_wgrad", "gemm_quant8",
-                    "gemm_run_scaled8", "gemm_destroy", "gemm_status_string", "gemm_plan")
+                    "gemm_run_scaled8", "gemm_route_work", "gemm_route", "gemm_route_grad", "gemm_destroy", "gemm_status_string", "gemm_plan")
 GEMM_OFFSETS_I32 = 16
+GEMM_ROUTE_NORMALIZE = 32
 GEMM_E4M3, GEMM_E5M2 = 0, 1
 GEMM_ERR_SCRATCH = 5
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -30,6 +31,12 @@ class Q8Operand(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("ld", ctypes.c_int64),
                 ("scale_row", ctypes.c_int64), ("scale_k", ctypes.c_int64), ("group", ctypes.c_int64),
                 ("scale_group", ctypes.c_int64), ("type", ctypes.c_int)]
+
+
+class RouteTables(ctypes.Structure):
+    """gemm_route_t: what gemm_route writes."""
+    _fields_ = [(name, ctypes.c_void_p) for name in ("experts", "weights", "lse", "counts", "offsets", "order", "place",
+                                                     "loss")]
 
 
 class GemmError(RuntimeError):
@@ -85,6 +92,13 @@ def load_library():
         lib.gemm_run_scaled8.restype = ci
         lib.gemm_run_scaled8.argtypes = [vp, ctypes.POINTER(Q8Operand), ctypes.POINTER(Q8Operand), vp, vp,
                                          vp, i64, i64, i64, i64, i64, cu, cf, cf, ci, ci, vp]
+        lib.gemm_route_work.restype = i64
+        lib.gemm_route_work.argtypes = [vp, i64, i64]
+        lib.gemm_route.restype = ci
+        lib.gemm_route.argtypes = [vp, vp, ci, i64, i64, i64, i64, vp, cu, ctypes.POINTER(RouteTables), vp, vp]
+        lib.gemm_route_grad.restype = ci
+        lib.gemm_route_grad.argtypes = [vp, vp, ci, i64, i64, i64, i64, cu, ctypes.POINTER(RouteTables), vp, cf, cf, vp,
+                                        i64, vp]
         lib.gemm_plan.restype = ctypes.c_int
         lib.gemm_plan.argtypes = [vp, i64, i64, i64, i64, i64, i64, ctypes.c_int, ctypes.c_uint,
                                   i64, ctypes.c_char_p, ctypes.c_size_t]
@@ -193,6 +207,21 @@ class Handle:
         return load_library().gemm_run_scaled8(self.ptr, ctypes.byref(A), ctypes.byref(B), C, D, offsets,
                                                groups, M, N, K, ldc, flags, alpha, beta, c_type, d_type,
                                                stream)
+
+    def route_work(self, T, E) -> int:
+        """Bytes of scratch that route() needs (-1: sizes that are refused)."""
+        return load_library().gemm_route_work(self.ptr, T, E)
+
+    def route(self, logits, x_type, T, E, ld, k, mask, flags, tables: RouteTables, work, stream=0) -> int:
+        """Raw-pointer call of gemm_route; returns the status code."""
+        return load_library().gemm_route(self.ptr, logits, x_type, T, E, ld, k, mask, flags, ctypes.byref(tables), work,
+                                         stream)
+
+    def route_grad(self, logits, x_type, T, E, ld, k, flags, tables: RouteTables, dweights, balance, z, dlogits, ldd,
+                   stream=0) -> int:
+        """Raw-pointer call of gemm_route_grad; returns the status code."""
+        return load_library().gemm_route_grad(self.ptr, logits, x_type, T, E, ld, k, flags, ctypes.byref(tables),
+                                              dweights, balance, z, dlogits, ldd, stream)
 
     def run_ex(self, *args, **kw) -> None:
         """Like status_ex() but raises on a non-zero status."""
@@ -703,4 +732,103 @@ def gemm_scaled8(A: Scaled8, B: Scaled8, offsets=None, C=None, out=None, alpha: 
         A.K, ldc, flags, alpha, beta, c_code, d_code, stream))
     if rc != GEMM_OK:
         raise GemmError(rc, "gemm_run_scaled8")
+    return out
+
+
+class Route:
+    """What route() found, on the logits' GPU: ``experts`` (T, k) int32 and ``weights``
+    (T, k) float32; ``counts`` (E,) and ``offsets`` (E + 1,) int32; ``order`` and ``place``
+    (T * k,) int32; ``lse`` (T,) float32; ``loss`` (2,) float32: the balance loss and the
+    mean of lse^2.  ``logits``, ``k`` and ``normalize`` are the call's: route_grad reads the
+    logits again, which must not have changed."""
+
+    def __init__(self, logits, k, normalize, experts, weights, lse, counts, offsets, order, place, stats):
+        self.logits, self.k, self.normalize = logits, k, normalize
+        self.experts, self.weights, self.lse = experts, weights, lse
+        self.counts, self.offsets, self.order, self.place = counts, offsets, order, place
+        self.loss, self._stats = stats[:2], stats
+
+    def _tables(self) -> RouteTables:
+        return RouteTables(*(t.data_ptr() for t in (self.experts, self.weights, self.lse, self.counts, self.offsets,
+                                                    self.order, self.place, self._stats)))
+
+
+def _check_logits(logits, k):
+    """(type code, T, E, row stride) of a router's logits."""
+    x_code = _out_code(logits.dtype)
+    if x_code not in _FLOAT_OUT:
+        raise TypeError("logits must be float32, float16 or bfloat16")
+    if logits.dim() != 2 or not logits.is_cuda:
+        raise ValueError("logits must be a 2-D GPU tensor (tokens, experts)")
+    T, E = logits.shape
+    if not 1 <= E <= 1024 or not 1 <= k <= min(E, 64):
+        raise ValueError("route takes 1 to 1024 experts, and k of 1 to min(experts, 64)")
+    return x_code, T, E, _rows_of(logits, "logits")
+
+
+def route(logits, k: int, mask=None, normalize: bool = False, handle: Handle | None = None) -> Route:
+    """The experts of every token, on the current stream: from logits (T, E) float32 /
+    float16 / bfloat16, row-major, the k experts of largest logit (the lower number
+    among equals; an expert with a logit of -inf is not available, and a slot left over
+    is -1 with the weight 0), their weights (the softmax over all experts, or with
+    ``normalize`` over the chosen ones), the rows of every expert, and the balance loss.
+    mask: (T,) bool, False for tokens that do not count (padding): they get no expert.
+
+    With r = route(logits, k) the experts' products of X (T, K) are
+    gemm_grouped(X[r.order // k], W, r.offsets): ``order`` holds the slots (token * k +
+    choice) sorted by expert, those without an expert behind the last group, and ``place``
+    its inverse, so that choice j of token t is row place[t * k + j] of the product.
+
+    r.loss[0] = E * sum_e (counts_e / slots) * (mean over the tokens of p_e), and r.loss[1] =
+    the mean of logsumexp^2; route_grad has their gradients."""
+    import torch
+    x_code, T, E, ld = _check_logits(logits, k)
+    device = logits.device
+    if T * k > (1 << 31) - 1024:
+        raise ValueError("tokens times k must stay below 2^31 - 1024")
+    if mask is not None:
+        if mask.dtype not in (torch.bool, torch.uint8):
+            raise TypeError("mask must be bool")
+        if mask.shape != (T,) or mask.device != device or (T > 1 and mask.stride(0) != 1):
+            raise ValueError("mask must be a contiguous vector of one value to a token, on the logits' GPU")
+    S = T * k
+    experts, order, place, counts, offsets = torch.empty(3 * S + 2 * E + 1, dtype=torch.int32, device=device).split(
+        (S, S, S, E, E + 1))
+    weights, lse, stats = torch.empty(S + T + 4, dtype=torch.float32, device=device).split((S, T, 4))
+    r = Route(logits, k, bool(normalize), experts.view(T, k), weights.view(T, k), lse, counts, offsets, order, place, stats)
+
+    def call(h, stream):
+        work = torch.empty(h.route_work(T, E), dtype=torch.uint8, device=device)
+        return h.route(logits.data_ptr(), x_code, T, E, ld, k, mask.data_ptr() if mask is not None else 0,
+                       GEMM_ROUTE_NORMALIZE if normalize else 0, r._tables(), work.data_ptr(), stream)
+
+    rc = _on(device, handle, call)
+    if rc != GEMM_OK:
+        raise GemmError(rc, "gemm_route")
+    return r
+
+
+def route_grad(r: Route, d_weights=None, balance: float = 0.0, z: float = 0.0, out=None, handle: Handle | None = None):
+    """The gradient of sum(d_weights * r.weights) + balance * r.loss[0] + z * r.loss[1] in
+    r.logits (the counts held), on the current stream.  d_weights: (T, k) float32,
+    contiguous, or None.  The result has the logits' shape and type, a new tensor unless
+    ``out`` is given (row-major; it may be the logits)."""
+    import torch
+    logits = r.logits
+    x_code, T, E, ld = _check_logits(logits, r.k)
+    if d_weights is not None:
+        if d_weights.dtype != torch.float32:
+            raise TypeError("d_weights must be float32")
+        if d_weights.shape != (T, r.k) or d_weights.device != logits.device or not d_weights.is_contiguous():
+            raise ValueError("d_weights must be contiguous (tokens, k), on the logits' GPU")
+    if out is None:
+        out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    if out.dtype != logits.dtype or out.shape != logits.shape or out.device != logits.device:
+        raise ValueError("out must have the logits' shape and type, on their GPU")
+    ldd = _rows_of(out, "out")
+    rc = _on(logits.device, handle, lambda h, stream: h.route_grad(
+        logits.data_ptr(), x_code, T, E, ld, r.k, GEMM_ROUTE_NORMALIZE if r.normalize else 0, r._tables(),
+        d_weights.data_ptr() if d_weights is not None else 0, balance, z, out.data_ptr(), ldd, stream))
+    if rc != GEMM_OK:
+        raise GemmError(rc, "gemm_route_grad")
     return out

@@ -1,0 +1,472 @@
+// route.hpp -- the router of the experts: which k experts a token goes to, the rows of
+// every expert's product, the balance loss, and the gradient in the logits.
+//
+// With x the token's logits over E experts, m their largest, p = exp(x - lse) and
+// lse = m + log(sum of exp(x - m)):
+//   experts   the k largest x, ties to the lower number; -inf is no expert (-1)
+//   weights   w_j = p[e_j], or exp(x[e_j] - m) over their sum (normalized)
+//   balance   E * sum over e of share_e * P_e, share_e = count_e / slots, P_e = mean over tokens of p_e
+//   z         mean over tokens of lse^2
+// and with dw, cb and cz the gradients in the weights and the two losses (counts held)
+//   dx_i = p_i (g_i - sum p g) + 2 cz lse p_i / n + (gradient through the weights),  g_e = cb E share_e / n,
+//   through the weights: [i = e_j] w_j dw_j - p_i sum w dw, normalized: [i = e_j] (w_j dw_j - w_j sum w dw).
+// A token that is masked, or has no expert, has lse = +inf, so that p = 0 everywhere.
+//
+// The data are small, so launches and latency set the time, and everything is done in
+// two launches (one where one workgroup's 16 waves take the tokens in a few turns).
+// choose: one wave to a token, E / 64 logits to a lane; sums and maxima go over the
+// wave in six steps of lane-crossing arithmetic; each choice is one maximum of the
+// logits' order-preserving bits and a ballot for the lowest number among equals.
+// Each workgroup leaves its counts and its sums of p.  place: every workgroup adds up
+// the counts before its own (all of them, from the caches, instead of a launch of its
+// own for a scan), and gives its slots their places in ascending order by matching
+// experts within a wave: the order is that of a stable sort, the same every run.
+// Sums of p are added in a fixed order too, 32 bits within a workgroup, 64 over them; those
+// of lse^2 in 64 bits.
+#pragma once
+#include "common.hpp"
+#include "ragged.hpp"
+#include "route_plan.hpp"
+
+namespace dmp {
+
+struct RouteArgs {
+    const void *x;            // logits, T rows of E, ld apart
+    const uint8_t *mask;      // T: zero where a token does not count, or NULL
+    int64_t T, ld;
+    int E, k, normalize;
+    int rows, blocks;         // tokens to a workgroup, workgroups that choose
+    int32_t *experts;         // T x k
+    float *weights;           // T x k
+    float *lse;               // T
+    int32_t *counts, *offsets, *order, *place;
+    float *loss;              // balance, z, tokens that count, slots
+    int32_t *hist;            // work: blocks x E
+    float *psum;              // work: blocks x E
+    double *zsum;             // work: blocks: sum of lse^2 (whose terms may pass the floats)
+    int32_t *tokens;          // work: blocks: tokens that count
+};
+
+// Reductions over a wave by lane-crossing moves inside the vector unit (six steps, where
+// shuffles would go through LDS each time); the result is that of lane 63, given to all.
+template <int CTRL>
+__device__ static inline uint32_t dpp_from(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false);
+}
+__device__ static inline uint32_t wave_max(uint32_t v) {
+    v = max(v, dpp_from<0x111>(v));  // row_shr:1, 2, 4, 8: within 16 lanes
+    v = max(v, dpp_from<0x112>(v));
+    v = max(v, dpp_from<0x114>(v));
+    v = max(v, dpp_from<0x118>(v));
+    v = max(v, dpp_from<0x142>(v));  // row_bcast:15, :31: to the rows after
+    v = max(v, dpp_from<0x143>(v));
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+template <int CTRL>
+__device__ static inline float dpp_add(float v) {
+    return v + __builtin_bit_cast(float, dpp_from<CTRL>(__builtin_bit_cast(uint32_t, v)));
+}
+__device__ static inline float wave_sum(float v) {
+    v = dpp_add<0x111>(v);
+    v = dpp_add<0x112>(v);
+    v = dpp_add<0x114>(v);
+    v = dpp_add<0x118>(v);
+    // (lanes that a broadcast does not reach add zero; lane 63 has the whole sum)
+    v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x142, 0xa, 0xf, false));
+    v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x143, 0xc, 0xf, false));
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
+
+// Bits whose order as unsigned numbers is that of the values; 0 for what cannot be
+// chosen (-inf, NaN).  -0 counts as +0.
+__device__ static inline uint32_t order_bits(float x) {
+    if (!(x > -INFINITY)) return 0;
+    const uint32_t b = __builtin_bit_cast(uint32_t, x + 0.0f);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ static inline float from_order_bits(uint32_t k) {
+    return __builtin_bit_cast(float, k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+
+template <int XT>
+__device__ static inline float load_logit(const void *x, int64_t i) {
+    if constexpr (XT == OUT_F32) return ((const float *)x)[i];
+    else return decode16(((const uint16_t *)x)[i], XT == OUT_F16);
+}
+
+// One wave's token: V logits to a lane, expert 64 v + lane.
+template <int XT, int V>
+__device__ static inline void load_row(const RouteArgs &p, int64_t t, int lane, float (&x)[V]) {
+    const bool in = t < p.T && (!p.mask || p.mask[t]);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int e = 64 * v + lane;
+        x[v] = in && e < p.E ? load_logit<XT>(p.x, t * p.ld + e) : -INFINITY;
+    }
+}
+
+constexpr int ROUTE_WAVES = 16, ROUTE_THREADS = 64 * ROUTE_WAVES;
+
+struct alignas(16) RouteLds {
+    int32_t before[1024], total[1024];  // slots of an expert before this workgroup's, and in all
+    int32_t scan[2][ROUTE_WAVES];
+    float part[ROUTE_THREADS];
+    double z[ROUTE_WAVES];
+    int32_t n[ROUTE_WAVES];
+};
+
+// Threads over E experts in `parts` parts: the experts take the least power of two from 64.
+__device__ static inline int route_width(int E) { return E <= 64 ? 64 : 1 << (32 - __builtin_clz(E - 1)); }
+
+// Slots before workgroup b's, and in all, of every expert.
+__device__ static inline void add_counts(const RouteArgs &p, int b, RouteLds &l) {
+    const int tid = threadIdx.x, es = route_width(p.E), e = tid & (es - 1), parts = ROUTE_THREADS / es;
+    l.before[tid] = 0;
+    l.total[tid] = 0;
+    __syncthreads();
+    if (e < p.E) {
+        int before = 0, total = 0;
+#pragma unroll 8
+        for (int i = tid / es; i < p.blocks; i += parts) {
+            const int n = p.hist[(int64_t)i * p.E + e];
+            total += n;
+            before += i < b ? n : 0;
+        }
+        if (before) atomicAdd(&l.before[e], before);
+        if (total) atomicAdd(&l.total[e], total);
+    }
+    __syncthreads();
+}
+
+// The sum of v over the threads before this one, and over all of them.
+__device__ static inline int scan_threads(int v, int32_t *scan, int &all) {
+    const int lane = lane_id(), wave = wave_id(), upto = wave_scan_add(v, lane);
+    if (lane == 63) scan[wave] = upto;
+    __syncthreads();
+    int start = upto - v;
+    all = 0;
+#pragma unroll
+    for (int w = 0; w < ROUTE_WAVES; ++w) {
+        const int n = scan[w];
+        start += w < wave ? n : 0;
+        all += n;
+    }
+    return start;
+}
+
+// Counts, offsets and losses: one workgroup, after add_counts.
+__device__ static inline void write_table(const RouteArgs &p, RouteLds &l) {
+    const int tid = threadIdx.x, lane = lane_id(), wave = wave_id();
+    int all;
+    const int start = scan_threads(l.total[tid], l.scan[0], all);
+    if (tid < p.E) {
+        p.counts[tid] = l.total[tid];
+        p.offsets[tid] = start;
+    }
+    const int es = route_width(p.E), e = tid & (es - 1), parts = ROUTE_THREADS / es;
+    float sum = 0.0f;
+    if (e < p.E) {
+#pragma unroll 8
+        for (int i = tid / es; i < p.blocks; i += parts) sum += p.psum[(int64_t)i * p.E + e];
+    }
+    l.part[tid] = sum;
+    double z = 0.0;
+    int n = 0;
+    for (int i = tid; i < p.blocks; i += ROUTE_THREADS) {
+        z += p.zsum[i];
+        n += p.tokens[i];
+    }
+#pragma unroll
+    for (int d = 32; d; d >>= 1) z += __shfl_xor(z, d, 64);
+    n = __builtin_amdgcn_readlane(wave_scan_add(n, lane), 63);
+    if (lane == 0) {
+        l.z[wave] = z;
+        l.n[wave] = n;
+    }
+    __syncthreads();
+    double v = 0.0;  // count_e * (sum of p_e)
+    if (tid < p.E) {
+        for (int i = 0; i < parts; ++i) v += (double)l.part[i * es + tid];
+        v *= (double)l.total[tid];
+    }
+    __syncthreads();
+    double *const w = (double *)l.part;
+#pragma unroll
+    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d, 64);
+    if (lane == 0) w[wave] = v;
+    __syncthreads();
+    if (tid == 0) {
+        double b = 0.0, zs = 0.0;
+        int tokens = 0;
+        for (int i = 0; i < ROUTE_WAVES; ++i) {
+            b += w[i];
+            zs += l.z[i];
+            tokens += l.n[i];
+        }
+        const double per = 1.0 / (double)max(tokens, 1);
+        p.offsets[p.E] = all;
+        p.loss[0] = (float)((double)p.E * b * per / (double)max(all, 1));
+        p.loss[1] = (float)(zs * per);
+        p.loss[2] = (float)tokens;
+        p.loss[3] = (float)all;
+    }
+}
+
+// Workgroup b's slots find their places (after add_counts).  wc: a row of E + 1 words
+// to each wave.
+__device__ static inline void place_slots(const RouteArgs &p, int b, RouteLds &l, int32_t *wc) {
+    const int tid = threadIdx.x, lane = lane_id(), wave = wave_id(), E1 = p.E + 1;
+    const int64_t t0 = min(p.T, (int64_t)b * p.rows), t1 = min(p.T, t0 + p.rows);
+    const int first = (int)(t0 * p.k), slots = (int)((t1 - t0) * p.k);
+    // a wave takes a run of the slots; its counts
+    const int run = ((slots + ROUTE_WAVES - 1) / ROUTE_WAVES + 63) / 64 * 64;
+    const int s0 = min(slots, wave * run), s1 = min(slots, s0 + run);
+    for (int i = lane; i < E1; i += 64) wc[wave * E1 + i] = 0;
+    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+    for (int i = s0 + lane; i < s1; i += 64) {
+        const int x = p.experts[first + i];
+        atomicAdd(&wc[wave * E1 + (x < 0 ? p.E : x)], 1);
+    }
+    int all, routed;  // slots with an expert, in all and before this workgroup
+    const int start = scan_threads(l.total[tid], l.scan[0], all);
+    scan_threads(l.before[tid], l.scan[1], routed);
+    __syncthreads();
+    for (int x = tid; x < E1; x += ROUTE_THREADS) {  // (a second turn only for x = E = 1024)
+        // the slots without an expert come behind all others
+        int at = x < p.E ? start + l.before[x] : all + first - routed;
+        for (int w = 0; w < ROUTE_WAVES; ++w) {
+            const int n = wc[w * E1 + x];
+            wc[w * E1 + x] = at;
+            at += n;
+        }
+    }
+    __syncthreads();
+    const int bits = 32 - __builtin_clz(p.E);  // of 0 .. E
+    for (int i = s0; i < s1; i += 64) {
+        const bool in = i + lane < s1;
+        int x = in ? p.experts[first + i + lane] : 0;
+        x = x < 0 ? p.E : x;
+        uint64_t same = __ballot(in);
+        for (int k = 0; k < bits; ++k) {
+            const uint64_t one = __ballot((x >> k) & 1);
+            same &= (x >> k) & 1 ? one : ~one;
+        }
+        const int rank = __popcll(same & ((1ull << lane) - 1));
+        if (in) {
+            const int at = wc[wave * E1 + x] + rank;
+            p.order[at] = first + i + lane;
+            p.place[first + i + lane] = at;
+        }
+        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+        if (in && rank == 0) wc[wave * E1 + x] += __popcll(same);
+        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+    }
+}
+
+// One token: its k experts and weights, to the lanes 0 .. k - 1 (e_mine, w_mine), its
+// lse, and its probabilities in x.
+template <int V>
+__device__ static inline void choose_token(const RouteArgs &p, int lane, float (&x)[V], int &e_mine, float &w_mine,
+                                           float &lse) {
+    uint32_t key[V];
+    uint32_t mine = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        key[v] = order_bits(x[v]);
+        mine = max(mine, key[v]);
+    }
+    uint32_t best = wave_max(mine);
+    const float top = best ? from_order_bits(best) : 0.0f;
+    float sum = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        x[v] = expf(x[v] - top);
+        sum += x[v];
+    }
+    sum = wave_sum(sum);
+    // no expert: p = 0, unless a NaN among the logits has to show
+    lse = sum == 0.0f ? INFINITY : top + logf(sum);
+    const float per = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v] *= per;
+    e_mine = -1;
+    uint32_t k_mine = 0;
+    for (int j = 0; j < p.k; ++j) {
+        if (j) {
+            mine = 0;
+#pragma unroll
+            for (int v = 0; v < V; ++v) mine = max(mine, key[v]);
+            best = wave_max(mine);
+        }
+        if (best == 0) break;
+        int e = -1;
+#pragma unroll
+        for (int v = V - 1; v >= 0; --v) {
+            const uint64_t has = __ballot(key[v] == best);
+            if (has) e = 64 * v + __ffsll((unsigned long long)has) - 1;
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (64 * v + lane == e) key[v] = 0;
+        if (lane == j) {
+            e_mine = e;
+            k_mine = best;
+        }
+    }
+    const float u = e_mine >= 0 ? expf(from_order_bits(k_mine) - top) : 0.0f;
+    w_mine = u * per;
+    if (p.normalize) {
+        const float s = wave_sum(lane < p.k ? u : 0.0f);
+        w_mine = s == 0.0f ? 0.0f : u / s;
+    }
+    // a token whose softmax is no number has no weights that are
+    if (sum != sum && e_mine >= 0) w_mine = sum;
+}
+
+template <int XT, int V>
+__global__ __launch_bounds__(ROUTE_THREADS) void route_choose(const RouteArgs p) {
+    __shared__ RouteLds l;
+    __shared__ int32_t words[ROUTE_WAVES * (64 * V + 1)];
+    const int tid = threadIdx.x, lane = lane_id(), wave = wave_id(), b = workgroup_id();
+    if (b >= p.blocks) return;
+    l.total[tid] = 0;
+    __syncthreads();
+    const int64_t t0 = (int64_t)b * p.rows, t1 = min(p.T, t0 + p.rows);
+    float ps[V] = {}, x[V], next[V];
+    double zs = 0.0;
+    int n = 0;
+    load_row<XT, V>(p, t0 + wave < t1 ? t0 + wave : p.T, lane, next);
+    for (int64_t t = t0 + wave; t < t1; t += ROUTE_WAVES) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[v] = next[v];
+        load_row<XT, V>(p, t + ROUTE_WAVES < t1 ? t + ROUTE_WAVES : p.T, lane, next);
+        int e;
+        float w, lse;
+        choose_token<V>(p, lane, x, e, w, lse);
+        if (lane < p.k) {
+            p.experts[t * p.k + lane] = e;
+            p.weights[t * p.k + lane] = w;
+            if (e >= 0) atomicAdd(&l.total[e], 1);
+        }
+        if (lane == 0) p.lse[t] = lse;
+#pragma unroll
+        for (int v = 0; v < V; ++v) ps[v] += x[v];
+        if (lse != INFINITY) {
+            zs += (double)lse * (double)lse;
+            ++n;
+        }
+    }
+    float *const wp = (float *)words;
+#pragma unroll
+    for (int v = 0; v < V; ++v) wp[wave * 64 * V + 64 * v + lane] = ps[v];
+    if (lane == 0) {
+        l.z[wave] = zs;
+        l.n[wave] = n;
+    }
+    __syncthreads();
+    if (tid < p.E) {
+        float s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < ROUTE_WAVES; ++w) s += wp[w * 64 * V + tid];
+        p.psum[(int64_t)b * p.E + tid] = s;
+        p.hist[(int64_t)b * p.E + tid] = l.total[tid];
+    }
+    if (tid == 0) {
+        for (int w = 1; w < ROUTE_WAVES; ++w) {
+            zs += l.z[w];
+            n += l.n[w];
+        }
+        p.zsum[b] = zs;
+        p.tokens[b] = n;
+    }
+    if (p.blocks > 1) return;
+    __threadfence_block();
+    __syncthreads();
+    add_counts(p, 0, l);
+    place_slots(p, 0, l, words);
+    __syncthreads();
+    write_table(p, l);
+}
+
+// Workgroups 0 .. blocks - 1 place the slots, the last one writes the table.
+template <int V>
+__global__ __launch_bounds__(ROUTE_THREADS) void route_place(const RouteArgs p) {
+    __shared__ RouteLds l;
+    __shared__ int32_t words[ROUTE_WAVES * (64 * V + 1)];
+    const int b = workgroup_id();
+    if (b > p.blocks) return;
+    add_counts(p, b, l);
+    if (b < p.blocks) place_slots(p, b, l, words);
+    else write_table(p, l);
+}
+
+struct RouteGradArgs {
+    const void *x;
+    void *dx;
+    int64_t T, ld, ldd;
+    int E, k, normalize;
+    const int32_t *experts;
+    const float *weights, *lse;
+    const int32_t *counts;
+    const float *loss;       // of the forward call: [2] tokens that count, [3] slots
+    const float *dw;         // T x k, or NULL
+    float balance, z;        // gradients in the two losses
+};
+
+// One wave to a token, four waves to a workgroup, a run of tokens to each wave.
+template <int XT, int V>
+__global__ __launch_bounds__(256) void route_grad(const RouteGradArgs p) {
+    const int lane = lane_id();
+    const int64_t waves = (int64_t)gridDim.x * 4;
+    const float n = fmaxf(p.loss[2], 1.0f), per = p.balance * (float)p.E / n / fmaxf(p.loss[3], 1.0f);
+    const float zn = 2.0f * p.z / n;
+    float g[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) g[v] = 64 * v + lane < p.E ? per * (float)p.counts[64 * v + lane] : 0.0f;
+    for (int64_t t = (int64_t)blockIdx.x * 4 + wave_id(); t < p.T; t += waves) {
+        float x[V], d[V];
+        const float lse = p.lse[t];
+        float pg = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int e = 64 * v + lane;
+            x[v] = e < p.E ? load_logit<XT>(p.x, t * p.ld + e) : -INFINITY;
+            // lse = +inf: a token that does not count, whatever its logits hold
+            x[v] = lse == INFINITY ? 0.0f : expf(x[v] - lse);
+            pg += x[v] * g[v];
+        }
+        pg = wave_sum(pg);
+        const float zl = lse == INFINITY ? 0.0f : zn * lse;
+        int e_mine = -1;
+        float w = 0.0f, back = 0.0f;
+        if (p.dw && lane < p.k) {
+            e_mine = p.experts[t * p.k + lane];
+            if (e_mine >= 0) {
+                w = p.weights[t * p.k + lane];
+                back = w * p.dw[t * p.k + lane];
+            }
+        }
+        const float all = wave_sum(back);
+        if (p.normalize) back -= w * all;
+        const float less = p.normalize ? 0.0f : all;
+#pragma unroll
+        for (int v = 0; v < V; ++v) d[v] = x[v] * ((g[v] - pg) + (zl - less));
+        if (p.dw)
+            for (int j = 0; j < p.k; ++j) {
+                const int e = __builtin_amdgcn_readlane(e_mine, j);
+                const float add = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, back), j));
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    if (64 * v + lane == e) d[v] += add;
+            }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int e = 64 * v + lane;
+            if (e >= p.E) continue;
+            if constexpr (XT == OUT_F32) ((float *)p.dx)[t * p.ldd + e] = d[v];
+            else ((uint16_t *)p.dx)[t * p.ldd + e] = encode16(d[v], XT == OUT_F16);
+        }
+    }
+}
+
+}  // namespace dmp

@@ -1,0 +1,92 @@
+// route_api.hip -- the entry points of the experts' router (declared in
+// include/dmp_gemm.h): argument checks and launches.
+#include <hip/hip_runtime.h>
+
+#include "../../include/dmp_gemm.h"
+#include "handle.hpp"
+#include "route.hpp"
+#include "route_plan.hpp"
+
+using namespace dmp;
+using namespace dmp::plan;
+
+namespace {
+
+template <int XT, int V>
+int launch_route(const RouteArgs &a, hipStream_t s) {
+    hipLaunchKernelGGL((route_choose<XT, V>), dim3((unsigned)a.blocks), dim3(ROUTE_THREADS), 0, s, a);
+    if (a.blocks > 1)
+        hipLaunchKernelGGL((route_place<V>), dim3((unsigned)a.blocks + 1), dim3(ROUTE_THREADS), 0, s, a);
+    return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
+}
+
+template <int XT, int V>
+int launch_grad(const RouteGradArgs &a, int num_cus, hipStream_t s) {
+    // 32 waves to a CU at most; with fewer tokens one to a wave
+    const int64_t grid = std::min<int64_t>(cdiv(a.T, 4), 8 * (int64_t)num_cus);
+    hipLaunchKernelGGL((route_grad<XT, V>), dim3((unsigned)grid), dim3(256), 0, s, a);
+    return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
+}
+
+// f(type, logits to a lane) for a call's type of logits and number of experts
+template <int XT, class F>
+int by_width(int64_t E, F f) {
+    const std::integral_constant<int, XT> x;
+    if (E <= 64) return f(x, std::integral_constant<int, 1>());
+    if (E <= 128) return f(x, std::integral_constant<int, 2>());
+    if (E <= 256) return f(x, std::integral_constant<int, 4>());
+    if (E <= 512) return f(x, std::integral_constant<int, 8>());
+    return f(x, std::integral_constant<int, 16>());
+}
+template <class F>
+int by_type(int x_type, int64_t E, F f) {
+    if (x_type == GEMM_OUT_F32) return by_width<OUT_F32>(E, f);
+    if (x_type == GEMM_OUT_F16) return by_width<OUT_F16>(E, f);
+    return by_width<OUT_BF16>(E, f);
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t gemm_route_work(gemm_handle_t h, int64_t T, int64_t E) {
+    if (!h || T < 0 || T > SIZE_MAX_1 || E < 1 || E > ROUTE_E_MAX) return -1;
+    return route_work(T, E, h->num_cus);
+}
+
+int gemm_route(gemm_handle_t h, const void *logits, int x_type, int64_t T, int64_t E, int64_t ld, int64_t k,
+               const uint8_t *mask, unsigned flags, const gemm_route_t *r, void *work, void *stream) {
+    const int rc = validate_route(h, logits, x_type, T, E, ld, k, flags, r, work);
+    if (rc != GEMM_OK) return rc;
+    RouteArgs a{};
+    a.x = logits; a.mask = mask;
+    a.T = T; a.ld = ld; a.E = (int)E; a.k = (int)k;
+    a.normalize = (flags & GEMM_ROUTE_NORMALIZE) != 0;
+    route_split(T, h->num_cus, a.rows, a.blocks);
+    a.experts = r->experts; a.weights = r->weights; a.lse = r->lse;
+    a.counts = r->counts; a.offsets = r->offsets; a.order = r->order; a.place = r->place;
+    a.loss = r->loss;
+    a.zsum = (double *)work;
+    a.hist = (int32_t *)(a.zsum + a.blocks);
+    a.psum = (float *)a.hist + a.blocks * E;
+    a.tokens = (int32_t *)a.psum + a.blocks * E;
+    hipStream_t s = (hipStream_t)stream;
+    return by_type(x_type, E, [&](auto xt, auto v) { return launch_route<xt.value, v.value>(a, s); });
+}
+
+int gemm_route_grad(gemm_handle_t h, const void *logits, int x_type, int64_t T, int64_t E, int64_t ld, int64_t k,
+                    unsigned flags, const gemm_route_t *r, const float *dweights, float balance, float z,
+                    void *dlogits, int64_t ldd, void *stream) {
+    const int rc = validate_route_grad(h, logits, x_type, T, E, ld, k, flags, r, dweights, dlogits, ldd);
+    if (rc != GEMM_OK || T == 0) return rc;
+    RouteGradArgs a{};
+    a.x = logits; a.dx = dlogits;
+    a.T = T; a.ld = ld; a.ldd = ldd; a.E = (int)E; a.k = (int)k;
+    a.normalize = (flags & GEMM_ROUTE_NORMALIZE) != 0;
+    a.experts = r->experts; a.weights = r->weights; a.lse = r->lse; a.counts = r->counts; a.loss = r->loss;
+    a.dw = dweights; a.balance = balance; a.z = z;
+    hipStream_t s = (hipStream_t)stream;
+    return by_type(x_type, E, [&](auto xt, auto v) { return launch_grad<xt.value, v.value>(a, h->num_cus, s); });
+}
+
+}  // extern "C"

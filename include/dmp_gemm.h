@@ -362,6 +362,65 @@ int gemm_run_scaled8(gemm_handle_t h, const gemm_q8_t *A, const gemm_q8_t *B, co
                      int64_t ldc, unsigned flags, float alpha, float beta, int c_type, int d_type,
                      void *stream);
 
+/*
+ * The router of the experts: from logits (T tokens x E experts, x_type
+ * GEMM_OUT_F32, _F16 or _BF16, rows ld >= E apart) to the groups of rows that the
+ * grouped products take, with the balance loss.  For every token, in fp32, with
+ * m its largest logit, lse = m + log(sum of exp(x - m)) and p = exp(x - lse):
+ *   experts  the k experts of largest logit, largest first, the lower number
+ *            first among equals.  An expert with a logit of -inf (or NaN) is
+ *            not available; where fewer than k are, the slots left over hold -1;
+ *   weights  p of the chosen experts, or with GEMM_ROUTE_NORMALIZE the softmax
+ *            over the chosen ones alone; 0 for a slot without an expert;
+ *   lse      as above; +inf for a token that does not count.
+ * A token does not count if its mask byte is zero (mask may be NULL: all
+ * count) or none of its experts is available; all its slots are -1.  A NaN or
+ * +inf among a token's logits makes its weights, its lse and the losses NaN.
+ * Slot t * k + j is choice j of token t.  Over all tokens:
+ *   counts   slots of each expert (E), offsets their exclusive sums (E + 1):
+ *            int32 row numbers as the grouped products take them;
+ *   order    the slots sorted by expert, slots of one expert in ascending order,
+ *            slots without an expert (also ascending) behind the last: row i of the
+ *            grouped products' operand is the token order[i] / k;
+ *   place    the inverse: order[place[s]] == s;
+ *   loss     4 floats: the balance loss E * sum over e of (counts[e] / slots) *
+ *            (mean of p_e over the tokens that count), the mean of lse^2 over them, their
+ *            number, and the number of slots with an expert.
+ * Every result is the same in every run (no sum depends on the order of
+ * arrival).  1 <= k <= min(E, 64), E <= 1024, T * k below 2^31 - 1024.
+ * work: device memory of gemm_route_work(h, T, E) bytes (-1 for sizes that are
+ * refused), 8-byte aligned, not shared with a call that can run at the same
+ * time.  Nothing is allocated, and the host reads nothing.  T == 0 writes
+ * zero counts, offsets and losses.
+ */
+enum { GEMM_ROUTE_NORMALIZE = 32u };
+typedef struct {
+    int32_t *experts; /* T x k */
+    float *weights;   /* T x k */
+    float *lse;       /* T */
+    int32_t *counts;  /* E */
+    int32_t *offsets; /* E + 1 */
+    int32_t *order;   /* T * k */
+    int32_t *place;   /* T * k */
+    float *loss;      /* 4 */
+} gemm_route_t;
+int64_t gemm_route_work(gemm_handle_t h, int64_t T, int64_t E);
+int gemm_route(gemm_handle_t h, const void *logits, int x_type, int64_t T, int64_t E, int64_t ld,
+               int64_t k, const uint8_t *mask, unsigned flags, const gemm_route_t *r, void *work,
+               void *stream);
+
+/*
+ * The gradient of sum(dweights * weights) + balance * loss[0] + z * loss[1] in
+ * the logits, from the same logits and what gemm_route wrote for them (flags
+ * as there); the counts are taken as constants.  dweights: T x k floats, or
+ * NULL for none; those of slots without an expert are not used.  dlogits has
+ * the logits' type, rows ldd >= E apart, and may be the logits themselves
+ * (with the same ld).  Tokens that do not count get zeros.
+ */
+int gemm_route_grad(gemm_handle_t h, const void *logits, int x_type, int64_t T, int64_t E, int64_t ld,
+                    int64_t k, unsigned flags, const gemm_route_t *r, const float *dweights,
+                    float balance, float z, void *dlogits, int64_t ldd, void *stream);
+
 /* Release the handle's workspace (after synchronising its device) and the handle. */
 int gemm_destroy(gemm_handle_t h);
 
