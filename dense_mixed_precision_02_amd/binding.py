@@ -15,9 +15,10 @@ GEMM_OK = 0
 
 EXPORTED_SYMBOLS = ("gemm_create", "gemm_run", "gemm_run_ex", "gemm_run_noalloc", "gemm_prune24",
                     "gemm_run_sparse24", "gemm_run_grouped", "gemm_run_grouped_wgrad", "gemm_quant8",
-                    "gemm_run_scaled8", "gemm_route_work", "gemm_route", "gemm_route_grad", "gemm_destroy", "gemm_status_string", "gemm_plan")
+                    "gemm_run_scaled8", "gemm_wgrad8_work", "gemm_run_wgrad8", "gemm_route_work", "gemm_route", "gemm_route_grad", "gemm_destroy", "gemm_status_string", "gemm_plan")
 GEMM_OFFSETS_I32 = 16
 GEMM_ROUTE_NORMALIZE = 32
+GEMM_SCALE_POW2 = 64
 GEMM_E4M3, GEMM_E5M2 = 0, 1
 GEMM_ERR_SCRATCH = 5
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -92,6 +93,11 @@ def load_library():
         lib.gemm_run_scaled8.restype = ci
         lib.gemm_run_scaled8.argtypes = [vp, ctypes.POINTER(Q8Operand), ctypes.POINTER(Q8Operand), vp, vp,
                                          vp, i64, i64, i64, i64, i64, cu, cf, cf, ci, ci, vp]
+        lib.gemm_wgrad8_work.restype = i64
+        lib.gemm_wgrad8_work.argtypes = [vp, i64, i64, i64, i64]
+        lib.gemm_run_wgrad8.restype = ci
+        lib.gemm_run_wgrad8.argtypes = [vp, ctypes.POINTER(Q8Operand), vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, ci,
+                                        cu, cf, cf, ci, ci, vp, vp]
         lib.gemm_route_work.restype = i64
         lib.gemm_route_work.argtypes = [vp, i64, i64]
         lib.gemm_route.restype = ci
@@ -207,6 +213,16 @@ class Handle:
         return load_library().gemm_run_scaled8(self.ptr, ctypes.byref(A), ctypes.byref(B), C, D, offsets,
                                                groups, M, N, K, ldc, flags, alpha, beta, c_type, d_type,
                                                stream)
+
+    def wgrad8_work(self, groups, M, N, K) -> int:
+        """Bytes of scratch that run_wgrad8() needs (-1: sizes that are refused)."""
+        return load_library().gemm_wgrad8_work(self.ptr, groups, M, N, K)
+
+    def run_wgrad8(self, X: Q8Operand, Y, C, D, offsets, groups, M, N, K, ldy, ldc, dtype, flags=0, alpha=1.0, beta=0.0,
+                   c_type=GEMM_OUT_F32, d_type=GEMM_OUT_F32, work=0, stream=0) -> int:
+        """Raw-pointer call of gemm_run_wgrad8; returns the status code."""
+        return load_library().gemm_run_wgrad8(self.ptr, ctypes.byref(X), Y, C, D, offsets, groups, M, N, K, ldy, ldc,
+                                              dtype, flags, alpha, beta, c_type, d_type, work, stream)
 
     def route_work(self, T, E) -> int:
         """Bytes of scratch that route() needs (-1: sizes that are refused)."""
@@ -664,13 +680,17 @@ class Scaled8:
         return Scaled8, (self.q, self.scale, self.block, self.K)
 
 
-def quant8(X, block: int = 1, dtype=None, handle: Handle | None = None) -> Scaled8:
+def quant8(X, block: int = 1, dtype=None, handle: Handle | None = None, pow2: bool = False) -> Scaled8:
     """Quantize X ((batch,) M, K; float32, float16 or bfloat16; row-major or a transposed
     view) to 8-bit floats (``dtype``: torch.float8_e4m3fn, the default, or float8_e5m2)
     with a scale for every block of 128 consecutive k of one row (block = 1: activations)
     or of 128 rows (block = 128: weights), on the current stream.  The result is
     K-contiguous whatever X's layout: the operand B of gemm_scaled8 for weights stored
-    (K, N) is quant8(W.t(), block=128)."""
+    (K, N) is quant8(W.t(), block=128).
+
+    ``pow2``: scales that are powers of two, so that every q * scale is a bfloat16 number
+    (from a float16 X a float16 one) and nothing is rounded again where it is used: the
+    form in which activations are kept for the backward pass (gemm_wgrad8)."""
     import torch
     dtype = torch.float8_e4m3fn if dtype is None else dtype
     code = _f8_code(dtype)
@@ -693,8 +713,8 @@ def quant8(X, block: int = 1, dtype=None, handle: Handle | None = None) -> Scale
     scale = torch.empty((*lead, kb, mb), dtype=torch.float32, device=X.device)
     at = q.data_ptr()
     rc = _on(X.device, handle, lambda h, stream: h.quant8(
-        X.data_ptr(), M, K, ldx, x_code, GEMM_A_COLMAJOR if col else 0, batch, block, code, at, scale.data_ptr(),
-        stream))
+        X.data_ptr(), M, K, ldx, x_code, (GEMM_A_COLMAJOR if col else 0) | (GEMM_SCALE_POW2 if pow2 else 0), batch, block,
+        code, at, scale.data_ptr(), stream))
     if rc != GEMM_OK:
         raise GemmError(rc, "gemm_quant8")
     r = Scaled8.__new__(Scaled8)  # what the constructor would check holds
@@ -732,6 +752,45 @@ def gemm_scaled8(A: Scaled8, B: Scaled8, offsets=None, C=None, out=None, alpha: 
         A.K, ldc, flags, alpha, beta, c_code, d_code, stream))
     if rc != GEMM_OK:
         raise GemmError(rc, "gemm_run_scaled8")
+    return out
+
+
+def gemm_wgrad8(X: Scaled8, Y, offsets=None, C=None, out=None, alpha: float = 1.0, beta: float = 1.0, out_dtype=None,
+                handle: Handle | None = None):
+    """D = alpha * X^T @ Y + beta * C of an activation X that was kept in 8 bits, on the
+    current stream: the weight gradient of a layer whose input was saved as
+    X = quant8(x, pow2=True) and whose output has the gradient Y.
+
+    X: (T, M), blocks of one row;  Y: (T, N) float16 / bfloat16, row-major;  D: (M, N).
+    With ``offsets`` (see gemm_grouped) every group has its own gradient: D (groups, M, N).
+    C, ``out`` and ``out_dtype`` (default float32) as in gemm_grouped_wgrad.  X's values are
+    rounded to Y's type, which is exact where pow2 made them (of the type's normal numbers)."""
+    x = X.operand
+    dt = {GEMM_OUT_F16: GEMM_F16, GEMM_OUT_BF16: GEMM_BF16}.get(_out_code(Y.dtype))
+    if dt is None:
+        raise TypeError("Y must be float16 or bfloat16")
+    device = X.q.device
+    if X.block != 1 or X.groups is not None:
+        raise ValueError("X must be (T, M) with blocks of one row")
+    ldy = _rows_of(Y, "Y")
+    if Y.device != device or Y.shape[0] != X.rows:
+        raise ValueError("X and Y must have the same rows, on the same GPU")
+    groups, flags = (1, 0) if offsets is None else _check_offsets(offsets, device)
+    T, M, N = X.rows, X.K, Y.shape[1]
+    shape, name = ((M, N), "(M, N)") if offsets is None else ((groups, M, N), "(groups, M, N)")
+    c, c_code, out, d_code, ldc, beta = _output(C, out, shape, out_dtype, beta, device, name)
+
+    def call(h, stream):
+        import torch
+        need = h.wgrad8_work(groups, M, N, T)
+        work = torch.empty(need, dtype=torch.uint8, device=device) if need > 0 else None
+        return h.run_wgrad8(x, Y.data_ptr(), c, out.data_ptr(), offsets.data_ptr() if offsets is not None else 0, groups,
+                            M, N, T, ldy, ldc, dt, flags, alpha, beta, c_code, d_code,
+                            work.data_ptr() if work is not None else 0, stream)
+
+    rc = _on(device, handle, call)
+    if rc != GEMM_OK:
+        raise GemmError(rc, "gemm_run_wgrad8")
     return out
 
 

@@ -11,6 +11,11 @@
 // patterns of |x|, whose order is that of the values with infinity and then
 // NaN above them all.
 //
+// pow2: scale = the smallest power of two for which a / scale <= top, and q = round8(x / scale).
+// Then x / scale and q * scale are exact, and q * scale is a bfloat16 number (from an X of
+// fp16 an fp16 one).  X is first clamped to the largest number of its type with no more than the
+// 8-bit type's digits, at most half a step away: rounding up from there would leave its type.
+//
 // Output: Q[b][i][k], rows of Kp = 16 ceil(K / 16) bytes, zeros past K (the
 // products read whole 16-byte granules), and scale[b][k / 128][i / block]: for
 // one k-block the factors of neighbouring rows lie next to each other, which is
@@ -35,11 +40,16 @@ struct Quant8Args {
     int64_t MB;                 // row blocks (rows, or ceil(M / 128))
     int64_t tiles_m;
     int batch;
+    int pow2;
 };
 
 template <int FMT> constexpr float F8_TOP = FMT == 0 ? 448.0f : 57344.0f;
 constexpr float QUANT8_LEAST = 0x1p-100f;
 constexpr uint32_t F32_INF_BITS = 0x7f800000u;
+// the type's largest value is 1.75 times 2 to this; the largest number of type XT with its digits
+template <int FMT> constexpr int F8_TOP_EXP = FMT == 0 ? 8 : 15;
+template <int XT, int FMT>
+constexpr float F8_IN_X = XT == OUT_F16 ? (FMT == 0 ? 61440.0f : 57344.0f) : (FMT == 0 ? 0x1.ep127f : 0x1.cp127f);
 
 // Sixteen consecutive elements as floats; n of them exist.  XT: OUT_F32, OUT_F16 or OUT_BF16.
 template <int XT>
@@ -77,15 +87,28 @@ __device__ static inline uint32_t abs_bits(float x) { return __builtin_bit_cast(
 // A block's scale and the factor its elements are multiplied by, from the bit
 // pattern of its largest magnitude; a factor of zero stands for "store zeros".
 template <int FMT>
-__device__ static inline void block_scale(uint32_t amax_bits, float &scale, float &factor) {
+__device__ static inline void block_scale(uint32_t amax_bits, int pow2, float &scale, float &factor) {
     if (amax_bits >= F32_INF_BITS) {
         scale = __builtin_bit_cast(float, 0x7fc00000u);
         factor = 0.0f;
         return;
     }
     const float a = fmaxf(__builtin_bit_cast(float, amax_bits), QUANT8_LEAST);
+    if (pow2) {  // a = 1.m * 2^(e - 127), e >= 27: scale and its inverse are normal numbers
+        const uint32_t bits = __builtin_bit_cast(uint32_t, a);
+        const uint32_t e = (bits >> 23) - F8_TOP_EXP<FMT> + ((bits & 0x7fffffu) > 0x600000u);
+        scale = __builtin_bit_cast(float, e << 23);
+        factor = __builtin_bit_cast(float, (254 - e) << 23);
+        return;
+    }
     scale = a / F8_TOP<FMT>;
     factor = F8_TOP<FMT> / a;
+}
+
+// An element on its way to 8 bits (after the block's maximum is taken).
+template <int XT, int FMT>
+__device__ static inline float in_range(float x, int pow2) {
+    return pow2 ? fminf(fmaxf(x, -F8_IN_X<XT, FMT>), F8_IN_X<XT, FMT>) : x;
 }
 
 // Four values times the factor, rounded to 8 bits, in one word.
@@ -136,10 +159,12 @@ __global__ __launch_bounds__(256) void quant8_rows(const Quant8Args p) {
 #pragma unroll
         for (int d = 1; d < 8; d <<= 1) am = max(am, (uint32_t)__shfl_xor((int)am, d, 64));
         float s, f;
-        block_scale<FMT>(am, s, f);
+        block_scale<FMT>(am, p.pow2, s, f);
         if ((lane & 7) == 0) sc[lane >> 3][wave * PER + t] = s;
         const int64_t i = m0 + wave * PER + t;
         if (i < p.M && k < p.Kp) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[t][e] = in_range<XT, FMT>(x[t][e], p.pow2);
             intx4 v;
 #pragma unroll
             for (int w = 0; w < 4; ++w)
@@ -206,17 +231,21 @@ __global__ __launch_bounds__(256) void quant8_tile(const Quant8Args p) {
     __syncthreads();
     float s, f[ROWS128 ? 1 : 16];
     if constexpr (ROWS128) {
-        block_scale<FMT>(max(max(am[0], am[1]), max(am[2], am[3])), s, f[0]);
+        block_scale<FMT>(max(max(am[0], am[1]), max(am[2], am[3])), p.pow2, s, f[0]);
         if (tid == 0) p.scale[(b * p.KB + kb) * p.MB + i0 / 128] = s;
     } else {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) block_scale<FMT>(am[16 * piece + e], s, f[e]);
+        for (int e = 0; e < 16; ++e) block_scale<FMT>(am[16 * piece + e], p.pow2, s, f[e]);
         if (tid < rows) {
             float unused;
-            block_scale<FMT>(am[tid], s, unused);
+            block_scale<FMT>(am[tid], p.pow2, s, unused);
             p.scale[(b * p.KB + kb) * p.MB + i0 + tid] = s;
         }
     }
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[t][e] = in_range<XT, FMT>(x[t][e], p.pow2);
     if constexpr (COL) {
 #pragma unroll
         for (int e = 0; e < 16; ++e)

@@ -174,6 +174,7 @@ int gemm_quant8(gemm_handle_t h, const void *X, int64_t M, int64_t K, int64_t ld
     if (rc != GEMM_OK || M == 0 || K == 0 || batch == 0) return rc;
     const bool col = flags & GEMM_A_COLMAJOR;
     Quant8Args a{};
+    a.pow2 = (flags & GEMM_SCALE_POW2) != 0;
     a.X = X; a.Q = (uint8_t *)Q; a.scale = scale;
     a.M = M; a.K = K; a.ldx = ldx; a.Kp = k16(K); a.sX = (col ? K : M) * ldx;
     a.KB = (int)cdiv(K, 128);

@@ -129,7 +129,7 @@ inline int validate_quant8(gemm_handle_t h, const void *X, int64_t M, int64_t K,
                            const void *scale) {
     if (!h || M < 0 || K < 0 || batch < 0 || batch > (1ll << 30) || M > SIZE_MAX_1 || K > SIZE_MAX_1)
         return GEMM_ERR_INVALID_ARG;
-    if (!float_out(x_type) || (flags & ~(unsigned)GEMM_A_COLMAJOR)) return GEMM_ERR_INVALID_ARG;
+    if (!float_out(x_type) || (flags & ~(unsigned)(GEMM_A_COLMAJOR | GEMM_SCALE_POW2))) return GEMM_ERR_INVALID_ARG;
     if ((block != 1 && block != 128) || (q_type != GEMM_E4M3 && q_type != GEMM_E5M2))
         return GEMM_ERR_INVALID_ARG;
     if (M == 0 || K == 0 || batch == 0) return GEMM_OK;

@@ -34,9 +34,9 @@ namespace dmp {
 
 // This lane's granules of one k-tile of an operand: chunks j = 0 .. CPW - 1, in the
 // places of Operand::issue.
-template <class DT, int R, int NW, bool KCONTIG, bool FAST>
+template <class DT, int R, int NW, bool KCONTIG, bool FAST, int PAD = 0>
 struct Staged {
-    using Op = Operand<DT, R, NW, KCONTIG>;
+    using Op = Operand<DT, R, NW, KCONTIG, PAD>;
     using elem = typename DT::elem;
     static constexpr int G = DT::G, CPW = Op::CPW, KT = Op::KT;
     Op op;

@@ -1,0 +1,89 @@
+// wgrad8_api.hip -- the entry point of the weight gradients from 8-bit checkpoints
+// (declared in include/dmp_gemm.h): argument checks, kernel choice and launches.
+#include <hip/hip_runtime.h>
+
+#include "../../include/dmp_gemm.h"
+#include "handle.hpp"
+#include "wgrad8.hpp"
+#include "wgrad8_plan.hpp"
+
+using namespace dmp;
+using namespace dmp::plan;
+
+namespace {
+
+template <class Args>
+int launch(void (*kernel)(Args), int64_t workgroups, int threads, hipStream_t s, const Args &a) {
+    GridShape g;
+    if (!grid_shape(workgroups, g)) return GEMM_ERR_INVALID_ARG;  // beyond one launch's grid
+    hipLaunchKernelGGL(kernel, dim3(g.x, g.y), dim3((unsigned)threads), 0, s, a);
+    return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
+}
+
+template <class DT, int FMT, int BM, int BN, int WM, int WN, bool FAST>
+int launch_tile(gemm_handle_t h, Wgrad8Args a, hipStream_t s) {
+    RaggedArgs &r = a.r;
+    r.tiles_m = (int)cdiv(r.M, BM);
+    r.tiles_n = (int)cdiv(r.N, BN);
+    const int64_t tiles = (int64_t)r.tiles_m * r.tiles_n;
+    // runs of tiles on an XCD: as many as it works on at a time, but every XCD gets some
+    r.run = (int)std::max<int64_t>(1, std::min<int64_t>(h->num_cus / 8 * (8 / (WM * WN)), cdiv(r.groups * tiles, 8)));
+    const int64_t units = cdiv(r.groups * cdiv(tiles, r.run), 8) * 8 * r.run;
+    if (units > 0x7fffffff) return GEMM_ERR_INVALID_ARG;
+    a.units = (int)units;
+    return launch(wgrad8_tile<DT, FMT, BM, BN, WM, WN, FAST>, units * a.splits, WM * WN * 64, s, a);
+}
+
+template <class DT, int FMT>
+int launch_wgrad8(gemm_handle_t h, bool large, bool fast, const Wgrad8Args &a, hipStream_t s) {
+    if (!fast) return launch_tile<DT, FMT, 64, 128, 1, 4, false>(h, a, s);
+    return large ? launch_tile<DT, FMT, 256, 256, 2, 4, true>(h, a, s) : launch_tile<DT, FMT, 64, 128, 1, 4, true>(h, a, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t gemm_wgrad8_work(gemm_handle_t h, int64_t groups, int64_t M, int64_t N, int64_t K) {
+    if (!h || !wgrad8_sizes_ok(groups, M, N, K)) return -1;
+    return wgrad8_work(h->num_cus, groups, M, N, K);
+}
+
+int gemm_run_wgrad8(gemm_handle_t h, const gemm_q8_t *X, const void *Y, const void *C, void *D, const void *offsets,
+                    int64_t groups, int64_t M, int64_t N, int64_t K, int64_t ldy, int64_t ldc, int dtype, unsigned flags,
+                    float alpha, float beta, int c_type, int d_type, void *work, void *stream) {
+    EpiParams ep;
+    ep.alpha = alpha; ep.beta = beta;
+    ep.c_type = c_type; ep.d_type = d_type;
+    ep.use_c = beta != 0.0f;
+    const int rc = validate_wgrad8(h, X, Y, C, D, offsets, groups, M, N, K, ldy, ldc, dtype, flags, ep);
+    if (rc != GEMM_OK || M == 0 || N == 0 || groups == 0) return rc;
+    Wgrad8Args a{};
+    a.splits = K > 0 ? wgrad8_splits(h->num_cus, groups, M, N, K) : 1;
+    if (a.splits > 1 && (!work || !aligned16(work))) return GEMM_ERR_INVALID_ARG;
+    RaggedArgs &r = a.r;
+    r.A = X->q; r.sa = X->scale; r.sa_row = X->scale_row; r.sa_k = X->scale_k; r.lda = X->ld;
+    r.B = Y; r.ldb = ldy; r.offsets = offsets;
+    r.M = M; r.N = N; r.K = K;
+    r.groups = (int)groups;
+    r.off32 = (flags & GEMM_OFFSETS_I32) != 0;
+    r.C = C; r.D = D; r.ldc = ldc; r.sC = M * ldc; r.ep = ep;
+    if (a.splits > 1) {
+        r.D = work; r.ldc = N; r.sC = M * N;
+        r.ep.alpha = 1.0f; r.ep.use_c = 0; r.ep.d_type = OUT_F32;
+        a.part = groups * M * N;
+    }
+    hipStream_t s = (hipStream_t)stream;
+    const bool large = wgrad8_large(h->num_cus, groups, M, N), fast = K > 0 && wgrad8_fast(Y, N, ldy);
+    const bool e4 = X->type == GEMM_E4M3;
+    int st;
+    if (dtype == GEMM_F16) st = e4 ? launch_wgrad8<F16, 0>(h, large, fast, a, s) : launch_wgrad8<F16, 1>(h, large, fast, a, s);
+    else st = e4 ? launch_wgrad8<BF16, 0>(h, large, fast, a, s) : launch_wgrad8<BF16, 1>(h, large, fast, a, s);
+    if (st != GEMM_OK || a.splits == 1) return st;
+    Wgrad8JoinArgs j{};
+    j.part = (const float *)work; j.C = C; j.D = D;
+    j.rows = groups * M; j.N = N; j.ldc = ldc; j.splits = a.splits; j.ep = ep;
+    return launch(wgrad8_join, cdiv(j.rows * cdiv(N, 4), 256), 256, s, j);
+}
+
+}  // extern "C"

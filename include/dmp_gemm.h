@@ -302,13 +302,20 @@ typedef enum { GEMM_E4M3 = 0, GEMM_E5M2 = 1 } gemm_f8_t;
  *
  *     scale = a / top,   q = round8(x * (top / a))   (to nearest even)
  *
- * so that x is about q * scale.  A block with an infinity or a NaN has the
+ * so that x is about q * scale.  With GEMM_SCALE_POW2 in flags the scale is
+ * instead the smallest power of two with a / scale <= top, and q = round8(x /
+ * scale): q * scale is then exact in fp32 and in bfloat16, the form for
+ * activations that are kept for the backward pass (gemm_run_wgrad8).  (X is
+ * first clamped to the largest number of its type that has no more digits than
+ * the 8-bit one, fp16: 61440, for e5m2 57344, so that q * scale is a number of
+ * its type.)  A block with an infinity or a NaN has the
  * scale NaN and zeros for q.  Output, always K-contiguous:
  *   Q:     batch x M x Kp bytes, Kp = 16 * ceil(K / 16), zeros past K; 16-byte
  *          aligned;
  *   scale: batch x ceil(K / 128) x ceil(M / block) floats.
  * K == 0 enqueues nothing.  X needs element alignment.
  */
+enum { GEMM_SCALE_POW2 = 64u };
 int gemm_quant8(gemm_handle_t h, const void *X, int64_t M, int64_t K, int64_t ldx, int x_type,
                 unsigned flags, int64_t batch, int block, int q_type, void *Q, float *scale,
                 void *stream);
@@ -361,6 +368,31 @@ int gemm_run_scaled8(gemm_handle_t h, const gemm_q8_t *A, const gemm_q8_t *B, co
                      void *D, const void *offsets, int64_t groups, int64_t M, int64_t N, int64_t K,
                      int64_t ldc, unsigned flags, float alpha, float beta, int c_type, int d_type,
                      void *stream);
+
+/*
+ * Weight gradients from 8-bit checkpoints of activations: D_g = cvt_D(alpha *
+ * X_g^T * Y_g + beta * C_g) for every group g, where X (K rows of M values) is
+ * an operand of 8-bit floats with blocks of one row by 128 columns (gemm_q8_t
+ * with rows for K rows and its "k" the M columns: gemm_quant8's output with
+ * block 1), and Y (K x N, row-major) has dtype GEMM_F16 or GEMM_BF16.  With
+ * offsets NULL (groups == 1) all K rows are one group.  Every value q * scale
+ * of X is rounded to Y's type (beyond its largest number: an infinity), which
+ * is exact for powers of two as scales as long as the value is a normal number
+ * of the type; products and sums are those of gemm_run_grouped_wgrad, which
+ * with such values for X gives the same within its error bound.  A NaN scale
+ * makes its columns NaN.  Everything else as there.
+ *
+ * work: gemm_wgrad8_work(h, groups, M, N, K) bytes of device memory (0: none
+ * needed, work may be NULL; -1: sizes that are refused), 16-byte aligned, for
+ * partial sums where the rows are split to fill the device; they are added in
+ * a fixed order.  It must not be shared with a call that can run at the same
+ * time.  Nothing is allocated.
+ */
+int64_t gemm_wgrad8_work(gemm_handle_t h, int64_t groups, int64_t M, int64_t N, int64_t K);
+int gemm_run_wgrad8(gemm_handle_t h, const gemm_q8_t *X, const void *Y, const void *C, void *D,
+                    const void *offsets, int64_t groups, int64_t M, int64_t N, int64_t K, int64_t ldy,
+                    int64_t ldc, int dtype, unsigned flags, float alpha, float beta, int c_type,
+                    int d_type, void *work, void *stream);
 
 /*
  * The router of the experts: from logits (T tokens x E experts, x_type
