@@ -15,10 +15,11 @@ GEMM_OK = 0
 
 EXPORTED_SYMBOLS = ("gemm_create", "gemm_run", "gemm_run_ex", "gemm_run_noalloc", "gemm_prune24",
                     "gemm_run_sparse24", "gemm_run_grouped", "gemm_run_grouped_wgrad", "gemm_quant8",
-                    "gemm_run_scaled8", "gemm_wgrad8_work", "gemm_run_wgrad8", "gemm_route_work", "gemm_route", "gemm_route_grad", "gemm_destroy", "gemm_status_string", "gemm_plan")
+                    "gemm_run_scaled8", "gemm_adapters_work", "gemm_run_adapters", "gemm_wgrad8_work", "gemm_run_wgrad8", "gemm_route_work", "gemm_route", "gemm_route_grad", "gemm_destroy", "gemm_status_string", "gemm_plan")
 GEMM_OFFSETS_I32 = 16
 GEMM_ROUTE_NORMALIZE = 32
 GEMM_SCALE_POW2 = 64
+GEMM_ADAPTER_A_COLMAJOR = 128
 GEMM_E4M3, GEMM_E5M2 = 0, 1
 GEMM_ERR_SCRATCH = 5
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -32,6 +33,12 @@ class Q8Operand(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("ld", ctypes.c_int64),
                 ("scale_row", ctypes.c_int64), ("scale_k", ctypes.c_int64), ("group", ctypes.c_int64),
                 ("scale_group", ctypes.c_int64), ("type", ctypes.c_int)]
+
+
+class AdapterOperands(ctypes.Structure):
+    """gemm_adapters_t: the adapters of gemm_run_adapters."""
+    _fields_ = [("A", ctypes.c_void_p), ("B", ctypes.c_void_p), ("ids", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("adapters", ctypes.c_int64), ("rank", ctypes.c_int64), ("lda", ctypes.c_int64), ("ldb", ctypes.c_int64)]
 
 
 class RouteTables(ctypes.Structure):
@@ -93,6 +100,11 @@ def load_library():
         lib.gemm_run_scaled8.restype = ci
         lib.gemm_run_scaled8.argtypes = [vp, ctypes.POINTER(Q8Operand), ctypes.POINTER(Q8Operand), vp, vp,
                                          vp, i64, i64, i64, i64, i64, cu, cf, cf, ci, ci, vp]
+        lib.gemm_adapters_work.restype = i64
+        lib.gemm_adapters_work.argtypes = [vp, i64, i64, ci]
+        lib.gemm_run_adapters.restype = ci
+        lib.gemm_run_adapters.argtypes = [vp, vp, vp, ctypes.POINTER(AdapterOperands), vp, vp, vp, i64, i64, i64, i64,
+                                          i64, i64, i64, ci, cu, cf, cf, ci, ci, vp, i64, vp, vp]
         lib.gemm_wgrad8_work.restype = i64
         lib.gemm_wgrad8_work.argtypes = [vp, i64, i64, i64, i64]
         lib.gemm_run_wgrad8.restype = ci
@@ -213,6 +225,18 @@ class Handle:
         return load_library().gemm_run_scaled8(self.ptr, ctypes.byref(A), ctypes.byref(B), C, D, offsets,
                                                groups, M, N, K, ldc, flags, alpha, beta, c_type, d_type,
                                                stream)
+
+    def adapters_work(self, M, rank, d_type) -> int:
+        """Bytes of scratch that run_adapters() needs (-1: sizes that are refused)."""
+        return load_library().gemm_adapters_work(self.ptr, M, rank, d_type)
+
+    def run_adapters(self, X, W, adapters: AdapterOperands, C, D, offsets, requests, M, N, K, ldx, ldw, ldc, dtype,
+                     flags=0, alpha=1.0, beta=0.0, c_type=GEMM_OUT_F32, d_type=GEMM_OUT_F32, hidden=0, ld_hidden=0,
+                     work=0, stream=0) -> int:
+        """Raw-pointer call of gemm_run_adapters; returns the status code."""
+        return load_library().gemm_run_adapters(self.ptr, X, W, ctypes.byref(adapters), C, D, offsets, requests, M, N, K,
+                                                ldx, ldw, ldc, dtype, flags, alpha, beta, c_type, d_type, hidden,
+                                                ld_hidden, work, stream)
 
     def wgrad8_work(self, groups, M, N, K) -> int:
         """Bytes of scratch that run_wgrad8() needs (-1: sizes that are refused)."""
@@ -752,6 +776,103 @@ def gemm_scaled8(A: Scaled8, B: Scaled8, offsets=None, C=None, out=None, alpha: 
         A.K, ldc, flags, alpha, beta, c_code, d_code, stream))
     if rc != GEMM_OK:
         raise GemmError(rc, "gemm_run_scaled8")
+    return out
+
+
+def _layouts(X, rows: int, cols: int, name: str):
+    """{col_major: ld} of the layouts that a rows x cols matrix view (last two dims) has: both
+    where it is one row or column."""
+    s_r, s_c = X.stride(-2), X.stride(-1)
+    found = {}
+    if (s_c == 1 or cols <= 1) and (s_r >= cols or rows <= 1):
+        found[False] = max(s_r if rows > 1 else cols, cols, 1)
+    if (s_r == 1 or rows <= 1) and (s_c >= rows or cols <= 1):
+        found[True] = max(s_c if cols > 1 else rows, rows, 1)
+    if not found:
+        raise ValueError(f"{name} must be row-major or column-major in its last two dims")
+    return found
+
+
+def gemm_adapters(X, W, A, B, offsets, ids=None, scale=None, C=None, out=None, alpha: float = 1.0, beta: float = 1.0,
+                  out_dtype=None, hidden=None, handle: Handle | None = None):
+    """D[i] = alpha * (X[i] @ W + scale[a] * (X[i] @ A[a]) @ B[a]) + beta * C[i] for the rows i of
+    every request and its adapter a, on the current stream: a projection that all requests
+    share, with a low-rank adapter beside it for each.
+
+    X: (T, K) float16 / bfloat16, row-major, the rows sorted by request;  offsets:
+    requests + 1 ascending row numbers (see gemm_grouped);  ids: (requests,) int32, the
+    adapter of each request (-1, or any number outside 0 .. adapters - 1: none), or None:
+    request g has adapter g;  scale: (adapters,) float32, or None (1).
+    W: (K, N), A: (adapters, K, r), B: (adapters, r, N) of X's dtype, row-major or transposed
+    views (of the (N, K), (adapters, r, K) and (adapters, N, r) of linear layers); W and B
+    must be laid out alike, and adapters lie one after the other.
+    C, ``out`` and ``out_dtype`` (default float32) as in gemm_grouped; rows that no request
+    owns are left as they are in ``out``.
+
+    hidden: a (T, r) tensor of X's dtype for scale[a] * X[i] @ A[a].  With it the gradients,
+    where every adapter has one run of rows (ids None), are
+        dX = gemm_adapters(dY, W.t(), B.transpose(1, 2), A.transpose(1, 2), offsets, scale=scale, hidden=g)
+        dA = gemm_grouped_wgrad(X, g, offsets)
+        dB = gemm_grouped_wgrad(hidden, dY, offsets)"""
+    import torch
+    dt = _sixteen_bit(X, W, "X and W")
+    if X.dim() != 2 or W.dim() != 2 or A.dim() != 3 or B.dim() != 3:
+        raise ValueError("X must be (T, K), W (K, N), A (adapters, K, r) and B (adapters, r, N)")
+    (T, K), N, (adapters, _, rank) = X.shape, W.shape[1], A.shape
+    if W.shape[0] != K or A.shape[1] != K or B.shape != (adapters, rank, N):
+        raise ValueError("X must be (T, K), W (K, N), A (adapters, K, r) and B (adapters, r, N)")
+    device = X.device
+    if A.dtype != X.dtype or B.dtype != X.dtype:
+        raise TypeError("A and B must have X's dtype")
+    if A.device != device or B.device != device:
+        raise ValueError("A and B must be on X's GPU")
+    if not 1 <= rank <= 1024:
+        raise ValueError("the adapters' rank must be 1 to 1024")
+    requests, flags = _check_offsets(offsets, device)
+    if ids is None:
+        if requests != adapters:
+            raise ValueError("without ids, offsets must hold one number more than there are adapters")
+    else:
+        if ids.dtype != torch.int32:
+            raise TypeError("ids must be int32")
+        if ids.shape != (requests,) or ids.device != device or (requests > 1 and ids.stride(0) != 1):
+            raise ValueError("ids must be a contiguous vector of one adapter to a request, on X's GPU")
+    if scale is not None:
+        if scale.dtype != torch.float32:
+            raise TypeError("scale must be float32")
+        if scale.shape != (adapters,) or scale.device != device or (adapters > 1 and scale.stride(0) != 1):
+            raise ValueError("scale must be a contiguous vector of one number to an adapter, on X's GPU")
+    ldx = _rows_of(X, "X")
+    w, b, a = _layouts(W, K, N, "W"), _layouts(B, rank, N, "B"), _layouts(A, K, rank, "A")
+    both = [c for c in w if c in b]
+    if not both:
+        raise ValueError("W and B must be laid out alike: both row-major, or both transposed views")
+    col, a_col = both[0], next(iter(a))
+    ldw, ldb, lda = w[col], b[col], a[a_col]
+    if adapters > 1 and K > 0 and N > 0 and (A.stride(0) != (rank if a_col else K) * lda or
+                                             B.stride(0) != (N if col else rank) * ldb):
+        raise ValueError("the adapters must lie one after the other")
+    ld_hidden = 0
+    if hidden is not None:
+        if hidden.dtype != X.dtype:
+            raise TypeError("hidden must have X's dtype")
+        if hidden.shape != (T, rank) or hidden.device != device:
+            raise ValueError("hidden must be (T, r), on X's GPU")
+        ld_hidden = _rows_of(hidden, "hidden")
+    c, c_code, out, d_code, ldc, beta = _output(C, out, (T, N), out_dtype, beta, device, "(T, N)")
+    operands = AdapterOperands(A.data_ptr(), B.data_ptr(), ids.data_ptr() if ids is not None else None,
+                               scale.data_ptr() if scale is not None else None, adapters, rank, lda, ldb)
+    flags |= (GEMM_B_COLMAJOR if col else 0) | (GEMM_ADAPTER_A_COLMAJOR if a_col else 0)
+
+    def call(h, stream):
+        work = torch.empty(max(h.adapters_work(T, rank, d_code), 16), dtype=torch.uint8, device=device)
+        return h.run_adapters(X.data_ptr(), W.data_ptr(), operands, c, out.data_ptr(), offsets.data_ptr(), requests, T, N,
+                              K, ldx, ldw, ldc, dt, flags, alpha, beta, c_code, d_code,
+                              hidden.data_ptr() if hidden is not None else 0, ld_hidden, work.data_ptr(), stream)
+
+    rc = _on(device, handle, call)
+    if rc != GEMM_OK:
+        raise GemmError(rc, "gemm_run_adapters")
     return out
 
 

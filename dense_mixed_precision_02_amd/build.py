@@ -7,7 +7,8 @@ import sys
 import tempfile
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
-SOURCES = [os.path.join(_HERE, "csrc", f) for f in ("gemm_api.hip", "ragged_api.hip", "wgrad8_api.hip", "route_api.hip")]
+SOURCES = [os.path.join(_HERE, "csrc", f) for f in ("gemm_api.hip", "ragged_api.hip", "adapter_api.hip", "wgrad8_api.hip",
+                                                       "route_api.hip")]
 OUT = os.path.join(_HERE, "libdmp_gemm.so")
 # The race-check variant: every pipeline step waits for its copies and meets
 # every wave; its results must equal the library's bit for bit.

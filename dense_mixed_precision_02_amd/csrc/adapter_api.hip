@@ -1,0 +1,101 @@
+// adapter_api.hip -- the entry point of the low-rank adapters beside a shared projection
+// (declared in include/dmp_gemm.h): argument checks, kernel choice and launches.
+#include <hip/hip_runtime.h>
+
+#include "../../include/dmp_gemm.h"
+#include "adapter.hpp"
+#include "adapter_plan.hpp"
+#include "handle.hpp"
+
+using namespace dmp;
+using namespace dmp::plan;
+
+namespace {
+
+int launch(void (*kernel)(AdapterArgs), int64_t workgroups, int threads, hipStream_t s, const AdapterArgs &a) {
+    GridShape g;
+    if (!grid_shape(workgroups, g)) return GEMM_ERR_INVALID_ARG;  // beyond one launch's grid
+    hipLaunchKernelGGL(kernel, dim3(g.x, g.y), dim3((unsigned)threads), 0, s, a);
+    return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
+}
+
+// 16 TM rows of a request by 16 TN columns (TN == 0: 16 rows, 128 columns) to a workgroup
+template <class DT, int TM, int TN, bool FAST>
+int launch_hidden(AdapterArgs a, hipStream_t s) {
+    a.tiles_r = (int)cdiv(a.rank, TN ? 16 * TN : 128);
+    return launch(adapter_hidden<DT, TM, TN, FAST>, (cdiv(a.r.M, 16 * TM) + a.r.groups) * a.tiles_r, HIDDEN_WAVES * 64, s, a);
+}
+
+template <class DT>
+int run_hidden(const AdapterArgs &a, bool a_col, bool fast, hipStream_t s) {
+    if (!a_col) return fast ? launch_hidden<DT, 1, 0, true>(a, s) : launch_hidden<DT, 1, 0, false>(a, s);
+    if (!fast) return launch_hidden<DT, 1, 1, false>(a, s);
+    if (a.r.M <= 32 * (int64_t)a.r.groups) return launch_hidden<DT, 1, 1, true>(a, s);
+    return a.rank <= 16 ? launch_hidden<DT, 4, 1, true>(a, s) : launch_hidden<DT, 4, 2, true>(a, s);
+}
+
+template <class DT, int BM, int BN, int WM, int WN, bool BKC, bool FAST>
+int launch_staged(AdapterArgs a, hipStream_t s) {
+    a.r.tiles_n = (int)cdiv(a.r.N, BN);
+    return launch(adapter_staged<DT, BM, BN, WM, WN, BKC, FAST>, cdiv(a.r.M, BM) * a.r.tiles_n, WM * WN * 64, s, a);
+}
+
+template <class DT, bool BKC>
+int run_product(const AdapterArgs &a, bool fast, hipStream_t s) {
+    return fast ? launch_staged<DT, 128, 128, 2, 2, BKC, true>(a, s) : launch_staged<DT, 64, 128, 1, 4, BKC, false>(a, s);
+}
+
+template <class DT>
+int run_adapters(const AdapterArgs &a, bool a_col, bool b_col, bool hidden_f, bool fast, hipStream_t s) {
+    if (a.r.K > 0 || a.hidden) {
+        const int rc = run_hidden<DT>(a, a_col, hidden_f, s);
+        if (rc != GEMM_OK) return rc;
+    }
+    return b_col ? run_product<DT, true>(a, fast, s) : run_product<DT, false>(a, fast, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t gemm_adapters_work(gemm_handle_t h, int64_t M, int64_t rank, int d_type) {
+    if (!h || M < 0 || M > SIZE_MAX_1 || rank < 1 || rank > ADAPTER_RANK_MAX || !float_out(d_type)) return -1;
+    return adapter_work(M, rank, d_type);
+}
+
+int gemm_run_adapters(gemm_handle_t h, const void *X, const void *W, const gemm_adapters_t *ad, const void *C, void *D,
+                      const void *offsets, int64_t requests, int64_t M, int64_t N, int64_t K, int64_t ldx, int64_t ldw,
+                      int64_t ldc, int dtype, unsigned flags, float alpha, float beta, int c_type, int d_type,
+                      void *hidden, int64_t ld_hidden, void *work, void *stream) {
+    EpiParams ep;
+    ep.alpha = alpha; ep.beta = beta;
+    ep.c_type = c_type; ep.d_type = d_type;
+    ep.use_c = beta != 0.0f;
+    const int rc = validate_adapters(h, X, W, ad, C, D, offsets, requests, M, N, K, ldx, ldw, ldc, dtype, flags, ep,
+                                     hidden, ld_hidden, work);
+    if (rc != GEMM_OK || M == 0 || N == 0 || requests == 0) return rc;
+    const bool bc = flags & GEMM_B_COLMAJOR, ac = flags & GEMM_ADAPTER_A_COLMAJOR;
+    AdapterArgs a{};
+    RaggedArgs &r = a.r;
+    r.A = X; r.B = W; r.C = C; r.D = D; r.offsets = offsets;
+    r.M = M; r.N = N; r.K = K; r.lda = ldx; r.ldb = ldw; r.ldc = ldc;
+    r.groups = (int)requests;
+    r.off32 = (flags & GEMM_OFFSETS_I32) != 0;
+    r.ep = ep;
+    a.A = ad->A; a.B = ad->B; a.ids = ad->ids; a.scale = ad->scale;
+    a.lda = ad->lda; a.ldb = ad->ldb;
+    a.sA = (ac ? ad->rank : K) * ad->lda;
+    a.sB = (bc ? N : ad->rank) * ad->ldb;
+    a.adapters = K > 0 ? (int)ad->adapters : 0;
+    a.rank = (int)ad->rank;
+    a.H = (char *)work;
+    a.rp = (int)adapter_rp(ad->rank);
+    a.parts = adapter_parts(d_type);
+    a.hidden = hidden; a.ld_hidden = ld_hidden;
+    const bool fast = K > 0 && product_fast(X, W, *ad, M, N, K, ldx, ldw, bc);
+    const bool hf = K > 0 && hidden_fast(X, *ad, K, ldx, ac);
+    hipStream_t s = (hipStream_t)stream;
+    return dtype == GEMM_F16 ? run_adapters<F16>(a, ac, bc, hf, fast, s) : run_adapters<BF16>(a, ac, bc, hf, fast, s);
+}
+
+}  // extern "C"

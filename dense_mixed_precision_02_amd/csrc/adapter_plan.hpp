@@ -1,0 +1,68 @@
+// adapter_plan.hpp -- host-side argument checks and kernel choice of the low-rank adapters
+// beside a shared projection (plain C++: no HIP types).
+#pragma once
+#include "ragged_plan.hpp"
+
+namespace dmp {
+namespace plan {
+
+constexpr unsigned ADAPTER_FLAGS = GEMM_B_COLMAJOR | GEMM_OFFSETS_I32 | GEMM_ADAPTER_A_COLMAJOR;
+constexpr int64_t ADAPTER_RANK_MAX = 1024;
+
+inline int64_t adapter_rp(int64_t rank) { return cdiv(rank, 8) * 8; }
+inline int adapter_parts(int d_type) { return d_type == GEMM_OUT_F32 ? 2 : 1; }
+inline int64_t adapter_work(int64_t M, int64_t rank, int d_type) { return adapter_parts(d_type) * M * adapter_rp(rank) * 2; }
+
+inline int validate_adapters(gemm_handle_t h, const void *X, const void *W, const gemm_adapters_t *ad, const void *C,
+                             const void *D, const void *offsets, int64_t requests, int64_t M, int64_t N, int64_t K,
+                             int64_t ldx, int64_t ldw, int64_t ldc, int dtype, unsigned flags, const EpiParams &ep,
+                             const void *hidden, int64_t ld_hidden, const void *work) {
+    int rc = check_sizes(h, requests, M, N, K, ldc, ep);
+    if (rc != GEMM_OK) return rc;
+    if (dtype != GEMM_F16 && dtype != GEMM_BF16) return GEMM_ERR_INVALID_ARG;
+    if ((flags & ~ADAPTER_FLAGS) || !ad) return GEMM_ERR_INVALID_ARG;
+    if (ad->rank < 1 || ad->rank > ADAPTER_RANK_MAX || ad->adapters < 0 || ad->adapters > GROUPS_MAX)
+        return GEMM_ERR_INVALID_ARG;
+    const bool bc = flags & GEMM_B_COLMAJOR, ac = flags & GEMM_ADAPTER_A_COLMAJOR;
+    if (K > 0) {
+        if (ldx < K || ldx > LD_MAX || ldw < std::max<int64_t>(1, bc ? K : N) || ldw > LD_MAX) return GEMM_ERR_INVALID_ARG;
+        if (ad->lda < (ac ? K : ad->rank) || ad->lda > LD_MAX || ad->ldb < std::max<int64_t>(1, bc ? ad->rank : N) ||
+            ad->ldb > LD_MAX)
+            return GEMM_ERR_INVALID_ARG;
+    }
+    if (hidden && (ld_hidden < ad->rank || ld_hidden > LD_MAX || (uintptr_t)hidden % 2)) return GEMM_ERR_INVALID_ARG;
+    if (M == 0 || N == 0 || requests == 0) return GEMM_OK;
+    if (!extent_ok(1, M, ldc, N) || (hidden && !extent_ok(1, M, ld_hidden, ad->rank))) return GEMM_ERR_INVALID_ARG;
+    const int64_t n = std::max<int64_t>(1, ad->adapters);
+    if (K > 0 && (!extent_ok(1, M, ldx, K) || !extent_ok(1, bc ? N : K, ldw, bc ? K : N) ||
+                  !extent_ok(n, ac ? ad->rank : K, ad->lda, ac ? K : ad->rank) ||
+                  !extent_ok(n, bc ? N : ad->rank, ad->ldb, bc ? ad->rank : N)))
+        return GEMM_ERR_INVALID_ARG;
+    if (!offsets_ok(offsets, flags)) return GEMM_ERR_INVALID_ARG;
+    if ((uintptr_t)ad->ids % 4 || (uintptr_t)ad->scale % 4) return GEMM_ERR_INVALID_ARG;
+    if (K > 0) {
+        if (!X || !W || (uintptr_t)X % 2 || (uintptr_t)W % 2) return GEMM_ERR_INVALID_ARG;
+        if (ad->adapters > 0 && (!ad->A || !ad->B || (uintptr_t)ad->A % 2 || (uintptr_t)ad->B % 2))
+            return GEMM_ERR_INVALID_ARG;
+    }
+    if (!work || !aligned16(work)) return GEMM_ERR_INVALID_ARG;
+    return check_outputs(C, D, ep);
+}
+
+// The hidden rows: can X's and A_a's granules be loaded whole?
+inline bool hidden_fast(const void *X, const gemm_adapters_t &ad, int64_t K, int64_t ldx, bool a_col) {
+    if (!aligned16(X) || !aligned16(ad.A) || ldx % 8 || ad.lda % 8 || K % 8) return false;
+    if (!a_col) return ad.rank % 8 == 0;
+    const int64_t lim = (1ll << 31) - (1ll << 22);
+    return (64 * ldx + K) * 2 < lim && (64 * ad.lda + K) * 2 < lim;
+}
+
+// The product: can the granules of X, W and B_a be loaded whole, with 31-bit offsets in a tile?
+inline bool product_fast(const void *X, const void *W, const gemm_adapters_t &ad, int64_t M, int64_t N, int64_t K,
+                         int64_t ldx, int64_t ldw, bool b_col) {
+    return granule_ok(X, W, M, N, K, ldx, ldw, GEMM_F16, false, b_col, true) &&
+           granule_ok(ad.B, ad.B, M, N, b_col ? ad.rank : 8, 8, ad.ldb, GEMM_F16, false, b_col, true);
+}
+
+}  // namespace plan
+}  // namespace dmp

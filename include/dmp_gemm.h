@@ -370,6 +370,57 @@ int gemm_run_scaled8(gemm_handle_t h, const gemm_q8_t *A, const gemm_q8_t *B, co
                      void *stream);
 
 /*
+ * Low-rank adapters of many requests beside a shared projection: the rows of X
+ * (M x K, row-major) are sorted by request, `offsets` holds requests + 1 row
+ * numbers as above, and for the rows i of every request with the adapter a,
+ *
+ *     D[i] = cvt_D(alpha * (X[i] * W + h[i] * B_a) + beta * C[i]),  h[i] = scale[a] * X[i] * A_a
+ *
+ * W: K x N, row-major or with GEMM_B_COLMAJOR column-major; A_a: K x rank,
+ * row-major (ld lda >= rank) or with GEMM_ADAPTER_A_COLMAJOR column-major (lda
+ * >= K); B_a: rank x N, row-major (ldb >= N) or column-major (ldb >= rank) as W
+ * is; each adapter's A (B) begins K (rank) * lda (ldb) elements after the one
+ * before, column-major rank (N) * lda (ldb).  ids: the adapter of each
+ * request, several may have the same; a value outside 0 .. adapters - 1 (as
+ * -1) is no adapter, h = 0.  ids NULL: request g has adapter g.  scale: a float for
+ * each adapter, or NULL: 1.  Rows of D that no request owns are left as they were.
+ *
+ * h is summed in fp32 and rounded to dtype, as an input of the matrix
+ * instructions; where D is fp32 it is kept as a sum of two such values.  So
+ * per element |D - D_exact| <= gemm_run_grouped's bound with K + rank products
+ * + |alpha| * e * sum over j of |h_ij * b_jn|, e = 2^-8 (bf16) or 2^-11 (fp16),
+ * for fp32 D 2^-16 (2^-22) (as long as h and its parts are normal numbers of
+ * dtype), + the bound of h's own sum, 4 * K * 2^-24 * sum of |x_ik * a_kj|,
+ * times |scale| * |b_jn|.  K == 0 gives D = cvt(beta * C).
+ *
+ * hidden: NULL, or M x rank values of dtype, rows ld_hidden >= rank apart, for h
+ * (zeros for a request without an adapter; rows that no request owns are left).
+ * The gradients of a layer D = X W + h B from dD, rows sorted by adapter (ids
+ * NULL): dX is the same call on dD with W, A and B replaced by the transposes of W,
+ * B and A, whose hidden rows are g = scale * dD * B_a^T; dA = X_a^T g_a and dB =
+ * h_a^T dD_a by gemm_run_grouped_wgrad.
+ *
+ * work: gemm_adapters_work(h, M, rank, d_type) bytes of device memory (-1: sizes
+ * that are refused), 16-byte aligned, not shared with a call that can run at the
+ * same time.  Nothing is allocated.  rank: 1 .. 1024; adapters and requests at
+ * most 2^20.  Everything else as in gemm_run_grouped.
+ */
+enum { GEMM_ADAPTER_A_COLMAJOR = 128u };
+typedef struct {
+    const void *A, *B;
+    const int32_t *ids;
+    const float *scale;
+    int64_t adapters, rank;
+    int64_t lda, ldb;
+} gemm_adapters_t;
+int64_t gemm_adapters_work(gemm_handle_t h, int64_t M, int64_t rank, int d_type);
+int gemm_run_adapters(gemm_handle_t h, const void *X, const void *W, const gemm_adapters_t *ad,
+                      const void *C, void *D, const void *offsets, int64_t requests, int64_t M,
+                      int64_t N, int64_t K, int64_t ldx, int64_t ldw, int64_t ldc, int dtype,
+                      unsigned flags, float alpha, float beta, int c_type, int d_type, void *hidden,
+                      int64_t ld_hidden, void *work, void *stream);
+
+/*
  * Weight gradients from 8-bit checkpoints of activations: D_g = cvt_D(alpha *
  * X_g^T * Y_g + beta * C_g) for every group g, where X (K rows of M values) is
  * an operand of 8-bit floats with blocks of one row by 128 columns (gemm_q8_t
