@@ -10,8 +10,8 @@
 //            of the columns; its eight waves split K, each streams its part of X and A_a
 //            straight into matrix-instruction operands, and their sums meet in LDS.
 //   product  [X | H] [W; B_a]: the projection's K loop runs on, over r more for each request
-//            that has rows in the tile, with the rows of H outside that request as zeros.  So
-//            D is written once; adding H B_a in a pass of its own would read and write it again.
+//            that has rows in the tile.  So D is written once; adding H B_a in a pass of its
+//            own would read and write it again.
 //
 // H is rounded to the inputs' type, as an input of the matrix instructions; its error
 // relative to H B_a is that of rounding X.  Where D has 32 bits H is kept as the sum of two
@@ -19,12 +19,13 @@
 //
 // A tile finds its requests by scanning the offsets (ragged.hpp's GroupWalk), 64 at a time.
 //
-// Zeros times an infinity or a NaN are no zeros: an adapter that holds one would spoil the
-// other requests' rows of the tile.  So the parts of B_a that a tile uses are looked at on
-// their way (a few instructions for each request), and a tile that found one is
-// computed again, one request at a time.
+// Zeros times an infinity or a NaN are no zeros: with rows of zeros for the other requests an
+// adapter that holds one would spoil theirs.  So a 16-row block of the tile that lies in
+// one request adds its adapter's products in the accumulators, one that does not is
+// skipped, and one on the border sums them apart and adds those of the request's rows.
 #pragma once
 #include "ragged_staged.hpp"
+#include "skinny.hpp"
 
 namespace dmp {
 
@@ -49,6 +50,15 @@ __device__ static inline int adapter_of(const AdapterArgs &p, int g) {
     return (uint32_t)a < (uint32_t)p.adapters ? a : -1;
 }
 
+// The same of a group found by a walk: `own` is what this lane's group of the first 64 has,
+// loaded along with the offsets.
+__device__ static inline int first_adapters(const AdapterArgs &p, int lane) {
+    return lane < p.r.groups ? adapter_of(p, lane) : -1;
+}
+__device__ static inline int adapter_of(const AdapterArgs &p, int g, int own) {
+    return __builtin_amdgcn_readfirstlane(g < 64 ? __builtin_amdgcn_readlane(own, g & 63) : adapter_of(p, g));
+}
+
 // Up to eight 16-bit values from e on, of which n exist (n <= 0: none is touched).
 __device__ static inline intx4 load8(const uint16_t *e, int n) {
     intx4 v = {0, 0, 0, 0};
@@ -62,43 +72,61 @@ __device__ static inline intx4 load8(const uint16_t *e, int n) {
     return v;
 }
 
+// Loads that were issued stay in front of what follows: the compiler would else sink a stage's
+// loads to where they are needed, with only one stage on its way.
+__device__ static inline void issued() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// Byte offsets of granules as a row's part and a k's part: where either does not exist it is
+// OOB_OFFSET, and the sum (below 2^32) is out of range.
+__device__ static inline int row_part(int row, int rows, int64_t ld) { return row < rows ? row * (int)ld * 2 : OOB_OFFSET; }
+__device__ static inline int k_part(int k, int end) { return k < end ? k * 2 : OOB_OFFSET; }
+__device__ static inline int joined(int a, int b) { return (int)((uint32_t)a + (uint32_t)b); }
+
 constexpr int HIDDEN_WAVES = 8;
 
 // H of `rows` rows from row0 on (rows <= 16 TM), adapter a, columns c0 .. c0 + 16 TN - 1;
 // A_a K-contiguous.
 template <class DT, int TM, int TN, bool FAST>
 __device__ static inline void hidden_sum(const AdapterArgs &p, int a, int64_t row0, int rows, int c0, float *lds) {
-    constexpr int U = TM + TN <= 2 ? 4 : TM + TN <= 5 ? 2 : 1;  // k-tiles of 64 in a stage
+    constexpr int U = TM + TN <= 2 ? 4 : TM + TN <= 4 ? 2 : 1;  // k-tiles of 64 in a stage
     const int lane = lane_id(), wave = wave_id(), r16 = lane & 15, K = (int)p.r.K;
     const int nkt = (K + 63) / 64, per = (nkt + HIDDEN_WAVES - 1) / HIDDEN_WAVES;
-    const int kt0 = min(wave * per, nkt), kt1 = min(kt0 + per, nkt);
+    const int kt0 = min(wave * per, nkt), kt1 = min(kt0 + per, nkt), kend = min(K, kt1 * 64);
     const int cols = p.rank - c0;
     const char *xb = (const char *)p.r.A + row0 * p.r.lda * 2, *ab = (const char *)p.A + (a * p.sA + c0 * p.lda) * 2;
     const __amdgpu_buffer_rsrc_t rx = make_rsrc(xb), ra = make_rsrc(ab);
     floatx4 acc[TM][TN] = {};
     intx4 fx[2][U][TM][2], fa[2][U][TN][2];
-    auto one = [&](const __amdgpu_buffer_rsrc_t &rs, const char *base, int64_t ld, int row, bool there, int k) {
-        if constexpr (FAST) {
-            return __builtin_bit_cast(intx4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                 rs, there && k < K ? (row * (int)ld + k) * 2 : OOB_OFFSET, 0, 0));
-        } else {
-            return load8((const uint16_t *)base + row * ld + k, there ? K - k : 0);
-        }
-    };
+    int xo[TM], ao[TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i) xo[i] = row_part(i * 16 + r16, rows, p.r.lda);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) ao[j] = row_part(j * 16 + r16, cols, p.lda);
     auto load = [&](int st, int kt) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int k = (kt + u) * 64 + 32 * h + 8 * (lane >> 4);
-                const bool in = kt + u < kt1;
+                if constexpr (FAST) {
+                    const int ko = k_part(k, kend);
 #pragma unroll
-                for (int j = 0; j < TN; ++j)
-                    fa[st][u][j][h] = one(ra, ab, p.lda, j * 16 + r16, in && j * 16 + r16 < cols, k);
+                    for (int j = 0; j < TN; ++j) fa[st][u][j][h] = load_granule(ra, joined(ao[j], ko));
 #pragma unroll
-                for (int i = 0; i < TM; ++i)
-                    fx[st][u][i][h] = one(rx, xb, p.r.lda, i * 16 + r16, in && i * 16 + r16 < rows, k);
+                    for (int i = 0; i < TM; ++i) fx[st][u][i][h] = load_granule(rx, joined(xo[i], ko));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < TN; ++j)
+                        fa[st][u][j][h] = load8((const uint16_t *)ab + (j * 16 + r16) * p.lda + k, j * 16 + r16 < cols ? kend - k : 0);
+#pragma unroll
+                    for (int i = 0; i < TM; ++i)
+                        fx[st][u][i][h] = load8((const uint16_t *)xb + (i * 16 + r16) * p.r.lda + k, i * 16 + r16 < rows ? kend - k : 0);
+                }
             }
+        issued();
     };
     auto multiply = [&](int st) {
 #pragma unroll
@@ -175,10 +203,9 @@ __device__ static inline void hidden_sum_n(const AdapterArgs &p, int a, int64_t 
 // The waves' sums, added in their order, times the adapter's scale, rounded into H (and the
 // caller's copy).
 template <class DT, int CW, int SZ>
-__device__ static inline void hidden_store(const AdapterArgs &p, int a, int64_t row0, int rows, int c0, const float *lds) {
+__device__ static inline void hidden_store(const AdapterArgs &p, int a, float s, int64_t row0, int rows, int c0, const float *lds) {
     constexpr bool f16 = std::is_same_v<DT, F16>;
     __syncthreads();
-    const float s = p.scale && a >= 0 ? p.scale[a] : 1.0f;
     const int cols = min(CW, p.rp - c0);
     for (int e = threadIdx.x; e < rows * CW; e += HIDDEN_WAVES * 64) {
         const int r = e / CW, c = e % CW;
@@ -209,19 +236,21 @@ __global__ __launch_bounds__(HIDDEN_WAVES * 64, 2) void adapter_hidden(const Ada
     __shared__ float lds[HIDDEN_WAVES * SZ];
     const int id = workgroup_id(), lane = lane_id(), total = (int)p.r.M;
     const int tile = id / p.tiles_r, c0 = (id - tile * p.tiles_r) * CW;
+    const int own = first_adapters(p, lane);
     GroupWalk<BM> walk;
     walk.load(p.r, total, lane);
     int g, r0, r1, tile0;
     if (!walk.find(p.r, total, lane, tile, g, r0, r1, tile0)) return;
-    const int a = __builtin_amdgcn_readfirstlane(adapter_of(p, g));
+    const int a = adapter_of(p, g, own);
     if (a < 0 && !p.hidden) return;
+    const float scale = p.scale && a >= 0 ? p.scale[a] : 1.0f;
     const int64_t row0 = r0 + (int64_t)(tile - tile0) * BM;
     const int rows = (int)min((int64_t)BM, r1 - row0);
     if (a >= 0) {
         if constexpr (TN > 0) hidden_sum<DT, TM, TN, FAST>(p, a, row0, rows, c0, lds);
         else hidden_sum_n<DT, FAST>(p, a, row0, rows, c0, lds);
     }
-    hidden_store<DT, CW, SZ>(p, a, row0, rows, c0, lds);
+    hidden_store<DT, CW, SZ>(p, a, scale, row0, rows, c0, lds);
 }
 
 // A tile's requests that have an adapter: rows lo .. hi - 1 of the tile, in ascending order.
@@ -234,13 +263,14 @@ struct AdapterEntry {
 template <int BM>
 __device__ static inline int adapter_entries(const AdapterArgs &p, int row0, int rows, DMP_LDS AdapterEntry *list) {
     const int lane = lane_id(), total = (int)p.r.M;
+    const int own = first_adapters(p, lane);
     GroupWalk<BM> walk;
     walk.load(p.r, total, lane);
     int n = 0;
     do {
         const int lo = max(walk.lo, row0) - row0, hi = min(walk.hi, row0 + rows) - row0;
         int a = -1;
-        if (lo < hi) a = adapter_of(p, walk.chunk + lane);  // (an empty request is none past the last)
+        if (lo < hi) a = walk.chunk == 0 ? own : adapter_of(p, walk.chunk + lane);  // (a request with rows is none past the last)
         const uint64_t has = __ballot(a >= 0);
         if (a >= 0) {
             const int at = n + __popcll(has & ((1ull << lane) - 1));
@@ -275,64 +305,61 @@ __device__ static inline bool adapter_tile_at(const AdapterArgs &p, TileAt &at) 
     return true;
 }
 
-// Does a granule hold an infinity or a NaN?
-template <class DT>
-__device__ static inline bool not_finite(const intx4 &v) {
-    constexpr uint32_t E = std::is_same_v<DT, F16> ? 0x7c00u : 0x7f80u;
-    bool bad = false;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) bad |= ((uint32_t)v[w] & E) == E || ((uint32_t)v[w] & E << 16) == E << 16;
-    return bad;
-}
-
-// The rows and entries of a pass over a tile: all of them first (pass < 0); where that found
-// a B_a with an infinity or a NaN, one pass to each entry (odd passes) and to the rows before,
-// between and behind them (even ones).
-struct AdapterPass {
-    int first, entries;  // entries of the list
-    int lo, hi;          // rows of the tile that are stored
-};
-__device__ static inline AdapterPass adapter_pass(const DMP_LDS AdapterEntry *list, int entries, int rows, int pass) {
-    if (pass < 0) return {0, entries, 0, rows};
-    const int e = pass / 2;
-    if (pass % 2) return {e, 1, list[e].rows & 0xffff, (int)((uint32_t)list[e].rows >> 16)};
-    return {e, 0, e > 0 ? (int)((uint32_t)list[e - 1].rows >> 16) : 0, e < entries ? list[e].rows & 0xffff : rows};
-}
-
 // What a k-tile is read from.
 struct AdapterSource {
     const char *A, *B;   // first element of the tile's rows and columns at the k-tile's first k
     int left;            // k that are left
-    int lo, hi;          // rows of the tile that are not zeros
-    bool more;           // past the projection's K: H and B_a
 };
 
-// K-tile kt of a tile: the projection's first, then for each request ceil(rank / 64) of its
-// adapter, times parts.
+// K-tile x past the projection's: for each entry ceil(rank / 64) of its adapter, times
+// parts; past the last entry nothing is left.
 template <class DT, bool BKC>
 __device__ static inline AdapterSource adapter_source(const AdapterArgs &p, const TileAt &at, const DMP_LDS AdapterEntry *list,
-                                                      int entries, int nkt, int kt) {
+                                                      int entries, int x) {
     AdapterSource s;
-    s.more = kt >= nkt;
-    if (!s.more) {
-        s.A = at.A + (int64_t)kt * 128;
-        s.B = at.B + (BKC ? (int64_t)kt * 128 : (int64_t)kt * 128 * p.r.ldb);
-        s.left = at.k - kt * 64;
-        s.lo = 0;
-        s.hi = at.rows;
-        return s;
-    }
-    const int nr = (p.rank + 63) / 64, e = (kt - nkt) / (nr * p.parts), j = (kt - nkt) - e * nr * p.parts;
+    const int nr = (p.rank + 63) / 64, e = x / (nr * p.parts), j = x - e * nr * p.parts;
     const int part = j / nr, k = 64 * (j - part * nr);
     const bool there = e < entries;
-    const int rows = there ? list[e].rows : 0, a = there ? list[e].adapter : 0;
-    s.lo = __builtin_amdgcn_readfirstlane(rows & 0xffff);
-    s.hi = __builtin_amdgcn_readfirstlane((uint32_t)rows >> 16);
+    const int a = __builtin_amdgcn_readfirstlane(there ? list[e].adapter : 0);
     s.left = there ? p.rank - k : 0;
     s.A = p.H + (part * p.r.M * p.rp + at.row0 * p.rp + k) * 2;
-    const int64_t b = (int64_t)__builtin_amdgcn_readfirstlane(a) * p.sB;
-    s.B = (const char *)p.B + (b + (BKC ? at.col0 * p.ldb + k : k * p.ldb + at.col0)) * 2;
+    s.B = (const char *)p.B + (a * p.sB + (BKC ? at.col0 * p.ldb + k : k * p.ldb + at.col0)) * 2;
     return s;
+}
+
+// One k-tile of an entry on a wave's TM x TN blocks, whose first row is `row` of the tile.
+// fragA(i, s), fragB(j, s): fragments of step s; in(acc, a, b): a step in the accumulators.
+template <class DT, int TM, int TN, class FA, class FB, class In>
+__device__ static inline void adapter_blocks(floatx4 (&acc)[TM][TN], int rows, int row, int lane, FA fragA, FB fragB, In in) {
+    const int lo = rows & 0xffff, hi = (int)((uint32_t)rows >> 16);
+    if (hi <= row || lo >= row + 16 * TM) return;
+    intx4 fb[2][TN];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) fb[s][j] = fragB(j, s);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+        const int r = row + 16 * i;
+        if (hi <= r || lo >= r + 16) continue;
+        const intx4 fa[2] = {fragA(i, 0), fragA(i, 1)};
+        if (lo <= r && hi >= r + 16) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) in(acc[i][j], fa[s], fb[s][j]);
+        } else {
+            const int mine = r + 4 * (lane >> 4);
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                floatx4 c = {0, 0, 0, 0};
+#pragma unroll
+                for (int s = 0; s < 2; ++s) c = mma16<DT>(fa[s], fb[s][j], c);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) acc[i][j][q] += mine + q >= lo && mine + q < hi ? c[q] : 0.0f;
+            }
+        }
+    }
 }
 
 // The product, operands staged through registers as in ragged_staged.hpp.  FAST: all
@@ -356,7 +383,10 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void adapter_staged(const AdapterAr
         if (lane == 0) count = n;
     }
     __syncthreads();
-    const int all = __builtin_amdgcn_readfirstlane(count), nkt0 = at.k / 64 + (at.k % 64 != 0);
+    const DMP_LDS AdapterEntry *entry = (const DMP_LDS AdapterEntry *)list;
+    const int entries = __builtin_amdgcn_readfirstlane(count), per = (p.rank + 63) / 64 * p.parts;
+    // an even number of the projection's k-tiles, the last of which may be empty (zeros)
+    const int nkt0 = (at.k / 64 + (at.k % 64 != 0) + 1) & ~1, more = entries * per;
     OpA opa, oph;
     OpB opb, opr;
     opa.init(wave, lane, p.r.lda, 0, BM);
@@ -364,47 +394,40 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void adapter_staged(const AdapterAr
     opb.init(wave, lane, p.r.ldb, 0, BN);
     opr.init(wave, lane, p.ldb, 0, BN);
 
-    floatx4 acc[TM][TN];
+    floatx4 acc[TM][TN] = {};
     intx4 ra[DEPTH][OpA::CPW], rb[DEPTH][OpB::CPW];
-    const DMP_LDS AdapterEntry *entry = (const DMP_LDS AdapterEntry *)list;
-    int entries = all, nkt = 0;
-    bool odd = false;
-    auto fetch = [&](int kt, int slot) {
-        const AdapterSource s = adapter_source<DT, BKC>(p, at, entry, entries, nkt0, kt);
+    // a lane's granules of a k-tile: of the projection, and (MORE) of H and B_a
+    auto read = [&](auto more_c, const AdapterSource &s, const OpA &oa, const OpB &ob, int64_t ldb, int slot) {
+        constexpr bool MORE = decltype(more_c)::value;
         const __amdgpu_buffer_rsrc_t rsa = make_rsrc(s.A), rsb = make_rsrc(s.B);
-        const int a0 = s.more ? oph.off0 : opa.off0, as = s.more ? oph.step : opa.step;
 #pragma unroll
         for (int j = 0; j < OpA::CPW; ++j) {
-            const int row = opa.row_or_k + 8 * NW * j;
-            if (FAST || s.more) {  // (H is laid out in whole granules)
-                const bool ok = row >= s.lo && row < s.hi && opa.fixed < s.left;
-                ra[slot][j] = __builtin_bit_cast(
-                    intx4, __builtin_amdgcn_raw_buffer_load_b128(rsa, ok ? a0 + j * as : OOB_OFFSET, 0, 0));
-            } else {
-                ra[slot][j] = load8((const uint16_t *)s.A + row * p.r.lda + opa.fixed, row < s.hi ? s.left - opa.fixed : 0);
-            }
+            const int row = oa.row_or_k + 8 * NW * j;
+            if constexpr (FAST || MORE)  // (H is laid out in whole granules)
+                ra[slot][j] = load_granule(rsa, row < at.rows && oa.fixed < s.left ? oa.off0 + j * oa.step : OOB_OFFSET);
+            else
+                ra[slot][j] = load8((const uint16_t *)s.A + row * p.r.lda + oa.fixed, row < at.rows ? s.left - oa.fixed : 0);
         }
-        const int64_t ldb = s.more ? p.ldb : p.r.ldb;
-        const int b0 = s.more ? opr.off0 : opb.off0, bs = s.more ? opr.step : opb.step;
 #pragma unroll
         for (int j = 0; j < OpB::CPW; ++j) {
-            const int r = BKC ? opb.row_or_k + 8 * NW * j : opb.fixed;
-            const int k = BKC ? opb.fixed : opb.row_or_k + OpB::KSTEP * j;
+            const int r = BKC ? ob.row_or_k + 8 * NW * j : ob.fixed;
+            const int k = BKC ? ob.fixed : ob.row_or_k + OpB::KSTEP * j;
             const bool ok = r < at.cols && k < s.left;
-            if constexpr (FAST) {
-                rb[slot][j] = __builtin_bit_cast(
-                    intx4, __builtin_amdgcn_raw_buffer_load_b128(rsb, ok ? b0 + j * bs : OOB_OFFSET, 0, 0));
-            } else {
-                rb[slot][j] = load8((const uint16_t *)s.B + (BKC ? r * ldb + k : k * ldb + r),
-                                    ok ? (BKC ? s.left - k : at.cols - r) : 0);
-            }
+            if constexpr (FAST)
+                rb[slot][j] = load_granule(rsb, ok ? ob.off0 + j * ob.step : OOB_OFFSET);
+            else
+                rb[slot][j] = load8((const uint16_t *)s.B + (BKC ? r * ldb + k : k * ldb + r), ok ? (BKC ? s.left - k : at.cols - r) : 0);
         }
+        issued();
     };
-    auto put = [&](int kt, int slot, int buf) {
-        if (kt >= nkt0) {
-#pragma unroll
-            for (int j = 0; j < OpB::CPW; ++j) odd |= not_finite<DT>(rb[slot][j]);
-        }
+    auto fetch = [&](int kt, int slot) {
+        const AdapterSource s = {at.A + (int64_t)kt * 128, at.B + (int64_t)kt * (BKC ? 128 : 128 * p.r.ldb), at.k - kt * 64};
+        read(std::false_type{}, s, opa, opb, p.r.ldb, slot);
+    };
+    auto fetch_more = [&](int x, int slot) {
+        read(std::true_type{}, adapter_source<DT, BKC>(p, at, entry, entries, x), oph, opr, p.ldb, slot);
+    };
+    auto put = [&](int slot, int buf) {
 #pragma unroll
         for (int j = 0; j < OpA::CPW; ++j)
             *(DMP_LDS intx4 *)((DMP_LDS char *)lds_a[buf] + OpA::chunk_offset(j * NW + wave) + lane * 16) = ra[slot][j];
@@ -412,15 +435,20 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void adapter_staged(const AdapterAr
         for (int j = 0; j < OpB::CPW; ++j)
             *(DMP_LDS intx4 *)((DMP_LDS char *)lds_b[buf] + OpB::chunk_offset(j * NW + wave) + lane * 16) = rb[slot][j];
     };
+    auto fragA = [&](int buf, int i, int s) {
+        return frag16<DT, OpA, BM, true>((const DMP_LDS char *)lds_a[buf], wm * WTM + i * 16, s, lane);
+    };
+    auto fragB = [&](int buf, int j, int s) {
+        return frag16<DT, OpB, BN, BKC>((const DMP_LDS char *)lds_b[buf], wn * WTN + j * 16, s, lane);
+    };
     auto multiply = [&](int buf) {
-        const DMP_LDS char *la = (const DMP_LDS char *)lds_a[buf], *lb = (const DMP_LDS char *)lds_b[buf];
         intx4 fa[2][TM], fb[2][TN];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
 #pragma unroll
-            for (int i = 0; i < TM; ++i) fa[s][i] = frag16<DT, OpA, BM, true>(la, wm * WTM + i * 16, s, lane);
+            for (int i = 0; i < TM; ++i) fa[s][i] = fragA(buf, i, s);
 #pragma unroll
-            for (int j = 0; j < TN; ++j) fb[s][j] = frag16<DT, OpB, BN, BKC>(lb, wn * WTN + j * 16, s, lane);
+            for (int j = 0; j < TN; ++j) fb[s][j] = fragB(buf, j, s);
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -430,55 +458,333 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void adapter_staged(const AdapterAr
 #pragma unroll
                 for (int j = 0; j < TN; ++j) acc[i][j] = mma16<DT>(fa[s][i], fb[s][j], acc[i][j]);
     };
+    auto multiply_more = [&](int x, int buf) {
+        adapter_blocks<DT, TM, TN>(acc, __builtin_amdgcn_readfirstlane(entry[x / per].rows), wm * WTM, lane,
+                                   [&](int i, int s) { return fragA(buf, i, s); }, [&](int j, int s) { return fragB(buf, j, s); },
+                                   [](floatx4 &c, const intx4 &a, const intx4 &b) { c = mma16<DT>(a, b, c); });
+    };
+    auto turn = [&](int buf) {  // the k-tile in the registers `buf` into the LDS buffer, when all are done with it
+        put(buf, buf);
+        step_sync();
+        barrier_vmcnt<63>();
+    };
+    if (nkt0 > 0) {
+        fetch(0, 0);
+        fetch(1, 1);
+        turn(0);
+        // k-tile kt is in LDS buffer 0, the next one on its way; past the projection's come the adapters'
+        for (int kt = 0; kt + 2 < nkt0; kt += 2) {
+            fetch(kt + 2, 0);
+            step_sync();
+            multiply(0);
+            turn(1);
+            fetch(kt + 3, 1);
+            step_sync();
+            multiply(1);
+            turn(0);
+        }
+        fetch_more(0, 0);
+        step_sync();
+        multiply(0);
+        turn(1);
+        fetch_more(1, 1);
+        step_sync();
+        multiply(1);
+        turn(0);
+        for (int x = 0; x < more; x += 2) {
+            fetch_more(x + 2, 0);
+            step_sync();
+            multiply_more(x, 0);
+            turn(1);
+            fetch_more(x + 3, 1);
+            step_sync();
+            if (x + 1 < more) multiply_more(x + 1, 1);
+            turn(0);
+        }
+    }
+    __syncthreads();
     constexpr int SLAB = 32 * (WTN + 4) * 4, INA = 2 * OpA::BYTES / SLAB;
     static_assert(NW <= INA || (NW - INA) * SLAB <= 2 * OpB::BYTES, "slabs must fit");
     DMP_LDS char *slab = wave < INA ? (DMP_LDS char *)&lds_a[0][0] + wave * SLAB
                                     : (DMP_LDS char *)&lds_b[0][0] + (wave - INA) * SLAB;
     const EpiParams &ep = p.r.ep;
     const int64_t first = at.row0 * p.r.ldc + at.col0;
-    for (int pass = -1; pass <= 2 * all; ++pass) {
-        const AdapterPass q = adapter_pass((const DMP_LDS AdapterEntry *)list, all, at.rows, pass);
-        if (q.lo >= q.hi) continue;
-        entry = (const DMP_LDS AdapterEntry *)list + q.first;
-        entries = __builtin_amdgcn_readfirstlane(q.entries);
-        nkt = nkt0 + entries * ((p.rank + 63) / 64) * p.parts;
+    store_wave_tile<WTM, WTN>((DMP_LDS float *)slab, ep, (const char *)p.r.C + first * out_size(ep.c_type),
+                              (char *)p.r.D + first * out_size(ep.d_type), p.r.ldc, at.rows, at.cols, wm * WTM,
+                              wn * WTN, lane, [&](int i, int j) { return acc[i][j]; });
+}
+
+// The product on 256 x 256 tiles: the K loop of Tile16 (ragged_tile.hpp), whose copies run on
+// into H and B_a; their k-tiles follow one at a time, the next one's copies in flight.
+template <class DT, bool BKC>
+__global__ __launch_bounds__(256) void adapter_tile(const AdapterArgs p) {
+    constexpr int BM = 256, BN = 256, WM = 2, WN = 2, NW = 4;
+    constexpr int WTM = BM / WM, WTN = BN / WN, TM = WTM / 16, TN = WTN / 16, NI = TM * TN;
+    using OpA = Operand<DT, BM, NW, true>;
+    using OpB = Operand<DT, BN, NW, BKC, BKC ? 0 : 32>;
+    constexpr int NC = OpA::CPW + OpB::CPW;
+    __shared__ __attribute__((aligned(1024))) char lds_a0[OpA::BYTES];
+    __shared__ __attribute__((aligned(1024))) char lds_b0[OpB::BYTES];
+    __shared__ __attribute__((aligned(1024))) char lds_a1[OpA::BYTES];
+    __shared__ __attribute__((aligned(1024))) char lds_b1[OpB::BYTES];
+    __shared__ AdapterEntry list[BM];
+    __shared__ int count;
+    DMP_LDS char *LA[2] = {(DMP_LDS char *)lds_a0, (DMP_LDS char *)lds_a1};
+    DMP_LDS char *LB[2] = {(DMP_LDS char *)lds_b0, (DMP_LDS char *)lds_b1};
+    const int lane = lane_id(), wave = wave_id();
+    const int wm = wave / WN, wn = wave % WN;
+    TileAt at;
+    if (!adapter_tile_at<BM, BN, DT, BKC>(p, at)) return;
+    if (wave == 0) {
+        const int n = adapter_entries<BM>(p, (int)at.row0, at.rows, (DMP_LDS AdapterEntry *)list);
+        if (lane == 0) count = n;
+    }
+    __syncthreads();
+    const DMP_LDS AdapterEntry *entry = (const DMP_LDS AdapterEntry *)list;
+    const int entries = __builtin_amdgcn_readfirstlane(count), per = (p.rank + 63) / 64 * p.parts;
+    // an even number of the projection's k-tiles, the last of which may be empty (zeros)
+    const int nkt0 = (at.k / 64 + (at.k % 64 != 0) + 1) & ~1, more = entries * per;
+    OpA opa, oph;
+    OpB opb, opr;
+    opa.init(wave, lane, p.r.lda, 0, BM);
+    oph.init(wave, lane, p.rp, 0, BM);
+    opb.init(wave, lane, p.r.ldb, 0, BN);
+    opr.init(wave, lane, p.ldb, 0, BN);
+    floatx4 acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = floatx4{0, 0, 0, 0};
+    auto pin_acc = [&]() {  // see tile16_gemm
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
-            for (int j = 0; j < TN; ++j) acc[i][j] = floatx4{0, 0, 0, 0};
-        if (nkt > 0) {
+            for (int j = 0; j < TN; ++j) asm volatile("" : "+a"(acc[i][j]));
+    };
+    // copy c (A's chunks, then B's) of the projection's k-tile kt, and of a k-tile of H and B_a
+    auto copy = [&](int kt, int buf, int c) {
+        const int kleft = at.k - kt * 64;
+        if (c < OpA::CPW)
+            opa.issue(make_rsrc(OpA::tile_base(at.A, p.r.lda, 0, (int64_t)kt * 64)), LA[buf], wave, c, kleft, at.rows);
+        else
+            opb.issue(make_rsrc(OpB::tile_base(at.B, p.r.ldb, 0, (int64_t)kt * 64)), LB[buf], wave, c - OpA::CPW, kleft, at.cols);
+    };
+    auto source = [&](int x) { return adapter_source<DT, BKC>(p, at, entry, entries, x); };
+    auto copy_more = [&](const AdapterSource &s, DMP_LDS char *la, DMP_LDS char *lb, int c) {
+        if (c < OpA::CPW) oph.issue(make_rsrc(s.A), la, wave, c, s.left, at.rows);
+        else opr.issue(make_rsrc(s.B), lb, wave, c - OpA::CPW, s.left, at.cols);
+    };
+    auto fragA = [&](int buf, int i, int s) { return frag16<DT, OpA, BM, true>(LA[buf], wm * WTM + i * 16, s, lane); };
+    auto fragB = [&](int buf, int j, int s) { return frag16<DT, OpB, BN, BKC>(LB[buf], wn * WTN + j * 16, s, lane); };
+    // fragment sets and their reading between the instructions: as in Tile16
+    constexpr int NSB = BKC ? 2 : 4;
+    intx4 fa[2][TM], fb[NSB][TN];
+    auto setb = [](int buf, int s) { return BKC ? s : 2 * buf + s; };
+    auto read_mn = [&](int buf) {
+        if constexpr (!BKC) {
 #pragma unroll
-            for (int s = 0; s < DEPTH; ++s) fetch(s, s);
-            put(0, 0, 0);
-            barrier_vmcnt<63>();
-            bool done = nkt == 1;
-            for (int kt = 0; !done; kt += DEPTH) {
+            for (int s2 = 0; s2 < 2; ++s2)
 #pragma unroll
-                for (int s = 0; s < DEPTH; ++s) {
-                    // k-tile kt + s is in LDS buffer s % 2, the next DEPTH - 1 are on their way
-                    fetch(kt + s + DEPTH, s);
-                    asm volatile("" ::: "memory");
-                    __builtin_amdgcn_sched_barrier(0);
-                    step_sync();
-                    multiply(s % 2);
-                    put(kt + s + 1, (s + 1) % DEPTH, (s + 1) % 2);
-                    step_sync();
-                    barrier_vmcnt<63>();
-                    if (kt + s + 2 >= nkt) {
-                        done = true;
-                        break;
+                for (int j = 0; j < TN; ++j) fb[setb(buf, s2)][j] = fragB(buf, j, s2);
+        }
+    };
+    auto read_one = [&](int buf, int s, int r) {
+        if (r < TM) {
+            fa[s][r] = fragA(buf, r, s);
+        } else {
+            if constexpr (BKC) fb[setb(buf, s)][r - TM] = fragB(buf, r - TM, s);
+        }
+    };
+    // LAST: the projection's last two k-tiles, behind which come the adapters' first two
+    auto ktile = [&](auto last, int kt, int cur) {
+        constexpr bool LAST = decltype(last)::value;
+        AdapterSource next;
+        if constexpr (LAST) next = source(cur);
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                Mma16<DT>::run(acc[i][j], fa[0][i], fb[setb(cur, 0)][j]);
+                const int q = i * TN + j;
+                if (slot_has(q, TM + TN, NI)) read_one(cur, 1, q * (TM + TN) / NI);
+            }
+        wait_vmcnt<0>();
+        __syncthreads();
+        read_mn(cur ^ 1);
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                Mma16<DT>::run(acc[i][j], fa[1][i], fb[setb(cur, 1)][j]);
+                const int q = i * TN + j;
+                if (slot_has(q, NC, NI)) {
+                    if constexpr (LAST) copy_more(next, LA[cur], LB[cur], q * NC / NI);
+                    else copy(kt + 2, cur, q * NC / NI);
+                }
+                if (slot_has(q, TM + TN, NI)) read_one(cur ^ 1, 0, q * (TM + TN) / NI);
+            }
+        step_sync();
+    };
+#pragma unroll
+    for (int c = 0; c < NC; ++c) copy(0, 0, c);
+    wait_vmcnt<0>();
+    __syncthreads();
+    read_mn(0);
+#pragma unroll
+    for (int r = 0; r < TM + TN; ++r) read_one(0, 0, r);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) copy(1, 1, c);
+    pin_acc();
+    asm volatile("s_nop 7" ::);
+    for (int kt = 0; kt + 2 < nkt0; kt += 2) {
+        ktile(std::false_type{}, kt, 0);
+        ktile(std::false_type{}, kt + 1, 1);
+    }
+    ktile(std::true_type{}, nkt0 - 2, 0);
+    ktile(std::true_type{}, nkt0 - 1, 1);
+    mma_drain();
+    pin_acc();
+    // the adapters' k-tiles: x is in buffer x % 2, x + 1 on its way
+    for (int x = 0; x < more; ++x) {
+        const int rows = __builtin_amdgcn_readfirstlane(entry[x / per].rows);
+        DMP_LDS char *la = x & 1 ? LA[1] : LA[0], *lb = x & 1 ? LB[1] : LB[0];
+        adapter_blocks<DT, TM, TN>(acc, rows, wm * WTM, lane,
+                                   [&](int i, int s) { return frag16<DT, OpA, BM, true>(la, wm * WTM + i * 16, s, lane); },
+                                   [&](int j, int s) { return frag16<DT, OpB, BN, BKC>(lb, wn * WTN + j * 16, s, lane); },
+                                   [](floatx4 &c, const intx4 &a, const intx4 &b) { c = mma16<DT>(a, b, c); });
+        wait_vmcnt<0>();
+        __syncthreads();
+        if (x + 2 < more) {
+            const AdapterSource next = source(x + 2);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) copy_more(next, la, lb, c);
+        }
+    }
+    wait_vmcnt<0>();  // the zero-fill copies past the last k-tile have landed
+    __syncthreads();  // every wave is done with the operand buffers
+    DMP_LDS char *slab = wave == 0 ? LA[0] : wave == 1 ? LB[0] : wave == 2 ? LA[1] : LB[1];
+    static_assert(32 * (WTN + 4) * 4 <= OpA::BYTES && 32 * (WTN + 4) * 4 <= OpB::BYTES, "slab must fit");
+    const EpiParams &ep = p.r.ep;
+    const int64_t first = at.row0 * p.r.ldc + at.col0;
+    store_wave_tile<WTM, WTN>((DMP_LDS float *)slab, ep, (const char *)p.r.C + first * out_size(ep.c_type),
+                              (char *)p.r.D + first * out_size(ep.d_type), p.r.ldc, at.rows, at.cols, wm * WTM,
+                              wn * WTN, lane, [&](int i, int j) { return acc[i][j]; });
+}
+
+// The product of few rows by K-contiguous W and B_a (decoding), as skinny.hpp: a workgroup
+// takes 16 TN columns, its waves split K and stream W into matrix-instruction operands; then
+// each takes its share of the requests and streams their B_a, and the sums meet in LDS.
+// Rows go 16 TM at a time.  A request's products are summed apart and added to its rows.
+template <class DT, int TM, int TN>
+__global__ __launch_bounds__(512, 2) void adapter_skinny(const AdapterArgs p) {
+    constexpr int NW = 8, BM = 16 * TM, U = TM + TN <= 2 ? 4 : TM + TN <= 5 ? 2 : 1, CW = 16 * TN, SZ = BM * CW;
+    __shared__ __attribute__((aligned(16))) float lds[NW * SZ];
+    __shared__ AdapterEntry lists[NW][BM];
+    const int lane = lane_id(), wave = wave_id(), r16 = lane & 15, total = (int)p.r.M, K = (int)p.r.K;
+    const int64_t col0 = (int64_t)workgroup_id() * CW;
+    if (col0 >= p.r.N) return;
+    const int cols = (int)min((int64_t)CW, p.r.N - col0);
+    const int last = __builtin_amdgcn_readfirstlane(load_offset(p.r, p.r.groups, total));
+    const int nkt = (K + 63) / 64, per = (nkt + NW - 1) / NW, kt0 = min(wave * per, nkt), kt1 = min(kt0 + per, nkt);
+    const int kend = min(K, kt1 * 64);
+    const __amdgpu_buffer_rsrc_t rw = make_rsrc((const char *)p.r.B + col0 * p.r.ldb * 2);
+    DMP_LDS AdapterEntry *list = (DMP_LDS AdapterEntry *)lists[wave];
+    for (int row0 = __builtin_amdgcn_readfirstlane(load_offset(p.r, 0, total)); row0 < last; row0 += BM) {
+        const int rows = min(BM, last - row0);
+        const __amdgpu_buffer_rsrc_t rx = make_rsrc((const char *)p.r.A + row0 * p.r.lda * 2);
+        floatx4 acc[TM][TN] = {};
+        intx4 fx[2][U][TM][2], fw[2][U][TN][2];
+        int xo[TM], wo[TN];
+#pragma unroll
+        for (int i = 0; i < TM; ++i) xo[i] = row_part(i * 16 + r16, rows, p.r.lda);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) wo[j] = row_part(j * 16 + r16, cols, p.r.ldb);
+        auto load = [&](int st, int kt) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int ko = k_part((kt + u) * 64 + 32 * h + 8 * (lane >> 4), kend);
+#pragma unroll
+                    for (int j = 0; j < TN; ++j) fw[st][u][j][h] = load_granule(rw, joined(wo[j], ko));
+#pragma unroll
+                    for (int i = 0; i < TM; ++i) fx[st][u][i][h] = load_granule(rx, joined(xo[i], ko));
+                }
+            issued();
+        };
+        auto multiply = [&](int st) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < TM; ++i)
+#pragma unroll
+                        for (int j = 0; j < TN; ++j) acc[i][j] = mma16<DT>(fx[st][u][i][h], fw[st][u][j][h], acc[i][j]);
+        };
+        if (kt0 < kt1) load(0, kt0);
+        // the requests of these rows, while the first loads are on their way
+        const int entries = adapter_entries<BM>(p, row0, rows, list);
+        for (int kt = kt0; kt < kt1; kt += 2 * U) {
+            load(1, kt + U);
+            multiply(0);
+            load(0, kt + 2 * U);
+            multiply(1);
+        }
+        // this wave's requests, EB at a time: all their loads before the first product
+        constexpr int EB = 4;
+        const __amdgpu_buffer_rsrc_t rh = make_rsrc(p.H + row0 * (int64_t)p.rp * 2);
+        for (int e0 = wave; e0 < entries; e0 += NW * EB)
+            for (int kr = 0; kr < p.rank; kr += 32) {
+                const int k = kr + 8 * (lane >> 4);
+                intx4 fb[EB][TN];
+                int lo[EB], hi[EB];
+#pragma unroll
+                for (int b = 0; b < EB; ++b) {
+                    const int e = e0 + NW * b;
+                    const bool there = e < entries;
+                    const int rr = __builtin_amdgcn_readfirstlane(there ? list[e].rows : 0);
+                    const int a = __builtin_amdgcn_readfirstlane(there ? list[e].adapter : 0);
+                    lo[b] = rr & 0xffff;
+                    hi[b] = (int)((uint32_t)rr >> 16);
+                    const __amdgpu_buffer_rsrc_t rb = make_rsrc((const char *)p.B + (a * p.sB + col0 * p.ldb) * 2);
+#pragma unroll
+                    for (int j = 0; j < TN; ++j) {
+                        const int c = j * 16 + r16;
+                        fb[b][j] = load_granule(rb, there && c < cols && k < p.rank ? (c * (int)p.ldb + k) * 2 : OOB_OFFSET);
+                    }
+                }
+                for (int part = 0; part < p.parts; ++part) {
+                    const __amdgpu_buffer_rsrc_t rp = part ? make_rsrc(p.H + (p.r.M + row0) * (int64_t)p.rp * 2) : rh;
+#pragma unroll
+                    for (int i = 0; i < TM; ++i) {
+                        const int r = i * 16 + r16;
+                        const intx4 fh = load_granule(rp, r < rows && k < p.rank ? (r * p.rp + k) * 2 : OOB_OFFSET);
+                        const int mine = 16 * i + 4 * (lane >> 4);
+#pragma unroll
+                        for (int b = 0; b < EB; ++b) {
+                            if (hi[b] <= 16 * i || lo[b] >= 16 * i + 16) continue;
+#pragma unroll
+                            for (int j = 0; j < TN; ++j) {
+                                const floatx4 c = mma16<DT>(fh, fb[b][j], floatx4{0, 0, 0, 0});
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    acc[i][j][q] += mine + q >= lo[b] && mine + q < hi[b] ? c[q] : 0.0f;
+                            }
+                        }
                     }
                 }
             }
-            multiply((nkt - 1) % 2);
-        }
-        if (pass < 0 && all > 0 && __syncthreads_or(odd)) continue;
-        __syncthreads();
-        store_wave_tile<WTM, WTN, true>((DMP_LDS float *)slab, ep, (const char *)p.r.C + first * out_size(ep.c_type),
-                                        (char *)p.r.D + first * out_size(ep.d_type), p.r.ldc, q.hi, at.cols, wm * WTM,
-                                        wn * WTN, lane, [&](int i, int j) { return acc[i][j]; }, q.lo);
-        if (pass < 0) break;
-        __syncthreads();
+        step_sync();
+        __syncthreads();  // the sums of the rows before are read
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    lds[wave * SZ + (i * 16 + 4 * (lane >> 4) + q) * CW + j * 16 + r16] = acc[i][j][q];
+        join_waves<NW, CW, SZ>(p.r, lds, row0, rows, col0, cols);
     }
 }
 

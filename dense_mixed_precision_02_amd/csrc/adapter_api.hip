@@ -31,7 +31,8 @@ int run_hidden(const AdapterArgs &a, bool a_col, bool fast, hipStream_t s) {
     if (!a_col) return fast ? launch_hidden<DT, 1, 0, true>(a, s) : launch_hidden<DT, 1, 0, false>(a, s);
     if (!fast) return launch_hidden<DT, 1, 1, false>(a, s);
     if (a.r.M <= 32 * (int64_t)a.r.groups) return launch_hidden<DT, 1, 1, true>(a, s);
-    return a.rank <= 16 ? launch_hidden<DT, 4, 1, true>(a, s) : launch_hidden<DT, 4, 2, true>(a, s);
+    if (a.rank <= 16) return launch_hidden<DT, 2, 1, true>(a, s);
+    return a.rank <= 32 ? launch_hidden<DT, 2, 2, true>(a, s) : launch_hidden<DT, 2, 4, true>(a, s);
 }
 
 template <class DT, int BM, int BN, int WM, int WN, bool BKC, bool FAST>
@@ -40,18 +41,33 @@ int launch_staged(AdapterArgs a, hipStream_t s) {
     return launch(adapter_staged<DT, BM, BN, WM, WN, BKC, FAST>, cdiv(a.r.M, BM) * a.r.tiles_n, WM * WN * 64, s, a);
 }
 
+template <class DT, int TM, int TN>
+int launch_skinny(const AdapterArgs &a, hipStream_t s) {
+    return launch(adapter_skinny<DT, TM, TN>, cdiv(a.r.N, 16 * TN), 512, s, a);
+}
+
 template <class DT, bool BKC>
-int run_product(const AdapterArgs &a, bool fast, hipStream_t s) {
-    return fast ? launch_staged<DT, 128, 128, 2, 2, BKC, true>(a, s) : launch_staged<DT, 64, 128, 1, 4, BKC, false>(a, s);
+int run_product(const AdapterArgs &a, int cfg, hipStream_t s) {
+    if constexpr (BKC) {
+        if (cfg == CFG_SKINNY1) return launch_skinny<DT, 1, 1>(a, s);
+        if (cfg == CFG_SKINNY2) return launch_skinny<DT, 2, 1>(a, s);
+        if (cfg == CFG_SKINNY4) return launch_skinny<DT, 4, 1>(a, s);
+    }
+    if (cfg == CFG_L) {
+        AdapterArgs b = a;
+        b.r.tiles_n = (int)cdiv(a.r.N, 256);
+        return launch(adapter_tile<DT, BKC>, cdiv(a.r.M, 256) * b.r.tiles_n, 256, s, b);
+    }
+    return cfg == CFG_M ? launch_staged<DT, 128, 128, 2, 2, BKC, true>(a, s) : launch_staged<DT, 64, 128, 1, 4, BKC, false>(a, s);
 }
 
 template <class DT>
-int run_adapters(const AdapterArgs &a, bool a_col, bool b_col, bool hidden_f, bool fast, hipStream_t s) {
+int run_adapters(const AdapterArgs &a, bool a_col, bool b_col, bool hidden_f, int cfg, hipStream_t s) {
     if (a.r.K > 0 || a.hidden) {
         const int rc = run_hidden<DT>(a, a_col, hidden_f, s);
         if (rc != GEMM_OK) return rc;
     }
-    return b_col ? run_product<DT, true>(a, fast, s) : run_product<DT, false>(a, fast, s);
+    return b_col ? run_product<DT, true>(a, cfg, s) : run_product<DT, false>(a, cfg, s);
 }
 
 }  // namespace
@@ -92,10 +108,10 @@ int gemm_run_adapters(gemm_handle_t h, const void *X, const void *W, const gemm_
     a.rp = (int)adapter_rp(ad->rank);
     a.parts = adapter_parts(d_type);
     a.hidden = hidden; a.ld_hidden = ld_hidden;
-    const bool fast = K > 0 && product_fast(X, W, *ad, M, N, K, ldx, ldw, bc);
+    const int cfg = adapter_cfg(h->num_cus, X, W, *ad, M, N, K, ldx, ldw, bc);
     const bool hf = K > 0 && hidden_fast(X, *ad, K, ldx, ac);
     hipStream_t s = (hipStream_t)stream;
-    return dtype == GEMM_F16 ? run_adapters<F16>(a, ac, bc, hf, fast, s) : run_adapters<BF16>(a, ac, bc, hf, fast, s);
+    return dtype == GEMM_F16 ? run_adapters<F16>(a, ac, bc, hf, cfg, s) : run_adapters<BF16>(a, ac, bc, hf, cfg, s);
 }
 
 }  // extern "C"

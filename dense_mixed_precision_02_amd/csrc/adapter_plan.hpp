@@ -64,5 +64,15 @@ inline bool product_fast(const void *X, const void *W, const gemm_adapters_t &ad
            granule_ok(ad.B, ad.B, M, N, b_col ? ad.rank : 8, 8, ad.ldb, GEMM_F16, false, b_col, true);
 }
 
+// Which product kernel (CFG_GENERIC: any alignment).
+inline int adapter_cfg(int num_cus, const void *X, const void *W, const gemm_adapters_t &ad, int64_t M, int64_t N,
+                       int64_t K, int64_t ldx, int64_t ldw, bool b_col) {
+    if (K == 0 || !product_fast(X, W, ad, M, N, K, ldx, ldw, b_col)) return CFG_GENERIC;
+    const int64_t t128 = cdiv(M, 128) * cdiv(N, 128);
+    if (b_col && (M <= 64 || (M <= 256 && 2 * t128 <= num_cus)))
+        return M <= 16 ? CFG_SKINNY1 : M <= 32 ? CFG_SKINNY2 : CFG_SKINNY4;
+    return M >= 192 && t128 > 2 * (int64_t)num_cus ? CFG_L : CFG_M;
+}
+
 }  // namespace plan
 }  // namespace dmp

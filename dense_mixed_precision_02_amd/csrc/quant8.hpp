@@ -105,10 +105,11 @@ __device__ static inline void block_scale(uint32_t amax_bits, int pow2, float &s
     factor = F8_TOP<FMT> / a;
 }
 
-// An element on its way to 8 bits (after the block's maximum is taken).
-template <int XT, int FMT>
-__device__ static inline float in_range(float x, int pow2) {
-    return pow2 ? fminf(fmaxf(x, -F8_IN_X<XT, FMT>), F8_IN_X<XT, FMT>) : x;
+// Elements on their way to 8 bits with a power of two (after the block's maximum is taken).
+template <int XT, int FMT, int N>
+__device__ static inline void clamp_pow2(float (&x)[N]) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) x[e] = __builtin_amdgcn_fmed3f(x[e], -F8_IN_X<XT, FMT>, F8_IN_X<XT, FMT>);
 }
 
 // Four values times the factor, rounded to 8 bits, in one word.
@@ -163,8 +164,7 @@ __global__ __launch_bounds__(256) void quant8_rows(const Quant8Args p) {
         if ((lane & 7) == 0) sc[lane >> 3][wave * PER + t] = s;
         const int64_t i = m0 + wave * PER + t;
         if (i < p.M && k < p.Kp) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[t][e] = in_range<XT, FMT>(x[t][e], p.pow2);
+            if (p.pow2) clamp_pow2<XT, FMT>(x[t]);
             intx4 v;
 #pragma unroll
             for (int w = 0; w < 4; ++w)
@@ -242,10 +242,10 @@ __global__ __launch_bounds__(256) void quant8_tile(const Quant8Args p) {
             p.scale[(b * p.KB + kb) * p.MB + i0 + tid] = s;
         }
     }
+    if (p.pow2) {
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x[t][e] = in_range<XT, FMT>(x[t][e], p.pow2);
+        for (int t = 0; t < 4; ++t) clamp_pow2<XT, FMT>(x[t]);
+    }
     if constexpr (COL) {
 #pragma unroll
         for (int e = 0; e < 16; ++e)

@@ -61,12 +61,11 @@ __device__ static inline void grouped_order(int t, int tiles_m, int tiles_n, int
 // point at the tile's first element.  Accumulators (`get(i, j)`: instruction
 // block i, j; lane L, register G: row 4 (L / 16) + G, column L % 16) pass
 // through the wave's LDS slab, 32 rows at a time, so that C and D move as
-// vectors of four.  LOW: rows before `low` are not stored either.
-template <int WTM, int WTN, bool LOW = false, class Get>
+// vectors of four.
+template <int WTM, int WTN, class Get>
 __device__ static inline void store_wave_tile(DMP_LDS float *slab, const EpiParams &ep, const char *Cb,
                                               char *Db, int64_t ldc, int rows, int cols, int r0,
-                                              int c0, int lane, Get get, int low = 0) {
-    auto stored = [&](int row) { return row < rows && (!LOW || row >= low); };
+                                              int c0, int lane, Get get) {
     constexpr int TN = WTN / 16, SP = WTN + 4;
     constexpr int LPR = WTN / 4, RPP = 64 / LPR, PASSES = 32 / RPP;
     const bool c_f16 = ep.c_type == OUT_F16, d_f16 = ep.d_type == OUT_F16;
@@ -97,7 +96,7 @@ __device__ static inline void store_wave_tile(DMP_LDS float *slab, const EpiPara
                     dst[u] = floatx4{0, 0, 0, 0};
                     if constexpr (CS != 0) {
                         const int r = q * 32 + u * RPP;
-                        if (stored(r0 + r + rl))
+                        if (r0 + r + rl < rows)
                             dst[u] = load4s<float, CS>(Cb, at + r * ldc, c_f16, true, 4);
                     }
                 }
@@ -112,7 +111,7 @@ __device__ static inline void store_wave_tile(DMP_LDS float *slab, const EpiPara
                 for (int u = 0; u < PASSES; ++u) {
                     const floatx4 v = *(const DMP_LDS floatx4 *)(slab + (u * RPP + rl) * SP + cl);
                     const int r = q * 32 + u * RPP;
-                    if (stored(r0 + r + rl))
+                    if (r0 + r + rl < rows)
                         store4s<float, DS>(Db, at + r * ldc, finish4(v, cv[q & 1][u], ep), d_f16, true, 4);
                 }
                 __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
@@ -125,7 +124,7 @@ __device__ static inline void store_wave_tile(DMP_LDS float *slab, const EpiPara
 #pragma unroll 1
             for (int u = 0; u < PASSES; ++u) {
                 const int r = q * 32 + u * RPP;
-                const int n = stored(r0 + r + rl) ? cols_in(cols, c0 + cl) : 0;
+                const int n = r0 + r + rl < rows ? cols_in(cols, c0 + cl) : 0;
                 floatx4 c = {0, 0, 0, 0};
                 if constexpr (CS != 0) c = load4s<float, CS>(Cb, at + r * ldc, c_f16, vec, n);
                 const floatx4 v = *(const DMP_LDS floatx4 *)(slab + (u * RPP + rl) * SP + cl);
