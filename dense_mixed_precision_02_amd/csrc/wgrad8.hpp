@@ -53,6 +53,10 @@ __device__ static inline void widen16(const intx4 &q, float s, intx4 (&out)[2]) 
     }
 }
 
+__device__ static inline intx4 load_granule_at(__amdgpu_buffer_rsrc_t r, int off) {
+    return __builtin_bit_cast(intx4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+
 // This lane's granules (16 columns of a row) of a k-tile of X, widened into the panel Op.
 template <class DT, int FMT, int R, int NW, int PAD>
 struct Widened {
@@ -85,7 +89,7 @@ struct Widened {
         for (int j = 0; j < CPW; ++j) {
             const int kk = k + KSTEP * j, row = kt * 64 + kk;
             const bool ok = in && row < span;
-            v[j] = __builtin_bit_cast(intx4, __builtin_amdgcn_raw_buffer_load_b128(rs, ok ? kk * ld + mn : OOB_OFFSET, 0, 0));
+            v[j] = load_granule_at(rs, ok ? kk * ld + mn : OOB_OFFSET);
             s[j] = sc[(int64_t)min(row, span - 1) * sa_row];  // a row that exists
         }
     }
@@ -221,6 +225,148 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void wgrad8_tile(const Wgrad8Args p
     DMP_LDS char *slab = wave < INA ? (DMP_LDS char *)&lds_a[0][0] + wave * SLAB
                                     : (DMP_LDS char *)&lds_b[0][0] + (wave - INA) * SLAB;
     const int64_t first = (int64_t)split * p.part + at.group * r.sC + at.row0 * r.ldc + at.col0;
+    store_wave_tile<WTM, WTN>((DMP_LDS float *)slab, r.ep, (const char *)r.C + first * out_size(r.ep.c_type),
+                              (char *)r.D + first * out_size(r.ep.d_type), r.ldc, at.rows, at.cols, wm * WTM,
+                              wn * WTN, lane, [&](int i, int j) { return acc[i][j]; });
+}
+
+// 256 x 256 tiles on four waves, each 128 x 128 with its accumulators tied in place
+// (tile16_gemm.hpp).  Four waves read 128 KB of fragments from LDS for a k-tile where eight
+// of 128 x 64 read 192, next to 64 written: 1536 cycles of LDS beside 2048 of the
+// matrix units.  One wave to a SIMD has nothing beside it, so everything is spread
+// over the gaps between the matrix instructions (which leave 12 of 16 cycles): in the
+// k-tile's first half the fragments of the second, and the next k-tile's granules from
+// registers into LDS, X's widened on the way, each followed by the load of the one
+// after it; in the second half, behind the barrier, the next k-tile's first fragments.
+template <class DT, int FMT>
+__global__ __launch_bounds__(256) void wgrad8_large_tile(const Wgrad8Args p) {
+    constexpr int BM = 256, BN = 256, WN = 2, NW = 4, WTM = 128, WTN = 128, TM = 8, TN = 8, NI = TM * TN;
+    using SA = Widened<DT, FMT, BM, NW, 32>;
+    using SB = Staged<DT, BN, NW, false, true, 32>;
+    __shared__ __attribute__((aligned(1024))) char lds_a0[SA::Op::BYTES];
+    __shared__ __attribute__((aligned(1024))) char lds_b0[SB::Op::BYTES];
+    __shared__ __attribute__((aligned(1024))) char lds_a1[SA::Op::BYTES];
+    __shared__ __attribute__((aligned(1024))) char lds_b1[SB::Op::BYTES];
+    DMP_LDS char *LA[2] = {(DMP_LDS char *)lds_a0, (DMP_LDS char *)lds_a1};
+    DMP_LDS char *LB[2] = {(DMP_LDS char *)lds_b0, (DMP_LDS char *)lds_b1};
+    const int lane = lane_id(), wave = wave_id();
+    const int wm = wave / WN, wn = wave % WN;
+    TileAt at;
+    int split, row0;
+    if (!wgrad8_at<DT, BM, BN>(p, lane, at, split, row0)) return;
+    const RaggedArgs &r = p.r;
+    const int nkt = at.k / 64 + (at.k % 64 != 0);
+    floatx4 acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = floatx4{0, 0, 0, 0};
+    auto pin_acc = [&]() {  // see tile16_gemm
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) asm volatile("" : "+a"(acc[i][j]));
+    };
+    if (nkt > 0) {
+        SA a;
+        SB b;
+        a.init(r, at.A, row0, at.row0, at.rows, at.k, wave, lane);
+        b.init(at.B, wave, lane, r.ldb, at.cols);
+        intx4 ra[SA::CPW], rb[SB::CPW];
+        float rs[SA::CPW];
+        const int srow = (int)r.sa_row * 4;
+        auto load_a = [&](int kt, int j) {
+            const __amdgpu_buffer_rsrc_t q = make_rsrc(a.base + (int64_t)kt * 64 * a.ld);
+            const __amdgpu_buffer_rsrc_t f = make_rsrc(r.sa + (row0 + (int64_t)kt * 64) * r.sa_row + (at.row0 >> 7) * r.sa_k);
+            const int kk = a.k + SA::KSTEP * j;
+            const bool ok = a.in && kt * 64 + kk < at.k;
+            ra[j] = load_granule_at(q, ok ? kk * a.ld + a.mn : OOB_OFFSET);
+            // (a row past the end: the factor 0)
+            rs[j] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(f, ok ? kk * srow + (a.mn >> 7) * (int)r.sa_k * 4 : OOB_OFFSET, 0, 0));
+        };
+        auto load_b = [&](int kt, int j) {
+            const __amdgpu_buffer_rsrc_t q = make_rsrc(SB::Op::tile_base(b.base, b.ld, 0, (int64_t)kt * 64));
+            const bool ok = b.op.fixed < at.cols && b.op.row_or_k + SB::Op::KSTEP * j < at.k - kt * 64;
+            rb[j] = load_granule_at(q, ok ? b.op.off0 + j * b.op.step : OOB_OFFSET);
+        };
+        auto put_a = [&](int buf, int j) {
+            intx4 w[2];
+            widen16<DT, FMT>(ra[j], rs[j], w);
+            DMP_LDS char *to = LA[buf] + a.at + j * (SA::KSTEP / 4) * SA::Op::ROW_BYTES;
+            *(DMP_LDS intx4 *)to = w[0];
+            *(DMP_LDS intx4 *)(to + 16) = w[1];
+        };
+        auto put_b = [&](int buf, int j) {
+            *(DMP_LDS intx4 *)(LB[buf] + SB::Op::chunk_offset(j * NW + wave) + lane * 16) = rb[j];
+        };
+        intx4 fa[2][TM], fb[2][TN];
+        auto read_one = [&](int buf, int s, int x) {
+            if (x < TN) fb[s][x] = frag16<DT, typename SB::Op, BN, false>(LB[buf], wn * WTN + x * 16, s, lane);
+            else fa[s][x - TN] = frag16<DT, typename SA::Op, BM, false>(LA[buf], wm * WTM + (x - TN) * 16, s, lane);
+        };
+        auto ktile = [&](int kt, int cur) {
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    Mma16<DT>::run(acc[i][j], fa[0][i], fb[0][j]);
+                    const int q = i * TN + j;
+                    if (slot_has(q, TM + TN, NI)) read_one(cur, 1, q * (TM + TN) / NI);
+                    if (slot_has(q, SB::CPW, NI)) {
+                        const int c = q * SB::CPW / NI;
+                        put_b(cur ^ 1, c);
+                        load_b(kt + 2, c);
+                    }
+                    if (slot_has(q, SA::CPW, NI)) {
+                        const int c = q * SA::CPW / NI;
+                        put_a(cur ^ 1, c);
+                        load_a(kt + 2, c);
+                    }
+                }
+            step_sync();
+            barrier_vmcnt<63>();
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    Mma16<DT>::run(acc[i][j], fa[1][i], fb[1][j]);
+                    const int q = i * TN + j;
+                    if (slot_has(q, TM + TN, NI)) read_one(cur ^ 1, 0, q * (TM + TN) / NI);
+                }
+            step_sync();
+        };
+#pragma unroll
+        for (int j = 0; j < SA::CPW; ++j) load_a(0, j);
+#pragma unroll
+        for (int j = 0; j < SB::CPW; ++j) load_b(0, j);
+#pragma unroll
+        for (int j = 0; j < SA::CPW; ++j) {
+            put_a(0, j);
+            load_a(1, j);
+        }
+#pragma unroll
+        for (int j = 0; j < SB::CPW; ++j) {
+            put_b(0, j);
+            load_b(1, j);
+        }
+        barrier_vmcnt<63>();
+#pragma unroll
+        for (int x = 0; x < TM + TN; ++x) read_one(0, 0, x);
+        pin_acc();
+        asm volatile("s_nop 7" ::);
+        // two k-tiles to a trip so that each buffer is named statically; an odd count
+        // runs one zero-filled k-tile more
+        for (int kt = 0; kt < nkt; kt += 2) {
+            ktile(kt, 0);
+            ktile(kt + 1, 1);
+        }
+        mma_drain();
+        pin_acc();
+    }
+    __syncthreads();
+    DMP_LDS char *slab = wave == 0 ? LA[0] : wave == 1 ? LB[0] : wave == 2 ? LA[1] : LB[1];
+    static_assert(32 * (WTN + 4) * 4 <= SA::Op::BYTES && 32 * (WTN + 4) * 4 <= SB::Op::BYTES, "slab must fit");
+    const int64_t first = at.group * r.sC + at.row0 * r.ldc + at.col0;
     store_wave_tile<WTM, WTN>((DMP_LDS float *)slab, r.ep, (const char *)r.C + first * out_size(r.ep.c_type),
                               (char *)r.D + first * out_size(r.ep.d_type), r.ldc, at.rows, at.cols, wm * WTM,
                               wn * WTN, lane, [&](int i, int j) { return acc[i][j]; });

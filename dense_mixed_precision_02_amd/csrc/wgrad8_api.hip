@@ -20,24 +20,25 @@ int launch(void (*kernel)(Args), int64_t workgroups, int threads, hipStream_t s,
     return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
 }
 
-template <class DT, int FMT, int BM, int BN, int WM, int WN, bool FAST>
-int launch_tile(gemm_handle_t h, Wgrad8Args a, hipStream_t s) {
+// per_cu: workgroups that a CU holds
+int launch_tile(gemm_handle_t h, void (*kernel)(Wgrad8Args), int BM, int BN, int threads, int per_cu, Wgrad8Args a, hipStream_t s) {
     RaggedArgs &r = a.r;
     r.tiles_m = (int)cdiv(r.M, BM);
     r.tiles_n = (int)cdiv(r.N, BN);
     const int64_t tiles = (int64_t)r.tiles_m * r.tiles_n;
     // runs of tiles on an XCD: as many as it works on at a time, but every XCD gets some
-    r.run = (int)std::max<int64_t>(1, std::min<int64_t>(h->num_cus / 8 * (8 / (WM * WN)), cdiv(r.groups * tiles, 8)));
+    r.run = (int)std::max<int64_t>(1, std::min<int64_t>(h->num_cus / 8 * per_cu, cdiv(r.groups * tiles, 8)));
     const int64_t units = cdiv(r.groups * cdiv(tiles, r.run), 8) * 8 * r.run;
     if (units > 0x7fffffff) return GEMM_ERR_INVALID_ARG;
     a.units = (int)units;
-    return launch(wgrad8_tile<DT, FMT, BM, BN, WM, WN, FAST>, units * a.splits, WM * WN * 64, s, a);
+    return launch(kernel, units * a.splits, threads, s, a);
 }
 
 template <class DT, int FMT>
 int launch_wgrad8(gemm_handle_t h, bool large, bool fast, const Wgrad8Args &a, hipStream_t s) {
-    if (!fast) return launch_tile<DT, FMT, 64, 128, 1, 4, false>(h, a, s);
-    return large ? launch_tile<DT, FMT, 256, 256, 2, 4, true>(h, a, s) : launch_tile<DT, FMT, 64, 128, 1, 4, true>(h, a, s);
+    if (!fast) return launch_tile(h, wgrad8_tile<DT, FMT, 64, 128, 1, 4, false>, 64, 128, 256, 2, a, s);
+    if (large) return launch_tile(h, wgrad8_large_tile<DT, FMT>, 256, 256, 256, 1, a, s);
+    return launch_tile(h, wgrad8_tile<DT, FMT, 64, 128, 1, 4, true>, 64, 128, 256, 2, a, s);
 }
 
 }  // namespace
@@ -74,7 +75,7 @@ int gemm_run_wgrad8(gemm_handle_t h, const gemm_q8_t *X, const void *Y, const vo
         a.part = groups * M * N;
     }
     hipStream_t s = (hipStream_t)stream;
-    const bool large = wgrad8_large(h->num_cus, groups, M, N), fast = K > 0 && wgrad8_fast(Y, N, ldy);
+    const bool large = wgrad8_large(h->num_cus, groups, M, N) && wgrad8_narrow(*X), fast = K > 0 && wgrad8_fast(Y, N, ldy);
     const bool e4 = X->type == GEMM_E4M3;
     int st;
     if (dtype == GEMM_F16) st = e4 ? launch_wgrad8<F16, 0>(h, large, fast, a, s) : launch_wgrad8<F16, 1>(h, large, fast, a, s);

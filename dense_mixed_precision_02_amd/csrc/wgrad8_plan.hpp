@@ -49,6 +49,9 @@ inline int validate_wgrad8(gemm_handle_t h, const gemm_q8_t *X, const void *Y, c
     return check_outputs(C, D, ep);
 }
 
+// The large tiles read X's factors by 31-bit offsets inside a k-tile.
+inline bool wgrad8_narrow(const gemm_q8_t &X) { return X.scale_row < (1ll << 22) && X.scale_k < (1ll << 26); }
+
 // Can Y's 16-byte granules be loaded whole?
 inline bool wgrad8_fast(const void *Y, int64_t N, int64_t ldy) {
     return aligned16(Y) && N % 8 == 0 && ldy % 8 == 0 && 128 * ldy < (1ll << 31) - (1ll << 22);
