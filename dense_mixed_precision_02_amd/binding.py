@@ -101,7 +101,7 @@ def load_library():
         lib.gemm_run_scaled8.argtypes = [vp, ctypes.POINTER(Q8Operand), ctypes.POINTER(Q8Operand), vp, vp,
                                          vp, i64, i64, i64, i64, i64, cu, cf, cf, ci, ci, vp]
         lib.gemm_adapters_work.restype = i64
-        lib.gemm_adapters_work.argtypes = [vp, i64, i64, ci]
+        lib.gemm_adapters_work.argtypes = [vp, i64, i64, i64, i64, i64, ci]
         lib.gemm_run_adapters.restype = ci
         lib.gemm_run_adapters.argtypes = [vp, vp, vp, ctypes.POINTER(AdapterOperands), vp, vp, vp, i64, i64, i64, i64,
                                           i64, i64, i64, ci, cu, cf, cf, ci, ci, vp, i64, vp, vp]
@@ -226,9 +226,9 @@ class Handle:
                                                groups, M, N, K, ldc, flags, alpha, beta, c_type, d_type,
                                                stream)
 
-    def adapters_work(self, M, rank, d_type) -> int:
+    def adapters_work(self, requests, M, N, K, rank, d_type) -> int:
         """Bytes of scratch that run_adapters() needs (-1: sizes that are refused)."""
-        return load_library().gemm_adapters_work(self.ptr, M, rank, d_type)
+        return load_library().gemm_adapters_work(self.ptr, requests, M, N, K, rank, d_type)
 
     def run_adapters(self, X, W, adapters: AdapterOperands, C, D, offsets, requests, M, N, K, ldx, ldw, ldc, dtype,
                      flags=0, alpha=1.0, beta=0.0, c_type=GEMM_OUT_F32, d_type=GEMM_OUT_F32, hidden=0, ld_hidden=0,
@@ -865,7 +865,7 @@ def gemm_adapters(X, W, A, B, offsets, ids=None, scale=None, C=None, out=None, a
     flags |= (GEMM_B_COLMAJOR if col else 0) | (GEMM_ADAPTER_A_COLMAJOR if a_col else 0)
 
     def call(h, stream):
-        work = torch.empty(max(h.adapters_work(T, rank, d_code), 16), dtype=torch.uint8, device=device)
+        work = torch.empty(max(h.adapters_work(requests, T, N, K, rank, d_code), 16), dtype=torch.uint8, device=device)
         return h.run_adapters(X.data_ptr(), W.data_ptr(), operands, c, out.data_ptr(), offsets.data_ptr(), requests, T, N,
                               K, ldx, ldw, ldc, dt, flags, alpha, beta, c_code, d_code,
                               hidden.data_ptr() if hidden is not None else 0, ld_hidden, work.data_ptr(), stream)

@@ -259,35 +259,73 @@ struct AdapterEntry {
     int adapter;
 };
 
-// By one wave; returns their number (at most BM: no two share a row).
+// What a list of a tile's requests is made from, this lane's of 64 requests: loaded ahead of
+// other loads, so that it arrives first.
+struct RequestLoad {
+    int start, end, adapter;  // first row of all the requests; this one's end; its adapter
+};
+__device__ static inline RequestLoad load_requests(const AdapterArgs &p, int chunk, int lane) {
+    const int g = chunk + lane, total = (int)p.r.M;
+    RequestLoad q;
+    q.start = load_offset(p.r, 0, total);
+    q.end = g < p.r.groups ? load_offset(p.r, g + 1, total) : 0;
+    q.adapter = g < p.r.groups ? adapter_of(p, g) : -1;
+    return q;
+}
+
+// The largest of this lane's value and those before it.
+__device__ static inline int scan_max(int v) {
+    // (row offsets are not negative: a lane that a move does not reach gets 0)
+    v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false));  // row_shr:1, 2, 4, 8
+    v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false));
+    v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false));
+    v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false));
+    v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false));  // row_bcast:15, :31
+    return max(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false));
+}
+
+// By one wave; returns their number (at most BM: no two share a row, since each
+// request's end is the largest so far, as in GroupWalk).
 template <int BM>
-__device__ static inline int adapter_entries(const AdapterArgs &p, int row0, int rows, DMP_LDS AdapterEntry *list) {
-    const int lane = lane_id(), total = (int)p.r.M;
-    const int own = first_adapters(p, lane);
-    GroupWalk<BM> walk;
-    walk.load(p.r, total, lane);
-    int n = 0;
-    do {
-        const int lo = max(walk.lo, row0) - row0, hi = min(walk.hi, row0 + rows) - row0;
-        int a = -1;
-        if (lo < hi) a = walk.chunk == 0 ? own : adapter_of(p, walk.chunk + lane);  // (a request with rows is none past the last)
-        const uint64_t has = __ballot(a >= 0);
-        if (a >= 0) {
+__device__ static inline int adapter_entries(const AdapterArgs &p, int row0, int rows, DMP_LDS AdapterEntry *list, RequestLoad q) {
+    const int lane = lane_id();
+    int n = 0, from = __builtin_amdgcn_readfirstlane(q.start);
+    for (int chunk = 0;; chunk += 64) {
+        const int end = max(scan_max(q.end), from);
+        int start = __shfl_up(end, 1, 64);
+        if (lane == 0) start = from;
+        const int lo = max(start, row0) - row0, hi = min(end, row0 + rows) - row0;
+        const bool mine = lo < hi && q.adapter >= 0;
+        const uint64_t has = __ballot(mine);
+        if (mine) {
             const int at = n + __popcll(has & ((1ull << lane) - 1));
             list[at].rows = lo | hi << 16;
-            list[at].adapter = a;
+            list[at].adapter = q.adapter;
         }
         n += __popcll(has);
-    } while (__builtin_amdgcn_readlane(walk.hi, 63) < row0 + rows && walk.next(p.r, total, lane));
-    return n;
+        from = __builtin_amdgcn_readlane(end, 63);
+        if (from >= row0 + rows || chunk + 64 >= p.r.groups) return n;
+        q = load_requests(p, chunk + 64, lane);
+    }
+}
+template <int BM>
+__device__ static inline int adapter_entries(const AdapterArgs &p, int row0, int rows, DMP_LDS AdapterEntry *list) {
+    return adapter_entries<BM>(p, row0, rows, list, load_requests(p, 0, lane_id()));
+}
+
+// Row number i of the offsets (0 .. groups), by a scalar load: it waits for no vector load.
+__device__ static inline int scalar_offset(const RaggedArgs &p, int i, int total) {
+    typedef const __attribute__((address_space(4))) int32_t *words;
+    const words o = (words)p.offsets;
+    const int lo = p.off32 ? o[i] : o[2 * (int64_t)i], hi = p.off32 ? lo >> 31 : o[2 * (int64_t)i + 1];
+    return hi < 0 ? 0 : (hi > 0 || (uint32_t)lo > (uint32_t)total) ? total : lo;
 }
 
 // This workgroup's tile of the rows that the requests own; false: it has none.
 template <int BM, int BN, class DT, bool BKC>
 __device__ static inline bool adapter_tile_at(const AdapterArgs &p, TileAt &at) {
     const int total = (int)p.r.M;
-    const int first = __builtin_amdgcn_readfirstlane(load_offset(p.r, 0, total));
-    const int last = __builtin_amdgcn_readfirstlane(load_offset(p.r, p.r.groups, total));
+    const int first = scalar_offset(p.r, 0, total), last = scalar_offset(p.r, p.r.groups, total);
     if (last <= first) return false;
     const int tiles_m = (last - first - 1) / BM + 1, id = workgroup_id();
     const int64_t tiles = (int64_t)tiles_m * p.r.tiles_n;

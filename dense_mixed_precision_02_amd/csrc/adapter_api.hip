@@ -4,6 +4,7 @@
 
 #include "../../include/dmp_gemm.h"
 #include "adapter.hpp"
+#include "adapter_few.hpp"
 #include "adapter_plan.hpp"
 #include "handle.hpp"
 
@@ -12,7 +13,8 @@ using namespace dmp::plan;
 
 namespace {
 
-int launch(void (*kernel)(AdapterArgs), int64_t workgroups, int threads, hipStream_t s, const AdapterArgs &a) {
+template <class Args>
+int launch(void (*kernel)(Args), int64_t workgroups, int threads, hipStream_t s, const Args &a) {
     GridShape g;
     if (!grid_shape(workgroups, g)) return GEMM_ERR_INVALID_ARG;  // beyond one launch's grid
     hipLaunchKernelGGL(kernel, dim3(g.x, g.y), dim3((unsigned)threads), 0, s, a);
@@ -49,8 +51,6 @@ int launch_skinny(const AdapterArgs &a, hipStream_t s) {
 template <class DT, bool BKC>
 int run_product(const AdapterArgs &a, int cfg, hipStream_t s) {
     if constexpr (BKC) {
-        if (cfg == CFG_SKINNY1) return launch_skinny<DT, 1, 1>(a, s);
-        if (cfg == CFG_SKINNY2) return launch_skinny<DT, 2, 1>(a, s);
         if (cfg == CFG_SKINNY4) return launch_skinny<DT, 4, 1>(a, s);
     }
     if (cfg == CFG_L) {
@@ -61,8 +61,33 @@ int run_product(const AdapterArgs &a, int cfg, hipStream_t s) {
     return cfg == CFG_M ? launch_staged<DT, 128, 128, 2, 2, BKC, true>(a, s) : launch_staged<DT, 64, 128, 1, 4, BKC, false>(a, s);
 }
 
+template <class DT, int BM>
+int launch_few(const AdapterFewArgs &f, hipStream_t s) {
+    const int64_t grid = (int64_t)f.blocks * f.splits;
+    const int rc = f.per <= 4   ? launch(adapter_few<DT, BM, 4>, grid, 256, s, f)
+                   : f.per <= 8 ? launch(adapter_few<DT, BM, 8>, grid, 256, s, f)
+                                : launch(adapter_few<DT, BM, 16>, grid, 256, s, f);
+    if (rc != GEMM_OK) return rc;
+    const int64_t join = cdiv(f.a.r.N, 16);
+    return f.a.parts > 1 ? launch(adapter_few_join<DT, BM, 2>, join, 512, s, f) : launch(adapter_few_join<DT, BM, 1>, join, 512, s, f);
+}
+
 template <class DT>
-int run_adapters(const AdapterArgs &a, bool a_col, bool b_col, bool hidden_f, int cfg, hipStream_t s) {
+int run_few(int num_cus, const AdapterArgs &a, hipStream_t s) {
+    const FewPlan q = few_plan(num_cus, a.r.groups, a.r.M, a.r.N, a.r.K, a.rank);
+    AdapterFewArgs f{};
+    f.a = a;
+    f.splits = q.splits; f.per = q.per; f.blocks = q.blocks;
+    f.r16 = (int)cdiv(a.rank, 16) * 16;
+    f.part = (float *)a.H;
+    f.hpart = (float *)(a.H + q.splits * (cdiv(a.r.M * a.r.N * 4, 16) * 16));
+    if (a.r.M <= 16) return launch_few<DT, 16>(f, s);
+    return a.r.M <= 32 ? launch_few<DT, 32>(f, s) : launch_few<DT, 64>(f, s);
+}
+
+template <class DT>
+int run_adapters(int num_cus, const AdapterArgs &a, bool a_col, bool b_col, bool hidden_f, int cfg, hipStream_t s) {
+    if (cfg == CFG_SKINNY1) return run_few<DT>(num_cus, a, s);
     if (a.r.K > 0 || a.hidden) {
         const int rc = run_hidden<DT>(a, a_col, hidden_f, s);
         if (rc != GEMM_OK) return rc;
@@ -74,9 +99,11 @@ int run_adapters(const AdapterArgs &a, bool a_col, bool b_col, bool hidden_f, in
 
 extern "C" {
 
-int64_t gemm_adapters_work(gemm_handle_t h, int64_t M, int64_t rank, int d_type) {
-    if (!h || M < 0 || M > SIZE_MAX_1 || rank < 1 || rank > ADAPTER_RANK_MAX || !float_out(d_type)) return -1;
-    return adapter_work(M, rank, d_type);
+int64_t gemm_adapters_work(gemm_handle_t h, int64_t requests, int64_t M, int64_t N, int64_t K, int64_t rank, int d_type) {
+    if (!h || requests < 0 || requests > GROUPS_MAX || M < 0 || N < 0 || K < 0 || M > SIZE_MAX_1 || N > SIZE_MAX_1 || K > SIZE_MAX_1 || rank < 1 ||
+        rank > ADAPTER_RANK_MAX || !float_out(d_type))
+        return -1;
+    return adapter_work(h->num_cus, requests, M, N, K, rank, d_type);
 }
 
 int gemm_run_adapters(gemm_handle_t h, const void *X, const void *W, const gemm_adapters_t *ad, const void *C, void *D,
@@ -108,10 +135,11 @@ int gemm_run_adapters(gemm_handle_t h, const void *X, const void *W, const gemm_
     a.rp = (int)adapter_rp(ad->rank);
     a.parts = adapter_parts(d_type);
     a.hidden = hidden; a.ld_hidden = ld_hidden;
-    const int cfg = adapter_cfg(h->num_cus, X, W, *ad, M, N, K, ldx, ldw, bc);
+    const int cfg = adapter_cfg(h->num_cus, X, W, *ad, M, N, K, ldx, ldw, ac, bc);
     const bool hf = K > 0 && hidden_fast(X, *ad, K, ldx, ac);
     hipStream_t s = (hipStream_t)stream;
-    return dtype == GEMM_F16 ? run_adapters<F16>(a, ac, bc, hf, cfg, s) : run_adapters<BF16>(a, ac, bc, hf, cfg, s);
+    return dtype == GEMM_F16 ? run_adapters<F16>(h->num_cus, a, ac, bc, hf, cfg, s)
+                              : run_adapters<BF16>(h->num_cus, a, ac, bc, hf, cfg, s);
 }
 
 }  // extern "C"

@@ -1,0 +1,310 @@
+// adapter_few.hpp -- adapters beside a shared projection for few rows (decoding: up to 64 rows).
+//
+// With few rows the time is that of reading W (and the adapters) once, and of what has to
+// wait for what.  As hidden and product (adapter.hpp) three reads follow each other: A_a,
+// then W, then B_a.  Here the projection's part is split over K as well as over columns,
+// enough to give every CU its share, and has no need of the hidden rows:
+//
+//   adapter_few       A workgroup takes 64 columns (16 to a wave) and up to 1024 of K.  Its
+//                     part of X goes straight to LDS, its part of W straight into
+//                     matrix-instruction operands, everything on its way at once.  With X in LDS
+//                     it also computes hidden sums over its K: 16 columns of A_a for one
+//                     request, the requests dealt out over the workgroups.  All sums go to
+//                     memory in 32 bits.
+//   adapter_few_join  A workgroup takes 16 columns: the K parts' sums in their order, the
+//                     hidden rows scaled and rounded, each request's product with B_a, and
+//                     the output stage.  The sums are read while B_a is on its way.
+#pragma once
+#include "adapter.hpp"
+
+namespace dmp {
+
+struct AdapterFewArgs {
+    AdapterArgs a;
+    float *part;        // splits x M x N: sums of the projection
+    float *hpart;       // splits x M x r16: sums of the hidden rows
+    int r16;            // rank, rounded up to 16
+    int splits, per;    // parts of K, and k-tiles of 64 in each
+    int blocks;         // workgroups to a part: cdiv(N, 64) or more
+};
+
+// BM: rows (at least those there are); KT: k-tiles to a part at most
+template <class DT, int BM, int KT>
+__global__ __launch_bounds__(256, 1) void adapter_few(const AdapterFewArgs p) {
+    constexpr int NW = 4, TM = BM / 16, RC = BM / 8, HT = (KT + NW - 1) / NW;
+    __shared__ __attribute__((aligned(1024))) char lds_x[KT * BM * 128];
+    __shared__ float red[NW][BM * 16];
+    __shared__ AdapterEntry lists[NW][BM];
+    const AdapterArgs &a = p.a;
+    const RaggedArgs &r = a.r;
+    const int lane = lane_id(), wave = wave_id(), r16 = lane & 15, total = (int)r.M, K = (int)r.K;
+    const int id = workgroup_id(), split = id / p.blocks, cb = id - split * p.blocks;
+    if (split >= p.splits) return;
+    const int kt0 = split * p.per, nkt = min(p.per, (K + 63) / 64 - kt0), kend = min(K, (kt0 + nkt) * 64);
+    const int64_t col0 = (int64_t)cb * 64 + wave * 16;
+    const int cols = (int)max((int64_t)0, min((int64_t)16, r.N - col0));
+    // In the order in which they are needed first: the requests, X, W.
+    const RequestLoad requests = load_requests(a, 0, lane);
+    issued();
+    const int first = scalar_offset(r, 0, total), rows = min(BM, scalar_offset(r, r.groups, total) - first);
+    if (rows <= 0) return;
+    // X's part: 1 KB (8 rows of a k-tile) to a copy
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc((const char *)r.A + first * r.lda * 2);
+    // (a wave's copies are of rows whose number in eights has its own parity, so that one swizzle serves)
+    constexpr int XC = RC >= NW ? RC / NW : 1, XT = RC >= NW ? 1 : NW / RC;  // copies to a k-tile; k-tiles at a time
+    int xo[XC];
+#pragma unroll
+    for (int j = 0; j < XC; ++j) xo[j] = row_part((wave + NW * j) % RC * 8 + (lane >> 3), rows, r.lda);
+    const int xk = ((lane & 7) ^ swz((wave & 1) * 8 + (lane >> 3))) * 8;
+    // (all KT k-tiles: zeros past the part's end, so that nothing below depends on how many there are)
+#pragma unroll
+    for (int t0 = 0; t0 < KT; t0 += XT) {
+        const int t = XT > 1 ? t0 + wave / RC : t0;
+        const int ko = k_part((kt0 + t) * 64 + xk, kend);
+#pragma unroll
+        for (int j = 0; j < XC; ++j)
+            load_granule_to_lds(rx, (DMP_LDS char *)lds_x + t * (BM * 128) + (wave + NW * j) % RC * 1024, joined(xo[j], ko));
+    }
+    // W's: this wave's columns
+    const __amdgpu_buffer_rsrc_t rw = make_rsrc((const char *)r.B + min(col0, r.N - 1) * r.ldb * 2);
+    const int wo = row_part(r16, cols, r.ldb);
+    intx4 fw[KT][2];
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            fw[t][h] = load_granule(rw, joined(wo, k_part((kt0 + t) * 64 + 32 * h + 8 * (lane >> 4), kend)));
+    issued();
+    DMP_LDS AdapterEntry *list = (DMP_LDS AdapterEntry *)lists[wave];
+    const int entries = adapter_entries<BM>(a, first, rows, list, requests);
+    // hidden sums: 16 columns of an entry's A_a, the waves take its k-tiles in turn
+    const int rt = p.r16 / 16, tasks = entries * rt;
+    intx4 fa[HT][2];
+    int task = cb, e = 0, rc = 0;
+    auto load_a = [&]() {
+        e = __builtin_amdgcn_readfirstlane(task / rt);
+        rc = __builtin_amdgcn_readfirstlane(task - e * rt) * 16;
+        const int ad = __builtin_amdgcn_readfirstlane(list[e].adapter);
+        const __amdgpu_buffer_rsrc_t ra = make_rsrc((const char *)a.A + (ad * a.sA + rc * a.lda) * 2);
+        const int ao = row_part(r16, a.rank - rc, a.lda);
+#pragma unroll
+        for (int t = 0; t < HT; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                fa[t][h] = load_granule(ra, joined(ao, k_part((kt0 + wave + NW * t) * 64 + 32 * h + 8 * (lane >> 4), kend)));
+        issued();
+    };
+    if (task < tasks) load_a();
+    wait_vmcnt<0>();
+    __syncthreads();
+    auto fragX = [&](int t, int h, int i) {
+        const int row = i * 16 + r16, g = 4 * h + (lane >> 4);
+        return *(const DMP_LDS intx4 *)((const DMP_LDS char *)lds_x + t * (BM * 128) + row * 128 + ((g ^ swz(row)) << 4));
+    };
+    while (task < tasks) {
+        const int rr = __builtin_amdgcn_readfirstlane(list[e].rows), lo = rr & 0xffff, hi = (int)((uint32_t)rr >> 16);
+        floatx4 acc[TM] = {};
+#pragma unroll
+        for (int t = 0; t < HT; ++t) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+                    if (hi > 16 * i && lo < 16 * i + 16) acc[i] = mma16<DT>(fragX(wave + NW * t, h, i), fa[t][h], acc[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) red[wave][(i * 16 + 4 * (lane >> 4) + q) * 16 + r16] = acc[i][q];
+        const int at = rc;
+        task += p.blocks;
+        if (task < tasks) load_a();
+        barrier_vmcnt<63>();
+        for (int x = lo * 16 + threadIdx.x; x < hi * 16; x += 256) {
+            float v = red[0][x];
+#pragma unroll
+            for (int w = 1; w < NW; ++w) v += red[w][x];
+            p.hpart[((int64_t)split * r.M + first + x / 16) * p.r16 + at + x % 16] = v;
+        }
+        barrier_vmcnt<63>();
+    }
+    if (cols <= 0) return;
+    floatx4 acc[TM] = {};
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < TM; ++i) acc[i] = mma16<DT>(fragX(t, h, i), fw[t][h], acc[i]);
+    }
+    float *out = p.part + ((int64_t)split * r.M + first) * r.N + col0 + r16;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int row = i * 16 + 4 * (lane >> 4) + q;
+            if (row < rows && r16 < cols) out[(int64_t)row * r.N] = acc[i][q];
+        }
+}
+
+__device__ static inline float load_float(__amdgpu_buffer_rsrc_t r, int off) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+}
+
+// Parts s .. s + 3 of sums that lie `step` floats apart, as many as there are, each thread's
+// values at byte offsets `at`: all loads before the first addition.
+template <int N>
+__device__ static inline void add_parts(const float *base, int s, int parts, int64_t step, const int (&at)[N], float (&sum)[N]) {
+    float v[4][N];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const __amdgpu_buffer_rsrc_t q = make_rsrc(base + min(s + j, parts - 1) * step);
+#pragma unroll
+        for (int m = 0; m < N; ++m) v[j][m] = load_float(q, s + j < parts ? at[m] : OOB_OFFSET);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int m = 0; m < N; ++m) sum[m] += v[j][m];
+}
+
+constexpr int FEW_RANK = 128;  // of the hidden rows in LDS
+
+// BM: rows (at least those there are); PARTS: numbers that a hidden value is kept in
+template <class DT, int BM, int PARTS>
+__global__ __launch_bounds__(512, 2) void adapter_few_join(const AdapterFewArgs p) {
+    constexpr int NW = 8, TM = BM / 16, LD = FEW_RANK + 8, EB = BM / NW, MINE = (BM * 16 + 511) / 512, HEACH = (BM * 32 + 511) / 512;
+    constexpr bool f16 = std::is_same_v<DT, F16>;
+    __shared__ __attribute__((aligned(16))) uint16_t hl[PARTS][BM][LD];
+    __shared__ float red[NW][BM * 16];
+    __shared__ AdapterEntry lists[NW][BM];
+    __shared__ int owner[BM];
+    __shared__ float scales[BM];
+    const AdapterArgs &a = p.a;
+    const RaggedArgs &r = a.r;
+    const int lane = lane_id(), wave = wave_id(), r16 = lane & 15, total = (int)r.M, tid = threadIdx.x;
+    const int64_t col0 = (int64_t)workgroup_id() * 16;
+    if (col0 >= r.N) return;
+    const int cols = (int)min((int64_t)16, r.N - col0);
+    const RequestLoad requests = load_requests(a, 0, lane);
+    const int first = scalar_offset(r, 0, total), rows = min(BM, scalar_offset(r, r.groups, total) - first);
+    if (rows <= 0) return;
+    // (barrier_vmcnt: only LDS is exchanged, and what is on its way stays so)
+    if (tid < BM) owner[tid] = 0;
+    barrier_vmcnt<63>();
+    DMP_LDS AdapterEntry *list = (DMP_LDS AdapterEntry *)lists[wave];
+    const int entries = adapter_entries<BM>(a, first, rows, list, requests);
+    float scale = 1.0f;  // of entry `lane`
+    if (wave == 0 && lane < entries && a.scale) scale = a.scale[list[lane].adapter];
+    // this wave's entries (wave, wave + NW, ...: EB at most), 32 of the rank at a time
+    const int nk = (a.rank + 31) / 32;
+    intx4 fb[2][EB];
+    auto load_b = [&](int st, int kb) {
+        const int ko = k_part(kb * 32 + 8 * (lane >> 4), a.rank), co = row_part(r16, cols, a.ldb);
+#pragma unroll
+        for (int x = 0; x < EB; ++x) {
+            const int e = wave + NW * x;
+            const int ad = __builtin_amdgcn_readfirstlane(e < entries ? list[e].adapter : 0);
+            const __amdgpu_buffer_rsrc_t rb = make_rsrc((const char *)a.B + (ad * a.sB + col0 * a.ldb) * 2);
+            fb[st][x] = load_granule(rb, e < entries ? joined(co, ko) : OOB_OFFSET);
+        }
+        issued();
+    };
+    load_b(0, 0);
+    // sums of the K parts: of the hidden rows, 32 columns at a time (row x / 32, column x % 32), and of
+    // the projection (row x / 16, column x % 16).  (Rows without an adapter have none: they are not used.)
+    float hsum[HEACH] = {}, sum[MINE] = {};
+    auto load_h = [&](int kb) {
+        int at[HEACH];
+#pragma unroll
+        for (int m = 0; m < HEACH; ++m) {
+            const int x = tid + 512 * m, row = x / 32, c = kb * 32 + x % 32;
+            at[m] = row < rows && c < a.rank ? (row * p.r16 + c) * 4 : OOB_OFFSET;
+            hsum[m] = 0.0f;
+        }
+        for (int s = 0; s < p.splits; s += 4) add_parts(p.hpart + (int64_t)first * p.r16, s, p.splits, r.M * p.r16, at, hsum);
+    };
+    load_h(0);
+    int at[MINE];
+#pragma unroll
+    for (int m = 0; m < MINE; ++m) {
+        const int x = tid + 512 * m, row = x / 16, c = x % 16;
+        at[m] = row < rows && c < cols ? (row * (int)r.N + c) * 4 : OOB_OFFSET;
+    }
+    for (int s = 0; s < p.splits; s += 4) add_parts(p.part + (int64_t)first * r.N + col0, s, p.splits, r.M * r.N, at, sum);
+    if (wave == 0 && lane < entries) {  // whose rows have an adapter
+        const int rr = list[lane].rows;
+        for (int x = rr & 0xffff; x < (int)((uint32_t)rr >> 16); ++x) {
+            owner[x] = 1;
+            scales[x] = scale;
+        }
+    }
+    barrier_vmcnt<63>();
+    // the hidden rows, scaled and rounded; zeros past the rank and for rows without an adapter
+    for (int kb = 0; kb < nk; ++kb) {
+        if (kb) load_h(kb);
+#pragma unroll
+        for (int m = 0; m < HEACH; ++m) {
+            const int x = tid + 512 * m, row = x / 32, c = kb * 32 + x % 32;
+            if (row >= BM) continue;
+            const float v = owner[row] ? hsum[m] * scales[row] : 0.0f;
+            const uint16_t hi = encode16(v, f16);
+            hl[0][row][c] = hi;
+            if constexpr (PARTS > 1) {
+                const float left = v - decode16(hi, f16);
+                hl[1][row][c] = encode16(__builtin_isfinite(left) ? left : 0.0f, f16);
+            }
+            if (a.hidden && workgroup_id() == 0 && row < rows && c < a.rank)
+                ((uint16_t *)a.hidden)[(int64_t)(first + row) * a.ld_hidden + c] = hi;
+        }
+    }
+    barrier_vmcnt<63>();
+    floatx4 acc[TM] = {};
+    auto multiply = [&](int st, int kb) {
+        intx4 fh[PARTS][TM];
+#pragma unroll
+        for (int w = 0; w < PARTS; ++w)
+#pragma unroll
+            for (int i = 0; i < TM; ++i) fh[w][i] = *(const intx4 *)&hl[w][i * 16 + r16][kb * 32 + 8 * (lane >> 4)];
+#pragma unroll
+        for (int x = 0; x < EB; ++x) {
+            const int e = wave + NW * x;
+            if (e >= entries) continue;
+            const int rr = __builtin_amdgcn_readfirstlane(list[e].rows), lo = rr & 0xffff, hi = (int)((uint32_t)rr >> 16);
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                if (hi <= 16 * i || lo >= 16 * i + 16) continue;
+                floatx4 c = {0, 0, 0, 0};
+#pragma unroll
+                for (int w = 0; w < PARTS; ++w) c = mma16<DT>(fh[w][i], fb[st][x], c);
+                const int at = 16 * i + 4 * (lane >> 4) - lo;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) acc[i][q] += (uint32_t)(at + q) < (uint32_t)(hi - lo) ? c[q] : 0.0f;
+            }
+        }
+    };
+    for (int kb = 0; kb < nk; kb += 2) {
+        load_b(1, kb + 1);
+        multiply(0, kb);
+        load_b(0, kb + 2);
+        if (kb + 1 < nk) multiply(1, kb + 1);
+    }
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) red[wave][(i * 16 + 4 * (lane >> 4) + q) * 16 + r16] = acc[i][q];
+    barrier_vmcnt<63>();
+#pragma unroll
+    for (int m = 0; m < MINE; ++m) {
+        const int x = tid + 512 * m, row = x / 16, c = x % 16;
+        if (row >= rows || c >= cols) continue;
+        float v = sum[m];
+#pragma unroll
+        for (int w = 0; w < NW; ++w) v += red[w][x];
+        const int64_t at = (int64_t)(first + row) * r.ldc + col0 + c;
+        const floatx4 cv = r.ep.use_c ? load4<float>(r.C, at, r.ep.c_type, false, 1) : floatx4{0, 0, 0, 0};
+        store4<float>(r.D, at, finish4(floatx4{v, 0, 0, 0}, cv, r.ep), r.ep.d_type, false, 1);
+    }
+}
+
+}  // namespace dmp

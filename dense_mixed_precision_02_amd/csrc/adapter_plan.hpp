@@ -11,7 +11,35 @@ constexpr int64_t ADAPTER_RANK_MAX = 1024;
 
 inline int64_t adapter_rp(int64_t rank) { return cdiv(rank, 8) * 8; }
 inline int adapter_parts(int d_type) { return d_type == GEMM_OUT_F32 ? 2 : 1; }
-inline int64_t adapter_work(int64_t M, int64_t rank, int d_type) { return adapter_parts(d_type) * M * adapter_rp(rank) * 2; }
+
+// Up to 64 rows (adapter_few.hpp): parts of K, of at most 16 k-tiles of 64 and of 2 at least,
+// as many as give every CU a workgroup of the columns' or of the hidden sums'.
+struct FewPlan {
+    int splits, per, blocks;
+};
+inline FewPlan few_plan(int num_cus, int64_t requests, int64_t M, int64_t N, int64_t K, int64_t rank) {
+    FewPlan f;
+    const int64_t nkt = cdiv(K, 64), nb = cdiv(N, 64), tasks = std::min(M, requests) * cdiv(rank, 16);
+    const int64_t wide = std::max(nb, tasks);
+    const int64_t want = std::max(cdiv(nkt, 16), std::min<int64_t>(num_cus / std::min<int64_t>(wide, num_cus), cdiv(nkt, 2)));
+    f.per = (int)cdiv(nkt, want);
+    f.splits = (int)cdiv(nkt, f.per);
+    // workgroups past the columns' for hidden sums: two to a CU at most
+    f.blocks = (int)std::max(nb, std::min<int64_t>(tasks, std::max<int64_t>(1, 2 * num_cus / f.splits)));
+    return f;
+}
+constexpr int64_t FEW_ROWS = 64, FEW_RANK_MAX = 128, FEW_N_MAX = 1 << 22;  // N: 31-bit offsets in 64 rows of sums
+inline int64_t few_work(int splits, int64_t M, int64_t N, int64_t rank) {
+    return splits * (cdiv(M * N * 4, 16) * 16 + cdiv(M * cdiv(rank, 16) * 64, 16) * 16);
+}
+
+// Scratch: the hidden rows, or the sums of the K parts.
+inline int64_t adapter_work(int num_cus, int64_t requests, int64_t M, int64_t N, int64_t K, int64_t rank, int d_type) {
+    int64_t b = adapter_parts(d_type) * M * adapter_rp(rank) * 2;
+    if (M > 0 && N > 0 && K > 0 && requests > 0 && M <= FEW_ROWS && rank <= FEW_RANK_MAX && N <= FEW_N_MAX)
+        b = std::max(b, few_work(few_plan(num_cus, requests, M, N, K, rank).splits, M, N, rank));
+    return b;
+}
 
 inline int validate_adapters(gemm_handle_t h, const void *X, const void *W, const gemm_adapters_t *ad, const void *C,
                              const void *D, const void *offsets, int64_t requests, int64_t M, int64_t N, int64_t K,
@@ -64,13 +92,13 @@ inline bool product_fast(const void *X, const void *W, const gemm_adapters_t &ad
            granule_ok(ad.B, ad.B, M, N, b_col ? ad.rank : 8, 8, ad.ldb, GEMM_F16, false, b_col, true);
 }
 
-// Which product kernel (CFG_GENERIC: any alignment).
+// Which product kernel (CFG_GENERIC: any alignment; CFG_SKINNY1: the kernels for few rows).
 inline int adapter_cfg(int num_cus, const void *X, const void *W, const gemm_adapters_t &ad, int64_t M, int64_t N,
-                       int64_t K, int64_t ldx, int64_t ldw, bool b_col) {
+                       int64_t K, int64_t ldx, int64_t ldw, bool a_col, bool b_col) {
     if (K == 0 || !product_fast(X, W, ad, M, N, K, ldx, ldw, b_col)) return CFG_GENERIC;
+    if (b_col && a_col && M <= FEW_ROWS && ad.rank <= FEW_RANK_MAX && N <= FEW_N_MAX && hidden_fast(X, ad, K, ldx, a_col)) return CFG_SKINNY1;
     const int64_t t128 = cdiv(M, 128) * cdiv(N, 128);
-    if (b_col && (M <= 64 || (M <= 256 && 2 * t128 <= num_cus)))
-        return M <= 16 ? CFG_SKINNY1 : M <= 32 ? CFG_SKINNY2 : CFG_SKINNY4;
+    if (b_col && M <= 256 && 2 * t128 <= num_cus) return CFG_SKINNY4;
     return M >= 192 && t128 > 2 * (int64_t)num_cus ? CFG_L : CFG_M;
 }
 
