@@ -29,14 +29,21 @@
 
 namespace dmp {
 
+// The requests: their row offsets (groups + 1, int32_t if off32, else int64_t) and adapters.
+struct RequestTable {
+    const void *offsets;
+    const int32_t *ids;      // adapter of each request, or NULL: its number
+    int groups, adapters, off32, rows;
+};
+
 struct AdapterArgs {
     RaggedArgs r;            // A: X; B: W; groups, offsets: the requests
+    RequestTable t;
     const void *A, *B;       // the adapters'
-    const int32_t *ids;      // adapter of each request, or NULL: its number
     const float *scale;      // of each adapter, or NULL: 1
     int64_t lda, ldb;        // leading dimensions of A_a, B_a
     int64_t sA, sB;          // elements from one adapter's to the next
-    int adapters, rank;
+    int rank;
     char *H;                 // parts x M x rp 16-bit values, zeros from rank to rp
     int rp, parts;
     void *hidden;            // M x rank, ld_hidden apart, or NULL: H for the caller
@@ -45,18 +52,17 @@ struct AdapterArgs {
 };
 
 // Request g's adapter; -1: none.
-__device__ static inline int adapter_of(const AdapterArgs &p, int g) {
-    const int a = p.ids ? p.ids[g] : g;
-    return (uint32_t)a < (uint32_t)p.adapters ? a : -1;
+__device__ static inline int adapter_of(const RequestTable &t, int g) {
+    const int a = t.ids ? t.ids[g] : g;
+    return (uint32_t)a < (uint32_t)t.adapters ? a : -1;
 }
-
 // The same of a group found by a walk: `own` is what this lane's group of the first 64 has,
 // loaded along with the offsets.
-__device__ static inline int first_adapters(const AdapterArgs &p, int lane) {
-    return lane < p.r.groups ? adapter_of(p, lane) : -1;
+__device__ static inline int first_adapters(const RequestTable &t, int lane) {
+    return lane < t.groups ? adapter_of(t, lane) : -1;
 }
-__device__ static inline int adapter_of(const AdapterArgs &p, int g, int own) {
-    return __builtin_amdgcn_readfirstlane(g < 64 ? __builtin_amdgcn_readlane(own, g & 63) : adapter_of(p, g));
+__device__ static inline int adapter_of(const RequestTable &t, int g, int own) {
+    return __builtin_amdgcn_readfirstlane(g < 64 ? __builtin_amdgcn_readlane(own, g & 63) : adapter_of(t, g));
 }
 
 // Up to eight 16-bit values from e on, of which n exist (n <= 0: none is touched).
@@ -236,12 +242,12 @@ __global__ __launch_bounds__(HIDDEN_WAVES * 64, 2) void adapter_hidden(const Ada
     __shared__ float lds[HIDDEN_WAVES * SZ];
     const int id = workgroup_id(), lane = lane_id(), total = (int)p.r.M;
     const int tile = id / p.tiles_r, c0 = (id - tile * p.tiles_r) * CW;
-    const int own = first_adapters(p, lane);
+    const int own = first_adapters(p.t, lane);
     GroupWalk<BM> walk;
     walk.load(p.r, total, lane);
     int g, r0, r1, tile0;
     if (!walk.find(p.r, total, lane, tile, g, r0, r1, tile0)) return;
-    const int a = adapter_of(p, g, own);
+    const int a = adapter_of(p.t, g, own);
     if (a < 0 && !p.hidden) return;
     const float scale = p.scale && a >= 0 ? p.scale[a] : 1.0f;
     const int64_t row0 = r0 + (int64_t)(tile - tile0) * BM;
@@ -259,18 +265,33 @@ struct AdapterEntry {
     int adapter;
 };
 
+// A row number of the offsets as its two words, brought into 0 .. rows.
+__device__ static inline int offset_value(int lo, int hi, int rows) {
+    return hi < 0 ? 0 : (hi > 0 || (uint32_t)lo > (uint32_t)rows) ? rows : lo;
+}
 // What a list of a tile's requests is made from, this lane's of 64 requests: loaded ahead of
-// other loads, so that it arrives first.
+// other loads, so that it arrives first, without branches, so that all of it is on its way
+// at once (a 32-bit offset's second word is the first again; requests past the last one: the last).
 struct RequestLoad {
-    int start, end, adapter;  // first row of all the requests; this one's end; its adapter
+    int lo, hi, id;
 };
-__device__ static inline RequestLoad load_requests(const AdapterArgs &p, int chunk, int lane) {
-    const int g = chunk + lane, total = (int)p.r.M;
+__device__ static inline RequestLoad load_requests(const RequestTable &t, int chunk, int lane) {
+    const int g = min(chunk + lane, t.groups - 1), w = t.off32 ? 1 : 2;
+    const int32_t *o = (const int32_t *)t.offsets + (int64_t)(g + 1) * w;
     RequestLoad q;
-    q.start = load_offset(p.r, 0, total);
-    q.end = g < p.r.groups ? load_offset(p.r, g + 1, total) : 0;
-    q.adapter = g < p.r.groups ? adapter_of(p, g) : -1;
+    q.lo = o[0];
+    q.hi = o[w - 1];
+    q.id = t.ids ? t.ids[g] : g;
     return q;
+}
+
+// Row number i of the offsets (0 .. groups), by scalar loads: they wait for no vector load.
+__device__ static inline int scalar_offset(const RequestTable &t, int i) {
+    typedef const __attribute__((address_space(4))) int32_t *words;
+    const int w = t.off32 ? 1 : 2;
+    const words o = (words)t.offsets + (int64_t)i * w;
+    const int lo = o[0], hi = o[w - 1];
+    return offset_value(lo, w == 1 ? lo >> 31 : hi, t.rows);
 }
 
 // The largest of this lane's value and those before it.
@@ -285,47 +306,36 @@ __device__ static inline int scan_max(int v) {
 }
 
 // By one wave; returns their number (at most BM: no two share a row, since each
-// request's end is the largest so far, as in GroupWalk).
+// request's end is the largest so far, as in GroupWalk).  from: the requests' first row.
 template <int BM>
-__device__ static inline int adapter_entries(const AdapterArgs &p, int row0, int rows, DMP_LDS AdapterEntry *list, RequestLoad q) {
+__device__ static inline int adapter_entries(const RequestTable &t, int from, int row0, int rows, DMP_LDS AdapterEntry *list,
+                                             RequestLoad q) {
     const int lane = lane_id();
-    int n = 0, from = __builtin_amdgcn_readfirstlane(q.start);
+    int n = 0;
     for (int chunk = 0;; chunk += 64) {
-        const int end = max(scan_max(q.end), from);
+        const int own = offset_value(q.lo, t.off32 ? q.lo >> 31 : q.hi, t.rows);
+        const int end = max(scan_max(chunk + lane < t.groups ? own : 0), from);
         int start = __shfl_up(end, 1, 64);
         if (lane == 0) start = from;
         const int lo = max(start, row0) - row0, hi = min(end, row0 + rows) - row0;
-        const bool mine = lo < hi && q.adapter >= 0;
+        const bool mine = lo < hi && (uint32_t)q.id < (uint32_t)t.adapters;
         const uint64_t has = __ballot(mine);
         if (mine) {
             const int at = n + __popcll(has & ((1ull << lane) - 1));
             list[at].rows = lo | hi << 16;
-            list[at].adapter = q.adapter;
+            list[at].adapter = q.id;
         }
         n += __popcll(has);
         from = __builtin_amdgcn_readlane(end, 63);
-        if (from >= row0 + rows || chunk + 64 >= p.r.groups) return n;
-        q = load_requests(p, chunk + 64, lane);
+        if (from >= row0 + rows || chunk + 64 >= t.groups) return n;
+        q = load_requests(t, chunk + 64, lane);
     }
-}
-template <int BM>
-__device__ static inline int adapter_entries(const AdapterArgs &p, int row0, int rows, DMP_LDS AdapterEntry *list) {
-    return adapter_entries<BM>(p, row0, rows, list, load_requests(p, 0, lane_id()));
-}
-
-// Row number i of the offsets (0 .. groups), by a scalar load: it waits for no vector load.
-__device__ static inline int scalar_offset(const RaggedArgs &p, int i, int total) {
-    typedef const __attribute__((address_space(4))) int32_t *words;
-    const words o = (words)p.offsets;
-    const int lo = p.off32 ? o[i] : o[2 * (int64_t)i], hi = p.off32 ? lo >> 31 : o[2 * (int64_t)i + 1];
-    return hi < 0 ? 0 : (hi > 0 || (uint32_t)lo > (uint32_t)total) ? total : lo;
 }
 
 // This workgroup's tile of the rows that the requests own; false: it has none.
 template <int BM, int BN, class DT, bool BKC>
 __device__ static inline bool adapter_tile_at(const AdapterArgs &p, TileAt &at) {
-    const int total = (int)p.r.M;
-    const int first = scalar_offset(p.r, 0, total), last = scalar_offset(p.r, p.r.groups, total);
+    const int first = scalar_offset(p.t, 0), last = scalar_offset(p.t, p.t.groups);
     if (last <= first) return false;
     const int tiles_m = (last - first - 1) / BM + 1, id = workgroup_id();
     const int64_t tiles = (int64_t)tiles_m * p.r.tiles_n;
@@ -417,7 +427,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void adapter_staged(const AdapterAr
     TileAt at;
     if (!adapter_tile_at<BM, BN, DT, BKC>(p, at)) return;
     if (wave == 0) {
-        const int n = at.k > 0 ? adapter_entries<BM>(p, (int)at.row0, at.rows, (DMP_LDS AdapterEntry *)list) : 0;
+        const int n = at.k > 0 ? adapter_entries<BM>(p.t, scalar_offset(p.t, 0), (int)at.row0, at.rows, (DMP_LDS AdapterEntry *)list, load_requests(p.t, 0, lane)) : 0;
         if (lane == 0) count = n;
     }
     __syncthreads();
@@ -574,7 +584,7 @@ __global__ __launch_bounds__(256) void adapter_tile(const AdapterArgs p) {
     TileAt at;
     if (!adapter_tile_at<BM, BN, DT, BKC>(p, at)) return;
     if (wave == 0) {
-        const int n = adapter_entries<BM>(p, (int)at.row0, at.rows, (DMP_LDS AdapterEntry *)list);
+        const int n = adapter_entries<BM>(p.t, scalar_offset(p.t, 0), (int)at.row0, at.rows, (DMP_LDS AdapterEntry *)list, load_requests(p.t, 0, lane));
         if (lane == 0) count = n;
     }
     __syncthreads();
@@ -718,16 +728,16 @@ __global__ __launch_bounds__(512, 2) void adapter_skinny(const AdapterArgs p) {
     constexpr int NW = 8, BM = 16 * TM, U = TM + TN <= 2 ? 4 : TM + TN <= 5 ? 2 : 1, CW = 16 * TN, SZ = BM * CW;
     __shared__ __attribute__((aligned(16))) float lds[NW * SZ];
     __shared__ AdapterEntry lists[NW][BM];
-    const int lane = lane_id(), wave = wave_id(), r16 = lane & 15, total = (int)p.r.M, K = (int)p.r.K;
+    const int lane = lane_id(), wave = wave_id(), r16 = lane & 15, K = (int)p.r.K;
     const int64_t col0 = (int64_t)workgroup_id() * CW;
     if (col0 >= p.r.N) return;
     const int cols = (int)min((int64_t)CW, p.r.N - col0);
-    const int last = __builtin_amdgcn_readfirstlane(load_offset(p.r, p.r.groups, total));
+    const int last = scalar_offset(p.t, p.t.groups);
     const int nkt = (K + 63) / 64, per = (nkt + NW - 1) / NW, kt0 = min(wave * per, nkt), kt1 = min(kt0 + per, nkt);
     const int kend = min(K, kt1 * 64);
     const __amdgpu_buffer_rsrc_t rw = make_rsrc((const char *)p.r.B + col0 * p.r.ldb * 2);
     DMP_LDS AdapterEntry *list = (DMP_LDS AdapterEntry *)lists[wave];
-    for (int row0 = __builtin_amdgcn_readfirstlane(load_offset(p.r, 0, total)); row0 < last; row0 += BM) {
+    for (int row0 = scalar_offset(p.t, 0); row0 < last; row0 += BM) {
         const int rows = min(BM, last - row0);
         const __amdgpu_buffer_rsrc_t rx = make_rsrc((const char *)p.r.A + row0 * p.r.lda * 2);
         floatx4 acc[TM][TN] = {};
@@ -762,7 +772,7 @@ __global__ __launch_bounds__(512, 2) void adapter_skinny(const AdapterArgs p) {
         };
         if (kt0 < kt1) load(0, kt0);
         // the requests of these rows, while the first loads are on their way
-        const int entries = adapter_entries<BM>(p, row0, rows, list);
+        const int entries = adapter_entries<BM>(p.t, scalar_offset(p.t, 0), row0, rows, list, load_requests(p.t, 0, lane));
         for (int kt = kt0; kt < kt1; kt += 2 * U) {
             load(1, kt + U);
             multiply(0);

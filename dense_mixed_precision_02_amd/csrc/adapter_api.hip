@@ -62,27 +62,32 @@ int run_product(const AdapterArgs &a, int cfg, hipStream_t s) {
 }
 
 template <class DT, int BM>
-int launch_few(const AdapterFewArgs &f, hipStream_t s) {
+int launch_few(const AdapterFewArgs &f, int parts, hipStream_t s) {
     const int64_t grid = (int64_t)f.blocks * f.splits;
     const int rc = f.per <= 4   ? launch(adapter_few<DT, BM, 4>, grid, 256, s, f)
                    : f.per <= 8 ? launch(adapter_few<DT, BM, 8>, grid, 256, s, f)
                                 : launch(adapter_few<DT, BM, 16>, grid, 256, s, f);
     if (rc != GEMM_OK) return rc;
-    const int64_t join = cdiv(f.a.r.N, 16);
-    return f.a.parts > 1 ? launch(adapter_few_join<DT, BM, 2>, join, 512, s, f) : launch(adapter_few_join<DT, BM, 1>, join, 512, s, f);
+    const int64_t join = cdiv(f.N, 16);
+    return parts > 1 ? launch(adapter_few_join<DT, BM, 2>, join, 512, s, f) : launch(adapter_few_join<DT, BM, 1>, join, 512, s, f);
 }
 
 template <class DT>
 int run_few(int num_cus, const AdapterArgs &a, hipStream_t s) {
-    const FewPlan q = few_plan(num_cus, a.r.groups, a.r.M, a.r.N, a.r.K, a.rank);
+    const FewPlan q = few_plan(num_cus, a.t.groups, a.r.M, a.r.N, a.r.K, a.rank);
     AdapterFewArgs f{};
-    f.a = a;
+    f.t = a.t;
+    f.X = a.r.A; f.W = a.r.B; f.A = a.A; f.B = a.B; f.scale = a.scale;
+    f.M = (int)a.r.M; f.N = (int)a.r.N; f.K = (int)a.r.K;
+    f.ldx = (int)a.r.lda; f.ldw = (int)a.r.ldb; f.lda = (int)a.lda; f.ldb = (int)a.ldb;
+    f.rank = a.rank; f.r16 = (int)cdiv(a.rank, 16) * 16;
     f.splits = q.splits; f.per = q.per; f.blocks = q.blocks;
-    f.r16 = (int)cdiv(a.rank, 16) * 16;
+    f.sA = a.sA; f.sB = a.sB;
+    f.C = a.r.C; f.D = a.r.D; f.hidden = a.hidden; f.ldc = a.r.ldc; f.ld_hidden = a.ld_hidden; f.ep = a.r.ep;
     f.part = (float *)a.H;
     f.hpart = (float *)(a.H + q.splits * (cdiv(a.r.M * a.r.N * 4, 16) * 16));
-    if (a.r.M <= 16) return launch_few<DT, 16>(f, s);
-    return a.r.M <= 32 ? launch_few<DT, 32>(f, s) : launch_few<DT, 64>(f, s);
+    if (a.r.M <= 16) return launch_few<DT, 16>(f, a.parts, s);
+    return a.r.M <= 32 ? launch_few<DT, 32>(f, a.parts, s) : launch_few<DT, 64>(f, a.parts, s);
 }
 
 template <class DT>
@@ -125,11 +130,12 @@ int gemm_run_adapters(gemm_handle_t h, const void *X, const void *W, const gemm_
     r.groups = (int)requests;
     r.off32 = (flags & GEMM_OFFSETS_I32) != 0;
     r.ep = ep;
-    a.A = ad->A; a.B = ad->B; a.ids = ad->ids; a.scale = ad->scale;
+    a.A = ad->A; a.B = ad->B; a.scale = ad->scale;
+    a.t.offsets = offsets; a.t.ids = ad->ids; a.t.groups = (int)requests; a.t.off32 = r.off32; a.t.rows = (int)M;
+    a.t.adapters = K > 0 ? (int)ad->adapters : 0;
     a.lda = ad->lda; a.ldb = ad->ldb;
     a.sA = (ac ? ad->rank : K) * ad->lda;
     a.sB = (bc ? N : ad->rank) * ad->ldb;
-    a.adapters = K > 0 ? (int)ad->adapters : 0;
     a.rank = (int)ad->rank;
     a.H = (char *)work;
     a.rp = (int)adapter_rp(ad->rank);

@@ -20,12 +20,21 @@
 namespace dmp {
 
 struct AdapterFewArgs {
-    AdapterArgs a;
-    float *part;        // splits x M x N: sums of the projection
-    float *hpart;       // splits x M x r16: sums of the hidden rows
-    int r16;            // rank, rounded up to 16
-    int splits, per;    // parts of K, and k-tiles of 64 in each
-    int blocks;         // workgroups to a part: cdiv(N, 64) or more
+    RequestTable t;
+    const void *X, *W, *A, *B;
+    const float *scale;  // of each adapter, or NULL
+    float *part;         // splits x M x N: sums of the projection
+    float *hpart;        // splits x M x r16: sums of the hidden rows
+    int M, N, K;
+    int ldx, ldw, lda, ldb;
+    int rank, r16;       // r16: rank, rounded up to 16
+    int splits, per;     // parts of K, and k-tiles of 64 in each
+    int blocks;          // workgroups to a part: cdiv(N, 64) or more
+    int64_t sA, sB;      // elements from one adapter's A, B to the next
+    const void *C;
+    void *D, *hidden;
+    int64_t ldc, ld_hidden;
+    EpiParams ep;
 };
 
 // BM: rows (at least those there are); KT: k-tiles to a part at most
@@ -35,26 +44,24 @@ __global__ __launch_bounds__(256, 1) void adapter_few(const AdapterFewArgs p) {
     __shared__ __attribute__((aligned(1024))) char lds_x[KT * BM * 128];
     __shared__ float red[NW][BM * 16];
     __shared__ AdapterEntry lists[NW][BM];
-    const AdapterArgs &a = p.a;
-    const RaggedArgs &r = a.r;
-    const int lane = lane_id(), wave = wave_id(), r16 = lane & 15, total = (int)r.M, K = (int)r.K;
+    const int lane = lane_id(), wave = wave_id(), r16 = lane & 15, K = p.K;
     const int id = workgroup_id(), split = id / p.blocks, cb = id - split * p.blocks;
     if (split >= p.splits) return;
     const int kt0 = split * p.per, nkt = min(p.per, (K + 63) / 64 - kt0), kend = min(K, (kt0 + nkt) * 64);
     const int64_t col0 = (int64_t)cb * 64 + wave * 16;
-    const int cols = (int)max((int64_t)0, min((int64_t)16, r.N - col0));
+    const int cols = (int)max((int64_t)0, min((int64_t)16, p.N - col0));
     // In the order in which they are needed first: the requests, X, W.
-    const RequestLoad requests = load_requests(a, 0, lane);
+    const RequestLoad requests = load_requests(p.t, 0, lane);
     issued();
-    const int first = scalar_offset(r, 0, total), rows = min(BM, scalar_offset(r, r.groups, total) - first);
+    const int first = scalar_offset(p.t, 0), rows = min(BM, scalar_offset(p.t, p.t.groups) - first);
     if (rows <= 0) return;
     // X's part: 1 KB (8 rows of a k-tile) to a copy
-    const __amdgpu_buffer_rsrc_t rx = make_rsrc((const char *)r.A + first * r.lda * 2);
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc((const char *)p.X + (int64_t)first * p.ldx * 2);
     // (a wave's copies are of rows whose number in eights has its own parity, so that one swizzle serves)
     constexpr int XC = RC >= NW ? RC / NW : 1, XT = RC >= NW ? 1 : NW / RC;  // copies to a k-tile; k-tiles at a time
     int xo[XC];
 #pragma unroll
-    for (int j = 0; j < XC; ++j) xo[j] = row_part((wave + NW * j) % RC * 8 + (lane >> 3), rows, r.lda);
+    for (int j = 0; j < XC; ++j) xo[j] = row_part((wave + NW * j) % RC * 8 + (lane >> 3), rows, p.ldx);
     const int xk = ((lane & 7) ^ swz((wave & 1) * 8 + (lane >> 3))) * 8;
     // (all KT k-tiles: zeros past the part's end, so that nothing below depends on how many there are)
 #pragma unroll
@@ -66,8 +73,8 @@ __global__ __launch_bounds__(256, 1) void adapter_few(const AdapterFewArgs p) {
             load_granule_to_lds(rx, (DMP_LDS char *)lds_x + t * (BM * 128) + (wave + NW * j) % RC * 1024, joined(xo[j], ko));
     }
     // W's: this wave's columns
-    const __amdgpu_buffer_rsrc_t rw = make_rsrc((const char *)r.B + min(col0, r.N - 1) * r.ldb * 2);
-    const int wo = row_part(r16, cols, r.ldb);
+    const __amdgpu_buffer_rsrc_t rw = make_rsrc((const char *)p.W + min(col0, (int64_t)p.N - 1) * p.ldw * 2);
+    const int wo = row_part(r16, cols, p.ldw);
     intx4 fw[KT][2];
 #pragma unroll
     for (int t = 0; t < KT; ++t)
@@ -76,7 +83,7 @@ __global__ __launch_bounds__(256, 1) void adapter_few(const AdapterFewArgs p) {
             fw[t][h] = load_granule(rw, joined(wo, k_part((kt0 + t) * 64 + 32 * h + 8 * (lane >> 4), kend)));
     issued();
     DMP_LDS AdapterEntry *list = (DMP_LDS AdapterEntry *)lists[wave];
-    const int entries = adapter_entries<BM>(a, first, rows, list, requests);
+    const int entries = adapter_entries<BM>(p.t, first, first, rows, list, requests);
     // hidden sums: 16 columns of an entry's A_a, the waves take its k-tiles in turn
     const int rt = p.r16 / 16, tasks = entries * rt;
     intx4 fa[HT][2];
@@ -85,8 +92,8 @@ __global__ __launch_bounds__(256, 1) void adapter_few(const AdapterFewArgs p) {
         e = __builtin_amdgcn_readfirstlane(task / rt);
         rc = __builtin_amdgcn_readfirstlane(task - e * rt) * 16;
         const int ad = __builtin_amdgcn_readfirstlane(list[e].adapter);
-        const __amdgpu_buffer_rsrc_t ra = make_rsrc((const char *)a.A + (ad * a.sA + rc * a.lda) * 2);
-        const int ao = row_part(r16, a.rank - rc, a.lda);
+        const __amdgpu_buffer_rsrc_t ra = make_rsrc((const char *)p.A + (ad * p.sA + (int64_t)rc * p.lda) * 2);
+        const int ao = row_part(r16, p.rank - rc, p.lda);
 #pragma unroll
         for (int t = 0; t < HT; ++t)
 #pragma unroll
@@ -124,7 +131,7 @@ __global__ __launch_bounds__(256, 1) void adapter_few(const AdapterFewArgs p) {
             float v = red[0][x];
 #pragma unroll
             for (int w = 1; w < NW; ++w) v += red[w][x];
-            p.hpart[((int64_t)split * r.M + first + x / 16) * p.r16 + at + x % 16] = v;
+            p.hpart[((int64_t)split * p.M + first + x / 16) * p.r16 + at + x % 16] = v;
         }
         barrier_vmcnt<63>();
     }
@@ -137,13 +144,13 @@ __global__ __launch_bounds__(256, 1) void adapter_few(const AdapterFewArgs p) {
 #pragma unroll
             for (int i = 0; i < TM; ++i) acc[i] = mma16<DT>(fragX(t, h, i), fw[t][h], acc[i]);
     }
-    float *out = p.part + ((int64_t)split * r.M + first) * r.N + col0 + r16;
+    float *out = p.part + ((int64_t)split * p.M + first) * p.N + col0 + r16;
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const int row = i * 16 + 4 * (lane >> 4) + q;
-            if (row < rows && r16 < cols) out[(int64_t)row * r.N] = acc[i][q];
+            if (row < rows && r16 < cols) out[(int64_t)row * p.N] = acc[i][q];
         }
 }
 
@@ -180,33 +187,33 @@ __global__ __launch_bounds__(512, 2) void adapter_few_join(const AdapterFewArgs 
     __shared__ AdapterEntry lists[NW][BM];
     __shared__ int owner[BM];
     __shared__ float scales[BM];
-    const AdapterArgs &a = p.a;
-    const RaggedArgs &r = a.r;
-    const int lane = lane_id(), wave = wave_id(), r16 = lane & 15, total = (int)r.M, tid = threadIdx.x;
+    const int lane = lane_id(), wave = wave_id(), r16 = lane & 15, tid = threadIdx.x;
     const int64_t col0 = (int64_t)workgroup_id() * 16;
-    if (col0 >= r.N) return;
-    const int cols = (int)min((int64_t)16, r.N - col0);
-    const RequestLoad requests = load_requests(a, 0, lane);
-    const int first = scalar_offset(r, 0, total), rows = min(BM, scalar_offset(r, r.groups, total) - first);
+    if (col0 >= p.N) return;
+    const int cols = (int)min((int64_t)16, p.N - col0);
+    const RequestLoad requests = load_requests(p.t, 0, lane);
+    const int first = scalar_offset(p.t, 0), rows = min(BM, scalar_offset(p.t, p.t.groups) - first);
     if (rows <= 0) return;
     // (barrier_vmcnt: only LDS is exchanged, and what is on its way stays so)
     if (tid < BM) owner[tid] = 0;
     barrier_vmcnt<63>();
     DMP_LDS AdapterEntry *list = (DMP_LDS AdapterEntry *)lists[wave];
-    const int entries = adapter_entries<BM>(a, first, rows, list, requests);
-    float scale = 1.0f;  // of entry `lane`
-    if (wave == 0 && lane < entries && a.scale) scale = a.scale[list[lane].adapter];
+    const int entries = adapter_entries<BM>(p.t, first, first, rows, list, requests);
+    // entry `lane`, where wave 0 needs it, and this wave's entry `lane`
+    const int ia = min(lane, max(entries - 1, 0)), im = min(wave + NW * lane, max(entries - 1, 0));
+    const int all_rows = list[ia].rows, my_rows = list[im].rows, my_adapter = list[im].adapter;
+    float scale = 1.0f;
+    if (wave == 0 && p.scale && entries > 0) scale = p.scale[list[ia].adapter];
     // this wave's entries (wave, wave + NW, ...: EB at most), 32 of the rank at a time
-    const int nk = (a.rank + 31) / 32;
+    const int nk = (p.rank + 31) / 32;
     intx4 fb[2][EB];
     auto load_b = [&](int st, int kb) {
-        const int ko = k_part(kb * 32 + 8 * (lane >> 4), a.rank), co = row_part(r16, cols, a.ldb);
+        const int at = joined(row_part(r16, cols, p.ldb), k_part(kb * 32 + 8 * (lane >> 4), p.rank));
 #pragma unroll
         for (int x = 0; x < EB; ++x) {
-            const int e = wave + NW * x;
-            const int ad = __builtin_amdgcn_readfirstlane(e < entries ? list[e].adapter : 0);
-            const __amdgpu_buffer_rsrc_t rb = make_rsrc((const char *)a.B + (ad * a.sB + col0 * a.ldb) * 2);
-            fb[st][x] = load_granule(rb, e < entries ? joined(co, ko) : OOB_OFFSET);
+            const int64_t ad = __builtin_amdgcn_readlane(my_adapter, x);
+            const __amdgpu_buffer_rsrc_t rb = make_rsrc((const char *)p.B + (ad * p.sB + col0 * p.ldb) * 2);
+            fb[st][x] = load_granule(rb, wave + NW * x < entries ? at : OOB_OFFSET);
         }
         issued();
     };
@@ -219,21 +226,21 @@ __global__ __launch_bounds__(512, 2) void adapter_few_join(const AdapterFewArgs 
 #pragma unroll
         for (int m = 0; m < HEACH; ++m) {
             const int x = tid + 512 * m, row = x / 32, c = kb * 32 + x % 32;
-            at[m] = row < rows && c < a.rank ? (row * p.r16 + c) * 4 : OOB_OFFSET;
+            at[m] = row < rows && c < p.rank ? (row * p.r16 + c) * 4 : OOB_OFFSET;
             hsum[m] = 0.0f;
         }
-        for (int s = 0; s < p.splits; s += 4) add_parts(p.hpart + (int64_t)first * p.r16, s, p.splits, r.M * p.r16, at, hsum);
+        for (int s = 0; s < p.splits; s += 4) add_parts(p.hpart + (int64_t)first * p.r16, s, p.splits, (int64_t)p.M * p.r16, at, hsum);
     };
     load_h(0);
     int at[MINE];
 #pragma unroll
     for (int m = 0; m < MINE; ++m) {
         const int x = tid + 512 * m, row = x / 16, c = x % 16;
-        at[m] = row < rows && c < cols ? (row * (int)r.N + c) * 4 : OOB_OFFSET;
+        at[m] = row < rows && c < cols ? (row * p.N + c) * 4 : OOB_OFFSET;
     }
-    for (int s = 0; s < p.splits; s += 4) add_parts(p.part + (int64_t)first * r.N + col0, s, p.splits, r.M * r.N, at, sum);
+    for (int s = 0; s < p.splits; s += 4) add_parts(p.part + (int64_t)first * p.N + col0, s, p.splits, (int64_t)p.M * p.N, at, sum);
     if (wave == 0 && lane < entries) {  // whose rows have an adapter
-        const int rr = list[lane].rows;
+        const int rr = all_rows;
         for (int x = rr & 0xffff; x < (int)((uint32_t)rr >> 16); ++x) {
             owner[x] = 1;
             scales[x] = scale;
@@ -254,8 +261,8 @@ __global__ __launch_bounds__(512, 2) void adapter_few_join(const AdapterFewArgs 
                 const float left = v - decode16(hi, f16);
                 hl[1][row][c] = encode16(__builtin_isfinite(left) ? left : 0.0f, f16);
             }
-            if (a.hidden && workgroup_id() == 0 && row < rows && c < a.rank)
-                ((uint16_t *)a.hidden)[(int64_t)(first + row) * a.ld_hidden + c] = hi;
+            if (p.hidden && workgroup_id() == 0 && row < rows && c < p.rank)
+                ((uint16_t *)p.hidden)[(int64_t)(first + row) * p.ld_hidden + c] = hi;
         }
     }
     barrier_vmcnt<63>();
@@ -268,9 +275,8 @@ __global__ __launch_bounds__(512, 2) void adapter_few_join(const AdapterFewArgs 
             for (int i = 0; i < TM; ++i) fh[w][i] = *(const intx4 *)&hl[w][i * 16 + r16][kb * 32 + 8 * (lane >> 4)];
 #pragma unroll
         for (int x = 0; x < EB; ++x) {
-            const int e = wave + NW * x;
-            if (e >= entries) continue;
-            const int rr = __builtin_amdgcn_readfirstlane(list[e].rows), lo = rr & 0xffff, hi = (int)((uint32_t)rr >> 16);
+            if (wave + NW * x >= entries) continue;
+            const int rr = __builtin_amdgcn_readlane(my_rows, x), lo = rr & 0xffff, hi = (int)((uint32_t)rr >> 16);
 #pragma unroll
             for (int i = 0; i < TM; ++i) {
                 if (hi <= 16 * i || lo >= 16 * i + 16) continue;
@@ -301,9 +307,9 @@ __global__ __launch_bounds__(512, 2) void adapter_few_join(const AdapterFewArgs 
         float v = sum[m];
 #pragma unroll
         for (int w = 0; w < NW; ++w) v += red[w][x];
-        const int64_t at = (int64_t)(first + row) * r.ldc + col0 + c;
-        const floatx4 cv = r.ep.use_c ? load4<float>(r.C, at, r.ep.c_type, false, 1) : floatx4{0, 0, 0, 0};
-        store4<float>(r.D, at, finish4(floatx4{v, 0, 0, 0}, cv, r.ep), r.ep.d_type, false, 1);
+        const int64_t at = (int64_t)(first + row) * p.ldc + col0 + c;
+        const floatx4 cv = p.ep.use_c ? load4<float>(p.C, at, p.ep.c_type, false, 1) : floatx4{0, 0, 0, 0};
+        store4<float>(p.D, at, finish4(floatx4{v, 0, 0, 0}, cv, p.ep), p.ep.d_type, false, 1);
     }
 }
 
