@@ -779,18 +779,18 @@ def gemm_scaled8(A: Scaled8, B: Scaled8, offsets=None, C=None, out=None, alpha: 
     return out
 
 
-def _layouts(X, rows: int, cols: int, name: str):
-    """{col_major: ld} of the layouts that a rows x cols matrix view (last two dims) has: both
-    where it is one row or column."""
-    s_r, s_c = X.stride(-2), X.stride(-1)
-    found = {}
+def _layouts(strides, rows: int, cols: int, name: str):
+    """(ld if row-major, ld if column-major) of a rows x cols matrix view (the last two
+    strides), 0 for a layout that it does not have: one row or column has both."""
+    s_r, s_c = strides[-2], strides[-1]
+    row = col = 0
     if (s_c == 1 or cols <= 1) and (s_r >= cols or rows <= 1):
-        found[False] = max(s_r if rows > 1 else cols, cols, 1)
+        row = max(s_r if rows > 1 else cols, cols, 1)
     if (s_r == 1 or rows <= 1) and (s_c >= rows or cols <= 1):
-        found[True] = max(s_c if cols > 1 else rows, rows, 1)
-    if not found:
+        col = max(s_c if cols > 1 else rows, rows, 1)
+    if not row and not col:
         raise ValueError(f"{name} must be row-major or column-major in its last two dims")
-    return found
+    return row, col
 
 
 def gemm_adapters(X, W, A, B, offsets, ids=None, scale=None, C=None, out=None, alpha: float = 1.0, beta: float = 1.0,
@@ -816,19 +816,24 @@ def gemm_adapters(X, W, A, B, offsets, ids=None, scale=None, C=None, out=None, a
         dB = gemm_grouped_wgrad(hidden, dY, offsets)"""
     import torch
     dt = _sixteen_bit(X, W, "X and W")
-    if X.dim() != 2 or W.dim() != 2 or A.dim() != 3 or B.dim() != 3:
+    device, dtype = X.device, X.dtype
+    xs, ws, as_, bs = X.shape, W.shape, A.shape, B.shape
+    if len(xs) != 2 or len(ws) != 2 or len(as_) != 3 or len(bs) != 3:
         raise ValueError("X must be (T, K), W (K, N), A (adapters, K, r) and B (adapters, r, N)")
-    (T, K), N, (adapters, _, rank) = X.shape, W.shape[1], A.shape
-    if W.shape[0] != K or A.shape[1] != K or B.shape != (adapters, rank, N):
+    T, K = xs
+    N = ws[1]
+    adapters, ka, rank = as_
+    if ws[0] != K or ka != K or bs[0] != adapters or bs[1] != rank or bs[2] != N:
         raise ValueError("X must be (T, K), W (K, N), A (adapters, K, r) and B (adapters, r, N)")
-    device = X.device
-    if A.dtype != X.dtype or B.dtype != X.dtype:
+    if A.dtype != dtype or B.dtype != dtype:
         raise TypeError("A and B must have X's dtype")
     if A.device != device or B.device != device:
         raise ValueError("A and B must be on X's GPU")
     if not 1 <= rank <= 1024:
         raise ValueError("the adapters' rank must be 1 to 1024")
     requests, flags = _check_offsets(offsets, device)
+    ids_at = scale_at = hidden_at = None
+    ld_hidden = 0
     if ids is None:
         if requests != adapters:
             raise ValueError("without ids, offsets must hold one number more than there are adapters")
@@ -837,38 +842,41 @@ def gemm_adapters(X, W, A, B, offsets, ids=None, scale=None, C=None, out=None, a
             raise TypeError("ids must be int32")
         if ids.shape != (requests,) or ids.device != device or (requests > 1 and ids.stride(0) != 1):
             raise ValueError("ids must be a contiguous vector of one adapter to a request, on X's GPU")
+        ids_at = ids.data_ptr()
     if scale is not None:
         if scale.dtype != torch.float32:
             raise TypeError("scale must be float32")
         if scale.shape != (adapters,) or scale.device != device or (adapters > 1 and scale.stride(0) != 1):
             raise ValueError("scale must be a contiguous vector of one number to an adapter, on X's GPU")
+        scale_at = scale.data_ptr()
     ldx = _rows_of(X, "X")
-    w, b, a = _layouts(W, K, N, "W"), _layouts(B, rank, N, "B"), _layouts(A, K, rank, "A")
-    both = [c for c in w if c in b]
-    if not both:
+    ast, bst = A.stride(), B.stride()
+    w, b, a = _layouts(W.stride(), K, N, "W"), _layouts(bst, rank, N, "B"), _layouts(ast, K, rank, "A")
+    col = 0 if w[0] and b[0] else 1  # row-major, or column-major
+    ldw, ldb = w[col], b[col]
+    if not ldw or not ldb:
         raise ValueError("W and B must be laid out alike: both row-major, or both transposed views")
-    col, a_col = both[0], next(iter(a))
-    ldw, ldb, lda = w[col], b[col], a[a_col]
-    if adapters > 1 and K > 0 and N > 0 and (A.stride(0) != (rank if a_col else K) * lda or
-                                             B.stride(0) != (N if col else rank) * ldb):
+    a_col = 0 if a[0] else 1
+    lda = a[a_col]
+    if adapters > 1 and K > 0 and N > 0 and (ast[0] != (rank if a_col else K) * lda or bst[0] != (N if col else rank) * ldb):
         raise ValueError("the adapters must lie one after the other")
-    ld_hidden = 0
     if hidden is not None:
-        if hidden.dtype != X.dtype:
+        if hidden.dtype != dtype:
             raise TypeError("hidden must have X's dtype")
         if hidden.shape != (T, rank) or hidden.device != device:
             raise ValueError("hidden must be (T, r), on X's GPU")
-        ld_hidden = _rows_of(hidden, "hidden")
+        ld_hidden, hidden_at = _rows_of(hidden, "hidden"), hidden.data_ptr()
     c, c_code, out, d_code, ldc, beta = _output(C, out, (T, N), out_dtype, beta, device, "(T, N)")
-    operands = AdapterOperands(A.data_ptr(), B.data_ptr(), ids.data_ptr() if ids is not None else None,
-                               scale.data_ptr() if scale is not None else None, adapters, rank, lda, ldb)
+    operands = AdapterOperands(A.data_ptr(), B.data_ptr(), ids_at, scale_at, adapters, rank, lda, ldb)
     flags |= (GEMM_B_COLMAJOR if col else 0) | (GEMM_ADAPTER_A_COLMAJOR if a_col else 0)
 
     def call(h, stream):
-        work = torch.empty(max(h.adapters_work(requests, T, N, K, rank, d_code), 16), dtype=torch.uint8, device=device)
-        return h.run_adapters(X.data_ptr(), W.data_ptr(), operands, c, out.data_ptr(), offsets.data_ptr(), requests, T, N,
-                              K, ldx, ldw, ldc, dt, flags, alpha, beta, c_code, d_code,
-                              hidden.data_ptr() if hidden is not None else 0, ld_hidden, work.data_ptr(), stream)
+        lib = load_library()
+        work = torch.empty(max(lib.gemm_adapters_work(h.ptr, requests, T, N, K, rank, d_code), 16), dtype=torch.uint8,
+                           device=device)
+        return lib.gemm_run_adapters(h.ptr, X.data_ptr(), W.data_ptr(), ctypes.byref(operands), c, out.data_ptr(),
+                                     offsets.data_ptr(), requests, T, N, K, ldx, ldw, ldc, dt, flags, alpha, beta, c_code,
+                                     d_code, hidden_at, ld_hidden, work.data_ptr(), stream)
 
     rc = _on(device, handle, call)
     if rc != GEMM_OK:
@@ -971,21 +979,24 @@ def route(logits, k: int, mask=None, normalize: bool = False, handle: Handle | N
             raise TypeError("mask must be bool")
         if mask.shape != (T,) or mask.device != device or (T > 1 and mask.stride(0) != 1):
             raise ValueError("mask must be a contiguous vector of one value to a token, on the logits' GPU")
-    S = T * k
-    experts, order, place, counts, offsets = torch.empty(3 * S + 2 * E + 1, dtype=torch.int32, device=device).split(
-        (S, S, S, E, E + 1))
-    weights, lse, stats = torch.empty(S + T + 4, dtype=torch.float32, device=device).split((S, T, 4))
-    r = Route(logits, k, bool(normalize), experts.view(T, k), weights.view(T, k), lse, counts, offsets, order, place, stats)
+    S, dims = T * k, (T, k)
+    ints = torch.empty(3 * S + 2 * E + 1, dtype=torch.int32, device=device)
+    floats = torch.empty(S + T + 4, dtype=torch.float32, device=device)
+    experts, order, place, counts, offsets = torch.split_with_sizes(ints, (S, S, S, E, E + 1))
+    weights, lse, stats = torch.split_with_sizes(floats, (S, T, 4))
+    i, f = ints.data_ptr(), floats.data_ptr()
+    tables = RouteTables(i, f, f + 4 * S, i + 12 * S, i + 4 * (3 * S + E), i + 4 * S, i + 8 * S, f + 4 * (S + T))
 
     def call(h, stream):
-        work = torch.empty(h.route_work(T, E), dtype=torch.uint8, device=device)
-        return h.route(logits.data_ptr(), x_code, T, E, ld, k, mask.data_ptr() if mask is not None else 0,
-                       GEMM_ROUTE_NORMALIZE if normalize else 0, r._tables(), work.data_ptr(), stream)
+        lib = load_library()
+        work = torch.empty(lib.gemm_route_work(h.ptr, T, E), dtype=torch.uint8, device=device)
+        return lib.gemm_route(h.ptr, logits.data_ptr(), x_code, T, E, ld, k, mask.data_ptr() if mask is not None else None,
+                              GEMM_ROUTE_NORMALIZE if normalize else 0, ctypes.byref(tables), work.data_ptr(), stream)
 
     rc = _on(device, handle, call)
     if rc != GEMM_OK:
         raise GemmError(rc, "gemm_route")
-    return r
+    return Route(logits, k, bool(normalize), experts.view(dims), weights.view(dims), lse, counts, offsets, order, place, stats)
 
 
 def route_grad(r: Route, d_weights=None, balance: float = 0.0, z: float = 0.0, out=None, handle: Handle | None = None):
