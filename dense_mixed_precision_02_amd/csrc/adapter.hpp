@@ -557,7 +557,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void adapter_staged(const AdapterAr
                                     : (DMP_LDS char *)&lds_b[0][0] + (wave - INA) * SLAB;
     const EpiParams &ep = p.r.ep;
     const int64_t first = at.row0 * p.r.ldc + at.col0;
-    store_wave_tile<WTM, WTN>((DMP_LDS float *)slab, ep, (const char *)p.r.C + first * out_size(ep.c_type),
+    store_wave_tile<WTM, WTN, true>((DMP_LDS float *)slab, ep, (const char *)p.r.C + first * out_size(ep.c_type),
                               (char *)p.r.D + first * out_size(ep.d_type), p.r.ldc, at.rows, at.cols, wm * WTM,
                               wn * WTN, lane, [&](int i, int j) { return acc[i][j]; });
 }
@@ -714,7 +714,7 @@ __global__ __launch_bounds__(256) void adapter_tile(const AdapterArgs p) {
     static_assert(32 * (WTN + 4) * 4 <= OpA::BYTES && 32 * (WTN + 4) * 4 <= OpB::BYTES, "slab must fit");
     const EpiParams &ep = p.r.ep;
     const int64_t first = at.row0 * p.r.ldc + at.col0;
-    store_wave_tile<WTM, WTN>((DMP_LDS float *)slab, ep, (const char *)p.r.C + first * out_size(ep.c_type),
+    store_wave_tile<WTM, WTN, true>((DMP_LDS float *)slab, ep, (const char *)p.r.C + first * out_size(ep.c_type),
                               (char *)p.r.D + first * out_size(ep.d_type), p.r.ldc, at.rows, at.cols, wm * WTM,
                               wn * WTN, lane, [&](int i, int j) { return acc[i][j]; });
 }

@@ -3,6 +3,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "epi.hpp"
 
 namespace dmp {
@@ -166,15 +168,19 @@ __device__ static inline uint16_t encode16(float x, bool f16) {
     return f16 ? a : b;
 }
 
+// A vector of four at an address that is a multiple of one element's size only.
+template <class T> using vec4_at = T __attribute__((ext_vector_type(4), aligned(sizeof(T))));
+
 // Four consecutive elements [idx, idx + 4) of one row, SZ bytes each in memory
 // (sizeof(T): the accumulator type itself; 2: fp16 / bf16, float accumulators only).
-// n of them (0..4) lie inside the matrix; vec: one aligned vector access is allowed.
-template <class T, int SZ>
+// n of them (0..4) lie inside the matrix; vec: one vector access is allowed, aligned
+// to its size or (ANY) to an element's.
+template <class T, int SZ, bool ANY = false>
 __device__ static inline vec4_of<T> load4s(const void *base, int64_t idx, bool f16, bool vec, int n) {
     vec4_of<T> r = {0, 0, 0, 0};
     if constexpr (SZ == sizeof(T)) {
         const T *q = (const T *)base + idx;
-        if (vec && n == 4) return *(const vec4_of<T> *)q;
+        if (vec && n == 4) return *(const std::conditional_t<ANY, vec4_at<T>, vec4_of<T>> *)q;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             if (e < n) r[e] = q[e];
@@ -182,7 +188,7 @@ __device__ static inline vec4_of<T> load4s(const void *base, int64_t idx, bool f
         static_assert(is_float_acc<T>, "16-bit storage needs a float accumulator");
         const uint16_t *q = (const uint16_t *)base + idx;
         if (vec && n == 4) {
-            const ushortx4 h = *(const ushortx4 *)q;
+            const ushortx4 h = *(const std::conditional_t<ANY, vec4_at<uint16_t>, ushortx4> *)q;
 #pragma unroll
             for (int e = 0; e < 4; ++e) r[e] = decode16(h[e], f16);
             return r;
@@ -203,12 +209,12 @@ __device__ static inline vec4_of<T> load4s(const void *base, int64_t idx, bool f
 // a consumer reading D right after finds it in HBM, not in the cache.  The
 // policy is fixed at compile time: the compiler merges a run-time choice
 // between a non-temporal and a plain store into one plain store.
-template <class T, int SZ>
+template <class T, int SZ, bool ANY = false>
 __device__ static inline void store4s(void *base, int64_t idx, vec4_of<T> v, bool f16, bool vec, int n) {
     if constexpr (SZ == sizeof(T)) {
         T *q = (T *)base + idx;
         if (vec && n == 4) {
-            __builtin_nontemporal_store(v, (vec4_of<T> *)q);
+            __builtin_nontemporal_store(v, (std::conditional_t<ANY, vec4_at<T>, vec4_of<T>> *)q);
             return;
         }
 #pragma unroll
@@ -221,7 +227,7 @@ __device__ static inline void store4s(void *base, int64_t idx, vec4_of<T> v, boo
 #pragma unroll
         for (int e = 0; e < 4; ++e) h[e] = encode16(v[e], f16);
         if (vec && n == 4) {
-            __builtin_nontemporal_store(h, (ushortx4 *)q);
+            __builtin_nontemporal_store(h, (std::conditional_t<ANY, vec4_at<uint16_t>, ushortx4> *)q);
             return;
         }
 #pragma unroll
@@ -231,19 +237,19 @@ __device__ static inline void store4s(void *base, int64_t idx, vec4_of<T> v, boo
 }
 
 // The same with the storage type t (OUT_*) known only at run time.
-template <class T>
+template <class T, bool ANY = false>
 __device__ static inline vec4_of<T> load4(const void *base, int64_t idx, int t, bool vec, int n) {
     if constexpr (sizeof(T) == 4 && is_float_acc<T>) {
-        if (t != OUT_F32) return load4s<T, 2>(base, idx, t == OUT_F16, vec, n);
+        if (t != OUT_F32) return load4s<T, 2, ANY>(base, idx, t == OUT_F16, vec, n);
     }
-    return load4s<T, sizeof(T)>(base, idx, false, vec, n);
+    return load4s<T, sizeof(T), ANY>(base, idx, false, vec, n);
 }
-template <class T>
+template <class T, bool ANY = false>
 __device__ static inline void store4(void *base, int64_t idx, vec4_of<T> v, int t, bool vec, int n) {
     if constexpr (sizeof(T) == 4 && is_float_acc<T>) {
-        if (t != OUT_F32) return store4s<T, 2>(base, idx, v, t == OUT_F16, vec, n);
+        if (t != OUT_F32) return store4s<T, 2, ANY>(base, idx, v, t == OUT_F16, vec, n);
     }
-    store4s<T, sizeof(T)>(base, idx, v, false, vec, n);
+    store4s<T, sizeof(T), ANY>(base, idx, v, false, vec, n);
 }
 
 // alpha * acc + beta * c, each product and the sum rounded separately.

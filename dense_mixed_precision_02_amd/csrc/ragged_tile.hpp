@@ -61,8 +61,9 @@ __device__ static inline void grouped_order(int t, int tiles_m, int tiles_n, int
 // point at the tile's first element.  Accumulators (`get(i, j)`: instruction
 // block i, j; lane L, register G: row 4 (L / 16) + G, column L % 16) pass
 // through the wave's LDS slab, 32 rows at a time, so that C and D move as
-// vectors of four.
-template <int WTM, int WTN, class Get>
+// vectors of four.  ANY: also where rows do not begin at such vectors' alignment (global
+// memory takes them at any element's).
+template <int WTM, int WTN, bool ANY = false, class Get>
 __device__ static inline void store_wave_tile(DMP_LDS float *slab, const EpiParams &ep, const char *Cb,
                                               char *Db, int64_t ldc, int rows, int cols, int r0,
                                               int c0, int lane, Get get) {
@@ -83,8 +84,8 @@ __device__ static inline void store_wave_tile(DMP_LDS float *slab, const EpiPara
     };
     auto run = [&](auto cs_c, auto ds_c) {
         constexpr int CS = decltype(cs_c)::value, DS = decltype(ds_c)::value;
-        const bool vec = ldc % 4 == 0 && (CS == 0 || (uintptr_t)Cb % (4 * (CS ? CS : 1)) == 0) &&
-                         (uintptr_t)Db % (4 * DS) == 0;
+        const bool vec = ANY || (ldc % 4 == 0 && (CS == 0 || (uintptr_t)Cb % (4 * (CS ? CS : 1)) == 0) &&
+                                 (uintptr_t)Db % (4 * DS) == 0);
         const int rl = lane / LPR, cl = (lane % LPR) * 4;
         const int64_t at = (int64_t)(r0 + rl) * ldc + c0 + cl;
         if (vec && c0 + WTN <= cols) {
@@ -97,7 +98,7 @@ __device__ static inline void store_wave_tile(DMP_LDS float *slab, const EpiPara
                     if constexpr (CS != 0) {
                         const int r = q * 32 + u * RPP;
                         if (r0 + r + rl < rows)
-                            dst[u] = load4s<float, CS>(Cb, at + r * ldc, c_f16, true, 4);
+                            dst[u] = load4s<float, CS, ANY>(Cb, at + r * ldc, c_f16, true, 4);
                     }
                 }
             };
@@ -112,7 +113,7 @@ __device__ static inline void store_wave_tile(DMP_LDS float *slab, const EpiPara
                     const floatx4 v = *(const DMP_LDS floatx4 *)(slab + (u * RPP + rl) * SP + cl);
                     const int r = q * 32 + u * RPP;
                     if (r0 + r + rl < rows)
-                        store4s<float, DS>(Db, at + r * ldc, finish4(v, cv[q & 1][u], ep), d_f16, true, 4);
+                        store4s<float, DS, ANY>(Db, at + r * ldc, finish4(v, cv[q & 1][u], ep), d_f16, true, 4);
                 }
                 __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
             }
@@ -126,9 +127,9 @@ __device__ static inline void store_wave_tile(DMP_LDS float *slab, const EpiPara
                 const int r = q * 32 + u * RPP;
                 const int n = r0 + r + rl < rows ? cols_in(cols, c0 + cl) : 0;
                 floatx4 c = {0, 0, 0, 0};
-                if constexpr (CS != 0) c = load4s<float, CS>(Cb, at + r * ldc, c_f16, vec, n);
+                if constexpr (CS != 0) c = load4s<float, CS, ANY>(Cb, at + r * ldc, c_f16, vec, n);
                 const floatx4 v = *(const DMP_LDS floatx4 *)(slab + (u * RPP + rl) * SP + cl);
-                store4s<float, DS>(Db, at + r * ldc, finish4(v, c, ep), d_f16, vec, n);
+                store4s<float, DS, ANY>(Db, at + r * ldc, finish4(v, c, ep), d_f16, vec, n);
             }
             __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
         }

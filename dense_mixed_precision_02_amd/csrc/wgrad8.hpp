@@ -225,7 +225,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void wgrad8_tile(const Wgrad8Args p
     DMP_LDS char *slab = wave < INA ? (DMP_LDS char *)&lds_a[0][0] + wave * SLAB
                                     : (DMP_LDS char *)&lds_b[0][0] + (wave - INA) * SLAB;
     const int64_t first = (int64_t)split * p.part + at.group * r.sC + at.row0 * r.ldc + at.col0;
-    store_wave_tile<WTM, WTN>((DMP_LDS float *)slab, r.ep, (const char *)r.C + first * out_size(r.ep.c_type),
+    store_wave_tile<WTM, WTN, true>((DMP_LDS float *)slab, r.ep, (const char *)r.C + first * out_size(r.ep.c_type),
                               (char *)r.D + first * out_size(r.ep.d_type), r.ldc, at.rows, at.cols, wm * WTM,
                               wn * WTN, lane, [&](int i, int j) { return acc[i][j]; });
 }
@@ -367,7 +367,7 @@ __global__ __launch_bounds__(256) void wgrad8_large_tile(const Wgrad8Args p) {
     DMP_LDS char *slab = wave == 0 ? LA[0] : wave == 1 ? LB[0] : wave == 2 ? LA[1] : LB[1];
     static_assert(32 * (WTN + 4) * 4 <= SA::Op::BYTES && 32 * (WTN + 4) * 4 <= SB::Op::BYTES, "slab must fit");
     const int64_t first = at.group * r.sC + at.row0 * r.ldc + at.col0;
-    store_wave_tile<WTM, WTN>((DMP_LDS float *)slab, r.ep, (const char *)r.C + first * out_size(r.ep.c_type),
+    store_wave_tile<WTM, WTN, true>((DMP_LDS float *)slab, r.ep, (const char *)r.C + first * out_size(r.ep.c_type),
                               (char *)r.D + first * out_size(r.ep.d_type), r.ldc, at.rows, at.cols, wm * WTM,
                               wn * WTN, lane, [&](int i, int j) { return acc[i][j]; });
 }
@@ -387,15 +387,12 @@ __global__ __launch_bounds__(256) void wgrad8_join(const Wgrad8JoinArgs p) {
     const int64_t row = i / quads, col = (i - row * quads) * 4;
     if (row >= p.rows) return;
     const int n = (int)min((int64_t)4, p.N - col);
-    const bool whole = p.N % 4 == 0;
     floatx4 v = {0, 0, 0, 0};
     for (int s = 0; s < p.splits; ++s)
-        v += load4s<float, 4>(p.part, ((int64_t)s * p.rows + row) * p.N + col, false, whole, n);
+        v += load4s<float, 4, true>(p.part, ((int64_t)s * p.rows + row) * p.N + col, false, true, n);
     const int64_t at = row * p.ldc + col;
-    const bool vec = p.ldc % 4 == 0 && (uintptr_t)p.D % (4 * out_size(p.ep.d_type)) == 0 &&
-                     (!p.ep.use_c || (uintptr_t)p.C % (4 * out_size(p.ep.c_type)) == 0);
-    const floatx4 c = p.ep.use_c ? load4<float>(p.C, at, p.ep.c_type, vec, n) : floatx4{0, 0, 0, 0};
-    store4<float>(p.D, at, finish4(v, c, p.ep), p.ep.d_type, vec, n);
+    const floatx4 c = p.ep.use_c ? load4<float, true>(p.C, at, p.ep.c_type, true, n) : floatx4{0, 0, 0, 0};
+    store4<float, true>(p.D, at, finish4(v, c, p.ep), p.ep.d_type, true, n);
 }
 
 }  // namespace dmp
