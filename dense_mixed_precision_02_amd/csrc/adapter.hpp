@@ -44,6 +44,7 @@ struct AdapterArgs {
     int64_t lda, ldb;        // leading dimensions of A_a, B_a
     int64_t sA, sB;          // elements from one adapter's to the next
     int rank;
+    int b_fast;              // K-contiguous B_a: its 16-byte granules are aligned and whole
     char *H;                 // parts x M x rp 16-bit values, zeros from rank to rp
     int rp, parts;
     void *hidden;            // M x rank, ld_hidden apart, or NULL: H for the caller
@@ -410,8 +411,111 @@ __device__ static inline void adapter_blocks(floatx4 (&acc)[TM][TN], int rows, i
     }
 }
 
-// The product, operands staged through registers as in ragged_staged.hpp.  FAST: all
-// operands' 16-byte granules are aligned and whole.
+// A 16 x 32 piece of B_a for the matrix instructions, columns c0 .. and rank k0 ..: lane L
+// gets column L % 16 and 8 consecutive k.  By whole granules, or (any layout and
+// alignment) value by value.
+template <bool BKC, bool GRANULES>
+struct AdapterPiece {
+    intx4 v[GRANULES ? 1 : 2];  // value by value: one to a half word, packed by get()
+    __device__ void load(const AdapterArgs &p, int a, int64_t c0, int cols, int k0, int lane) {
+        const int c = lane & 15, k = 8 * (lane >> 4);
+        const int64_t at = a * p.sB + (BKC ? c0 * p.ldb + k0 : k0 * p.ldb + c0);
+        const __amdgpu_buffer_rsrc_t r = make_rsrc((const char *)p.B + at * 2);
+        const int left = p.rank - k0;
+        if constexpr (GRANULES) {
+            v[0] = load_granule(r, joined(row_part(c, cols, p.ldb), k_part(k, left)));
+        } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const int off = BKC ? joined(row_part(c, cols, p.ldb), k_part(k + q, left))
+                                    : joined(row_part(k + q, left, p.ldb), k_part(c, cols));
+                v[q / 4][q % 4] = (int)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
+            }
+        }
+    }
+    __device__ intx4 get() const {
+        if constexpr (GRANULES) return v[0];
+        else return intx4{v[0][0] | v[0][1] << 16, v[0][2] | v[0][3] << 16, v[1][0] | v[1][1] << 16, v[1][2] | v[1][3] << 16};
+    }
+};
+
+// The adapters' part of a wave's TM x TN blocks, from `row` of the tile on: the entries
+// that have rows there, 32 of the rank at a time, straight from memory (H and B_a are in
+// the caches), the next piece on its way beside each.  No other wave is waited for: an
+// entry of one row costs its loads, where its own k-tile through LDS would cost the
+// whole workgroup a turn (0.7 us).
+template <class DT, bool BKC, bool GRANULES, int TM, int TN>
+__device__ static inline void adapter_direct(const AdapterArgs &p, const TileAt &at, const DMP_LDS AdapterEntry *list, int entries,
+                                             int row, int col, int lane, floatx4 (&acc)[TM][TN]) {
+    const int r16 = lane & 15;
+    intx4 fh[2][TM];
+    AdapterPiece<BKC, GRANULES> fb[2][TN];
+    int lo[2], hi[2], e = 0, k = 0, part = 0;
+    int ho[TM];
+#pragma unroll
+    for (int i = 0; i < TM; ++i) ho[i] = row_part(row + 16 * i + r16, at.rows, p.rp);
+    auto entry = [&](int x) { return __builtin_amdgcn_readfirstlane(list[x].rows); };
+    while (e < entries && (int)((uint32_t)entry(e) >> 16) <= row) ++e;
+    // piece (e, k, part) into slot st, and on to the next one; past the last: no rows
+    auto load = [&](int st) {
+        const int rr = e < entries ? entry(e) : 0;
+        lo[st] = max((rr & 0xffff) - row, 0);
+        hi[st] = (int)((uint32_t)rr >> 16) - row;
+        if (lo[st] >= 16 * TM || hi[st] <= 0) {
+            lo[st] = hi[st] = 0;
+            return;
+        }
+        const int a = __builtin_amdgcn_readfirstlane(list[e].adapter);
+        const __amdgpu_buffer_rsrc_t rh = make_rsrc(p.H + (part * p.r.M * p.rp + at.row0 * p.rp + k) * 2);
+        const int ko = k_part(8 * (lane >> 4), p.rp - k);
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+            fh[st][i] = load_granule(rh, hi[st] > 16 * i && lo[st] < 16 * i + 16 ? joined(ho[i], ko) : OOB_OFFSET);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) fb[st][j].load(p, a, at.col0 + col + 16 * j, at.cols - col - 16 * j, k, lane);
+        if ((k += 32) >= p.rank) {
+            k = 0;
+            if (++part == p.parts) {
+                part = 0;
+                ++e;
+            }
+        }
+    };
+    auto multiply = [&](int st) {
+        intx4 b[TN];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) b[j] = fb[st][j].get();
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            const int r = 16 * i;
+            if (hi[st] <= r || lo[st] >= r + 16) continue;
+            if (lo[st] <= r && hi[st] >= r + 16) {
+#pragma unroll
+                for (int j = 0; j < TN; ++j) acc[i][j] = mma16<DT>(fh[st][i], b[j], acc[i][j]);
+            } else {
+                const int mine = r + 4 * (lane >> 4) - lo[st];
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    const floatx4 c = mma16<DT>(fh[st][i], b[j], floatx4{0, 0, 0, 0});
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        acc[i][j][q] += (uint32_t)(mine + q) < (uint32_t)(hi[st] - lo[st]) ? c[q] : 0.0f;
+                }
+            }
+        }
+    };
+    load(0);
+    while (hi[0] > 0) {
+        load(1);
+        multiply(0);
+        if (hi[1] <= 0) break;
+        load(0);
+        multiply(1);
+    }
+}
+
+// The product, X and W staged through registers as in ragged_staged.hpp.  FAST: their
+// 16-byte granules are aligned and whole.
 template <class DT, int BM, int BN, int WM, int WN, bool BKC, bool FAST>
 __global__ __launch_bounds__(WM *WN * 64, 2) void adapter_staged(const AdapterArgs p) {
     constexpr int NW = WM * WN, WTM = BM / WM, WTN = BN / WN, TM = WTM / 16, TN = WTN / 16;
@@ -431,49 +535,39 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void adapter_staged(const AdapterAr
         if (lane == 0) count = n;
     }
     __syncthreads();
-    const DMP_LDS AdapterEntry *entry = (const DMP_LDS AdapterEntry *)list;
-    const int entries = __builtin_amdgcn_readfirstlane(count), per = (p.rank + 63) / 64 * p.parts;
-    // an even number of the projection's k-tiles, the last of which may be empty (zeros)
-    const int nkt0 = (at.k / 64 + (at.k % 64 != 0) + 1) & ~1, more = entries * per;
-    OpA opa, oph;
-    OpB opb, opr;
+    // an even number of k-tiles, the last of which may be empty (zeros)
+    const int nkt = (at.k / 64 + (at.k % 64 != 0) + 1) & ~1;
+    OpA opa;
+    OpB opb;
     opa.init(wave, lane, p.r.lda, 0, BM);
-    oph.init(wave, lane, p.rp, 0, BM);
     opb.init(wave, lane, p.r.ldb, 0, BN);
-    opr.init(wave, lane, p.ldb, 0, BN);
 
     floatx4 acc[TM][TN] = {};
     intx4 ra[DEPTH][OpA::CPW], rb[DEPTH][OpB::CPW];
-    // a lane's granules of a k-tile: of the projection, and (MORE) of H and B_a
-    auto read = [&](auto more_c, const AdapterSource &s, const OpA &oa, const OpB &ob, int64_t ldb, int slot) {
-        constexpr bool MORE = decltype(more_c)::value;
-        const __amdgpu_buffer_rsrc_t rsa = make_rsrc(s.A), rsb = make_rsrc(s.B);
+    // this lane's granules of k-tile kt; past the end: zeros, no memory is touched
+    auto fetch = [&](int kt, int slot) {
+        const char *A = at.A + (int64_t)kt * 128, *B = at.B + (int64_t)kt * (BKC ? 128 : 128 * p.r.ldb);
+        const __amdgpu_buffer_rsrc_t rsa = make_rsrc(A), rsb = make_rsrc(B);
+        const int left = at.k - kt * 64;
 #pragma unroll
         for (int j = 0; j < OpA::CPW; ++j) {
-            const int row = oa.row_or_k + 8 * NW * j;
-            if constexpr (FAST || MORE)  // (H is laid out in whole granules)
-                ra[slot][j] = load_granule(rsa, row < at.rows && oa.fixed < s.left ? oa.off0 + j * oa.step : OOB_OFFSET);
+            const int row = opa.row_or_k + 8 * NW * j;
+            if constexpr (FAST)
+                ra[slot][j] = load_granule(rsa, row < at.rows && opa.fixed < left ? opa.off0 + j * opa.step : OOB_OFFSET);
             else
-                ra[slot][j] = load8((const uint16_t *)s.A + row * p.r.lda + oa.fixed, row < at.rows ? s.left - oa.fixed : 0);
+                ra[slot][j] = load8((const uint16_t *)A + row * p.r.lda + opa.fixed, row < at.rows ? left - opa.fixed : 0);
         }
 #pragma unroll
         for (int j = 0; j < OpB::CPW; ++j) {
-            const int r = BKC ? ob.row_or_k + 8 * NW * j : ob.fixed;
-            const int k = BKC ? ob.fixed : ob.row_or_k + OpB::KSTEP * j;
-            const bool ok = r < at.cols && k < s.left;
+            const int r = BKC ? opb.row_or_k + 8 * NW * j : opb.fixed;
+            const int k = BKC ? opb.fixed : opb.row_or_k + OpB::KSTEP * j;
+            const bool ok = r < at.cols && k < left;
             if constexpr (FAST)
-                rb[slot][j] = load_granule(rsb, ok ? ob.off0 + j * ob.step : OOB_OFFSET);
+                rb[slot][j] = load_granule(rsb, ok ? opb.off0 + j * opb.step : OOB_OFFSET);
             else
-                rb[slot][j] = load8((const uint16_t *)s.B + (BKC ? r * ldb + k : k * ldb + r), ok ? (BKC ? s.left - k : at.cols - r) : 0);
+                rb[slot][j] = load8((const uint16_t *)B + (BKC ? r * p.r.ldb + k : k * p.r.ldb + r), ok ? (BKC ? left - k : at.cols - r) : 0);
         }
         issued();
-    };
-    auto fetch = [&](int kt, int slot) {
-        const AdapterSource s = {at.A + (int64_t)kt * 128, at.B + (int64_t)kt * (BKC ? 128 : 128 * p.r.ldb), at.k - kt * 64};
-        read(std::false_type{}, s, opa, opb, p.r.ldb, slot);
-    };
-    auto fetch_more = [&](int x, int slot) {
-        read(std::true_type{}, adapter_source<DT, BKC>(p, at, entry, entries, x), oph, opr, p.ldb, slot);
     };
     auto put = [&](int slot, int buf) {
 #pragma unroll
@@ -506,22 +600,17 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void adapter_staged(const AdapterAr
 #pragma unroll
                 for (int j = 0; j < TN; ++j) acc[i][j] = mma16<DT>(fa[s][i], fb[s][j], acc[i][j]);
     };
-    auto multiply_more = [&](int x, int buf) {
-        adapter_blocks<DT, TM, TN>(acc, __builtin_amdgcn_readfirstlane(entry[x / per].rows), wm * WTM, lane,
-                                   [&](int i, int s) { return fragA(buf, i, s); }, [&](int j, int s) { return fragB(buf, j, s); },
-                                   [](floatx4 &c, const intx4 &a, const intx4 &b) { c = mma16<DT>(a, b, c); });
-    };
     auto turn = [&](int buf) {  // the k-tile in the registers `buf` into the LDS buffer, when all are done with it
         put(buf, buf);
         step_sync();
         barrier_vmcnt<63>();
     };
-    if (nkt0 > 0) {
+    if (nkt > 0) {
         fetch(0, 0);
         fetch(1, 1);
         turn(0);
-        // k-tile kt is in LDS buffer 0, the next one on its way; past the projection's come the adapters'
-        for (int kt = 0; kt + 2 < nkt0; kt += 2) {
+        // k-tile kt is in LDS buffer 0, the next one on its way
+        for (int kt = 0; kt < nkt; kt += 2) {
             fetch(kt + 2, 0);
             step_sync();
             multiply(0);
@@ -531,24 +620,10 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void adapter_staged(const AdapterAr
             multiply(1);
             turn(0);
         }
-        fetch_more(0, 0);
-        step_sync();
-        multiply(0);
-        turn(1);
-        fetch_more(1, 1);
-        step_sync();
-        multiply(1);
-        turn(0);
-        for (int x = 0; x < more; x += 2) {
-            fetch_more(x + 2, 0);
-            step_sync();
-            multiply_more(x, 0);
-            turn(1);
-            fetch_more(x + 3, 1);
-            step_sync();
-            if (x + 1 < more) multiply_more(x + 1, 1);
-            turn(0);
-        }
+        const int entries = __builtin_amdgcn_readfirstlane(count);
+        const DMP_LDS AdapterEntry *entry = (const DMP_LDS AdapterEntry *)list;
+        if (BKC && p.b_fast) adapter_direct<DT, BKC, true>(p, at, entry, entries, wm * WTM, wn * WTN, lane, acc);
+        else adapter_direct<DT, BKC, false>(p, at, entry, entries, wm * WTM, wn * WTN, lane, acc);
     }
     __syncthreads();
     constexpr int SLAB = 32 * (WTN + 4) * 4, INA = 2 * OpA::BYTES / SLAB;

@@ -82,7 +82,7 @@ int run_few(int num_cus, const AdapterArgs &a, hipStream_t s) {
     f.ldx = (int)a.r.lda; f.ldw = (int)a.r.ldb; f.lda = (int)a.lda; f.ldb = (int)a.ldb;
     f.rank = a.rank; f.r16 = (int)cdiv(a.rank, 16) * 16;
     f.splits = q.splits; f.per = q.per; f.blocks = q.blocks;
-    f.sA = a.sA; f.sB = a.sB;
+    f.sA = a.sA; f.sB = a.sB; f.b_fast = a.b_fast;
     f.C = a.r.C; f.D = a.r.D; f.hidden = a.hidden; f.ldc = a.r.ldc; f.ld_hidden = a.ld_hidden; f.ep = a.r.ep;
     f.part = (float *)a.H;
     f.hpart = (float *)(a.H + q.splits * (cdiv(a.r.M * a.r.N * 4, 16) * 16));
@@ -137,11 +137,12 @@ int gemm_run_adapters(gemm_handle_t h, const void *X, const void *W, const gemm_
     a.sA = (ac ? ad->rank : K) * ad->lda;
     a.sB = (bc ? N : ad->rank) * ad->ldb;
     a.rank = (int)ad->rank;
+    a.b_fast = bc && adapter_b_fast(*ad);
     a.H = (char *)work;
     a.rp = (int)adapter_rp(ad->rank);
     a.parts = adapter_parts(d_type);
     a.hidden = hidden; a.ld_hidden = ld_hidden;
-    const int cfg = adapter_cfg(h->num_cus, X, W, *ad, M, N, K, ldx, ldw, ac, bc);
+    const int cfg = adapter_cfg(h->num_cus, X, W, *ad, requests, M, N, K, ldx, ldw, ac, bc);
     const bool hf = K > 0 && hidden_fast(X, *ad, K, ldx, ac);
     hipStream_t s = (hipStream_t)stream;
     return dtype == GEMM_F16 ? run_adapters<F16>(h->num_cus, a, ac, bc, hf, cfg, s)

@@ -31,6 +31,7 @@ struct AdapterFewArgs {
     int splits, per;     // parts of K, and k-tiles of 64 in each
     int blocks;          // workgroups to a part: cdiv(N, 64) or more
     int64_t sA, sB;      // elements from one adapter's A, B to the next
+    int b_fast;          // B's 16-byte granules are aligned and whole
     const void *C;
     void *D, *hidden;
     int64_t ldc, ld_hidden;
@@ -213,7 +214,19 @@ __global__ __launch_bounds__(512, 2) void adapter_few_join(const AdapterFewArgs 
         for (int x = 0; x < EB; ++x) {
             const int64_t ad = __builtin_amdgcn_readlane(my_adapter, x);
             const __amdgpu_buffer_rsrc_t rb = make_rsrc((const char *)p.B + (ad * p.sB + col0 * p.ldb) * 2);
-            fb[st][x] = load_granule(rb, wave + NW * x < entries ? at : OOB_OFFSET);
+            const bool there = wave + NW * x < entries;
+            if (p.b_fast) {
+                fb[st][x] = load_granule(rb, there ? at : OOB_OFFSET);
+            } else {  // value by value
+                const int co = there ? row_part(r16, cols, p.ldb) : OOB_OFFSET;
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    const int k = kb * 32 + 8 * (lane >> 4) + 2 * d;
+                    const uint32_t l = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rb, joined(co, k_part(k, p.rank)), 0, 0);
+                    const uint32_t h = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rb, joined(co, k_part(k + 1, p.rank)), 0, 0);
+                    fb[st][x][d] = (int)(l | h << 16);
+                }
+            }
         }
         issued();
     };

@@ -7,7 +7,7 @@ namespace dmp {
 namespace plan {
 
 constexpr unsigned ADAPTER_FLAGS = GEMM_B_COLMAJOR | GEMM_OFFSETS_I32 | GEMM_ADAPTER_A_COLMAJOR;
-constexpr int64_t ADAPTER_RANK_MAX = 1024;
+constexpr int64_t ADAPTER_RANK_MAX = 1024, ADAPTER_LD_MAX = 1ll << 24;  // 31-bit offsets in 64 rows of an adapter
 
 inline int64_t adapter_rp(int64_t rank) { return cdiv(rank, 8) * 8; }
 inline int adapter_parts(int d_type) { return d_type == GEMM_OUT_F32 ? 2 : 1; }
@@ -55,7 +55,7 @@ inline int validate_adapters(gemm_handle_t h, const void *X, const void *W, cons
     if (K > 0) {
         if (ldx < K || ldx > LD_MAX || ldw < std::max<int64_t>(1, bc ? K : N) || ldw > LD_MAX) return GEMM_ERR_INVALID_ARG;
         if (ad->lda < (ac ? K : ad->rank) || ad->lda > LD_MAX || ad->ldb < std::max<int64_t>(1, bc ? ad->rank : N) ||
-            ad->ldb > LD_MAX)
+            ad->ldb > ADAPTER_LD_MAX)
             return GEMM_ERR_INVALID_ARG;
     }
     if (hidden && (ld_hidden < ad->rank || ld_hidden > LD_MAX || (uintptr_t)hidden % 2)) return GEMM_ERR_INVALID_ARG;
@@ -85,21 +85,25 @@ inline bool hidden_fast(const void *X, const gemm_adapters_t &ad, int64_t K, int
     return (64 * ldx + K) * 2 < lim && (64 * ad.lda + K) * 2 < lim;
 }
 
-// The product: can the granules of X, W and B_a be loaded whole, with 31-bit offsets in a tile?
-inline bool product_fast(const void *X, const void *W, const gemm_adapters_t &ad, int64_t M, int64_t N, int64_t K,
-                         int64_t ldx, int64_t ldw, bool b_col) {
-    return granule_ok(X, W, M, N, K, ldx, ldw, GEMM_F16, false, b_col, true) &&
-           granule_ok(ad.B, ad.B, M, N, b_col ? ad.rank : 8, 8, ad.ldb, GEMM_F16, false, b_col, true);
+// Can B_a's granules be copied whole (along its contiguous extent)?
+inline bool adapter_b_panels(const gemm_adapters_t &ad, int64_t N, bool b_col) {
+    return aligned16(ad.B) && ad.ldb % 8 == 0 && (b_col ? ad.rank : N) % 8 == 0 && 256 * ad.ldb * 2 < (1ll << 31) - (1ll << 22);
 }
 
+// K-contiguous B_a: can its granules be loaded whole?
+inline bool adapter_b_fast(const gemm_adapters_t &ad) { return aligned16(ad.B) && ad.ldb % 8 == 0 && ad.rank % 8 == 0; }
+
 // Which product kernel (CFG_GENERIC: any alignment; CFG_SKINNY1: the kernels for few rows).
-inline int adapter_cfg(int num_cus, const void *X, const void *W, const gemm_adapters_t &ad, int64_t M, int64_t N,
+inline int adapter_cfg(int num_cus, const void *X, const void *W, const gemm_adapters_t &ad, int64_t requests, int64_t M, int64_t N,
                        int64_t K, int64_t ldx, int64_t ldw, bool a_col, bool b_col) {
-    if (K == 0 || !product_fast(X, W, ad, M, N, K, ldx, ldw, b_col)) return CFG_GENERIC;
-    if (b_col && a_col && M <= FEW_ROWS && ad.rank <= FEW_RANK_MAX && N <= FEW_N_MAX && hidden_fast(X, ad, K, ldx, a_col)) return CFG_SKINNY1;
+    // X's and W's granules whole, with 31-bit offsets in a tile
+    if (K == 0 || !granule_ok(X, W, M, N, K, ldx, ldw, GEMM_F16, false, b_col, true)) return CFG_GENERIC;
+    if (b_col && a_col && M <= FEW_ROWS && ad.rank <= FEW_RANK_MAX && N <= FEW_N_MAX && hidden_fast(X, ad, K, ldx, a_col))
+        return CFG_SKINNY1;
     const int64_t t128 = cdiv(M, 128) * cdiv(N, 128);
-    if (b_col && M <= 256 && 2 * t128 <= num_cus) return CFG_SKINNY4;
-    return M >= 192 && t128 > 2 * (int64_t)num_cus ? CFG_L : CFG_M;
+    const bool panels = adapter_b_panels(ad, N, b_col);
+    if (b_col && panels && M <= 256 && 2 * t128 <= num_cus) return CFG_SKINNY4;
+    return panels && M >= 192 && t128 > 2 * (int64_t)num_cus && M >= 32 * requests ? CFG_L : CFG_M;
 }
 
 }  // namespace plan

@@ -402,8 +402,8 @@ int gemm_run_scaled8(gemm_handle_t h, const gemm_q8_t *A, const gemm_q8_t *B, co
  *
  * work: gemm_adapters_work(h, requests, M, N, K, rank, d_type) bytes of device
  * memory (-1: sizes that are refused), 16-byte aligned, not shared with a call that can run at the
- * same time.  Nothing is allocated.  rank: 1 .. 1024; adapters and requests at
- * most 2^20.  Everything else as in gemm_run_grouped.
+ * same time.  Nothing is allocated.  rank: 1 .. 1024; ldb at most
+ * 2^24; adapters and requests at most 2^20.  Everything else as in gemm_run_grouped.
  */
 enum { GEMM_ADAPTER_A_COLMAJOR = 128u };
 typedef struct {
