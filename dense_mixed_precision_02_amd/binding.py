@@ -852,11 +852,11 @@ def gemm_adapters(X, W, A, B, offsets, ids=None, scale=None, C=None, out=None, a
     ldx = _rows_of(X, "X")
     ast, bst = A.stride(), B.stride()
     w, b, a = _layouts(W.stride(), K, N, "W"), _layouts(bst, rank, N, "B"), _layouts(ast, K, rank, "A")
-    col = 0 if w[0] and b[0] else 1  # row-major, or column-major
+    col = 1 if w[1] and b[1] else 0  # column-major where both can be: few rows have kernels of their own there
     ldw, ldb = w[col], b[col]
     if not ldw or not ldb:
         raise ValueError("W and B must be laid out alike: both row-major, or both transposed views")
-    a_col = 0 if a[0] else 1
+    a_col = 1 if a[1] else 0
     lda = a[a_col]
     if adapters > 1 and K > 0 and N > 0 and (ast[0] != (rank if a_col else K) * lda or bst[0] != (N if col else rank) * ldb):
         raise ValueError("the adapters must lie one after the other")

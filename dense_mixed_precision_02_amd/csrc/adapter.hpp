@@ -17,7 +17,7 @@
 // relative to H B_a is that of rounding X.  Where D has 32 bits H is kept as the sum of two
 // such numbers (within 2^-16 of it for bf16, 2^-22 for fp16), each multiplied by B_a.
 //
-// A tile finds its requests by scanning the offsets (ragged.hpp's GroupWalk), 64 at a time.
+// A tile finds its requests by scanning the offsets, 64 at a time.
 //
 // Zeros times an infinity or a NaN are no zeros: with rows of zeros for the other requests an
 // adapter that holds one would spoil theirs.  So a 16-row block of the tile that lies in
@@ -25,7 +25,6 @@
 // skipped, and one on the border sums them apart and adds those of the request's rows.
 #pragma once
 #include "ragged_staged.hpp"
-#include "skinny.hpp"
 
 namespace dmp {
 
@@ -36,6 +35,10 @@ struct RequestTable {
     int groups, adapters, off32, rows;
 };
 
+__device__ static inline intx4 load_granule(__amdgpu_buffer_rsrc_t r, int off) {
+    return __builtin_bit_cast(intx4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+
 struct AdapterArgs {
     RaggedArgs r;            // A: X; B: W; groups, offsets: the requests
     RequestTable t;
@@ -44,7 +47,7 @@ struct AdapterArgs {
     int64_t lda, ldb;        // leading dimensions of A_a, B_a
     int64_t sA, sB;          // elements from one adapter's to the next
     int rank;
-    int b_fast;              // K-contiguous B_a: its 16-byte granules are aligned and whole
+    int b_fast;              // B_a's 16-byte granules are aligned and whole
     char *H;                 // parts x M x rp 16-bit values, zeros from rank to rp
     int rp, parts;
     void *hidden;            // M x rank, ld_hidden apart, or NULL: H for the caller
@@ -52,18 +55,50 @@ struct AdapterArgs {
     int tiles_r;             // hidden: column tiles of A_a
 };
 
-// Request g's adapter; -1: none.
-__device__ static inline int adapter_of(const RequestTable &t, int g) {
-    const int a = t.ids ? t.ids[g] : g;
-    return (uint32_t)a < (uint32_t)t.adapters ? a : -1;
+// A tile's requests that have an adapter: rows lo .. hi - 1 of the tile, in ascending order.
+struct AdapterEntry {
+    int rows;      // lo | hi << 16
+    int adapter;
+};
+
+// A row number of the offsets as its two words, brought into 0 .. rows.
+__device__ static inline int offset_value(int lo, int hi, int rows) {
+    return hi < 0 ? 0 : (hi > 0 || (uint32_t)lo > (uint32_t)rows) ? rows : lo;
 }
-// The same of a group found by a walk: `own` is what this lane's group of the first 64 has,
-// loaded along with the offsets.
-__device__ static inline int first_adapters(const RequestTable &t, int lane) {
-    return lane < t.groups ? adapter_of(t, lane) : -1;
+// What a list of a tile's requests is made from, this lane's of 64 requests: loaded ahead of
+// other loads, so that it arrives first, without branches, so that all of it is on its way
+// at once (a 32-bit offset's second word is the first again; requests past the last one: the last).
+struct RequestLoad {
+    int lo, hi, id;
+};
+__device__ static inline RequestLoad load_requests(const RequestTable &t, int chunk, int lane) {
+    const int g = min(chunk + lane, t.groups - 1), w = t.off32 ? 1 : 2;
+    const int32_t *o = (const int32_t *)t.offsets + (int64_t)(g + 1) * w;
+    RequestLoad q;
+    q.lo = o[0];
+    q.hi = o[w - 1];
+    q.id = t.ids ? t.ids[g] : g;
+    return q;
 }
-__device__ static inline int adapter_of(const RequestTable &t, int g, int own) {
-    return __builtin_amdgcn_readfirstlane(g < 64 ? __builtin_amdgcn_readlane(own, g & 63) : adapter_of(t, g));
+
+// Row number i of the offsets (0 .. groups), by scalar loads: they wait for no vector load.
+__device__ static inline int scalar_offset(const RequestTable &t, int i) {
+    typedef const __attribute__((address_space(4))) int32_t *words;
+    const int w = t.off32 ? 1 : 2;
+    const words o = (words)t.offsets + (int64_t)i * w;
+    const int lo = o[0], hi = o[w - 1];
+    return offset_value(lo, w == 1 ? lo >> 31 : hi, t.rows);
+}
+
+// The largest of this lane's value and those before it.
+__device__ static inline int scan_max(int v) {
+    // (row offsets are not negative: a lane that a move does not reach gets 0)
+    v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false));  // row_shr:1, 2, 4, 8
+    v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false));
+    v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false));
+    v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false));
+    v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false));  // row_bcast:15, :31
+    return max(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false));
 }
 
 // Up to eight 16-bit values from e on, of which n exist (n <= 0: none is touched).
@@ -235,75 +270,80 @@ __device__ static inline void hidden_store(const AdapterArgs &p, int a, float s,
     }
 }
 
+// The request (and its adapter and rows) that holds row tile `tile` of BM rows, the tiles of all
+// requests numbered in ascending order, found by the whole workgroup: a request to a
+// thread, two scans over the workgroup (a wave alone would take a turn for each 64
+// requests).  False: there are fewer tiles.
+struct TileRequest {
+    int adapter, row0, rows;  // first row of the tile, rows
+};
+template <int BM, int THREADS>
+__device__ static inline bool find_tile(const RequestTable &t, int tile, TileRequest &out) {
+    constexpr int NW = THREADS / 64;
+    __shared__ int ends[NW], counts[NW];
+    __shared__ int found[3];
+    const int tid = threadIdx.x, lane = lane_id(), wave = wave_id();
+    int floor = scalar_offset(t, 0), first = 0;  // where this turn's requests begin: row, tile
+    for (int base = 0;; base += THREADS) {
+        const int g = base + tid;
+        const RequestLoad q = load_requests(t, base + wave * 64, lane);
+        int end = scan_max(g < t.groups ? offset_value(q.lo, t.off32 ? q.lo >> 31 : q.hi, t.rows) : 0);
+        if (lane == 63) ends[wave] = end;
+        __syncthreads();
+        int before = floor, all = floor;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            if (w < wave) before = max(before, ends[w]);
+            all = max(all, ends[w]);
+        }
+        end = max(end, before);
+        int start = __shfl_up(end, 1, 64);
+        if (lane == 0) start = before;
+        const int tiles = end > start ? (end - start - 1) / BM + 1 : 0, upto = wave_scan_add(tiles, lane);
+        if (lane == 63) counts[wave] = upto;
+        __syncthreads();
+        int mine = first + upto - tiles, total = first;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            if (w < wave) mine += counts[w];
+            total += counts[w];
+        }
+        if (tile >= mine && tile < mine + tiles) {
+            found[0] = (uint32_t)q.id < (uint32_t)t.adapters ? q.id : -1;
+            found[1] = start + (tile - mine) * BM;
+            found[2] = min(BM, end - start - (tile - mine) * BM);
+        }
+        __syncthreads();
+        if (tile < total) {
+            out.adapter = __builtin_amdgcn_readfirstlane(found[0]);
+            out.row0 = __builtin_amdgcn_readfirstlane(found[1]);
+            out.rows = __builtin_amdgcn_readfirstlane(found[2]);
+            return true;
+        }
+        if (base + THREADS >= t.groups) return false;
+        floor = all;
+        first = total;
+    }
+}
+
 // H.  TM, TN: 16 TM rows by 16 TN columns to a workgroup (K-contiguous A_a); TN == 0:
 // r-contiguous A_a, 16 rows by 128 columns.
 template <class DT, int TM, int TN, bool FAST>
 __global__ __launch_bounds__(HIDDEN_WAVES * 64, 2) void adapter_hidden(const AdapterArgs p) {
     constexpr int BM = 16 * TM, CW = TN ? 16 * TN : 128, SZ = BM * CW;
     __shared__ float lds[HIDDEN_WAVES * SZ];
-    const int id = workgroup_id(), lane = lane_id(), total = (int)p.r.M;
-    const int tile = id / p.tiles_r, c0 = (id - tile * p.tiles_r) * CW;
-    const int own = first_adapters(p.t, lane);
-    GroupWalk<BM> walk;
-    walk.load(p.r, total, lane);
-    int g, r0, r1, tile0;
-    if (!walk.find(p.r, total, lane, tile, g, r0, r1, tile0)) return;
-    const int a = adapter_of(p.t, g, own);
+    const int id = workgroup_id(), tile = id / p.tiles_r, c0 = (id - tile * p.tiles_r) * CW;
+    TileRequest q;
+    if (!find_tile<BM, HIDDEN_WAVES * 64>(p.t, tile, q)) return;
+    const int a = q.adapter, rows = q.rows;
     if (a < 0 && !p.hidden) return;
+    const int64_t row0 = q.row0;
     const float scale = p.scale && a >= 0 ? p.scale[a] : 1.0f;
-    const int64_t row0 = r0 + (int64_t)(tile - tile0) * BM;
-    const int rows = (int)min((int64_t)BM, r1 - row0);
     if (a >= 0) {
         if constexpr (TN > 0) hidden_sum<DT, TM, TN, FAST>(p, a, row0, rows, c0, lds);
         else hidden_sum_n<DT, FAST>(p, a, row0, rows, c0, lds);
     }
     hidden_store<DT, CW, SZ>(p, a, scale, row0, rows, c0, lds);
-}
-
-// A tile's requests that have an adapter: rows lo .. hi - 1 of the tile, in ascending order.
-struct AdapterEntry {
-    int rows;      // lo | hi << 16
-    int adapter;
-};
-
-// A row number of the offsets as its two words, brought into 0 .. rows.
-__device__ static inline int offset_value(int lo, int hi, int rows) {
-    return hi < 0 ? 0 : (hi > 0 || (uint32_t)lo > (uint32_t)rows) ? rows : lo;
-}
-// What a list of a tile's requests is made from, this lane's of 64 requests: loaded ahead of
-// other loads, so that it arrives first, without branches, so that all of it is on its way
-// at once (a 32-bit offset's second word is the first again; requests past the last one: the last).
-struct RequestLoad {
-    int lo, hi, id;
-};
-__device__ static inline RequestLoad load_requests(const RequestTable &t, int chunk, int lane) {
-    const int g = min(chunk + lane, t.groups - 1), w = t.off32 ? 1 : 2;
-    const int32_t *o = (const int32_t *)t.offsets + (int64_t)(g + 1) * w;
-    RequestLoad q;
-    q.lo = o[0];
-    q.hi = o[w - 1];
-    q.id = t.ids ? t.ids[g] : g;
-    return q;
-}
-
-// Row number i of the offsets (0 .. groups), by scalar loads: they wait for no vector load.
-__device__ static inline int scalar_offset(const RequestTable &t, int i) {
-    typedef const __attribute__((address_space(4))) int32_t *words;
-    const int w = t.off32 ? 1 : 2;
-    const words o = (words)t.offsets + (int64_t)i * w;
-    const int lo = o[0], hi = o[w - 1];
-    return offset_value(lo, w == 1 ? lo >> 31 : hi, t.rows);
-}
-
-// The largest of this lane's value and those before it.
-__device__ static inline int scan_max(int v) {
-    // (row offsets are not negative: a lane that a move does not reach gets 0)
-    v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false));  // row_shr:1, 2, 4, 8
-    v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false));
-    v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false));
-    v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false));
-    v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false));  // row_bcast:15, :31
-    return max(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false));
 }
 
 // By one wave; returns their number (at most BM: no two share a row, since each
@@ -411,80 +451,120 @@ __device__ static inline void adapter_blocks(floatx4 (&acc)[TM][TN], int rows, i
     }
 }
 
-// A 16 x 32 piece of B_a for the matrix instructions, columns c0 .. and rank k0 ..: lane L
-// gets column L % 16 and 8 consecutive k.  By whole granules, or (any layout and
-// alignment) value by value.
-template <bool BKC, bool GRANULES>
+// A piece of B_a, 16 TN columns from c0 on by 32 of the rank from k0 on, for the matrix
+// instructions (lane L: column L % 16 of a block, 8 consecutive k).  K-contiguous
+// granules come as they are needed; N-contiguous ones pass through LDS (4 KB of a wave's own, of
+// 128-byte blocks of 4 k x 16 columns, which the transposing reads take); any other layout
+// and alignment value by value.
+enum { PIECE_K, PIECE_N, PIECE_ANY };
+template <int HOW, bool BKC, int TN>
 struct AdapterPiece {
-    intx4 v[GRANULES ? 1 : 2];  // value by value: one to a half word, packed by get()
+    static constexpr int NV = HOW == PIECE_K ? TN : HOW == PIECE_N ? TN : 2 * TN;
+    intx4 v[NV];
     __device__ void load(const AdapterArgs &p, int a, int64_t c0, int cols, int k0, int lane) {
-        const int c = lane & 15, k = 8 * (lane >> 4);
+        const int left = p.rank - k0;
         const int64_t at = a * p.sB + (BKC ? c0 * p.ldb + k0 : k0 * p.ldb + c0);
         const __amdgpu_buffer_rsrc_t r = make_rsrc((const char *)p.B + at * 2);
-        const int left = p.rank - k0;
-        if constexpr (GRANULES) {
-            v[0] = load_granule(r, joined(row_part(c, cols, p.ldb), k_part(k, left)));
+        const int c = lane & 15, k = 8 * (lane >> 4);
+        if constexpr (HOW == PIECE_K) {
+            const int ko = k_part(k, left);
+#pragma unroll
+            for (int j = 0; j < TN; ++j) v[j] = load_granule(r, joined(row_part(16 * j + c, cols, p.ldb), ko));
+        } else if constexpr (HOW == PIECE_N) {
+            // granule x = 64 j + lane: 8 columns of one k, 2 TN of them to a k
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const int x = 64 * j + lane;
+                v[j] = load_granule(r, joined(row_part(x / (2 * TN), left, p.ldb), k_part(x % (2 * TN) * 8, cols)));
+            }
         } else {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const int off = BKC ? joined(row_part(c, cols, p.ldb), k_part(k + q, left))
-                                    : joined(row_part(k + q, left, p.ldb), k_part(c, cols));
-                v[q / 4][q % 4] = (int)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
+            for (int x = 0; x < 8 * TN; ++x) {
+                const int j = x / 8, q = x % 8;
+                const int off = BKC ? joined(row_part(16 * j + c, cols, p.ldb), k_part(k + q, left))
+                                    : joined(row_part(k + q, left, p.ldb), k_part(16 * j + c, cols));
+                v[x / 4][x % 4] = (int)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
             }
         }
     }
-    __device__ intx4 get() const {
-        if constexpr (GRANULES) return v[0];
-        else return intx4{v[0][0] | v[0][1] << 16, v[0][2] | v[0][3] << 16, v[1][0] | v[1][1] << 16, v[1][2] | v[1][3] << 16};
+    // the blocks' fragments; slab: 1 KB for each block of this wave's own
+    __device__ void get(DMP_LDS char *slab, int lane, intx4 (&b)[TN]) const {
+        if constexpr (HOW == PIECE_K) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j) b[j] = v[j];
+        } else if constexpr (HOW == PIECE_N) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const int x = 64 * j + lane, k = x / (2 * TN), g = x % (2 * TN);
+                *(DMP_LDS intx4 *)(slab + ((k >> 2) * TN + (g >> 1)) * 128 + (k & 3) * 32 + (g & 1) * 16) = v[j];
+            }
+            __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const int kb = 2 * (lane >> 4) + t;
+                    const intx2 w = __builtin_bit_cast(
+                        intx2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((DMP_LDS shortx4 *)(slab + (kb * TN + j) * 128 + (lane & 15) * 8)));
+                    b[j][2 * t] = w[0];
+                    b[j][2 * t + 1] = w[1];
+                }
+            __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+        } else {
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int d = 0; d < 4; ++d) b[j][d] = v[2 * j + d / 2][d % 2 * 2] | v[2 * j + d / 2][d % 2 * 2 + 1] << 16;
+        }
     }
 };
 
 // The adapters' part of a wave's TM x TN blocks, from `row` of the tile on: the entries
 // that have rows there, 32 of the rank at a time, straight from memory (H and B_a are in
-// the caches), the next piece on its way beside each.  No other wave is waited for: an
-// entry of one row costs its loads, where its own k-tile through LDS would cost the
-// whole workgroup a turn (0.7 us).
-template <class DT, bool BKC, bool GRANULES, int TM, int TN>
+// the caches), four pieces on their way at once.  No other wave is waited for: an entry of
+// one row costs its loads, where its own k-tile through LDS would cost the whole
+// workgroup a turn (0.7 us).
+template <class DT, bool BKC, int HOW, int TM, int TN>
 __device__ static inline void adapter_direct(const AdapterArgs &p, const TileAt &at, const DMP_LDS AdapterEntry *list, int entries,
-                                             int row, int col, int lane, floatx4 (&acc)[TM][TN]) {
+                                             int row, int col, int lane, DMP_LDS char *slab, floatx4 (&acc)[TM][TN]) {
+    constexpr int NS = HOW == PIECE_ANY ? 2 : 4, ROWS = 16 * TM;
+    static_assert(ROWS <= 64, "no more entries than lanes");
     const int r16 = lane & 15;
-    intx4 fh[2][TM];
-    AdapterPiece<BKC, GRANULES> fb[2][TN];
-    int lo[2], hi[2], e = 0, k = 0, part = 0;
     int ho[TM];
 #pragma unroll
     for (int i = 0; i < TM; ++i) ho[i] = row_part(row + 16 * i + r16, at.rows, p.rp);
-    auto entry = [&](int x) { return __builtin_amdgcn_readfirstlane(list[x].rows); };
-    while (e < entries && (int)((uint32_t)entry(e) >> 16) <= row) ++e;
-    // piece (e, k, part) into slot st, and on to the next one; past the last: no rows
+    // the entries with rows here, one to a lane
+    int e0 = 0;
+    while (e0 < entries && (int)((uint32_t)__builtin_amdgcn_readfirstlane(list[e0].rows) >> 16) <= row) ++e0;
+    const int x = min(e0 + lane, max(entries - 1, 0)), my_rows = list[x].rows, my_adapter = list[x].adapter;
+    const int n = __popcll(__ballot(e0 + lane < entries && (my_rows & 0xffff) < row + ROWS));
+    intx4 fh[NS][TM];
+    AdapterPiece<HOW, BKC, TN> fb[NS];
+    int lo[NS], hi[NS], e = 0, k = 0, part = 0;
+    // piece (e, k, part) into slot st, and on to the next one; past the last: no rows, and no memory
+    // is touched (without a branch, behind which each slot's loads would be waited for)
     auto load = [&](int st) {
-        const int rr = e < entries ? entry(e) : 0;
-        lo[st] = max((rr & 0xffff) - row, 0);
-        hi[st] = (int)((uint32_t)rr >> 16) - row;
-        if (lo[st] >= 16 * TM || hi[st] <= 0) {
-            lo[st] = hi[st] = 0;
-            return;
-        }
-        const int a = __builtin_amdgcn_readfirstlane(list[e].adapter);
+        const bool there = e < n;
+        const int rr = __builtin_amdgcn_readlane(my_rows, e & 63), a = __builtin_amdgcn_readlane(my_adapter, e & 63);
+        lo[st] = there ? max((rr & 0xffff) - row, 0) : 0;
+        hi[st] = there ? (int)((uint32_t)rr >> 16) - row : 0;
         const __amdgpu_buffer_rsrc_t rh = make_rsrc(p.H + (part * p.r.M * p.rp + at.row0 * p.rp + k) * 2);
         const int ko = k_part(8 * (lane >> 4), p.rp - k);
 #pragma unroll
         for (int i = 0; i < TM; ++i)
             fh[st][i] = load_granule(rh, hi[st] > 16 * i && lo[st] < 16 * i + 16 ? joined(ho[i], ko) : OOB_OFFSET);
-#pragma unroll
-        for (int j = 0; j < TN; ++j) fb[st][j].load(p, a, at.col0 + col + 16 * j, at.cols - col - 16 * j, k, lane);
-        if ((k += 32) >= p.rank) {
-            k = 0;
-            if (++part == p.parts) {
-                part = 0;
-                ++e;
-            }
-        }
+        fb[st].load(p, a, at.col0 + col, there ? at.cols - col : 0, k, lane);
+        k += 32;
+        const bool turn = k >= p.rank;
+        k = turn ? 0 : k;
+        part += turn;
+        const bool last = part == p.parts;
+        part = last ? 0 : part;
+        e += last;
     };
     auto multiply = [&](int st) {
         intx4 b[TN];
-#pragma unroll
-        for (int j = 0; j < TN; ++j) b[j] = fb[st][j].get();
+        fb[st].get(slab, lane, b);
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
             const int r = 16 * i;
@@ -504,14 +584,14 @@ __device__ static inline void adapter_direct(const AdapterArgs &p, const TileAt 
             }
         }
     };
-    load(0);
-    while (hi[0] > 0) {
-        load(1);
-        multiply(0);
-        if (hi[1] <= 0) break;
-        load(0);
-        multiply(1);
-    }
+    do {
+#pragma unroll
+        for (int st = 0; st < NS; ++st) load(st);
+        issued();
+#pragma unroll
+        for (int st = 0; st < NS; ++st)
+            if (hi[st] > 0) multiply(st);
+    } while (hi[NS - 1] > 0);
 }
 
 // The product, X and W staged through registers as in ragged_staged.hpp.  FAST: their
@@ -622,8 +702,13 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void adapter_staged(const AdapterAr
         }
         const int entries = __builtin_amdgcn_readfirstlane(count);
         const DMP_LDS AdapterEntry *entry = (const DMP_LDS AdapterEntry *)list;
-        if (BKC && p.b_fast) adapter_direct<DT, BKC, true>(p, at, entry, entries, wm * WTM, wn * WTN, lane, acc);
-        else adapter_direct<DT, BKC, false>(p, at, entry, entries, wm * WTM, wn * WTN, lane, acc);
+        // (every wave is past the last barrier's LDS reads: the panels are free)
+        DMP_LDS char *const own = (DMP_LDS char *)lds_b[1] + wave * (TN * 1024);
+        static_assert(NW * TN * 1024 <= OpB::BYTES, "a slab of each wave's own");
+        if (p.b_fast)
+            adapter_direct<DT, BKC, BKC ? PIECE_K : PIECE_N>(p, at, entry, entries, wm * WTM, wn * WTN, lane, own, acc);
+        else
+            adapter_direct<DT, BKC, PIECE_ANY>(p, at, entry, entries, wm * WTM, wn * WTN, lane, own, acc);
     }
     __syncthreads();
     constexpr int SLAB = 32 * (WTN + 4) * 4, INA = 2 * OpA::BYTES / SLAB;
@@ -775,6 +860,7 @@ __global__ __launch_bounds__(256) void adapter_tile(const AdapterArgs p) {
                                    [&](int i, int s) { return frag16<DT, OpA, BM, true>(la, wm * WTM + i * 16, s, lane); },
                                    [&](int j, int s) { return frag16<DT, OpB, BN, BKC>(lb, wn * WTN + j * 16, s, lane); },
                                    [](floatx4 &c, const intx4 &a, const intx4 &b) { c = mma16<DT>(a, b, c); });
+        step_sync();
         wait_vmcnt<0>();
         __syncthreads();
         if (x + 2 < more) {
@@ -792,123 +878,6 @@ __global__ __launch_bounds__(256) void adapter_tile(const AdapterArgs p) {
     store_wave_tile<WTM, WTN, true>((DMP_LDS float *)slab, ep, (const char *)p.r.C + first * out_size(ep.c_type),
                               (char *)p.r.D + first * out_size(ep.d_type), p.r.ldc, at.rows, at.cols, wm * WTM,
                               wn * WTN, lane, [&](int i, int j) { return acc[i][j]; });
-}
-
-// The product of few rows by K-contiguous W and B_a (decoding), as skinny.hpp: a workgroup
-// takes 16 TN columns, its waves split K and stream W into matrix-instruction operands; then
-// each takes its share of the requests and streams their B_a, and the sums meet in LDS.
-// Rows go 16 TM at a time.  A request's products are summed apart and added to its rows.
-template <class DT, int TM, int TN>
-__global__ __launch_bounds__(512, 2) void adapter_skinny(const AdapterArgs p) {
-    constexpr int NW = 8, BM = 16 * TM, U = TM + TN <= 2 ? 4 : TM + TN <= 5 ? 2 : 1, CW = 16 * TN, SZ = BM * CW;
-    __shared__ __attribute__((aligned(16))) float lds[NW * SZ];
-    __shared__ AdapterEntry lists[NW][BM];
-    const int lane = lane_id(), wave = wave_id(), r16 = lane & 15, K = (int)p.r.K;
-    const int64_t col0 = (int64_t)workgroup_id() * CW;
-    if (col0 >= p.r.N) return;
-    const int cols = (int)min((int64_t)CW, p.r.N - col0);
-    const int last = scalar_offset(p.t, p.t.groups);
-    const int nkt = (K + 63) / 64, per = (nkt + NW - 1) / NW, kt0 = min(wave * per, nkt), kt1 = min(kt0 + per, nkt);
-    const int kend = min(K, kt1 * 64);
-    const __amdgpu_buffer_rsrc_t rw = make_rsrc((const char *)p.r.B + col0 * p.r.ldb * 2);
-    DMP_LDS AdapterEntry *list = (DMP_LDS AdapterEntry *)lists[wave];
-    for (int row0 = scalar_offset(p.t, 0); row0 < last; row0 += BM) {
-        const int rows = min(BM, last - row0);
-        const __amdgpu_buffer_rsrc_t rx = make_rsrc((const char *)p.r.A + row0 * p.r.lda * 2);
-        floatx4 acc[TM][TN] = {};
-        intx4 fx[2][U][TM][2], fw[2][U][TN][2];
-        int xo[TM], wo[TN];
-#pragma unroll
-        for (int i = 0; i < TM; ++i) xo[i] = row_part(i * 16 + r16, rows, p.r.lda);
-#pragma unroll
-        for (int j = 0; j < TN; ++j) wo[j] = row_part(j * 16 + r16, cols, p.r.ldb);
-        auto load = [&](int st, int kt) {
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int ko = k_part((kt + u) * 64 + 32 * h + 8 * (lane >> 4), kend);
-#pragma unroll
-                    for (int j = 0; j < TN; ++j) fw[st][u][j][h] = load_granule(rw, joined(wo[j], ko));
-#pragma unroll
-                    for (int i = 0; i < TM; ++i) fx[st][u][i][h] = load_granule(rx, joined(xo[i], ko));
-                }
-            issued();
-        };
-        auto multiply = [&](int st) {
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int i = 0; i < TM; ++i)
-#pragma unroll
-                        for (int j = 0; j < TN; ++j) acc[i][j] = mma16<DT>(fx[st][u][i][h], fw[st][u][j][h], acc[i][j]);
-        };
-        if (kt0 < kt1) load(0, kt0);
-        // the requests of these rows, while the first loads are on their way
-        const int entries = adapter_entries<BM>(p.t, scalar_offset(p.t, 0), row0, rows, list, load_requests(p.t, 0, lane));
-        for (int kt = kt0; kt < kt1; kt += 2 * U) {
-            load(1, kt + U);
-            multiply(0);
-            load(0, kt + 2 * U);
-            multiply(1);
-        }
-        // this wave's requests, EB at a time: all their loads before the first product
-        constexpr int EB = 4;
-        const __amdgpu_buffer_rsrc_t rh = make_rsrc(p.H + row0 * (int64_t)p.rp * 2);
-        for (int e0 = wave; e0 < entries; e0 += NW * EB)
-            for (int kr = 0; kr < p.rank; kr += 32) {
-                const int k = kr + 8 * (lane >> 4);
-                intx4 fb[EB][TN];
-                int lo[EB], hi[EB];
-#pragma unroll
-                for (int b = 0; b < EB; ++b) {
-                    const int e = e0 + NW * b;
-                    const bool there = e < entries;
-                    const int rr = __builtin_amdgcn_readfirstlane(there ? list[e].rows : 0);
-                    const int a = __builtin_amdgcn_readfirstlane(there ? list[e].adapter : 0);
-                    lo[b] = rr & 0xffff;
-                    hi[b] = (int)((uint32_t)rr >> 16);
-                    const __amdgpu_buffer_rsrc_t rb = make_rsrc((const char *)p.B + (a * p.sB + col0 * p.ldb) * 2);
-#pragma unroll
-                    for (int j = 0; j < TN; ++j) {
-                        const int c = j * 16 + r16;
-                        fb[b][j] = load_granule(rb, there && c < cols && k < p.rank ? (c * (int)p.ldb + k) * 2 : OOB_OFFSET);
-                    }
-                }
-                for (int part = 0; part < p.parts; ++part) {
-                    const __amdgpu_buffer_rsrc_t rp = part ? make_rsrc(p.H + (p.r.M + row0) * (int64_t)p.rp * 2) : rh;
-#pragma unroll
-                    for (int i = 0; i < TM; ++i) {
-                        const int r = i * 16 + r16;
-                        const intx4 fh = load_granule(rp, r < rows && k < p.rank ? (r * p.rp + k) * 2 : OOB_OFFSET);
-                        const int mine = 16 * i + 4 * (lane >> 4);
-#pragma unroll
-                        for (int b = 0; b < EB; ++b) {
-                            if (hi[b] <= 16 * i || lo[b] >= 16 * i + 16) continue;
-#pragma unroll
-                            for (int j = 0; j < TN; ++j) {
-                                const floatx4 c = mma16<DT>(fh, fb[b][j], floatx4{0, 0, 0, 0});
-#pragma unroll
-                                for (int q = 0; q < 4; ++q)
-                                    acc[i][j][q] += mine + q >= lo[b] && mine + q < hi[b] ? c[q] : 0.0f;
-                            }
-                        }
-                    }
-                }
-            }
-        step_sync();
-        __syncthreads();  // the sums of the rows before are read
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    lds[wave * SZ + (i * 16 + 4 * (lane >> 4) + q) * CW + j * 16 + r16] = acc[i][j][q];
-        join_waves<NW, CW, SZ>(p.r, lds, row0, rows, col0, cols);
-    }
 }
 
 }  // namespace dmp

@@ -43,16 +43,8 @@ int launch_staged(AdapterArgs a, hipStream_t s) {
     return launch(adapter_staged<DT, BM, BN, WM, WN, BKC, FAST>, cdiv(a.r.M, BM) * a.r.tiles_n, WM * WN * 64, s, a);
 }
 
-template <class DT, int TM, int TN>
-int launch_skinny(const AdapterArgs &a, hipStream_t s) {
-    return launch(adapter_skinny<DT, TM, TN>, cdiv(a.r.N, 16 * TN), 512, s, a);
-}
-
 template <class DT, bool BKC>
 int run_product(const AdapterArgs &a, int cfg, hipStream_t s) {
-    if constexpr (BKC) {
-        if (cfg == CFG_SKINNY4) return launch_skinny<DT, 4, 1>(a, s);
-    }
     if (cfg == CFG_L) {
         AdapterArgs b = a;
         b.r.tiles_n = (int)cdiv(a.r.N, 256);
@@ -63,12 +55,12 @@ int run_product(const AdapterArgs &a, int cfg, hipStream_t s) {
 
 template <class DT, int BM>
 int launch_few(const AdapterFewArgs &f, int parts, hipStream_t s) {
-    const int64_t grid = (int64_t)f.blocks * f.splits;
+    const int64_t rows64 = cdiv(f.M, BM), grid = (int64_t)f.blocks * f.splits * rows64;
     const int rc = f.per <= 4   ? launch(adapter_few<DT, BM, 4>, grid, 256, s, f)
                    : f.per <= 8 ? launch(adapter_few<DT, BM, 8>, grid, 256, s, f)
                                 : launch(adapter_few<DT, BM, 16>, grid, 256, s, f);
     if (rc != GEMM_OK) return rc;
-    const int64_t join = cdiv(f.N, 16);
+    const int64_t join = f.joins * rows64;
     return parts > 1 ? launch(adapter_few_join<DT, BM, 2>, join, 512, s, f) : launch(adapter_few_join<DT, BM, 1>, join, 512, s, f);
 }
 
@@ -81,7 +73,7 @@ int run_few(int num_cus, const AdapterArgs &a, hipStream_t s) {
     f.M = (int)a.r.M; f.N = (int)a.r.N; f.K = (int)a.r.K;
     f.ldx = (int)a.r.lda; f.ldw = (int)a.r.ldb; f.lda = (int)a.lda; f.ldb = (int)a.ldb;
     f.rank = a.rank; f.r16 = (int)cdiv(a.rank, 16) * 16;
-    f.splits = q.splits; f.per = q.per; f.blocks = q.blocks;
+    f.splits = q.splits; f.per = q.per; f.blocks = q.blocks; f.joins = (int)cdiv(a.r.N, 16);
     f.sA = a.sA; f.sB = a.sB; f.b_fast = a.b_fast;
     f.C = a.r.C; f.D = a.r.D; f.hidden = a.hidden; f.ldc = a.r.ldc; f.ld_hidden = a.ld_hidden; f.ep = a.r.ep;
     f.part = (float *)a.H;
@@ -92,7 +84,7 @@ int run_few(int num_cus, const AdapterArgs &a, hipStream_t s) {
 
 template <class DT>
 int run_adapters(int num_cus, const AdapterArgs &a, bool a_col, bool b_col, bool hidden_f, int cfg, hipStream_t s) {
-    if (cfg == CFG_SKINNY1) return run_few<DT>(num_cus, a, s);
+    if (cfg == CFG_FEW) return run_few<DT>(num_cus, a, s);
     if (a.r.K > 0 || a.hidden) {
         const int rc = run_hidden<DT>(a, a_col, hidden_f, s);
         if (rc != GEMM_OK) return rc;
@@ -137,7 +129,7 @@ int gemm_run_adapters(gemm_handle_t h, const void *X, const void *W, const gemm_
     a.sA = (ac ? ad->rank : K) * ad->lda;
     a.sB = (bc ? N : ad->rank) * ad->ldb;
     a.rank = (int)ad->rank;
-    a.b_fast = bc && adapter_b_fast(*ad);
+    a.b_fast = adapter_b_fast(*ad, N, bc);
     a.H = (char *)work;
     a.rp = (int)adapter_rp(ad->rank);
     a.parts = adapter_parts(d_type);

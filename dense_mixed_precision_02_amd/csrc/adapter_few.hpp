@@ -1,4 +1,4 @@
-// adapter_few.hpp -- adapters beside a shared projection for few rows (decoding: up to 64 rows).
+// adapter_few.hpp -- adapters beside a shared projection for few rows (decoding: 64 at a time).
 //
 // With few rows the time is that of reading W (and the adapters) once, and of what has to
 // wait for what.  As hidden and product (adapter.hpp) three reads follow each other: A_a,
@@ -30,6 +30,7 @@ struct AdapterFewArgs {
     int rank, r16;       // r16: rank, rounded up to 16
     int splits, per;     // parts of K, and k-tiles of 64 in each
     int blocks;          // workgroups to a part: cdiv(N, 64) or more
+    int joins;           // the join's to 64 rows: cdiv(N, 16)
     int64_t sA, sB;      // elements from one adapter's A, B to the next
     int b_fast;          // B's 16-byte granules are aligned and whole
     const void *C;
@@ -46,15 +47,16 @@ __global__ __launch_bounds__(256, 1) void adapter_few(const AdapterFewArgs p) {
     __shared__ float red[NW][BM * 16];
     __shared__ AdapterEntry lists[NW][BM];
     const int lane = lane_id(), wave = wave_id(), r16 = lane & 15, K = p.K;
-    const int id = workgroup_id(), split = id / p.blocks, cb = id - split * p.blocks;
-    if (split >= p.splits) return;
+    const int id = workgroup_id(), part = id / p.blocks, cb = id - part * p.blocks;
+    const int rb = part / p.splits, split = part - rb * p.splits;  // 64 rows, part of K
     const int kt0 = split * p.per, nkt = min(p.per, (K + 63) / 64 - kt0), kend = min(K, (kt0 + nkt) * 64);
     const int64_t col0 = (int64_t)cb * 64 + wave * 16;
     const int cols = (int)max((int64_t)0, min((int64_t)16, p.N - col0));
     // In the order in which they are needed first: the requests, X, W.
     const RequestLoad requests = load_requests(p.t, 0, lane);
     issued();
-    const int first = scalar_offset(p.t, 0), rows = min(BM, scalar_offset(p.t, p.t.groups) - first);
+    const int from = scalar_offset(p.t, 0), first = from + rb * BM;
+    const int rows = min(BM, scalar_offset(p.t, p.t.groups) - first);
     if (rows <= 0) return;
     // X's part: 1 KB (8 rows of a k-tile) to a copy
     const __amdgpu_buffer_rsrc_t rx = make_rsrc((const char *)p.X + (int64_t)first * p.ldx * 2);
@@ -84,7 +86,7 @@ __global__ __launch_bounds__(256, 1) void adapter_few(const AdapterFewArgs p) {
             fw[t][h] = load_granule(rw, joined(wo, k_part((kt0 + t) * 64 + 32 * h + 8 * (lane >> 4), kend)));
     issued();
     DMP_LDS AdapterEntry *list = (DMP_LDS AdapterEntry *)lists[wave];
-    const int entries = adapter_entries<BM>(p.t, first, first, rows, list, requests);
+    const int entries = adapter_entries<BM>(p.t, from, first, rows, list, requests);
     // hidden sums: 16 columns of an entry's A_a, the waves take its k-tiles in turn
     const int rt = p.r16 / 16, tasks = entries * rt;
     intx4 fa[HT][2];
@@ -189,17 +191,18 @@ __global__ __launch_bounds__(512, 2) void adapter_few_join(const AdapterFewArgs 
     __shared__ int owner[BM];
     __shared__ float scales[BM];
     const int lane = lane_id(), wave = wave_id(), r16 = lane & 15, tid = threadIdx.x;
-    const int64_t col0 = (int64_t)workgroup_id() * 16;
-    if (col0 >= p.N) return;
+    const int id = workgroup_id(), rb = id / p.joins;
+    const int64_t col0 = (int64_t)(id - rb * p.joins) * 16;
     const int cols = (int)min((int64_t)16, p.N - col0);
     const RequestLoad requests = load_requests(p.t, 0, lane);
-    const int first = scalar_offset(p.t, 0), rows = min(BM, scalar_offset(p.t, p.t.groups) - first);
+    const int from = scalar_offset(p.t, 0), first = from + rb * BM;
+    const int rows = min(BM, scalar_offset(p.t, p.t.groups) - first);
     if (rows <= 0) return;
     // (barrier_vmcnt: only LDS is exchanged, and what is on its way stays so)
     if (tid < BM) owner[tid] = 0;
     barrier_vmcnt<63>();
     DMP_LDS AdapterEntry *list = (DMP_LDS AdapterEntry *)lists[wave];
-    const int entries = adapter_entries<BM>(p.t, first, first, rows, list, requests);
+    const int entries = adapter_entries<BM>(p.t, from, first, rows, list, requests);
     // entry `lane`, where wave 0 needs it, and this wave's entry `lane`
     const int ia = min(lane, max(entries - 1, 0)), im = min(wave + NW * lane, max(entries - 1, 0));
     const int all_rows = list[ia].rows, my_rows = list[im].rows, my_adapter = list[im].adapter;
@@ -274,7 +277,7 @@ __global__ __launch_bounds__(512, 2) void adapter_few_join(const AdapterFewArgs 
                 const float left = v - decode16(hi, f16);
                 hl[1][row][c] = encode16(__builtin_isfinite(left) ? left : 0.0f, f16);
             }
-            if (p.hidden && workgroup_id() == 0 && row < rows && c < p.rank)
+            if (p.hidden && col0 == 0 && row < rows && c < p.rank)
                 ((uint16_t *)p.hidden)[(int64_t)(first + row) * p.ld_hidden + c] = hi;
         }
     }

@@ -12,15 +12,15 @@ constexpr int64_t ADAPTER_RANK_MAX = 1024, ADAPTER_LD_MAX = 1ll << 24;  // 31-bi
 inline int64_t adapter_rp(int64_t rank) { return cdiv(rank, 8) * 8; }
 inline int adapter_parts(int d_type) { return d_type == GEMM_OUT_F32 ? 2 : 1; }
 
-// Up to 64 rows (adapter_few.hpp): parts of K, of at most 16 k-tiles of 64 and of 2 at least,
+// Few rows, 64 at a time (adapter_few.hpp): parts of K, of at most 16 k-tiles of 64 and of 2 at least,
 // as many as give every CU a workgroup of the columns' or of the hidden sums'.
 struct FewPlan {
     int splits, per, blocks;
 };
 inline FewPlan few_plan(int num_cus, int64_t requests, int64_t M, int64_t N, int64_t K, int64_t rank) {
     FewPlan f;
-    const int64_t nkt = cdiv(K, 64), nb = cdiv(N, 64), tasks = std::min(M, requests) * cdiv(rank, 16);
-    const int64_t wide = std::max(nb, tasks);
+    const int64_t nkt = cdiv(K, 64), nb = cdiv(N, 64), tasks = std::min<int64_t>(std::min<int64_t>(M, 64), requests) * cdiv(rank, 16);
+    const int64_t wide = std::max(nb, tasks) * cdiv(M, 64);
     const int64_t want = std::max(cdiv(nkt, 16), std::min<int64_t>(num_cus / std::min<int64_t>(wide, num_cus), cdiv(nkt, 2)));
     f.per = (int)cdiv(nkt, want);
     f.splits = (int)cdiv(nkt, f.per);
@@ -28,7 +28,7 @@ inline FewPlan few_plan(int num_cus, int64_t requests, int64_t M, int64_t N, int
     f.blocks = (int)std::max(nb, std::min<int64_t>(tasks, std::max<int64_t>(1, 2 * num_cus / f.splits)));
     return f;
 }
-constexpr int64_t FEW_ROWS = 64, FEW_RANK_MAX = 128, FEW_N_MAX = 1 << 22;  // N: 31-bit offsets in 64 rows of sums
+constexpr int64_t FEW_ROWS = 256, FEW_RANK_MAX = 128, FEW_N_MAX = 1 << 22;  // N: 31-bit offsets in 64 rows of sums
 inline int64_t few_work(int splits, int64_t M, int64_t N, int64_t rank) {
     return splits * (cdiv(M * N * 4, 16) * 16 + cdiv(M * cdiv(rank, 16) * 64, 16) * 16);
 }
@@ -85,25 +85,31 @@ inline bool hidden_fast(const void *X, const gemm_adapters_t &ad, int64_t K, int
     return (64 * ldx + K) * 2 < lim && (64 * ad.lda + K) * 2 < lim;
 }
 
-// Can B_a's granules be copied whole (along its contiguous extent)?
-inline bool adapter_b_panels(const gemm_adapters_t &ad, int64_t N, bool b_col) {
+// Can B_a's granules be loaded whole (along its contiguous extent)?
+inline bool adapter_b_fast(const gemm_adapters_t &ad, int64_t N, bool b_col) {
     return aligned16(ad.B) && ad.ldb % 8 == 0 && (b_col ? ad.rank : N) % 8 == 0 && 256 * ad.ldb * 2 < (1ll << 31) - (1ll << 22);
 }
 
-// K-contiguous B_a: can its granules be loaded whole?
-inline bool adapter_b_fast(const gemm_adapters_t &ad) { return aligned16(ad.B) && ad.ldb % 8 == 0 && ad.rank % 8 == 0; }
-
-// Which product kernel (CFG_GENERIC: any alignment; CFG_SKINNY1: the kernels for few rows).
+// Which kernels (CFG_FEW: adapter_few.hpp; CFG_GENERIC: any alignment).
+//
+// Few rows: up to 256 (us of both launches, few / hidden and 128 x 128 tiles, 4096 x 4096, rank 16: 128
+// rows of 128 requests 43 / 129, of 4: 38 / 64, 256 rows of 256 requests 79 / 128, of 4: 71 / 67;
+// 1024 x 1024: 128 rows of 16 requests 16 / 35, 256 rows of 256: 24 / 88, of 4, rank 64: 18 / 32).
+// 256 x 256 tiles where 128 x 128 ones, two to a CU, would take more than one round (us, 256 x 256 / 128 x
+// 128, rank 16: 512 small tiles, 2048 x 4096 x 4096: 97 / 83, 4096 x 2048 x 2048: 60 / 48; 640, 5003 x
+// 2048, K 4096: 123 / 137; 680, 5003 x 2056, K 1000, row-major: 57 / 57; 1024, 4096 x 4096 x
+// 4096: 116 / 172, 8192 x 2048 x 2048: 76 / 107; 2048, 8192 x 4096, K 512: 66 / 77, K 4096:
+// 231 / 340), and the requests are long: each costs a large tile a turn of its own (1024 rows of
+// 1024 requests, 2048 x 2048: 939 / 98).
+enum { CFG_FEW = 20 };
 inline int adapter_cfg(int num_cus, const void *X, const void *W, const gemm_adapters_t &ad, int64_t requests, int64_t M, int64_t N,
                        int64_t K, int64_t ldx, int64_t ldw, bool a_col, bool b_col) {
     // X's and W's granules whole, with 31-bit offsets in a tile
     if (K == 0 || !granule_ok(X, W, M, N, K, ldx, ldw, GEMM_F16, false, b_col, true)) return CFG_GENERIC;
     if (b_col && a_col && M <= FEW_ROWS && ad.rank <= FEW_RANK_MAX && N <= FEW_N_MAX && hidden_fast(X, ad, K, ldx, a_col))
-        return CFG_SKINNY1;
+        return CFG_FEW;
     const int64_t t128 = cdiv(M, 128) * cdiv(N, 128);
-    const bool panels = adapter_b_panels(ad, N, b_col);
-    if (b_col && panels && M <= 256 && 2 * t128 <= num_cus) return CFG_SKINNY4;
-    return panels && M >= 192 && t128 > 2 * (int64_t)num_cus && M >= 32 * requests ? CFG_L : CFG_M;
+    return adapter_b_fast(ad, N, b_col) && M >= 192 && t128 > 2 * (int64_t)num_cus && M >= 32 * requests ? CFG_L : CFG_M;
 }
 
 }  // namespace plan

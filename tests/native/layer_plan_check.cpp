@@ -1,0 +1,304 @@
+// Host-side check of the argument checks and kernel choice of the adapters, the 8-bit
+// gradients and the router (csrc/adapter_plan.hpp, wgrad8_plan.hpp, route_plan.hpp),
+// built with the address and undefined-behaviour sanitizers by
+// tests/test_layer_host.py: accepted and refused calls, the kernels that the GPU
+// tests' shapes reach, and a sweep over extreme arguments.  256 CUs.  Exit status 0: all
+// checks held.
+#include <cstdint>
+#include <cstdio>
+#include <vector>
+
+#include "../../dense_mixed_precision_02_amd/csrc/adapter_plan.hpp"
+#include "../../dense_mixed_precision_02_amd/csrc/route_plan.hpp"
+#include "../../dense_mixed_precision_02_amd/csrc/wgrad8_plan.hpp"
+
+using namespace dmp;
+using namespace dmp::plan;
+
+static int failures = 0;
+#define CHECK(cond)                                                        \
+    do {                                                                   \
+        if (!(cond)) {                                                     \
+            std::fprintf(stderr, "FAILED line %d: %s\n", __LINE__, #cond); \
+            ++failures;                                                    \
+        }                                                                  \
+    } while (0)
+
+static const int CUS = 256;
+static const int BAD = GEMM_ERR_INVALID_ARG;
+static gemm_handle_t H() { return reinterpret_cast<gemm_handle_t>(0x1000); }
+static void *P(uintptr_t a = 0x10000) { return reinterpret_cast<void *>(a); }
+static EpiParams ep(float beta = 0.0f, int c = GEMM_OUT_F32, int d = GEMM_OUT_F32) {
+    EpiParams e;
+    e.alpha = 1.0f;
+    e.beta = beta;
+    e.c_type = c;
+    e.d_type = d;
+    e.use_c = beta != 0.0f;
+    return e;
+}
+
+struct A {  // a good call of gemm_run_adapters, to change one thing of
+    gemm_handle_t h = H();
+    const void *X = P(), *W = P(), *C = nullptr, *D = P(), *off = P(), *hidden = nullptr, *work = P();
+    gemm_adapters_t ad = {P(), P(), nullptr, nullptr, 4, 16, 32, 16};
+    int64_t q = 4, M = 100, N = 64, K = 32, ldx = 32, ldw = 32, ldc = 64, ldh = 0;
+    int dt = GEMM_F16;
+    unsigned fl = GEMM_B_COLMAJOR | GEMM_ADAPTER_A_COLMAJOR;
+    EpiParams e = ep();
+    int ok(bool null_ad = false) const {
+        return validate_adapters(h, X, W, null_ad ? nullptr : &ad, C, D, off, q, M, N, K, ldx, ldw, ldc, dt, fl, e, hidden, ldh, work);
+    }
+};
+
+static gemm_q8_t q8(int64_t rows, int64_t K) {
+    gemm_q8_t o;
+    o.q = P();
+    o.scale = (const float *)P();
+    o.ld = k16(K);
+    o.scale_row = 1;
+    o.scale_k = rows;
+    o.group = 0;
+    o.scale_group = 0;
+    o.type = GEMM_E4M3;
+    return o;
+}
+struct W {
+    gemm_handle_t h = H();
+    gemm_q8_t x = q8(100, 64);
+    const void *Y = P(), *C = nullptr, *D = P(), *off = P();
+    int64_t g = 4, M = 64, N = 32, K = 100, ldy = 32, ldc = 32;
+    int dt = GEMM_BF16;
+    unsigned fl = 0;
+    EpiParams e = ep();
+    int ok(bool null_x = false) const {
+        return validate_wgrad8(h, null_x ? nullptr : &x, Y, C, D, off, g, M, N, K, ldy, ldc, dt, fl, e);
+    }
+};
+
+static gemm_route_t tables(void *p = P()) {
+    return {(int32_t *)p, (float *)p, (float *)p, (int32_t *)p, (int32_t *)p, (int32_t *)p, (int32_t *)p, (float *)p};
+}
+struct R {
+    gemm_handle_t h = H();
+    const void *x = P(), *work = P(), *dw = nullptr, *dx = P();
+    int xt = GEMM_OUT_F32;
+    int64_t T = 10, E = 8, ld = 8, k = 2, ldd = 8;
+    unsigned fl = GEMM_ROUTE_NORMALIZE;
+    gemm_route_t r = tables();
+    int ok(bool null_r = false) const { return validate_route(h, x, xt, T, E, ld, k, fl, null_r ? nullptr : &r, work); }
+    int grad() const { return validate_route_grad(h, x, xt, T, E, ld, k, fl, &r, dw, dx, ldd); }
+};
+
+// packed operands of linear layers (or row-major ones)
+static int cfg(int64_t q, int64_t M, int64_t K, int64_t N, int64_t r, bool linear = true, const void *X = P()) {
+    const gemm_adapters_t ad = {P(), P(), nullptr, nullptr, 4, r, linear ? K : r, linear ? r : N};
+    return adapter_cfg(CUS, X, P(), ad, q, M, N, K, K, linear ? K : N, linear, linear);
+}
+
+int main() {
+#define REFUSES(T, change)    \
+    do {                      \
+        T c;                  \
+        change;               \
+        CHECK(c.ok() == BAD); \
+    } while (0)
+#define TAKES(T, change)          \
+    do {                          \
+        T c;                      \
+        change;                   \
+        CHECK(c.ok() == GEMM_OK); \
+    } while (0)
+    // adapters
+    TAKES(A, (void)0);
+    TAKES(A, c.fl = 0; c.ldw = 64; c.ad.lda = 16; c.ad.ldb = 64);
+    TAKES(A, c.hidden = P(); c.ldh = 16);
+    TAKES(A, c.K = 0; c.X = c.W = nullptr; c.ad.A = c.ad.B = nullptr);
+    TAKES(A, c.ad.adapters = 0; c.ad.A = c.ad.B = nullptr);
+    TAKES(A, c.M = 0; c.X = c.D = c.off = c.work = nullptr);
+    TAKES(A, c.q = 0; c.off = nullptr);
+    TAKES(A, c.ad.rank = 1; c.ad.ldb = 1);
+    REFUSES(A, c.h = nullptr);
+    CHECK(A().ok(true) == BAD);
+    REFUSES(A, c.M = -1);
+    REFUSES(A, c.N = -1);
+    REFUSES(A, c.K = -1);
+    REFUSES(A, c.q = -1);
+    REFUSES(A, c.q = GROUPS_MAX + 1);
+    REFUSES(A, c.ad.adapters = -1);
+    REFUSES(A, c.ad.adapters = GROUPS_MAX + 1);
+    REFUSES(A, c.ad.rank = 0);
+    REFUSES(A, c.ad.rank = 1025; c.ad.ldb = 1025);
+    REFUSES(A, c.dt = GEMM_I8);
+    REFUSES(A, c.fl |= GEMM_A_COLMAJOR);
+    REFUSES(A, c.ldx = 31);
+    REFUSES(A, c.ldw = 31);
+    REFUSES(A, c.ldc = 63);
+    REFUSES(A, c.ad.lda = 31);
+    REFUSES(A, c.ad.ldb = 15);
+    REFUSES(A, c.ad.ldb = ADAPTER_LD_MAX + 1);
+    REFUSES(A, c.fl = 0; c.ldw = 64; c.ad.lda = 15; c.ad.ldb = 64);
+    REFUSES(A, c.fl = 0; c.ldw = 64; c.ad.lda = 16; c.ad.ldb = 63);
+    REFUSES(A, c.hidden = P(); c.ldh = 15);
+    REFUSES(A, c.hidden = P(0x10001); c.ldh = 16);
+    REFUSES(A, c.X = nullptr);
+    REFUSES(A, c.W = nullptr);
+    REFUSES(A, c.D = nullptr);
+    REFUSES(A, c.off = nullptr);
+    REFUSES(A, c.off = P(0x10004));
+    TAKES(A, c.off = P(0x10004); c.fl |= GEMM_OFFSETS_I32);
+    REFUSES(A, c.off = P(0x10002); c.fl |= GEMM_OFFSETS_I32);
+    REFUSES(A, c.ad.A = nullptr);
+    REFUSES(A, c.ad.B = P(0x10001));
+    REFUSES(A, c.ad.ids = (int32_t *)P(0x10002));
+    REFUSES(A, c.ad.scale = (float *)P(0x10001));
+    REFUSES(A, c.work = nullptr);
+    REFUSES(A, c.work = P(0x10008));
+    REFUSES(A, c.e = ep(1.0f));
+    REFUSES(A, c.e = ep(1.0f, GEMM_OUT_F16); c.C = c.D);
+    REFUSES(A, c.e = ep(0.0f, GEMM_OUT_F32, GEMM_OUT_I32));
+    REFUSES(A, c.M = 1ll << 31);
+    REFUSES(A, c.ldx = LD_MAX + 1);
+    REFUSES(A, c.ldx = LD_MAX);
+    REFUSES(A, c.ad.lda = LD_MAX);
+    // 8-bit gradients
+    TAKES(W, (void)0);
+    TAKES(W, c.off = nullptr; c.g = 1);
+    TAKES(W, c.K = 0; c.x.q = nullptr; c.Y = nullptr);
+    TAKES(W, c.M = 0; c.x.q = nullptr; c.D = nullptr);
+    TAKES(W, c.fl = GEMM_OFFSETS_I32; c.off = P(0x10004));
+    REFUSES(W, c.h = nullptr);
+    CHECK(W().ok(true) == BAD);
+    REFUSES(W, c.off = nullptr);
+    REFUSES(W, c.off = P(0x10004));
+    REFUSES(W, c.dt = GEMM_F64);
+    REFUSES(W, c.fl = GEMM_B_COLMAJOR);
+    REFUSES(W, c.ldy = 31);
+    REFUSES(W, c.ldc = 31);
+    REFUSES(W, c.Y = nullptr);
+    REFUSES(W, c.Y = P(0x10001));
+    REFUSES(W, c.D = nullptr);
+    REFUSES(W, c.x.q = P(0x10008));
+    REFUSES(W, c.x.ld = 48);
+    REFUSES(W, c.x.ld = 72);
+    REFUSES(W, c.x.ld = 1ll << 24);
+    REFUSES(W, c.x.type = 2);
+    REFUSES(W, c.x.scale = nullptr);
+    REFUSES(W, c.x.scale_row = -1);
+    REFUSES(W, c.x.scale_k = LD_MAX + 1);
+    REFUSES(W, c.g = GROUPS_MAX + 1);
+    REFUSES(W, c.K = 1ll << 31);
+    // router
+    TAKES(R, (void)0);
+    TAKES(R, c.T = 0; c.x = nullptr; c.r.experts = nullptr; c.r.weights = c.r.lse = nullptr; c.r.order = c.r.place = nullptr);
+    TAKES(R, c.E = c.ld = 1024; c.k = 64);
+    TAKES(R, c.xt = GEMM_OUT_BF16; c.x = P(0x10002));
+    REFUSES(R, c.h = nullptr);
+    CHECK(R().ok(true) == BAD);
+    REFUSES(R, c.T = -1);
+    REFUSES(R, c.E = 0);
+    REFUSES(R, c.E = c.ld = 1025);
+    REFUSES(R, c.k = 0);
+    REFUSES(R, c.k = 9);
+    REFUSES(R, c.E = c.ld = 100; c.k = 65);
+    REFUSES(R, c.T = 1ll << 30; c.k = 2);
+    REFUSES(R, c.ld = 7);
+    REFUSES(R, c.xt = GEMM_OUT_I32);
+    REFUSES(R, c.fl = 1);
+    REFUSES(R, c.x = nullptr);
+    REFUSES(R, c.x = P(0x10002));
+    REFUSES(R, c.work = nullptr);
+    REFUSES(R, c.work = P(0x10004));
+    REFUSES(R, c.r.counts = nullptr);
+    REFUSES(R, c.r.experts = nullptr);
+    REFUSES(R, c.r.place = (int32_t *)P(0x10002));
+    {
+        R c;
+        CHECK(c.grad() == GEMM_OK);
+        c.dw = P(0x10002);
+        CHECK(c.grad() == BAD);
+        c.dw = P();
+        c.ldd = 7;
+        CHECK(c.grad() == BAD);
+        c.ldd = 8;
+        c.dx = nullptr;
+        CHECK(c.grad() == BAD);
+        c.T = 0;
+        CHECK(c.grad() == GEMM_OK);
+    }
+
+    // which kernels: test_gpu_adapters' shapes
+    CHECK(cfg(64, 64, 1024, 528, 16) == CFG_FEW && cfg(171, 153, 1600, 136, 16) == CFG_FEW && cfg(5, 256, 264, 200, 128) == CFG_FEW);
+    CHECK(cfg(3, 68, 64, 72, 5) == CFG_FEW && cfg(3, 140, 2104, 1100, 33) == CFG_FEW && cfg(2, 32, 4160, 64, 48) == CFG_FEW);
+    CHECK(cfg(3, 135, 200, 136, 130) == CFG_M && cfg(3, 135, 200, 136, 200, false) == CFG_M);  // a rank past the few rows'
+    CHECK(cfg(180, 363, 136, 264, 13) == CFG_M && cfg(180, 363, 136, 264, 13, false) == CFG_M);
+    CHECK(cfg(180, 360, 135, 263, 40, false) == CFG_GENERIC && cfg(4, 182, 99, 33, 5) == CFG_GENERIC);
+    CHECK(cfg(4, 1000, 64, 64, 16, true, P(0x10002)) == CFG_GENERIC && cfg(4, 100, 0, 64, 16) == CFG_GENERIC);
+    CHECK(cfg(4, 2133, 72, 4104, 16) == CFG_L && cfg(4, 2135, 136, 4104, 72, false) == CFG_L && cfg(4, 2256, 200, 4099, 136) == CFG_L);
+    CHECK(cfg(2, 1300, 256, 1032, 32) == CFG_M);
+    CHECK(cfg(4, 256, 4096, 4096, 16) == CFG_FEW && cfg(4, 257, 4096, 4096, 16) == CFG_M);  // both sides of the borders
+    CHECK(cfg(4, 2048, 4096, 4096, 16) == CFG_M && cfg(4, 2176, 4096, 4096, 16) == CFG_L && cfg(69, 2176, 4096, 4096, 16) == CFG_M);
+    CHECK(cfg(4, 2176, 4096, 4096, 13) == CFG_M);  // no panels of whole granules
+    // parts of K: at most 16 k-tiles, no empty one, and the scratch holds them
+    for (int64_t M : {1, 16, 17, 64, 65, 256})
+        for (int64_t N : {1, 64, 65, 4096, 14336, 1 << 22})
+            for (int64_t K : {1, 64, 65, 128, 1024, 1025, 4096, 14336, 1 << 20})
+                for (int64_t r : {1, 16, 17, 128})
+                    for (int64_t q : {1, 5, 300}) {
+                        const FewPlan f = few_plan(CUS, q, M, N, K, r);
+                        const int64_t nkt = cdiv(K, 64);
+                        CHECK(f.per >= 1 && f.per <= 16 && f.splits >= 1);
+                        CHECK((int64_t)f.per * f.splits >= nkt && (int64_t)f.per * (f.splits - 1) < nkt);
+                        CHECK(f.blocks >= cdiv(N, 64));
+                        CHECK(adapter_work(CUS, q, M, N, K, r, GEMM_OUT_F32) >= f.splits * 4 * M * (N + cdiv(r, 16) * 16));
+                        CHECK(adapter_work(CUS, q, M, N, K, r, GEMM_OUT_F32) >= 4 * M * adapter_rp(r));
+                    }
+    // 8-bit gradients: large tiles, parts of the rows (at least 256, no more than the scratch holds)
+    CHECK(wgrad8_large(CUS, 1, 4096, 4096) && !wgrad8_large(CUS, 1, 4096, 3840) && !wgrad8_large(CUS, 8, 1024, 1024));
+    CHECK(wgrad8_large(CUS, 4, 2000, 2200) && !wgrad8_large(CUS, 100, 264, 264));
+    CHECK(wgrad8_splits(CUS, 1, 72, 40, 1000) == 3 && wgrad8_splits(CUS, 1, 130, 99, 3001) == 11);
+    CHECK(wgrad8_splits(CUS, 1, 4096, 4096, 8192) == 1 && wgrad8_splits(CUS, 1, 17, 264, 100000) == 32);
+    CHECK(wgrad8_splits(CUS, 4, 200, 72, 1606) == 1 && wgrad8_splits(CUS, 2, 128, 128, 8000) == 15);
+    for (int64_t g : {0, 1, 5, 1000})
+        for (int64_t M : {0, 1, 64, 1000, 5000})
+            for (int64_t N : {0, 1, 128, 1000, 5000})
+                for (int64_t K : {0, 1, 255, 256, 10000, 1 << 30}) {
+                    const int s = wgrad8_splits(CUS, g, M, N, K);
+                    CHECK(s >= 1 && s <= 32 && (s == 1 || K / g / s >= 256));
+                    CHECK(wgrad8_work(CUS, g, M, N, K) == (s > 1 ? 4 * s * g * M * N : 0));
+                }
+    gemm_q8_t x = q8(100, 64);
+    CHECK(wgrad8_narrow(x));
+    x.scale_row = 1ll << 22;
+    CHECK(!wgrad8_narrow(x));
+    CHECK(wgrad8_fast(P(), 64, 64) && !wgrad8_fast(P(), 60, 64) && !wgrad8_fast(P(), 64, 65) && !wgrad8_fast(P(0x10002), 64, 64));
+    // router: all tokens, no empty workgroup
+    for (int64_t T : {0ll, 1ll, 64ll, 65ll, 4096ll, 4097ll, 16384ll, 1000003ll, (1ll << 31) - 1024}) {
+        int rows, blocks;
+        route_split(T, CUS, rows, blocks);
+        CHECK(blocks >= 1 && rows >= 1 && (int64_t)rows * blocks >= T && (blocks == 1 || (int64_t)rows * (blocks - 1) < T));
+        CHECK(route_work(T, 8, CUS) >= blocks * (int64_t)(8 + 4 + 8 * 8));
+    }
+    // extreme arguments: no overflow on the way to a refusal
+    const std::vector<int64_t> xs = {-(1ll << 62), -1, 0, 1, 100, 1ll << 30, (1ll << 31) - 1024, 1ll << 31, 1ll << 48, 1ll << 62};
+    int taken = 0;
+    for (int64_t a : xs)
+        for (int64_t b : xs)
+            for (int64_t d : xs) {
+                A c;
+                c.M = a; c.N = b; c.K = d; c.ldx = d; c.ldw = b; c.ldc = b;
+                taken += c.ok() == GEMM_OK;
+                A e;
+                e.ldx = a; e.ad.lda = b; e.ldc = d;
+                taken += e.ok() == GEMM_OK;
+                W w;
+                w.M = a; w.N = b; w.K = d; w.ldc = b; w.ldy = b;
+                taken += w.ok() == GEMM_OK;
+                R r;
+                r.T = a; r.E = b; r.ld = d;
+                taken += r.ok() == GEMM_OK && r.grad() == GEMM_OK;
+            }
+    CHECK(taken > 0);
+    std::printf("%d failures\n", failures);
+    return failures != 0;
+}

@@ -114,6 +114,22 @@ CASES = [
     ("bf16", [2, 1, 0, 5, 16, 17], 0, 0, 6, None, 2048, 512, 16, True, "bf16", 1.0, 0.0),
     ("f16", [30], 0, 2, 4, [3], 4096, 264, 8, True, "f32", 1.0, 1.0),
     ("bf16", [2, 0, 12], 0, 1, 3, None, 1000, 130, 8, False, "bf16", 1.0, 0.0),
+    # few rows, more than 64 of them; long and empty requests; ranks that are no granules; the longest
+    # part of K, and one k-tile
+    ("bf16", [1] * 100 + [0] * 70 + [30], 3, 20, 7, [i * 5 % 9 - 1 for i in range(171)], 1600, 136, 16, True, "bf16", 1.0, 0.0),
+    ("f16", [64, 0, 1, 127, 64], 0, 0, 2, [1, 0, 1, 0, -1], 264, 200, 128, True, "f32", 0.5, 1.0),
+    ("bf16", [3, 40, 21], 0, 4, 3, None, 64, 72, 5, True, "f32", 1.0, 1.0),
+    ("f16", [2, 9], 1, 0, 2, [1, 0], 8, 17, 1, True, "f16", 1.0, 0.0),
+    ("bf16", [33, 90, 17], 0, 0, 3, None, 2104, 1100, 33, True, "bf16", 1.0, 0.0),
+    ("f16", [20, 12], 0, 0, 2, None, 4160, 64, 48, True, "f32", 1.0, 0.0),
+    # staged tiles: many requests, ranks that are no granules, both layouts
+    ("bf16", [1, 3] * 90, 2, 1, 5, [i % 6 - 1 for i in range(180)], 136, 264, 13, True, "bf16", 1.0, 0.0),
+    ("f16", [1, 3] * 90, 2, 1, 5, [i % 6 - 1 for i in range(180)], 136, 264, 13, False, "f32", 1.0, 1.0),
+    ("bf16", [1, 3] * 90, 0, 0, 5, [i % 6 - 1 for i in range(180)], 135, 263, 40, False, "f32", 1.0, 0.0),
+    # 256 x 256 tiles: requests that end inside a tile, a rank of more than one k-tile, both layouts
+    ("bf16", [700, 0, 1400, 30], 0, 3, 3, [2, 0, 1, -1], 72, 4104, 16, True, "bf16", 1.0, 0.0),
+    ("f16", [700, 0, 1400, 30], 5, 0, 3, [2, 0, -1, 1], 136, 4104, 72, False, "f32", 0.5, 1.0),
+    ("bf16", [100, 1, 1900, 255], 0, 0, 2, [0, 1, 1, 0], 200, 4099, 136, True, "f32", 1.0, 0.0),
 ]
 
 

@@ -135,7 +135,8 @@ CASES = [
     ("f16", "e5m2", None, 5000, 0, 17, 264, "f32", 2.0, 0.0),
     ("bf16", "e4m3", [0, 5, 64, 0, 65, 1, 0], 3, 9, 136, 200, "f32", 1.0, 1.0),
     ("f16", "e4m3", [17, 0, 129], 0, 5, 99, 33, "f16", 1.0, 0.0),
-    ("bf16", "e5m2", [700, 0, 1, 900], 2, 3, 200, 72, "bf16", 1.0, 1.0),  # groups split
+    ("bf16", "e5m2", [700, 0, 1, 900], 2, 3, 200, 72, "bf16", 1.0, 1.0),
+    ("f16", "e4m3", [2000, 0, 1, 3001], 2, 3, 200, 72, "f32", 1.0, 1.0),  # groups whose rows are split
     ("bf16", "e4m3", [3, 0, 70, 1] * 20, 0, 0, 64, 128, "f32", 1.0, 0.0),  # more than 64 groups
     ("bf16", "e4m3", None, 200, 0, 4096, 4096, "bf16", 1.0, 0.0),  # 256 x 256 tiles
     ("f16", "e5m2", [130, 0, 64, 61], 5, 6, 2000, 2200, "f32", 0.5, 1.0),  # the same, partial tiles
