@@ -53,19 +53,25 @@ int run_product(const AdapterArgs &a, int cfg, hipStream_t s) {
     return cfg == CFG_M ? launch_staged<DT, 128, 128, 2, 2, BKC, true>(a, s) : launch_staged<DT, 64, 128, 1, 4, BKC, false>(a, s);
 }
 
-template <class DT, int BM>
+template <class DT, int BM, bool KC, bool ALIGNED>
 int launch_few(const AdapterFewArgs &f, int parts, hipStream_t s) {
-    const int64_t rows64 = cdiv(f.M, BM), grid = (int64_t)f.blocks * f.splits * rows64;
-    const int rc = f.per <= 4   ? launch(adapter_few<DT, BM, 4>, grid, 256, s, f)
-                   : f.per <= 8 ? launch(adapter_few<DT, BM, 8>, grid, 256, s, f)
-                                : launch(adapter_few<DT, BM, 16>, grid, 256, s, f);
+    const int64_t rows = cdiv(f.M, BM), grid = (int64_t)f.blocks * f.splits * rows, join = f.joins * rows;
+    const int rc = f.per <= 4              ? launch(adapter_few<DT, BM, 4, KC, ALIGNED>, grid, 256, s, f)
+                   : ALIGNED && f.per <= 8 ? launch(adapter_few<DT, BM, ALIGNED ? 8 : 4, KC, ALIGNED>, grid, 256, s, f)
+                                           : launch(adapter_few<DT, BM, 16, KC, ALIGNED>, grid, 256, s, f);
     if (rc != GEMM_OK) return rc;
-    const int64_t join = f.joins * rows64;
-    return parts > 1 ? launch(adapter_few_join<DT, BM, 2>, join, 512, s, f) : launch(adapter_few_join<DT, BM, 1>, join, 512, s, f);
+    return parts > 1 ? launch(adapter_few_join<DT, BM, 2, KC>, join, 512, s, f) : launch(adapter_few_join<DT, BM, 1, KC>, join, 512, s, f);
+}
+
+template <class DT, bool KC>
+int launch_few(const AdapterFewArgs &f, int parts, bool aligned, hipStream_t s) {
+    if (!aligned) return launch_few<DT, 64, KC, false>(f, parts, s);
+    if (f.M <= 16) return launch_few<DT, 16, KC, true>(f, parts, s);
+    return f.M <= 32 ? launch_few<DT, 32, KC, true>(f, parts, s) : launch_few<DT, 64, KC, true>(f, parts, s);
 }
 
 template <class DT>
-int run_few(int num_cus, const AdapterArgs &a, hipStream_t s) {
+int run_few(int num_cus, const AdapterArgs &a, bool col, bool aligned, hipStream_t s) {
     const FewPlan q = few_plan(num_cus, a.t.groups, a.r.M, a.r.N, a.r.K, a.rank);
     AdapterFewArgs f{};
     f.t = a.t;
@@ -78,13 +84,12 @@ int run_few(int num_cus, const AdapterArgs &a, hipStream_t s) {
     f.C = a.r.C; f.D = a.r.D; f.hidden = a.hidden; f.ldc = a.r.ldc; f.ld_hidden = a.ld_hidden; f.ep = a.r.ep;
     f.part = (float *)a.H;
     f.hpart = (float *)(a.H + q.splits * (cdiv(a.r.M * a.r.N * 4, 16) * 16));
-    if (a.r.M <= 16) return launch_few<DT, 16>(f, a.parts, s);
-    return a.r.M <= 32 ? launch_few<DT, 32>(f, a.parts, s) : launch_few<DT, 64>(f, a.parts, s);
+    return col ? launch_few<DT, true>(f, a.parts, aligned, s) : launch_few<DT, false>(f, a.parts, aligned, s);
 }
 
 template <class DT>
-int run_adapters(int num_cus, const AdapterArgs &a, bool a_col, bool b_col, bool hidden_f, int cfg, hipStream_t s) {
-    if (cfg == CFG_FEW) return run_few<DT>(num_cus, a, s);
+int run_adapters(int num_cus, const AdapterArgs &a, bool a_col, bool b_col, bool hidden_f, bool few_a, int cfg, hipStream_t s) {
+    if (cfg == CFG_FEW) return run_few<DT>(num_cus, a, b_col, few_a, s);
     if (a.r.K > 0 || a.hidden) {
         const int rc = run_hidden<DT>(a, a_col, hidden_f, s);
         if (rc != GEMM_OK) return rc;
@@ -135,10 +140,11 @@ int gemm_run_adapters(gemm_handle_t h, const void *X, const void *W, const gemm_
     a.parts = adapter_parts(d_type);
     a.hidden = hidden; a.ld_hidden = ld_hidden;
     const int cfg = adapter_cfg(h->num_cus, X, W, *ad, requests, M, N, K, ldx, ldw, ac, bc);
+    const bool fa = few_aligned(X, W, *ad, N, K, ldx, ldw, bc);
     const bool hf = K > 0 && hidden_fast(X, *ad, K, ldx, ac);
     hipStream_t s = (hipStream_t)stream;
-    return dtype == GEMM_F16 ? run_adapters<F16>(h->num_cus, a, ac, bc, hf, cfg, s)
-                              : run_adapters<BF16>(h->num_cus, a, ac, bc, hf, cfg, s);
+    return dtype == GEMM_F16 ? run_adapters<F16>(h->num_cus, a, ac, bc, hf, fa, cfg, s)
+                              : run_adapters<BF16>(h->num_cus, a, ac, bc, hf, fa, cfg, s);
 }
 
 }  // extern "C"

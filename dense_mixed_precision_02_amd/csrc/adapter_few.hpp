@@ -11,6 +11,8 @@
 //                     it also computes hidden sums over its K: 16 columns of A_a for one
 //                     request, the requests dealt out over the workgroups.  All sums go to
 //                     memory in 32 bits.
+//                     N-contiguous W and A_a (the input's gradient) are turned on the way from the
+//                     registers, through 1 KB of LDS for 32 of K.
 //   adapter_few_join  A workgroup takes 16 columns: the K parts' sums in their order, the
 //                     hidden rows scaled and rounded, each request's product with B_a, and
 //                     the output stage.  The sums are read while B_a is on its way.
@@ -39,12 +41,52 @@ struct AdapterFewArgs {
     EpiParams ep;
 };
 
-// BM: rows (at least those there are); KT: k-tiles to a part at most
-template <class DT, int BM, int KT>
+// 32 k x 16 columns of an N-contiguous matrix, lane L's granule of columns 8 (L % 2) .. at k = L / 2
+// (turn_granule), as the instructions' operand.  slab: 1 KB of this wave's own, of 128-byte
+// blocks of 4 k x 16 columns.
+__device__ static inline void put_granule(DMP_LDS char *slab, int lane, const intx4 &v) {
+    const int k = lane >> 1;
+    *(DMP_LDS intx4 *)(slab + (k >> 2) * 128 + (k & 3) * 32 + (lane & 1) * 16) = v;
+}
+__device__ static inline intx4 turned_granule(const DMP_LDS char *slab, int lane) {
+    intx4 b;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const intx2 w = __builtin_bit_cast(intx2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                      (DMP_LDS shortx4 *)(slab + (2 * (lane >> 4) + t) * 128 + (lane & 15) * 8)));
+        b[2 * t] = w[0];
+        b[2 * t + 1] = w[1];
+    }
+    return b;
+}
+// NV of them at a time: all writes before the first read.
+template <int NV>
+__device__ static inline void turn_granules(DMP_LDS char *slabs, int lane, const intx4 (&v)[NV], intx4 (&b)[NV]) {
+#pragma unroll
+    for (int x = 0; x < NV; ++x) put_granule(slabs + x * 1024, lane, v[x]);
+    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+#pragma unroll
+    for (int x = 0; x < NV; ++x) b[x] = turned_granule(slabs + x * 1024, lane);
+    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+}
+
+// This lane's granule of 16 columns x 32 k, from (column 0, k 0) of the piece on: K-contiguous
+// the operand itself, else to be turned.  cols, left: columns and k that exist.
+template <bool KC, bool ALIGNED>
+__device__ static inline intx4 column_granule(const void *base, int64_t ld, int cols, int left, int lane) {
+    const int a = KC ? lane & 15 : lane >> 1, b = KC ? 8 * (lane >> 4) : 8 * (lane & 1);
+    const int rows = KC ? cols : left, end = KC ? left : cols;
+    if constexpr (ALIGNED) return load_granule(make_rsrc(base), joined(row_part(a, rows, ld), k_part(b, end)));
+    else return load8((const uint16_t *)base + a * ld + b, a < rows ? end - b : 0);
+}
+
+// BM: rows (at least those there are); KT: k-tiles to a part at most; KC: W and A_a are
+// K-contiguous; ALIGNED: the granules of X, W and A_a are aligned and whole
+template <class DT, int BM, int KT, bool KC, bool ALIGNED>
 __global__ __launch_bounds__(256, 1) void adapter_few(const AdapterFewArgs p) {
     constexpr int NW = 4, TM = BM / 16, RC = BM / 8, HT = (KT + NW - 1) / NW;
     __shared__ __attribute__((aligned(1024))) char lds_x[KT * BM * 128];
-    __shared__ float red[NW][BM * 16];
+    __shared__ __attribute__((aligned(16))) float red[NW][1024];  // each wave's sums, and its slabs
     __shared__ AdapterEntry lists[NW][BM];
     const int lane = lane_id(), wave = wave_id(), r16 = lane & 15, K = p.K;
     const int id = workgroup_id(), part = id / p.blocks, cb = id - part * p.blocks;
@@ -59,7 +101,8 @@ __global__ __launch_bounds__(256, 1) void adapter_few(const AdapterFewArgs p) {
     const int rows = min(BM, scalar_offset(p.t, p.t.groups) - first);
     if (rows <= 0) return;
     // X's part: 1 KB (8 rows of a k-tile) to a copy
-    const __amdgpu_buffer_rsrc_t rx = make_rsrc((const char *)p.X + (int64_t)first * p.ldx * 2);
+    const uint16_t *const X = (const uint16_t *)p.X + (int64_t)first * p.ldx;
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc(X);
     // (a wave's copies are of rows whose number in eights has its own parity, so that one swizzle serves)
     constexpr int XC = RC >= NW ? RC / NW : 1, XT = RC >= NW ? 1 : NW / RC;  // copies to a k-tile; k-tiles at a time
     int xo[XC];
@@ -69,21 +112,29 @@ __global__ __launch_bounds__(256, 1) void adapter_few(const AdapterFewArgs p) {
     // (all KT k-tiles: zeros past the part's end, so that nothing below depends on how many there are)
 #pragma unroll
     for (int t0 = 0; t0 < KT; t0 += XT) {
-        const int t = XT > 1 ? t0 + wave / RC : t0;
-        const int ko = k_part((kt0 + t) * 64 + xk, kend);
+        const int t = XT > 1 ? t0 + wave / RC : t0, k = (kt0 + t) * 64 + xk;
 #pragma unroll
-        for (int j = 0; j < XC; ++j)
-            load_granule_to_lds(rx, (DMP_LDS char *)lds_x + t * (BM * 128) + (wave + NW * j) % RC * 1024, joined(xo[j], ko));
+        for (int j = 0; j < XC; ++j) {
+            const int c = (wave + NW * j) % RC;
+            DMP_LDS char *to = (DMP_LDS char *)lds_x + t * (BM * 128) + c * 1024;
+            if constexpr (ALIGNED) {
+                load_granule_to_lds(rx, to, joined(xo[j], k_part(k, kend)));
+            } else {
+                const int row = c * 8 + (lane >> 3);
+                *(DMP_LDS intx4 *)(to + lane * 16) = load8(X + (int64_t)row * p.ldx + k, row < rows ? kend - k : 0);
+            }
+        }
     }
     // W's: this wave's columns
-    const __amdgpu_buffer_rsrc_t rw = make_rsrc((const char *)p.W + min(col0, (int64_t)p.N - 1) * p.ldw * 2);
-    const int wo = row_part(r16, cols, p.ldw);
+    const uint16_t *const W = (const uint16_t *)p.W + (KC ? min(col0, (int64_t)p.N - 1) * p.ldw : min(col0, (int64_t)p.N - 1));
     intx4 fw[KT][2];
 #pragma unroll
     for (int t = 0; t < KT; ++t)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            fw[t][h] = load_granule(rw, joined(wo, k_part((kt0 + t) * 64 + 32 * h + 8 * (lane >> 4), kend)));
+        for (int h = 0; h < 2; ++h) {
+            const int64_t k = (kt0 + t) * 64 + 32 * h;
+            fw[t][h] = column_granule<KC, ALIGNED>(W + k * (KC ? 1 : p.ldw), p.ldw, cols, kend - (int)k, lane);
+        }
     issued();
     DMP_LDS AdapterEntry *list = (DMP_LDS AdapterEntry *)lists[wave];
     const int entries = adapter_entries<BM>(p.t, from, first, rows, list, requests);
@@ -95,13 +146,14 @@ __global__ __launch_bounds__(256, 1) void adapter_few(const AdapterFewArgs p) {
         e = __builtin_amdgcn_readfirstlane(task / rt);
         rc = __builtin_amdgcn_readfirstlane(task - e * rt) * 16;
         const int ad = __builtin_amdgcn_readfirstlane(list[e].adapter);
-        const __amdgpu_buffer_rsrc_t ra = make_rsrc((const char *)p.A + (ad * p.sA + (int64_t)rc * p.lda) * 2);
-        const int ao = row_part(r16, p.rank - rc, p.lda);
+        const uint16_t *const A = (const uint16_t *)p.A + ad * p.sA + (int64_t)rc * (KC ? p.lda : 1);
 #pragma unroll
         for (int t = 0; t < HT; ++t)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                fa[t][h] = load_granule(ra, joined(ao, k_part((kt0 + wave + NW * t) * 64 + 32 * h + 8 * (lane >> 4), kend)));
+            for (int h = 0; h < 2; ++h) {
+                const int64_t k = (kt0 + wave + NW * t) * 64 + 32 * h;
+                fa[t][h] = column_granule<KC, ALIGNED>(A + k * (KC ? 1 : p.lda), p.lda, p.rank - rc, kend - (int)k, lane);
+            }
         issued();
     };
     if (task < tasks) load_a();
@@ -111,16 +163,27 @@ __global__ __launch_bounds__(256, 1) void adapter_few(const AdapterFewArgs p) {
         const int row = i * 16 + r16, g = 4 * h + (lane >> 4);
         return *(const DMP_LDS intx4 *)((const DMP_LDS char *)lds_x + t * (BM * 128) + row * 128 + ((g ^ swz(row)) << 4));
     };
+    DMP_LDS char *const slabs = (DMP_LDS char *)red[wave];
+    auto operands = [&](const intx4 (&v)[2], intx4 (&b)[2]) {
+        if constexpr (KC) {
+            b[0] = v[0];
+            b[1] = v[1];
+        } else {
+            turn_granules(slabs, lane, v, b);
+        }
+    };
     while (task < tasks) {
         const int rr = __builtin_amdgcn_readfirstlane(list[e].rows), lo = rr & 0xffff, hi = (int)((uint32_t)rr >> 16);
         floatx4 acc[TM] = {};
 #pragma unroll
         for (int t = 0; t < HT; ++t) {
+            intx4 b[2];
+            operands(fa[t], b);
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int i = 0; i < TM; ++i)
-                    if (hi > 16 * i && lo < 16 * i + 16) acc[i] = mma16<DT>(fragX(wave + NW * t, h, i), fa[t][h], acc[i]);
+                    if (hi > 16 * i && lo < 16 * i + 16) acc[i] = mma16<DT>(fragX(wave + NW * t, h, i), b[h], acc[i]);
         }
 #pragma unroll
         for (int i = 0; i < TM; ++i)
@@ -142,10 +205,12 @@ __global__ __launch_bounds__(256, 1) void adapter_few(const AdapterFewArgs p) {
     floatx4 acc[TM] = {};
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
+        intx4 b[2];
+        operands(fw[t], b);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int i = 0; i < TM; ++i) acc[i] = mma16<DT>(fragX(t, h, i), fw[t][h], acc[i]);
+            for (int i = 0; i < TM; ++i) acc[i] = mma16<DT>(fragX(t, h, i), b[h], acc[i]);
     }
     float *out = p.part + ((int64_t)split * p.M + first) * p.N + col0 + r16;
 #pragma unroll
@@ -181,12 +246,13 @@ __device__ static inline void add_parts(const float *base, int s, int parts, int
 constexpr int FEW_RANK = 128;  // of the hidden rows in LDS
 
 // BM: rows (at least those there are); PARTS: numbers that a hidden value is kept in
-template <class DT, int BM, int PARTS>
+// KC: B_a is K-contiguous
+template <class DT, int BM, int PARTS, bool KC>
 __global__ __launch_bounds__(512, 2) void adapter_few_join(const AdapterFewArgs p) {
     constexpr int NW = 8, TM = BM / 16, LD = FEW_RANK + 8, EB = BM / NW, MINE = (BM * 16 + 511) / 512, HEACH = (BM * 32 + 511) / 512;
     constexpr bool f16 = std::is_same_v<DT, F16>;
     __shared__ __attribute__((aligned(16))) uint16_t hl[PARTS][BM][LD];
-    __shared__ float red[NW][BM * 16];
+    __shared__ __attribute__((aligned(16))) float red[NW][BM * 16];  // each wave's sums, and before them its slab
     __shared__ AdapterEntry lists[NW][BM];
     __shared__ int owner[BM];
     __shared__ float scales[BM];
@@ -212,24 +278,12 @@ __global__ __launch_bounds__(512, 2) void adapter_few_join(const AdapterFewArgs 
     const int nk = (p.rank + 31) / 32;
     intx4 fb[2][EB];
     auto load_b = [&](int st, int kb) {
-        const int at = joined(row_part(r16, cols, p.ldb), k_part(kb * 32 + 8 * (lane >> 4), p.rank));
 #pragma unroll
         for (int x = 0; x < EB; ++x) {
             const int64_t ad = __builtin_amdgcn_readlane(my_adapter, x);
-            const __amdgpu_buffer_rsrc_t rb = make_rsrc((const char *)p.B + (ad * p.sB + col0 * p.ldb) * 2);
-            const bool there = wave + NW * x < entries;
-            if (p.b_fast) {
-                fb[st][x] = load_granule(rb, there ? at : OOB_OFFSET);
-            } else {  // value by value
-                const int co = there ? row_part(r16, cols, p.ldb) : OOB_OFFSET;
-#pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                    const int k = kb * 32 + 8 * (lane >> 4) + 2 * d;
-                    const uint32_t l = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rb, joined(co, k_part(k, p.rank)), 0, 0);
-                    const uint32_t h = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rb, joined(co, k_part(k + 1, p.rank)), 0, 0);
-                    fb[st][x][d] = (int)(l | h << 16);
-                }
-            }
+            const uint16_t *const B = (const uint16_t *)p.B + ad * p.sB + (KC ? col0 * p.ldb + kb * 32 : (int64_t)kb * 32 * p.ldb + col0);
+            const int n = wave + NW * x < entries ? cols : 0, left = p.rank - kb * 32;
+            fb[st][x] = p.b_fast ? column_granule<KC, true>(B, p.ldb, n, left, lane) : column_granule<KC, false>(B, p.ldb, n, left, lane);
         }
         issued();
     };
@@ -292,13 +346,20 @@ __global__ __launch_bounds__(512, 2) void adapter_few_join(const AdapterFewArgs 
 #pragma unroll
         for (int x = 0; x < EB; ++x) {
             if (wave + NW * x >= entries) continue;
+            intx4 b = fb[st][x];
+            if constexpr (!KC) {
+                const intx4 v[1] = {b};
+                intx4 w[1];
+                turn_granules((DMP_LDS char *)red[wave], lane, v, w);
+                b = w[0];
+            }
             const int rr = __builtin_amdgcn_readlane(my_rows, x), lo = rr & 0xffff, hi = (int)((uint32_t)rr >> 16);
 #pragma unroll
             for (int i = 0; i < TM; ++i) {
                 if (hi <= 16 * i || lo >= 16 * i + 16) continue;
                 floatx4 c = {0, 0, 0, 0};
 #pragma unroll
-                for (int w = 0; w < PARTS; ++w) c = mma16<DT>(fh[w][i], fb[st][x], c);
+                for (int w = 0; w < PARTS; ++w) c = mma16<DT>(fh[w][i], b, c);
                 const int at = 16 * i + 4 * (lane >> 4) - lo;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) acc[i][q] += (uint32_t)(at + q) < (uint32_t)(hi - lo) ? c[q] : 0.0f;

@@ -28,7 +28,7 @@ inline FewPlan few_plan(int num_cus, int64_t requests, int64_t M, int64_t N, int
     f.blocks = (int)std::max(nb, std::min<int64_t>(tasks, std::max<int64_t>(1, 2 * num_cus / f.splits)));
     return f;
 }
-constexpr int64_t FEW_ROWS = 256, FEW_RANK_MAX = 128, FEW_N_MAX = 1 << 22;  // N: 31-bit offsets in 64 rows of sums
+constexpr int64_t FEW_ROWS = 256, FEW_RANK_MAX = 128, FEW_N_MAX = 1 << 22, FEW_LD_MAX = 1 << 22;  // 31-bit offsets in 64 rows
 inline int64_t few_work(int splits, int64_t M, int64_t N, int64_t rank) {
     return splits * (cdiv(M * N * 4, 16) * 16 + cdiv(M * cdiv(rank, 16) * 64, 16) * 16);
 }
@@ -90,6 +90,13 @@ inline bool adapter_b_fast(const gemm_adapters_t &ad, int64_t N, bool b_col) {
     return aligned16(ad.B) && ad.ldb % 8 == 0 && (b_col ? ad.rank : N) % 8 == 0 && 256 * ad.ldb * 2 < (1ll << 31) - (1ll << 22);
 }
 
+// Few rows: are the granules of X, W and A_a whole?
+inline bool few_aligned(const void *X, const void *W, const gemm_adapters_t &ad, int64_t N, int64_t K, int64_t ldx,
+                        int64_t ldw, bool col) {
+    return aligned16(X) && aligned16(W) && aligned16(ad.A) && ldx % 8 == 0 && ldw % 8 == 0 && ad.lda % 8 == 0 && K % 8 == 0 &&
+           (col || (N % 8 == 0 && ad.rank % 8 == 0));
+}
+
 // Which kernels (CFG_FEW: adapter_few.hpp; CFG_GENERIC: any alignment).
 //
 // Few rows: up to 256 (us of both launches, few / hidden and 128 x 128 tiles, 4096 x 4096, rank 16: 128
@@ -104,10 +111,13 @@ inline bool adapter_b_fast(const gemm_adapters_t &ad, int64_t N, bool b_col) {
 enum { CFG_FEW = 20 };
 inline int adapter_cfg(int num_cus, const void *X, const void *W, const gemm_adapters_t &ad, int64_t requests, int64_t M, int64_t N,
                        int64_t K, int64_t ldx, int64_t ldw, bool a_col, bool b_col) {
-    // X's and W's granules whole, with 31-bit offsets in a tile
-    if (K == 0 || !granule_ok(X, W, M, N, K, ldx, ldw, GEMM_F16, false, b_col, true)) return CFG_GENERIC;
-    if (b_col && a_col && M <= FEW_ROWS && ad.rank <= FEW_RANK_MAX && N <= FEW_N_MAX && hidden_fast(X, ad, K, ldx, a_col))
+    if (K == 0) return CFG_GENERIC;
+    // W and A_a laid out alike (linear layers, and their input's gradient)
+    if (a_col == b_col && M <= FEW_ROWS && ad.rank <= FEW_RANK_MAX && N <= FEW_N_MAX && ldx <= FEW_LD_MAX && ldw <= FEW_LD_MAX &&
+        ad.lda <= FEW_LD_MAX)
         return CFG_FEW;
+    // X's and W's granules whole, with 31-bit offsets in a tile
+    if (!granule_ok(X, W, M, N, K, ldx, ldw, GEMM_F16, false, b_col, true)) return CFG_GENERIC;
     const int64_t t128 = cdiv(M, 128) * cdiv(N, 128);
     return adapter_b_fast(ad, N, b_col) && M >= 192 && t128 > 2 * (int64_t)num_cus && M >= 32 * requests ? CFG_L : CFG_M;
 }

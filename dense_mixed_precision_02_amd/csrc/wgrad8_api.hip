@@ -36,9 +36,9 @@ int launch_tile(gemm_handle_t h, void (*kernel)(Wgrad8Args), int BM, int BN, int
 
 template <class DT, int FMT>
 int launch_wgrad8(gemm_handle_t h, bool large, bool fast, const Wgrad8Args &a, hipStream_t s) {
-    if (!fast) return launch_tile(h, wgrad8_tile<DT, FMT, 64, 128, 1, 4, false>, 64, 128, 256, 2, a, s);
+    if (!fast) return launch_tile(h, wgrad8_tile<DT, FMT, 64, 128, 2, 2, false>, 64, 128, 256, 2, a, s);
     if (large) return launch_tile(h, wgrad8_large_tile<DT, FMT>, 256, 256, 256, 1, a, s);
-    return launch_tile(h, wgrad8_tile<DT, FMT, 64, 128, 1, 4, true>, 64, 128, 256, 2, a, s);
+    return launch_tile(h, wgrad8_tile<DT, FMT, 64, 128, 2, 2, true>, 64, 128, 256, 2, a, s);
 }
 
 }  // namespace

@@ -232,7 +232,16 @@ int main() {
     CHECK(cfg(3, 68, 64, 72, 5) == CFG_FEW && cfg(3, 140, 2104, 1100, 33) == CFG_FEW && cfg(2, 32, 4160, 64, 48) == CFG_FEW);
     CHECK(cfg(3, 135, 200, 136, 130) == CFG_M && cfg(3, 135, 200, 136, 200, false) == CFG_M);  // a rank past the few rows'
     CHECK(cfg(180, 363, 136, 264, 13) == CFG_M && cfg(180, 363, 136, 264, 13, false) == CFG_M);
-    CHECK(cfg(180, 360, 135, 263, 40, false) == CFG_GENERIC && cfg(4, 182, 99, 33, 5) == CFG_GENERIC);
+    CHECK(cfg(180, 360, 135, 263, 40, false) == CFG_GENERIC && cfg(4, 282, 99, 33, 5) == CFG_GENERIC);
+    CHECK(cfg(4, 182, 99, 33, 5) == CFG_FEW && cfg(4, 179, 99, 33, 5, false) == CFG_FEW && cfg(6, 147, 136, 200, 16, false) == CFG_FEW);
+    {
+        const gemm_adapters_t ad = {P(), P(), nullptr, nullptr, 4, 16, 16, 16};  // W column-major, A_a row-major
+        CHECK(adapter_cfg(CUS, P(), P(), ad, 4, 100, 64, 64, 64, 64, false, true) == CFG_M);
+    }
+    CHECK(few_aligned(P(), P(), {P(), P(), nullptr, nullptr, 4, 5, 64, 5}, 33, 64, 64, 64, true));
+    CHECK(!few_aligned(P(), P(), {P(), P(), nullptr, nullptr, 4, 5, 8, 40}, 40, 64, 64, 40, false));
+    CHECK(!few_aligned(P(), P(), {P(), P(), nullptr, nullptr, 4, 8, 60, 8}, 32, 60, 60, 60, true));
+    CHECK(!few_aligned(P(0x10002), P(), {P(), P(), nullptr, nullptr, 4, 8, 64, 8}, 32, 64, 64, 64, true));
     CHECK(cfg(4, 1000, 64, 64, 16, true, P(0x10002)) == CFG_GENERIC && cfg(4, 100, 0, 64, 16) == CFG_GENERIC);
     CHECK(cfg(4, 2133, 72, 4104, 16) == CFG_L && cfg(4, 2135, 136, 4104, 72, false) == CFG_L && cfg(4, 2256, 200, 4099, 136) == CFG_L);
     CHECK(cfg(2, 1300, 256, 1032, 32) == CFG_M);

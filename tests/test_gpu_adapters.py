@@ -122,6 +122,18 @@ CASES = [
     ("f16", [2, 9], 1, 0, 2, [1, 0], 8, 17, 1, True, "f16", 1.0, 0.0),
     ("bf16", [33, 90, 17], 0, 0, 3, None, 2104, 1100, 33, True, "bf16", 1.0, 0.0),
     ("f16", [20, 12], 0, 0, 2, None, 4160, 64, 48, True, "f32", 1.0, 0.0),
+    # few rows by N-contiguous operands, and by operands of any alignment
+    ("bf16", [1] * 40 + [0, 20], 1, 2, 5, [i % 6 - 1 for i in range(42)], 1600, 136, 16, False, "bf16", 1.0, 0.0),
+    ("f16", [9, 0, 7], 0, 0, 3, None, 4160, 72, 128, False, "f32", 0.5, 1.0),
+    ("bf16", [100, 3, 130], 0, 4, 2, [1, 0, 1], 264, 1096, 40, False, "f32", 1.0, 0.0),
+    ("f16", [30, 1], 2, 0, 2, None, 1031, 203, 77, False, "f32", 1.0, 1.0),
+    ("bf16", [30, 0, 61], 0, 0, 3, [2, 1, 0], 1030, 205, 33, True, "bf16", 1.0, 0.0),
+    ("bf16", [200, 40], 0, 5, 2, None, 67, 131, 120, False, "bf16", 1.0, 0.0),
+    ("f16", [3], 0, 0, 1, None, 7, 3, 3, False, "f16", 1.0, 0.0),
+    # the same past the few rows: staged tiles of any alignment
+    ("bf16", [117, 31, 0, 129], 0, 5, 2, [1, 1, 0, 1], 99, 33, 5, True, "f32", 1.0, 1.0),
+    ("f16", [117, 31, 0, 129], 2, 0, 2, [1, -1, 0, 7], 99, 33, 5, False, "bf16", 1.0, 1.0),
+    ("bf16", [300, 3, 90], 1, 1, 3, None, 200, 136, 130, False, "f32", 1.0, 0.0),
     # staged tiles: many requests, ranks that are no granules, both layouts
     ("bf16", [1, 3] * 90, 2, 1, 5, [i % 6 - 1 for i in range(180)], 136, 264, 13, True, "bf16", 1.0, 0.0),
     ("f16", [1, 3] * 90, 2, 1, 5, [i % 6 - 1 for i in range(180)], 136, 264, 13, False, "f32", 1.0, 1.0),
@@ -176,14 +188,15 @@ def test_nothing_to_do(dmp):
     X, W, A, B = (to_gpu(v) for v in operands(1, 0, 16, 24, 8, 2, torch.bfloat16, True))
     assert dmp.gemm_adapters(X, W, A, B, torch.zeros(3, dtype=torch.int64, device="cuda")).shape == (0, 24)
     # K == 0: beta * C, hidden rows of zeros
-    X, W, A, B = (to_gpu(v) for v in operands(1, 6, 0, 24, 8, 1, torch.bfloat16, False))
-    off = torch.tensor([1, 5], device="cuda")
-    C = normal(3, 6, 24).cuda()
-    h = torch.full((6, 8), 5.0, dtype=torch.bfloat16, device="cuda")
-    D.fill_(7.0)
-    dmp.gemm_adapters(X, W, A, B, off, C=C, out=D, beta=2.0, hidden=h)
-    assert torch.equal(D[1:5], 2 * C[1:5]) and (D[0] == 7).all() and (D[5] == 7).all()
-    assert not h[1:5].any() and (h[0] == 5).all() and (h[5] == 5).all()
+    for linear in (False, True):
+        X, W, A, B = (v.cuda() for v in operands(1, 6, 0, 24, 8, 1, torch.bfloat16, linear))
+        off = torch.tensor([1, 5], device="cuda")
+        C = normal(3, 6, 24).cuda()
+        h = torch.full((6, 8), 5.0, dtype=torch.bfloat16, device="cuda")
+        D.fill_(7.0)
+        dmp.gemm_adapters(X, W, A, B, off, C=C, out=D, beta=2.0, hidden=h)
+        assert torch.equal(D[1:5], 2 * C[1:5]) and (D[0] == 7).all() and (D[5] == 7).all()
+        assert not h[1:5].any() and (h[0] == 5).all() and (h[5] == 5).all()
 
 
 def test_offsets_that_are_wrong_stay_inside(dmp):
