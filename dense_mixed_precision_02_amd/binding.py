@@ -106,7 +106,7 @@ def load_library():
         lib.gemm_run_adapters.argtypes = [vp, vp, vp, ctypes.POINTER(AdapterOperands), vp, vp, vp, i64, i64, i64, i64,
                                           i64, i64, i64, ci, cu, cf, cf, ci, ci, vp, i64, vp, vp]
         lib.gemm_wgrad8_work.restype = i64
-        lib.gemm_wgrad8_work.argtypes = [vp, i64, i64, i64, i64]
+        lib.gemm_wgrad8_work.argtypes = [vp, vp, i64, i64, i64, i64, i64]
         lib.gemm_run_wgrad8.restype = ci
         lib.gemm_run_wgrad8.argtypes = [vp, ctypes.POINTER(Q8Operand), vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, ci,
                                         cu, cf, cf, ci, ci, vp, vp]
@@ -238,9 +238,9 @@ class Handle:
                                                 ldx, ldw, ldc, dtype, flags, alpha, beta, c_type, d_type, hidden,
                                                 ld_hidden, work, stream)
 
-    def wgrad8_work(self, groups, M, N, K) -> int:
+    def wgrad8_work(self, Y, groups, M, N, K, ldy) -> int:
         """Bytes of scratch that run_wgrad8() needs (-1: sizes that are refused)."""
-        return load_library().gemm_wgrad8_work(self.ptr, groups, M, N, K)
+        return load_library().gemm_wgrad8_work(self.ptr, Y, groups, M, N, K, ldy)
 
     def run_wgrad8(self, X: Q8Operand, Y, C, D, offsets, groups, M, N, K, ldy, ldc, dtype, flags=0, alpha=1.0, beta=0.0,
                    c_type=GEMM_OUT_F32, d_type=GEMM_OUT_F32, work=0, stream=0) -> int:
@@ -908,12 +908,13 @@ def gemm_wgrad8(X: Scaled8, Y, offsets=None, C=None, out=None, alpha: float = 1.
     T, M, N = X.rows, X.K, Y.shape[1]
     shape, name = ((M, N), "(M, N)") if offsets is None else ((groups, M, N), "(groups, M, N)")
     c, c_code, out, d_code, ldc, beta = _output(C, out, shape, out_dtype, beta, device, name)
+    y = Y.data_ptr()
 
     def call(h, stream):
         import torch
-        need = h.wgrad8_work(groups, M, N, T)
+        need = h.wgrad8_work(y, groups, M, N, T, ldy)
         work = torch.empty(need, dtype=torch.uint8, device=device) if need > 0 else None
-        return h.run_wgrad8(x, Y.data_ptr(), c, out.data_ptr(), offsets.data_ptr() if offsets is not None else 0, groups,
+        return h.run_wgrad8(x, y, c, out.data_ptr(), offsets.data_ptr() if offsets is not None else 0, groups,
                             M, N, T, ldy, ldc, dt, flags, alpha, beta, c_code, d_code,
                             work.data_ptr() if work is not None else 0, stream)
 

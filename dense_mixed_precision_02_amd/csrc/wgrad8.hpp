@@ -11,7 +11,7 @@
 // ahead in registers, two LDS buffers.  Four neighbouring lanes take the four rows of a
 // block: a wave's writes are one contiguous run of LDS.
 //
-// Rows are split where the gradients' tiles alone would leave CUs idle (wgrad8_splits);
+// Rows are split where the gradients' tiles alone would leave CUs idle (wgrad8_plan);
 // each part's sums go to memory in 32 bits, and wgrad8_join adds them in their order.
 #pragma once
 #include "ragged_staged.hpp"
@@ -145,13 +145,13 @@ __device__ static inline bool wgrad8_at(const Wgrad8Args &p, int lane, TileAt &a
     return true;
 }
 
-template <class DT, int FMT, int BM, int BN, int WM, int WN, bool FAST>
+template <class DT, int FMT, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(WM *WN * 64, 2) void wgrad8_tile(const Wgrad8Args p) {
     constexpr int NW = WM * WN, WTM = BM / WM, WTN = BN / WN, TM = WTM / 16, TN = WTN / 16, KT = 64;
     constexpr int DEPTH = 2;
     constexpr int PA = BM >= 128 ? 32 : 0, PB = BN >= 128 ? 32 : 0;  // see tile16_gemm
     using SA = Widened<DT, FMT, BM, NW, PA>;
-    using SB = Staged<DT, BN, NW, false, FAST, PB>;
+    using SB = Staged<DT, BN, NW, false, true, PB>;
     __shared__ __attribute__((aligned(1024))) char lds_a[2][SA::Op::BYTES];
     __shared__ __attribute__((aligned(1024))) char lds_b[2][SB::Op::BYTES];
     const int lane = lane_id(), wave = wave_id();
@@ -366,7 +366,7 @@ __global__ __launch_bounds__(256) void wgrad8_large_tile(const Wgrad8Args p) {
     __syncthreads();
     DMP_LDS char *slab = wave == 0 ? LA[0] : wave == 1 ? LB[0] : wave == 2 ? LA[1] : LB[1];
     static_assert(32 * (WTN + 4) * 4 <= SA::Op::BYTES && 32 * (WTN + 4) * 4 <= SB::Op::BYTES, "slab must fit");
-    const int64_t first = at.group * r.sC + at.row0 * r.ldc + at.col0;
+    const int64_t first = (int64_t)split * p.part + at.group * r.sC + at.row0 * r.ldc + at.col0;
     store_wave_tile<WTM, WTN, true>((DMP_LDS float *)slab, r.ep, (const char *)r.C + first * out_size(r.ep.c_type),
                               (char *)r.D + first * out_size(r.ep.d_type), r.ldc, at.rows, at.cols, wm * WTM,
                               wn * WTN, lane, [&](int i, int j) { return acc[i][j]; });

@@ -4,6 +4,7 @@
 
 #include "../../include/dmp_gemm.h"
 #include "handle.hpp"
+#include "pack.hpp"
 #include "wgrad8.hpp"
 #include "wgrad8_plan.hpp"
 
@@ -35,19 +36,19 @@ int launch_tile(gemm_handle_t h, void (*kernel)(Wgrad8Args), int BM, int BN, int
 }
 
 template <class DT, int FMT>
-int launch_wgrad8(gemm_handle_t h, bool large, bool fast, const Wgrad8Args &a, hipStream_t s) {
-    if (!fast) return launch_tile(h, wgrad8_tile<DT, FMT, 64, 128, 2, 2, false>, 64, 128, 256, 2, a, s);
-    if (large) return launch_tile(h, wgrad8_large_tile<DT, FMT>, 256, 256, 256, 1, a, s);
-    return launch_tile(h, wgrad8_tile<DT, FMT, 64, 128, 2, 2, true>, 64, 128, 256, 2, a, s);
+int launch_wgrad8(gemm_handle_t h, int edge, const Wgrad8Args &a, hipStream_t s) {
+    if (edge == 256) return launch_tile(h, wgrad8_large_tile<DT, FMT>, 256, 256, 256, 1, a, s);
+    if (edge == 128) return launch_tile(h, wgrad8_tile<DT, FMT, 128, 128, 2, 2>, 128, 128, 256, 2, a, s);
+    return launch_tile(h, wgrad8_tile<DT, FMT, 64, 128, 2, 2>, 64, 128, 256, 2, a, s);
 }
 
 }  // namespace
 
 extern "C" {
 
-int64_t gemm_wgrad8_work(gemm_handle_t h, int64_t groups, int64_t M, int64_t N, int64_t K) {
+int64_t gemm_wgrad8_work(gemm_handle_t h, const void *Y, int64_t groups, int64_t M, int64_t N, int64_t K, int64_t ldy) {
     if (!h || !wgrad8_sizes_ok(groups, M, N, K)) return -1;
-    return wgrad8_work(h->num_cus, groups, M, N, K);
+    return wgrad8_work(h->num_cus, Y, groups, M, N, K, ldy);
 }
 
 int gemm_run_wgrad8(gemm_handle_t h, const gemm_q8_t *X, const void *Y, const void *C, void *D, const void *offsets,
@@ -60,29 +61,39 @@ int gemm_run_wgrad8(gemm_handle_t h, const gemm_q8_t *X, const void *Y, const vo
     const int rc = validate_wgrad8(h, X, Y, C, D, offsets, groups, M, N, K, ldy, ldc, dtype, flags, ep);
     if (rc != GEMM_OK || M == 0 || N == 0 || groups == 0) return rc;
     Wgrad8Args a{};
-    a.splits = K > 0 ? wgrad8_splits(h->num_cus, groups, M, N, K) : 1;
-    if (a.splits > 1 && (!work || !aligned16(work))) return GEMM_ERR_INVALID_ARG;
+    Wgrad8Plan plan = wgrad8_plan(h->num_cus, groups, M, N, K);
+    if (plan.edge == 256 && !wgrad8_narrow(*X)) plan.edge = 128;
+    a.splits = plan.splits;
+    const int64_t pack = wgrad8_pack(Y, N, K, ldy);
+    if ((a.splits > 1 || pack > 0) && (!work || !aligned16(work))) return GEMM_ERR_INVALID_ARG;
+    char *const part = (char *)work + pack;
+    hipStream_t s = (hipStream_t)stream;
     RaggedArgs &r = a.r;
     r.A = X->q; r.sa = X->scale; r.sa_row = X->scale_row; r.sa_k = X->scale_k; r.lda = X->ld;
     r.B = Y; r.ldb = ldy; r.offsets = offsets;
+    if (pack > 0) {
+        PackArgs q{};
+        q.src = Y; q.dst = work; q.rows = K; q.cols = N; q.ld = ldy;
+        const int st = launch(pack_rows, cdiv(K * cdiv(N, 8), 256), 256, s, q);
+        if (st != GEMM_OK) return st;
+        r.B = work; r.ldb = cdiv(N, 8) * 8;
+    }
     r.M = M; r.N = N; r.K = K;
     r.groups = (int)groups;
     r.off32 = (flags & GEMM_OFFSETS_I32) != 0;
     r.C = C; r.D = D; r.ldc = ldc; r.sC = M * ldc; r.ep = ep;
     if (a.splits > 1) {
-        r.D = work; r.ldc = N; r.sC = M * N;
+        r.D = part; r.ldc = N; r.sC = M * N;
         r.ep.alpha = 1.0f; r.ep.use_c = 0; r.ep.d_type = OUT_F32;
         a.part = groups * M * N;
     }
-    hipStream_t s = (hipStream_t)stream;
-    const bool large = wgrad8_large(h->num_cus, groups, M, N) && wgrad8_narrow(*X), fast = K > 0 && wgrad8_fast(Y, N, ldy);
     const bool e4 = X->type == GEMM_E4M3;
     int st;
-    if (dtype == GEMM_F16) st = e4 ? launch_wgrad8<F16, 0>(h, large, fast, a, s) : launch_wgrad8<F16, 1>(h, large, fast, a, s);
-    else st = e4 ? launch_wgrad8<BF16, 0>(h, large, fast, a, s) : launch_wgrad8<BF16, 1>(h, large, fast, a, s);
+    if (dtype == GEMM_F16) st = e4 ? launch_wgrad8<F16, 0>(h, plan.edge, a, s) : launch_wgrad8<F16, 1>(h, plan.edge, a, s);
+    else st = e4 ? launch_wgrad8<BF16, 0>(h, plan.edge, a, s) : launch_wgrad8<BF16, 1>(h, plan.edge, a, s);
     if (st != GEMM_OK || a.splits == 1) return st;
     Wgrad8JoinArgs j{};
-    j.part = (const float *)work; j.C = C; j.D = D;
+    j.part = (const float *)part; j.C = C; j.D = D;
     j.rows = groups * M; j.N = N; j.ldc = ldc; j.splits = a.splits; j.ep = ep;
     return launch(wgrad8_join, cdiv(j.rows * cdiv(N, 4), 256), 256, s, j);
 }

@@ -6,30 +6,43 @@
 namespace dmp {
 namespace plan {
 
-// 256 x 256 tiles where they fill the device and lie mostly inside the gradients, else 64 x 128.
-inline bool wgrad8_large(int num_cus, int64_t groups, int64_t M, int64_t N) {
-    const int64_t t256 = cdiv(M, 256) * cdiv(N, 256);
-    return groups * t256 >= num_cus && (double)M * (double)N >= 0.75 * 65536.0 * (double)t256;
+// Tiles, and the parts that the rows are split into.
+struct Wgrad8Plan {
+    int edge;     // 256: 256 x 256 tiles; 128: 128 x 128; 64: 64 x 128
+    int splits;
+};
+inline Wgrad8Plan wgrad8_plan(int num_cus, int64_t groups, int64_t M, int64_t N, int64_t K) {
+    if (groups == 0 || M == 0 || N == 0) return {64, 1};
+    const int64_t rows = K / groups, t256 = groups * cdiv(M, 256) * cdiv(N, 256);
+    const bool inside = (double)M * (double)N >= 0.75 * 65536.0 * (double)(cdiv(M, 256) * cdiv(N, 256));
+    // 256 x 256 tiles where, with parts of 1024 rows at least, they fill most of the device and lie mostly
+    // inside the gradients, and their rows are worth a large tile's start and end
+    const int64_t large = t256 >= num_cus ? 1 : std::max<int64_t>(1, std::min(num_cus / t256, rows / 1024));
+    if (inside && rows >= 512 && 4 * t256 * large >= 3 * num_cus) return {256, (int)large};
+    // smaller ones, two to a CU, in parts of 256 rows at least
+    const int64_t t128 = groups * cdiv(M, 128) * cdiv(N, 128), tiles = groups * cdiv(M, 64) * cdiv(N, 128);
+    const int64_t s128 = std::max<int64_t>(1, std::min<int64_t>({2 * (int64_t)num_cus / t128, rows / 512, 16}));
+    if (rows >= 512 && 4 * t128 * s128 >= 3 * num_cus) return {128, (int)s128};
+    return {64, (int)std::max<int64_t>(1, std::min<int64_t>({2 * (int64_t)num_cus / tiles, rows / 256, 32}))};
 }
 
-// Parts that the rows are split into: by the number of rows and the gradients' 64 x 128
-// tiles, two to a CU, in parts of 256 rows at least.
-inline int wgrad8_splits(int num_cus, int64_t groups, int64_t M, int64_t N, int64_t K) {
-    if (groups == 0 || M == 0 || N == 0 || wgrad8_large(num_cus, groups, M, N)) return 1;
-    const int64_t tiles = groups * cdiv(M, 64) * cdiv(N, 128);
-    const int64_t s = std::min<int64_t>(2 * (int64_t)num_cus / tiles, K / groups / 256);
-    return (int)std::max<int64_t>(1, std::min<int64_t>(s, 32));
-}
+constexpr int64_t WGRAD8_LD_MAX = 1ll << 23;
 
 inline bool wgrad8_sizes_ok(int64_t groups, int64_t M, int64_t N, int64_t K) {
     return groups >= 0 && groups <= GROUPS_MAX && M >= 0 && N >= 0 && K >= 0 && M <= SIZE_MAX_1 && N <= SIZE_MAX_1 &&
            K <= SIZE_MAX_1;
 }
 
-// (splits only of few tiles: the product is below 2^31)
-inline int64_t wgrad8_work(int num_cus, int64_t groups, int64_t M, int64_t N, int64_t K) {
-    const int s = wgrad8_splits(num_cus, groups, M, N, K);
-    return s > 1 ? (int64_t)s * groups * M * N * 4 : 0;
+// Can Y's 16-byte granules be loaded whole?  (Else it is copied first: pack.hpp.)
+inline bool wgrad8_fast(const void *Y, int64_t N, int64_t ldy) { return aligned16(Y) && N % 8 == 0 && ldy % 8 == 0; }
+
+// Scratch: Y's copy, and the parts' sums.
+inline int64_t wgrad8_pack(const void *Y, int64_t N, int64_t K, int64_t ldy) {
+    return wgrad8_fast(Y, N, ldy) ? 0 : K * cdiv(N, 8) * 16;
+}
+inline int64_t wgrad8_work(int num_cus, const void *Y, int64_t groups, int64_t M, int64_t N, int64_t K, int64_t ldy) {
+    const int s = wgrad8_plan(num_cus, groups, M, N, K).splits;
+    return wgrad8_pack(Y, N, K, ldy) + (s > 1 ? s * groups * M * N * 4 : 0);
 }
 
 inline int validate_wgrad8(gemm_handle_t h, const gemm_q8_t *X, const void *Y, const void *C, const void *D,
@@ -40,7 +53,8 @@ inline int validate_wgrad8(gemm_handle_t h, const gemm_q8_t *X, const void *Y, c
     if (dtype != GEMM_F16 && dtype != GEMM_BF16) return GEMM_ERR_INVALID_ARG;
     if (flags & ~(unsigned)GEMM_OFFSETS_I32) return GEMM_ERR_INVALID_ARG;
     if (!X || (!offsets && groups != 1)) return GEMM_ERR_INVALID_ARG;
-    if (K > 0 && (ldy < std::max<int64_t>(1, N) || ldy > LD_MAX)) return GEMM_ERR_INVALID_ARG;
+    // (31-bit offsets in a k-tile of 64 rows)
+    if (K > 0 && (ldy < std::max<int64_t>(1, N) || ldy > WGRAD8_LD_MAX)) return GEMM_ERR_INVALID_ARG;
     if (M == 0 || N == 0 || groups == 0) return GEMM_OK;
     if (!extent_ok(groups, M, ldc, N)) return GEMM_ERR_INVALID_ARG;
     if (offsets && !offsets_ok(offsets, flags)) return GEMM_ERR_INVALID_ARG;
@@ -51,11 +65,6 @@ inline int validate_wgrad8(gemm_handle_t h, const gemm_q8_t *X, const void *Y, c
 
 // The large tiles read X's factors by 31-bit offsets inside a k-tile.
 inline bool wgrad8_narrow(const gemm_q8_t &X) { return X.scale_row < (1ll << 22) && X.scale_k < (1ll << 26); }
-
-// Can Y's 16-byte granules be loaded whole?
-inline bool wgrad8_fast(const void *Y, int64_t N, int64_t ldy) {
-    return aligned16(Y) && N % 8 == 0 && ldy % 8 == 0 && 128 * ldy < (1ll << 31) - (1ll << 22);
-}
 
 }  // namespace plan
 }  // namespace dmp

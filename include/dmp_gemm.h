@@ -434,13 +434,15 @@ int gemm_run_adapters(gemm_handle_t h, const void *X, const void *W, const gemm_
  * with such values for X gives the same within its error bound.  A NaN scale
  * makes its columns NaN.  Everything else as there.
  *
- * work: gemm_wgrad8_work(h, groups, M, N, K) bytes of device memory (0: none
- * needed, work may be NULL; -1: sizes that are refused), 16-byte aligned, for
- * partial sums where the rows are split to fill the device; they are added in
- * a fixed order.  It must not be shared with a call that can run at the same
+ * work: gemm_wgrad8_work(h, Y, groups, M, N, K, ldy) bytes of device memory (0:
+ * none needed, work may be NULL; -1: sizes that are refused), 16-byte aligned,
+ * for partial sums where the rows are split to fill the device (added in a
+ * fixed order), and for a copy of a Y whose rows are not whole 16-byte
+ * granules (of Y's address only the alignment counts).  ldy: at most 2^23.  It must not be shared with a call that can run at the same
  * time.  Nothing is allocated.
  */
-int64_t gemm_wgrad8_work(gemm_handle_t h, int64_t groups, int64_t M, int64_t N, int64_t K);
+int64_t gemm_wgrad8_work(gemm_handle_t h, const void *Y, int64_t groups, int64_t M, int64_t N, int64_t K,
+                         int64_t ldy);
 int gemm_run_wgrad8(gemm_handle_t h, const gemm_q8_t *X, const void *Y, const void *C, void *D,
                     const void *offsets, int64_t groups, int64_t M, int64_t N, int64_t K, int64_t ldy,
                     int64_t ldc, int dtype, unsigned flags, float alpha, float beta, int c_type,

@@ -174,6 +174,7 @@ int main() {
     REFUSES(W, c.dt = GEMM_F64);
     REFUSES(W, c.fl = GEMM_B_COLMAJOR);
     REFUSES(W, c.ldy = 31);
+    REFUSES(W, c.ldy = WGRAD8_LD_MAX + 1);
     REFUSES(W, c.ldc = 31);
     REFUSES(W, c.Y = nullptr);
     REFUSES(W, c.Y = P(0x10001));
@@ -263,18 +264,26 @@ int main() {
                         CHECK(adapter_work(CUS, q, M, N, K, r, GEMM_OUT_F32) >= 4 * M * adapter_rp(r));
                     }
     // 8-bit gradients: large tiles, parts of the rows (at least 256, no more than the scratch holds)
-    CHECK(wgrad8_large(CUS, 1, 4096, 4096) && !wgrad8_large(CUS, 1, 4096, 3840) && !wgrad8_large(CUS, 8, 1024, 1024));
-    CHECK(wgrad8_large(CUS, 4, 2000, 2200) && !wgrad8_large(CUS, 100, 264, 264));
-    CHECK(wgrad8_splits(CUS, 1, 72, 40, 1000) == 3 && wgrad8_splits(CUS, 1, 130, 99, 3001) == 11);
-    CHECK(wgrad8_splits(CUS, 1, 4096, 4096, 8192) == 1 && wgrad8_splits(CUS, 1, 17, 264, 100000) == 32);
-    CHECK(wgrad8_splits(CUS, 4, 200, 72, 1606) == 1 && wgrad8_splits(CUS, 2, 128, 128, 8000) == 15);
+    auto plan8 = [](int64_t g, int64_t M, int64_t N, int64_t K, int edge, int splits) {
+        const Wgrad8Plan p = wgrad8_plan(CUS, g, M, N, K);
+        return p.edge == edge && p.splits == splits;
+    };
+    // test_gpu_wgrad8's shapes
+    CHECK(plan8(1, 4096, 4096, 520, 256, 1) && plan8(4, 2000, 2200, 2266, 256, 1) && plan8(1, 2000, 1999, 4099, 256, 4));
+    CHECK(plan8(3, 1000, 1400, 2203, 128, 1) && plan8(1, 900, 650, 5003, 128, 9));
+    CHECK(plan8(1, 72, 40, 1000, 64, 3) && plan8(1, 130, 99, 3001, 64, 11) && plan8(4, 200, 72, 5006, 64, 4));
+    CHECK(plan8(1, 128, 128, 4000, 64, 15));
+    // borders
+    CHECK(plan8(1, 4096, 4096, 511, 64, 1) && plan8(1, 4096, 4096, 8192, 256, 1) && plan8(1, 17, 264, 100000, 64, 32));
+    CHECK(plan8(1, 2048, 2048, 8192, 256, 4) && plan8(1, 1024, 1024, 8192, 128, 8) && plan8(9, 1912, 1296, 32, 64, 1));
     for (int64_t g : {0, 1, 5, 1000})
         for (int64_t M : {0, 1, 64, 1000, 5000})
             for (int64_t N : {0, 1, 128, 1000, 5000})
                 for (int64_t K : {0, 1, 255, 256, 10000, 1 << 30}) {
-                    const int s = wgrad8_splits(CUS, g, M, N, K);
-                    CHECK(s >= 1 && s <= 32 && (s == 1 || K / g / s >= 256));
-                    CHECK(wgrad8_work(CUS, g, M, N, K) == (s > 1 ? 4 * s * g * M * N : 0));
+                    const int s = wgrad8_plan(CUS, g, M, N, K).splits;
+                    CHECK(s >= 1 && s <= 256 && (s == 1 || K / g / s >= 256));
+                    CHECK(wgrad8_work(CUS, P(), g, M, N, K, 5000) >= (s > 1 ? 4 * s * g * M * N : 0));
+                    CHECK(wgrad8_work(CUS, P(2), g, M, N, K, 5000) >= (s > 1 ? 4 * s * g * M * N : 0) + 2 * K * N);
                 }
     gemm_q8_t x = q8(100, 64);
     CHECK(wgrad8_narrow(x));

@@ -96,6 +96,8 @@ WGRAD = [
     (2100, 5, 2048, 2056, "f16", "f32", 0),
     (3000, 7, 520, 264, "bf16", "f32", 0),      # 64 x 128
     (9000, 0, 200, 136, "f16", "f16", 0),       # split rows
+    (5000, 4, 1000, 520, "bf16", "f32", 0),     # 128 x 128
+    (9000, 0, 2048, 2048, "f16", "bf16", 0),    # 256 x 256, split rows
     (3000, 7, 131, 99, "bf16", "bf16", 1),      # any alignment
 ]
 
@@ -113,7 +115,7 @@ def test_wgrad8(handles, case):
     res = []
     for lib, h in handles:
         D = torch.zeros(g, M, N, dtype=OUT[out][1], device="cuda")
-        need = lib.gemm_wgrad8_work(h, g, M, N, T)
+        need = lib.gemm_wgrad8_work(h, Y.data_ptr() + 2 * shift, g, M, N, T, N)
         work = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
         rc = lib.gemm_run_wgrad8(h, ctypes.byref(x.operand), Y.data_ptr() + 2 * shift, None, D.data_ptr(),
                                  off.data_ptr() if G else None, g, M, N, T, N, N, 0 if yt == "f16" else 1, 0, 1.0, 0.0, 0,

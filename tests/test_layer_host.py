@@ -24,7 +24,7 @@ def test_null_handle_is_refused():
     assert lib.gemm_adapters_work(None, 1, 1, 1, 1, 1, 0) == -1
     assert lib.gemm_run_adapters(None, 0, 0, ctypes.byref(a), 0, 0, 0, 1, 1, 1, 1, 1, 1, 1, 0, 0, 1.0, 0.0, 0, 0, 0, 0, 0,
                                  0) == 1
-    assert lib.gemm_wgrad8_work(None, 1, 1, 1, 1) == -1
+    assert lib.gemm_wgrad8_work(None, 0, 1, 1, 1, 1, 1) == -1
     assert lib.gemm_run_wgrad8(None, ctypes.byref(q), 0, 0, 0, 0, 1, 1, 1, 1, 1, 1, 0, 0, 1.0, 0.0, 0, 0, 0, 0) == 1
 
 
