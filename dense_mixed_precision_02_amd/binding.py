@@ -101,7 +101,7 @@ def load_library():
         lib.gemm_run_scaled8.argtypes = [vp, ctypes.POINTER(Q8Operand), ctypes.POINTER(Q8Operand), vp, vp,
                                          vp, i64, i64, i64, i64, i64, cu, cf, cf, ci, ci, vp]
         lib.gemm_adapters_work.restype = i64
-        lib.gemm_adapters_work.argtypes = [vp, i64, i64, i64, i64, i64, ci]
+        lib.gemm_adapters_work.argtypes = [vp, vp, vp, i64, i64, i64, i64, i64, i64, i64, ci, cu]
         lib.gemm_run_adapters.restype = ci
         lib.gemm_run_adapters.argtypes = [vp, vp, vp, ctypes.POINTER(AdapterOperands), vp, vp, vp, i64, i64, i64, i64,
                                           i64, i64, i64, ci, cu, cf, cf, ci, ci, vp, i64, vp, vp]
@@ -226,9 +226,10 @@ class Handle:
                                                groups, M, N, K, ldc, flags, alpha, beta, c_type, d_type,
                                                stream)
 
-    def adapters_work(self, requests, M, N, K, rank, d_type) -> int:
+    def adapters_work(self, X, W, requests, M, N, K, rank, ldx, ldw, d_type, flags=0) -> int:
         """Bytes of scratch that run_adapters() needs (-1: sizes that are refused)."""
-        return load_library().gemm_adapters_work(self.ptr, requests, M, N, K, rank, d_type)
+        return load_library().gemm_adapters_work(self.ptr, X, W, requests, M, N, K, rank, ldx, ldw, d_type,
+                                                 flags)
 
     def run_adapters(self, X, W, adapters: AdapterOperands, C, D, offsets, requests, M, N, K, ldx, ldw, ldc, dtype,
                      flags=0, alpha=1.0, beta=0.0, c_type=GEMM_OUT_F32, d_type=GEMM_OUT_F32, hidden=0, ld_hidden=0,
@@ -869,12 +870,13 @@ def gemm_adapters(X, W, A, B, offsets, ids=None, scale=None, C=None, out=None, a
     c, c_code, out, d_code, ldc, beta = _output(C, out, (T, N), out_dtype, beta, device, "(T, N)")
     operands = AdapterOperands(A.data_ptr(), B.data_ptr(), ids_at, scale_at, adapters, rank, lda, ldb)
     flags |= (GEMM_B_COLMAJOR if col else 0) | (GEMM_ADAPTER_A_COLMAJOR if a_col else 0)
+    x_at, w_at = X.data_ptr(), W.data_ptr()
 
     def call(h, stream):
         lib = load_library()
-        work = torch.empty(max(lib.gemm_adapters_work(h.ptr, requests, T, N, K, rank, d_code), 16), dtype=torch.uint8,
-                           device=device)
-        return lib.gemm_run_adapters(h.ptr, X.data_ptr(), W.data_ptr(), ctypes.byref(operands), c, out.data_ptr(),
+        need = lib.gemm_adapters_work(h.ptr, x_at, w_at, requests, T, N, K, rank, ldx, ldw, d_code, flags)
+        work = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+        return lib.gemm_run_adapters(h.ptr, x_at, w_at, ctypes.byref(operands), c, out.data_ptr(),
                                      offsets.data_ptr(), requests, T, N, K, ldx, ldw, ldc, dt, flags, alpha, beta, c_code,
                                      d_code, hidden_at, ld_hidden, work.data_ptr(), stream)
 

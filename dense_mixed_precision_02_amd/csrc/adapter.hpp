@@ -594,9 +594,9 @@ __device__ static inline void adapter_direct(const AdapterArgs &p, const TileAt 
     } while (hi[NS - 1] > 0);
 }
 
-// The product, X and W staged through registers as in ragged_staged.hpp.  FAST: their
-// 16-byte granules are aligned and whole.
-template <class DT, int BM, int BN, int WM, int WN, bool BKC, bool FAST>
+// The product, X and W staged through registers as in ragged_staged.hpp.  (Their rows are whole
+// 16-byte granules, with zeros past the end where K or N is none.)
+template <class DT, int BM, int BN, int WM, int WN, bool BKC>
 __global__ __launch_bounds__(WM *WN * 64, 2) void adapter_staged(const AdapterArgs p) {
     constexpr int NW = WM * WN, WTM = BM / WM, WTN = BN / WN, TM = WTM / 16, TN = WTN / 16;
     constexpr int DEPTH = 2;
@@ -630,22 +630,13 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void adapter_staged(const AdapterAr
         const __amdgpu_buffer_rsrc_t rsa = make_rsrc(A), rsb = make_rsrc(B);
         const int left = at.k - kt * 64;
 #pragma unroll
-        for (int j = 0; j < OpA::CPW; ++j) {
-            const int row = opa.row_or_k + 8 * NW * j;
-            if constexpr (FAST)
-                ra[slot][j] = load_granule(rsa, row < at.rows && opa.fixed < left ? opa.off0 + j * opa.step : OOB_OFFSET);
-            else
-                ra[slot][j] = load8((const uint16_t *)A + row * p.r.lda + opa.fixed, row < at.rows ? left - opa.fixed : 0);
-        }
+        for (int j = 0; j < OpA::CPW; ++j)
+            ra[slot][j] = load_granule(rsa, opa.row_or_k + 8 * NW * j < at.rows && opa.fixed < left ? opa.off0 + j * opa.step : OOB_OFFSET);
 #pragma unroll
         for (int j = 0; j < OpB::CPW; ++j) {
             const int r = BKC ? opb.row_or_k + 8 * NW * j : opb.fixed;
             const int k = BKC ? opb.fixed : opb.row_or_k + OpB::KSTEP * j;
-            const bool ok = r < at.cols && k < left;
-            if constexpr (FAST)
-                rb[slot][j] = load_granule(rsb, ok ? opb.off0 + j * opb.step : OOB_OFFSET);
-            else
-                rb[slot][j] = load8((const uint16_t *)B + (BKC ? r * p.r.ldb + k : k * p.r.ldb + r), ok ? (BKC ? left - k : at.cols - r) : 0);
+            rb[slot][j] = load_granule(rsb, r < at.cols && k < left ? opb.off0 + j * opb.step : OOB_OFFSET);
         }
         issued();
     };

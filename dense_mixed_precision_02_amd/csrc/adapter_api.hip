@@ -7,6 +7,7 @@
 #include "adapter_few.hpp"
 #include "adapter_plan.hpp"
 #include "handle.hpp"
+#include "pack.hpp"
 
 using namespace dmp;
 using namespace dmp::plan;
@@ -37,20 +38,26 @@ int run_hidden(const AdapterArgs &a, bool a_col, bool fast, hipStream_t s) {
     return a.rank <= 32 ? launch_hidden<DT, 2, 2, true>(a, s) : launch_hidden<DT, 2, 4, true>(a, s);
 }
 
-template <class DT, int BM, int BN, int WM, int WN, bool BKC, bool FAST>
-int launch_staged(AdapterArgs a, hipStream_t s) {
-    a.r.tiles_n = (int)cdiv(a.r.N, BN);
-    return launch(adapter_staged<DT, BM, BN, WM, WN, BKC, FAST>, cdiv(a.r.M, BM) * a.r.tiles_n, WM * WN * 64, s, a);
+template <class DT, bool BKC>
+int run_product(AdapterArgs a, int cfg, hipStream_t s) {
+    const int edge = cfg == CFG_L ? 256 : cfg == CFG_M ? 128 : 64;
+    a.r.tiles_n = (int)cdiv(a.r.N, edge);
+    return launch(cfg == CFG_L   ? adapter_tile<DT, BKC>
+                  : cfg == CFG_M ? adapter_staged<DT, 128, 128, 2, 2, BKC>
+                                 : adapter_staged<DT, 64, 64, 2, 2, BKC>,
+                  cdiv(a.r.M, edge) * a.r.tiles_n, 256, s, a);
 }
 
-template <class DT, bool BKC>
-int run_product(const AdapterArgs &a, int cfg, hipStream_t s) {
-    if (cfg == CFG_L) {
-        AdapterArgs b = a;
-        b.r.tiles_n = (int)cdiv(a.r.N, 256);
-        return launch(adapter_tile<DT, BKC>, cdiv(a.r.M, 256) * b.r.tiles_n, 256, s, b);
-    }
-    return cfg == CFG_M ? launch_staged<DT, 128, 128, 2, 2, BKC, true>(a, s) : launch_staged<DT, 64, 128, 1, 4, BKC, false>(a, s);
+// X or W (rows x cols) in whole granules: itself, or a copy at `to`, which is moved on.
+int whole(const void *&x, int64_t &ld, int64_t rows, int64_t cols, char *&to, hipStream_t s) {
+    const int64_t bytes = adapter_pack(x, rows, cols, ld);
+    if (bytes == 0) return GEMM_OK;
+    PackArgs p{};
+    p.src = x; p.dst = to; p.rows = rows; p.cols = cols; p.ld = ld;
+    x = to;
+    ld = cdiv(cols, 8) * 8;
+    to += bytes;
+    return launch(pack_rows, cdiv(rows * cdiv(cols, 8), 256), 256, s, p);
 }
 
 template <class DT, int BM, bool KC, bool ALIGNED>
@@ -88,10 +95,18 @@ int run_few(int num_cus, const AdapterArgs &a, bool col, bool aligned, hipStream
 }
 
 template <class DT>
-int run_adapters(int num_cus, const AdapterArgs &a, bool a_col, bool b_col, bool hidden_f, bool few_a, int cfg, hipStream_t s) {
-    if (cfg == CFG_FEW) return run_few<DT>(num_cus, a, b_col, few_a, s);
-    if (a.r.K > 0 || a.hidden) {
-        const int rc = run_hidden<DT>(a, a_col, hidden_f, s);
+int run_adapters(int num_cus, AdapterArgs a, const gemm_adapters_t &ad, bool a_col, bool b_col, hipStream_t s) {
+    RaggedArgs &r = a.r;
+    const int cfg = adapter_cfg(num_cus, ad, r.groups, r.M, r.N, r.K, r.lda, r.ldb, a_col, b_col);
+    if (cfg == CFG_FEW) return run_few<DT>(num_cus, a, b_col, few_aligned(r.A, r.B, ad, r.N, r.K, r.lda, r.ldb, b_col), s);
+    if (r.K > 0) {
+        char *to = a.H + cdiv((int64_t)a.parts * r.M * a.rp * 2, 16) * 16;
+        int rc = whole(r.A, r.lda, r.M, r.K, to, s);
+        if (rc == GEMM_OK) rc = b_col ? whole(r.B, r.ldb, r.N, r.K, to, s) : whole(r.B, r.ldb, r.K, r.N, to, s);
+        if (rc != GEMM_OK) return rc;
+    }
+    if (r.K > 0 || a.hidden) {
+        const int rc = run_hidden<DT>(a, a_col, r.K > 0 && hidden_fast(r.A, ad, r.K, r.lda, a_col), s);
         if (rc != GEMM_OK) return rc;
     }
     return b_col ? run_product<DT, true>(a, cfg, s) : run_product<DT, false>(a, cfg, s);
@@ -101,11 +116,12 @@ int run_adapters(int num_cus, const AdapterArgs &a, bool a_col, bool b_col, bool
 
 extern "C" {
 
-int64_t gemm_adapters_work(gemm_handle_t h, int64_t requests, int64_t M, int64_t N, int64_t K, int64_t rank, int d_type) {
-    if (!h || requests < 0 || requests > GROUPS_MAX || M < 0 || N < 0 || K < 0 || M > SIZE_MAX_1 || N > SIZE_MAX_1 || K > SIZE_MAX_1 || rank < 1 ||
-        rank > ADAPTER_RANK_MAX || !float_out(d_type))
+int64_t gemm_adapters_work(gemm_handle_t h, const void *X, const void *W, int64_t requests, int64_t M, int64_t N, int64_t K,
+                           int64_t rank, int64_t ldx, int64_t ldw, int d_type, unsigned flags) {
+    if (!h || requests < 0 || requests > GROUPS_MAX || M < 0 || N < 0 || K < 0 || M > SIZE_MAX_1 || N > ADAPTER_WIDTH_MAX ||
+        K > ADAPTER_WIDTH_MAX || rank < 1 || rank > ADAPTER_RANK_MAX || !float_out(d_type))
         return -1;
-    return adapter_work(h->num_cus, requests, M, N, K, rank, d_type);
+    return adapter_work(h->num_cus, X, W, requests, M, N, K, rank, ldx, ldw, d_type, (flags & GEMM_B_COLMAJOR) != 0);
 }
 
 int gemm_run_adapters(gemm_handle_t h, const void *X, const void *W, const gemm_adapters_t *ad, const void *C, void *D,
@@ -139,12 +155,8 @@ int gemm_run_adapters(gemm_handle_t h, const void *X, const void *W, const gemm_
     a.rp = (int)adapter_rp(ad->rank);
     a.parts = adapter_parts(d_type);
     a.hidden = hidden; a.ld_hidden = ld_hidden;
-    const int cfg = adapter_cfg(h->num_cus, X, W, *ad, requests, M, N, K, ldx, ldw, ac, bc);
-    const bool fa = few_aligned(X, W, *ad, N, K, ldx, ldw, bc);
-    const bool hf = K > 0 && hidden_fast(X, *ad, K, ldx, ac);
     hipStream_t s = (hipStream_t)stream;
-    return dtype == GEMM_F16 ? run_adapters<F16>(h->num_cus, a, ac, bc, hf, fa, cfg, s)
-                              : run_adapters<BF16>(h->num_cus, a, ac, bc, hf, fa, cfg, s);
+    return dtype == GEMM_F16 ? run_adapters<F16>(h->num_cus, a, *ad, ac, bc, s) : run_adapters<BF16>(h->num_cus, a, *ad, ac, bc, s);
 }
 
 }  // extern "C"

@@ -8,6 +8,7 @@ namespace plan {
 
 constexpr unsigned ADAPTER_FLAGS = GEMM_B_COLMAJOR | GEMM_OFFSETS_I32 | GEMM_ADAPTER_A_COLMAJOR;
 constexpr int64_t ADAPTER_RANK_MAX = 1024, ADAPTER_LD_MAX = 1ll << 24;  // 31-bit offsets in 64 rows of an adapter
+constexpr int64_t ADAPTER_WIDTH_MAX = 1ll << 21;  // K, N: 31-bit offsets in 256 rows of X and W
 
 inline int64_t adapter_rp(int64_t rank) { return cdiv(rank, 8) * 8; }
 inline int adapter_parts(int d_type) { return d_type == GEMM_OUT_F32 ? 2 : 1; }
@@ -28,16 +29,29 @@ inline FewPlan few_plan(int num_cus, int64_t requests, int64_t M, int64_t N, int
     f.blocks = (int)std::max(nb, std::min<int64_t>(tasks, std::max<int64_t>(1, 2 * num_cus / f.splits)));
     return f;
 }
-constexpr int64_t FEW_ROWS = 256, FEW_RANK_MAX = 128, FEW_N_MAX = 1 << 22, FEW_LD_MAX = 1 << 22;  // 31-bit offsets in 64 rows
+constexpr int64_t FEW_ROWS = 128, FEW_RANK_MAX = 128, FEW_LD_MAX = 1 << 22;  // 31-bit offsets in 64 rows
 inline int64_t few_work(int splits, int64_t M, int64_t N, int64_t rank) {
     return splits * (cdiv(M * N * 4, 16) * 16 + cdiv(M * cdiv(rank, 16) * 64, 16) * 16);
 }
 
-// Scratch: the hidden rows, or the sums of the K parts.
-inline int64_t adapter_work(int num_cus, int64_t requests, int64_t M, int64_t N, int64_t K, int64_t rank, int d_type) {
-    int64_t b = adapter_parts(d_type) * M * adapter_rp(rank) * 2;
-    if (M > 0 && N > 0 && K > 0 && requests > 0 && M <= FEW_ROWS && rank <= FEW_RANK_MAX && N <= FEW_N_MAX)
-        b = std::max(b, few_work(few_plan(num_cus, requests, M, N, K, rank).splits, M, N, rank));
+// Are a matrix's rows whole 16-byte granules, with 31-bit offsets in 256 of them?  (Else X and
+// W are copied first, past the few rows: pack.hpp.)
+inline bool adapter_whole(const void *X, int64_t cols, int64_t ld) {
+    return aligned16(X) && cols % 8 == 0 && ld % 8 == 0 && ld <= 2 * ADAPTER_WIDTH_MAX;
+}
+inline int64_t adapter_pack(const void *X, int64_t rows, int64_t cols, int64_t ld) {
+    return adapter_whole(X, cols, ld) ? 0 : rows * cdiv(cols, 8) * 16;
+}
+
+// Scratch: the hidden rows and X's and W's copies, or the sums of the K parts.
+inline int64_t adapter_work(int num_cus, const void *X, const void *W, int64_t requests, int64_t M, int64_t N, int64_t K,
+                            int64_t rank, int64_t ldx, int64_t ldw, int d_type, bool b_col) {
+    int64_t b = cdiv(adapter_parts(d_type) * M * adapter_rp(rank) * 2, 16) * 16;
+    if (M > 0 && N > 0 && K > 0 && requests > 0) {
+        b += adapter_pack(X, M, K, ldx) + (b_col ? adapter_pack(W, N, K, ldw) : adapter_pack(W, K, N, ldw));
+        if (M <= FEW_ROWS && rank <= FEW_RANK_MAX)
+            b = std::max(b, few_work(few_plan(num_cus, requests, M, N, K, rank).splits, M, N, rank));
+    }
     return b;
 }
 
@@ -47,6 +61,7 @@ inline int validate_adapters(gemm_handle_t h, const void *X, const void *W, cons
                              const void *hidden, int64_t ld_hidden, const void *work) {
     int rc = check_sizes(h, requests, M, N, K, ldc, ep);
     if (rc != GEMM_OK) return rc;
+    if (N > ADAPTER_WIDTH_MAX || K > ADAPTER_WIDTH_MAX) return GEMM_ERR_INVALID_ARG;
     if (dtype != GEMM_F16 && dtype != GEMM_BF16) return GEMM_ERR_INVALID_ARG;
     if ((flags & ~ADAPTER_FLAGS) || !ad) return GEMM_ERR_INVALID_ARG;
     if (ad->rank < 1 || ad->rank > ADAPTER_RANK_MAX || ad->adapters < 0 || ad->adapters > GROUPS_MAX)
@@ -97,29 +112,33 @@ inline bool few_aligned(const void *X, const void *W, const gemm_adapters_t &ad,
            (col || (N % 8 == 0 && ad.rank % 8 == 0));
 }
 
-// Which kernels (CFG_FEW: adapter_few.hpp; CFG_GENERIC: any alignment).
+// Which kernels (CFG_FEW: adapter_few.hpp).  In us, hidden rows with them, weights from memory,
+// rank 16 where none is named.
 //
-// Few rows: up to 256 (us of both launches, few / hidden and 128 x 128 tiles, 4096 x 4096, rank 16: 128
-// rows of 128 requests 43 / 129, of 4: 38 / 64, 256 rows of 256 requests 79 / 128, of 4: 71 / 67;
-// 1024 x 1024: 128 rows of 16 requests 16 / 35, 256 rows of 256: 24 / 88, of 4, rank 64: 18 / 32).
-// 256 x 256 tiles where 128 x 128 ones, two to a CU, would take more than one round (us, 256 x 256 / 128 x
-// 128, rank 16: 512 small tiles, 2048 x 4096 x 4096: 97 / 83, 4096 x 2048 x 2048: 60 / 48; 640, 5003 x
+// Few rows: up to 128 (few / 64 x 64 tiles, 4096 x 4096: 64 rows of 4 requests 26 / 48, 128 rows of 4: 44 /
+// 47, of 128: 48 / 59, 256 rows of 4: 83 / 49, of 256: 90 / 58; 1024 x 1024: 128 rows of 128: 19 / 32).
+//
+// 64 x 64 tiles while 128 x 128 ones leave CUs idle (product alone, 64 x 64 / 128 x 128 tiles: 512 x
+// 1024, K 4096: 23 / 54, 1024 x 2048, K 4096: 37 / 55; 256 large tiles, 1024 x 4096, K 4096: 63 / 59, 4096 x
+// 1024, K 512: 17 / 18; 512, 2048 x 4096, K 4096: 117 / 87), and where requests are of one or
+// two rows, which each cost a workgroup a turn, one after the other (2048 x 4096, K 1024, 2048
+// requests: 112 / 130; 4096 rows of 1024 requests, 4096 x 4096: 252 / 210).
+//
+// 256 x 256 tiles where 128 x 128 ones, two to a CU, would take more than one round (256 x 256 / 128 x
+// 128: 512 small tiles, 2048 x 4096 x 4096: 97 / 83, 4096 x 2048 x 2048: 60 / 48; 640, 5003 x
 // 2048, K 4096: 123 / 137; 680, 5003 x 2056, K 1000, row-major: 57 / 57; 1024, 4096 x 4096 x
 // 4096: 116 / 172, 8192 x 2048 x 2048: 76 / 107; 2048, 8192 x 4096, K 512: 66 / 77, K 4096:
-// 231 / 340), and the requests are long: each costs a large tile a turn of its own (1024 rows of
-// 1024 requests, 2048 x 2048: 939 / 98).
+// 231 / 340), and the requests are long (1024 rows of 1024 requests, 2048 x 2048: 939 / 98).
 enum { CFG_FEW = 20 };
-inline int adapter_cfg(int num_cus, const void *X, const void *W, const gemm_adapters_t &ad, int64_t requests, int64_t M, int64_t N,
-                       int64_t K, int64_t ldx, int64_t ldw, bool a_col, bool b_col) {
-    if (K == 0) return CFG_GENERIC;
+inline int adapter_cfg(int num_cus, const gemm_adapters_t &ad, int64_t requests, int64_t M, int64_t N, int64_t K, int64_t ldx,
+                       int64_t ldw, bool a_col, bool b_col) {
+    if (K == 0) return CFG_S;
     // W and A_a laid out alike (linear layers, and their input's gradient)
-    if (a_col == b_col && M <= FEW_ROWS && ad.rank <= FEW_RANK_MAX && N <= FEW_N_MAX && ldx <= FEW_LD_MAX && ldw <= FEW_LD_MAX &&
-        ad.lda <= FEW_LD_MAX)
+    if (a_col == b_col && M <= FEW_ROWS && ad.rank <= FEW_RANK_MAX && ldx <= FEW_LD_MAX && ldw <= FEW_LD_MAX && ad.lda <= FEW_LD_MAX)
         return CFG_FEW;
-    // X's and W's granules whole, with 31-bit offsets in a tile
-    if (!granule_ok(X, W, M, N, K, ldx, ldw, GEMM_F16, false, b_col, true)) return CFG_GENERIC;
     const int64_t t128 = cdiv(M, 128) * cdiv(N, 128);
-    return adapter_b_fast(ad, N, b_col) && M >= 192 && t128 > 2 * (int64_t)num_cus && M >= 32 * requests ? CFG_L : CFG_M;
+    if (t128 < num_cus || M <= 2 * requests) return CFG_S;
+    return adapter_b_fast(ad, N, b_col) && t128 > 2 * (int64_t)num_cus && M >= 32 * requests ? CFG_L : CFG_M;
 }
 
 }  // namespace plan

@@ -17,7 +17,7 @@ struct PackArgs {
 };
 
 // A granule to a thread.
-__global__ __launch_bounds__(256) void pack_rows(const PackArgs p) {
+static __global__ __launch_bounds__(256) void pack_rows(const PackArgs p) {
     const int64_t per = (p.cols + 7) / 8, i = (int64_t)workgroup_id() * 256 + threadIdx.x;
     const int64_t row = i / per, col = (i - row * per) * 8;
     if (row >= p.rows) return;

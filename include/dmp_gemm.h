@@ -400,10 +400,11 @@ int gemm_run_scaled8(gemm_handle_t h, const gemm_q8_t *A, const gemm_q8_t *B, co
  * B and A, whose hidden rows are g = scale * dD * B_a^T; dA = X_a^T g_a and dB =
  * h_a^T dD_a by gemm_run_grouped_wgrad.
  *
- * work: gemm_adapters_work(h, requests, M, N, K, rank, d_type) bytes of device
- * memory (-1: sizes that are refused), 16-byte aligned, not shared with a call that can run at the
- * same time.  Nothing is allocated.  rank: 1 .. 1024; ldb at most
- * 2^24; adapters and requests at most 2^20.  Everything else as in gemm_run_grouped.
+ * work: gemm_adapters_work(h, X, W, requests, M, N, K, rank, ldx, ldw, d_type,
+ * flags) bytes of device memory (-1: sizes that are refused; of X's and W's
+ * addresses only the alignment counts), 16-byte aligned, not shared with a call that can run at the
+ * same time.  Nothing is allocated.  rank: 1 .. 1024; K and N at
+ * most 2^21, ldb 2^24; adapters and requests at most 2^20.  Everything else as in gemm_run_grouped.
  */
 enum { GEMM_ADAPTER_A_COLMAJOR = 128u };
 typedef struct {
@@ -413,8 +414,8 @@ typedef struct {
     int64_t adapters, rank;
     int64_t lda, ldb;
 } gemm_adapters_t;
-int64_t gemm_adapters_work(gemm_handle_t h, int64_t requests, int64_t M, int64_t N, int64_t K, int64_t rank,
-                           int d_type);
+int64_t gemm_adapters_work(gemm_handle_t h, const void *X, const void *W, int64_t requests, int64_t M, int64_t N,
+                           int64_t K, int64_t rank, int64_t ldx, int64_t ldw, int d_type, unsigned flags);
 int gemm_run_adapters(gemm_handle_t h, const void *X, const void *W, const gemm_adapters_t *ad,
                       const void *C, void *D, const void *offsets, int64_t requests, int64_t M,
                       int64_t N, int64_t K, int64_t ldx, int64_t ldw, int64_t ldc, int dtype,

@@ -91,9 +91,9 @@ struct R {
 };
 
 // packed operands of linear layers (or row-major ones)
-static int cfg(int64_t q, int64_t M, int64_t K, int64_t N, int64_t r, bool linear = true, const void *X = P()) {
+static int cfg(int64_t q, int64_t M, int64_t K, int64_t N, int64_t r, bool linear = true) {
     const gemm_adapters_t ad = {P(), P(), nullptr, nullptr, 4, r, linear ? K : r, linear ? r : N};
-    return adapter_cfg(CUS, X, P(), ad, q, M, N, K, K, linear ? K : N, linear, linear);
+    return adapter_cfg(CUS, ad, q, M, N, K, K, linear ? K : N, linear, linear);
 }
 
 int main() {
@@ -158,6 +158,8 @@ int main() {
     REFUSES(A, c.e = ep(1.0f, GEMM_OUT_F16); c.C = c.D);
     REFUSES(A, c.e = ep(0.0f, GEMM_OUT_F32, GEMM_OUT_I32));
     REFUSES(A, c.M = 1ll << 31);
+    REFUSES(A, c.N = c.ldc = (1ll << 21) + 1);
+    REFUSES(A, c.K = c.ldx = c.ldw = c.ad.lda = (1ll << 21) + 1);
     REFUSES(A, c.ldx = LD_MAX + 1);
     REFUSES(A, c.ldx = LD_MAX);
     REFUSES(A, c.ad.lda = LD_MAX);
@@ -229,29 +231,31 @@ int main() {
     }
 
     // which kernels: test_gpu_adapters' shapes
-    CHECK(cfg(64, 64, 1024, 528, 16) == CFG_FEW && cfg(171, 153, 1600, 136, 16) == CFG_FEW && cfg(5, 256, 264, 200, 128) == CFG_FEW);
-    CHECK(cfg(3, 68, 64, 72, 5) == CFG_FEW && cfg(3, 140, 2104, 1100, 33) == CFG_FEW && cfg(2, 32, 4160, 64, 48) == CFG_FEW);
-    CHECK(cfg(3, 135, 200, 136, 130) == CFG_M && cfg(3, 135, 200, 136, 200, false) == CFG_M);  // a rank past the few rows'
-    CHECK(cfg(180, 363, 136, 264, 13) == CFG_M && cfg(180, 363, 136, 264, 13, false) == CFG_M);
-    CHECK(cfg(180, 360, 135, 263, 40, false) == CFG_GENERIC && cfg(4, 282, 99, 33, 5) == CFG_GENERIC);
-    CHECK(cfg(4, 182, 99, 33, 5) == CFG_FEW && cfg(4, 179, 99, 33, 5, false) == CFG_FEW && cfg(6, 147, 136, 200, 16, false) == CFG_FEW);
+    CHECK(cfg(64, 64, 1024, 528, 16) == CFG_FEW && cfg(171, 153, 1600, 136, 16) == CFG_S && cfg(5, 256, 264, 200, 128) == CFG_S);
+    CHECK(cfg(3, 68, 64, 72, 5) == CFG_FEW && cfg(3, 140, 2104, 1100, 33) == CFG_S && cfg(2, 32, 4160, 64, 48) == CFG_FEW);
+    CHECK(cfg(3, 100, 200, 136, 130) == CFG_S && cfg(3, 100, 200, 136, 200, false) == CFG_S);  // a rank past the few rows'
+    CHECK(cfg(180, 363, 136, 264, 13) == CFG_S && cfg(180, 363, 136, 264, 13, false) == CFG_S);
+    CHECK(cfg(180, 360, 135, 263, 40, false) == CFG_S && cfg(4, 282, 99, 33, 5) == CFG_S && cfg(4, 100, 0, 64, 16) == CFG_S);
+    CHECK(cfg(4, 112, 99, 33, 5) == CFG_FEW && cfg(4, 109, 99, 33, 5, false) == CFG_FEW && cfg(6, 107, 136, 200, 16, false) == CFG_FEW);
     {
         const gemm_adapters_t ad = {P(), P(), nullptr, nullptr, 4, 16, 16, 16};  // W column-major, A_a row-major
-        CHECK(adapter_cfg(CUS, P(), P(), ad, 4, 100, 64, 64, 64, 64, false, true) == CFG_M);
+        CHECK(adapter_cfg(CUS, ad, 4, 100, 64, 64, 64, 64, false, true) == CFG_S);
     }
     CHECK(few_aligned(P(), P(), {P(), P(), nullptr, nullptr, 4, 5, 64, 5}, 33, 64, 64, 64, true));
     CHECK(!few_aligned(P(), P(), {P(), P(), nullptr, nullptr, 4, 5, 8, 40}, 40, 64, 64, 40, false));
     CHECK(!few_aligned(P(), P(), {P(), P(), nullptr, nullptr, 4, 8, 60, 8}, 32, 60, 60, 60, true));
     CHECK(!few_aligned(P(0x10002), P(), {P(), P(), nullptr, nullptr, 4, 8, 64, 8}, 32, 64, 64, 64, true));
-    CHECK(cfg(4, 1000, 64, 64, 16, true, P(0x10002)) == CFG_GENERIC && cfg(4, 100, 0, 64, 16) == CFG_GENERIC);
+    CHECK(adapter_whole(P(), 64, 64) && !adapter_whole(P(0x10002), 64, 64) && !adapter_whole(P(), 63, 64) && !adapter_whole(P(), 64, 65));
+    CHECK(!adapter_whole(P(), 64, 1 << 23) && adapter_pack(P(), 10, 63, 64) == 10 * 64 * 2 && adapter_pack(P(), 10, 64, 64) == 0);
     CHECK(cfg(4, 2133, 72, 4104, 16) == CFG_L && cfg(4, 2135, 136, 4104, 72, false) == CFG_L && cfg(4, 2256, 200, 4099, 136) == CFG_L);
-    CHECK(cfg(2, 1300, 256, 1032, 32) == CFG_M);
-    CHECK(cfg(4, 256, 4096, 4096, 16) == CFG_FEW && cfg(4, 257, 4096, 4096, 16) == CFG_M);  // both sides of the borders
+    CHECK(cfg(2, 1300, 256, 1032, 32) == CFG_S && cfg(4, 1100, 72, 4104, 16) == CFG_M && cfg(4, 1101, 99, 4101, 21, false) == CFG_M);
+    CHECK(cfg(340, 1020, 136, 4104, 40, false) == CFG_M && cfg(1100, 1102, 72, 4104, 16) == CFG_S);
+    CHECK(cfg(4, 128, 4096, 4096, 16) == CFG_FEW && cfg(4, 129, 4096, 4096, 16) == CFG_S && cfg(4, 896, 4096, 4096, 16) == CFG_S && cfg(4, 897, 4096, 4096, 16) == CFG_M);  // both sides of the borders
     CHECK(cfg(4, 2048, 4096, 4096, 16) == CFG_M && cfg(4, 2176, 4096, 4096, 16) == CFG_L && cfg(69, 2176, 4096, 4096, 16) == CFG_M);
     CHECK(cfg(4, 2176, 4096, 4096, 13) == CFG_M);  // no panels of whole granules
     // parts of K: at most 16 k-tiles, no empty one, and the scratch holds them
-    for (int64_t M : {1, 16, 17, 64, 65, 256})
-        for (int64_t N : {1, 64, 65, 4096, 14336, 1 << 22})
+    for (int64_t M : {1, 16, 17, 64, 65, 128})
+        for (int64_t N : {1, 64, 65, 4096, 14336, 1 << 21})
             for (int64_t K : {1, 64, 65, 128, 1024, 1025, 4096, 14336, 1 << 20})
                 for (int64_t r : {1, 16, 17, 128})
                     for (int64_t q : {1, 5, 300}) {
@@ -260,8 +264,8 @@ int main() {
                         CHECK(f.per >= 1 && f.per <= 16 && f.splits >= 1);
                         CHECK((int64_t)f.per * f.splits >= nkt && (int64_t)f.per * (f.splits - 1) < nkt);
                         CHECK(f.blocks >= cdiv(N, 64));
-                        CHECK(adapter_work(CUS, q, M, N, K, r, GEMM_OUT_F32) >= f.splits * 4 * M * (N + cdiv(r, 16) * 16));
-                        CHECK(adapter_work(CUS, q, M, N, K, r, GEMM_OUT_F32) >= 4 * M * adapter_rp(r));
+                        CHECK(adapter_work(CUS, P(), P(), q, M, N, K, r, K, K, GEMM_OUT_F32, true) >= f.splits * 4 * M * (N + cdiv(r, 16) * 16));
+                        CHECK(adapter_work(CUS, P(2), P(2), q, M, N, K, r, K, K, GEMM_OUT_F32, true) >= 4 * M * adapter_rp(r) + 2 * (M + N) * K);
                     }
     // 8-bit gradients: large tiles, parts of the rows (at least 256, no more than the scratch holds)
     auto plan8 = [](int64_t g, int64_t M, int64_t N, int64_t K, int edge, int splits) {

@@ -130,7 +130,11 @@ CASES = [
     ("bf16", [30, 0, 61], 0, 0, 3, [2, 1, 0], 1030, 205, 33, True, "bf16", 1.0, 0.0),
     ("bf16", [200, 40], 0, 5, 2, None, 67, 131, 120, False, "bf16", 1.0, 0.0),
     ("f16", [3], 0, 0, 1, None, 7, 3, 3, False, "f16", 1.0, 0.0),
-    # the same past the few rows: staged tiles of any alignment
+    # more than 64 of the few rows
+    ("bf16", [1] * 60 + [0] * 70 + [30, 31], 3, 4, 7, [i * 5 % 9 - 1 for i in range(132)], 1600, 136, 16, True, "bf16", 1.0, 0.0),
+    ("f16", [50, 0, 1, 77], 0, 0, 2, [1, 0, 1, 0], 264, 200, 128, False, "f32", 0.5, 1.0),
+    ("bf16", [60, 7, 41], 2, 3, 3, None, 1031, 203, 77, True, "f32", 1.0, 1.0),
+    # past the few rows: copies of X and W in whole granules
     ("bf16", [117, 31, 0, 129], 0, 5, 2, [1, 1, 0, 1], 99, 33, 5, True, "f32", 1.0, 1.0),
     ("f16", [117, 31, 0, 129], 2, 0, 2, [1, -1, 0, 7], 99, 33, 5, False, "bf16", 1.0, 1.0),
     ("bf16", [300, 3, 90], 1, 1, 3, None, 200, 136, 130, False, "f32", 1.0, 0.0),
@@ -138,6 +142,13 @@ CASES = [
     ("bf16", [1, 3] * 90, 2, 1, 5, [i % 6 - 1 for i in range(180)], 136, 264, 13, True, "bf16", 1.0, 0.0),
     ("f16", [1, 3] * 90, 2, 1, 5, [i % 6 - 1 for i in range(180)], 136, 264, 13, False, "f32", 1.0, 1.0),
     ("bf16", [1, 3] * 90, 0, 0, 5, [i % 6 - 1 for i in range(180)], 135, 263, 40, False, "f32", 1.0, 0.0),
+    # 128 x 128 tiles, of few and many requests, copied or not
+    ("bf16", [500, 0, 7, 590], 2, 1, 4, None, 72, 4104, 16, True, "bf16", 1.0, 0.0),
+    ("f16", [500, 0, 7, 590], 0, 4, 3, [2, 0, -1, 1], 99, 4101, 21, False, "f32", 0.5, 1.0),
+    ("bf16", [3] * 340, 0, 0, 5, [i % 6 - 1 for i in range(340)], 136, 4104, 40, False, "bf16", 1.0, 0.0),
+    ("f16", [3] * 360, 1, 0, 5, [i % 6 - 1 for i in range(360)], 131, 4104, 40, True, "f16", 1.0, 0.0),
+    # many requests of one row
+    ("bf16", [1] * 1100, 0, 2, 5, [i % 6 - 1 for i in range(1100)], 72, 4104, 16, True, "f32", 1.0, 0.0),
     # 256 x 256 tiles: requests that end inside a tile, a rank of more than one k-tile, both layouts
     ("bf16", [700, 0, 1400, 30], 0, 3, 3, [2, 0, 1, -1], 72, 4104, 16, True, "bf16", 1.0, 0.0),
     ("f16", [700, 0, 1400, 30], 5, 0, 3, [2, 0, -1, 1], 136, 4104, 72, False, "f32", 0.5, 1.0),
@@ -207,11 +218,12 @@ def test_offsets_that_are_wrong_stay_inside(dmp):
         assert torch.equal(dmp.gemm_adapters(X, W, A, B, torch.tensor(off, device="cuda")), want)
 
 
-def test_not_a_number_stays_with_its_rows(dmp):
-    """A NaN in one adapter, or in one request's row, reaches no other request."""
+@pytest.mark.parametrize("T,K,N", [(90, 136, 264), (150, 136, 264), (150, 133, 264), (1100, 136, 4104), (2200, 136, 4104)])
+def test_not_a_number_stays_with_its_rows(dmp, T, K, N):
+    """A NaN in one adapter, or in one request's row, reaches no other request (each kernel)."""
     for linear in (True, False):
-        X, W, A, B = (to_gpu(v) for v in operands(1, 150, 136, 264, 16, 3, torch.bfloat16, linear))
-        off = torch.tensor([0, 10, 70, 150], device="cuda")
+        X, W, A, B = (to_gpu(v) for v in operands(1, T, K, N, 16, 3, torch.bfloat16, linear))
+        off = torch.tensor([0, 10, 70, T], device="cuda")
         want = dmp.gemm_adapters(X, W, A, B, off)
         A2, B2 = A.clone(), B.clone()
         A2[1] = float("nan")

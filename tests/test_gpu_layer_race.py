@@ -51,13 +51,16 @@ def bits(x):
 ADAPTERS = [
     (8200, 5, 200, 2048, 72, True, "bf16", 0),    # 256 x 256 tiles
     (8200, 5, 264, 2048, 16, False, "f32", 0),
-    (900, 40, 1000, 520, 24, True, "f32", 0),     # 128 x 128
+    (1100, 40, 264, 4104, 24, True, "f32", 0),    # 128 x 128
+    (1100, 40, 264, 4104, 24, False, "bf16", 0),
+    (900, 40, 1000, 520, 24, True, "f32", 0),     # 64 x 64
     (900, 40, 1000, 520, 24, False, "bf16", 0),
     (900, 40, 1000, 520, 13, True, "f16", 0),
     (900, 40, 1003, 517, 13, False, "f32", 1),    # any alignment
     (900, 40, 1003, 517, 13, True, "bf16", 1),
     (64, 64, 4096, 1024, 16, True, "bf16", 0),    # few rows
-    (200, 30, 1000, 264, 40, True, "f32", 0),
+    (120, 30, 1000, 264, 40, True, "f32", 0),
+    (120, 30, 1003, 517, 13, False, "f32", 1),
     (5, 5, 512, 520, 8, True, "f16", 0),
 ]
 
@@ -79,7 +82,8 @@ def test_adapters(handles, case):
     for lib, h in handles:
         D = torch.zeros(T, N, dtype=OUT[out][1], device="cuda")
         hidden = torch.zeros(T, r, dtype=dt, device="cuda")
-        work = torch.empty(lib.gemm_adapters_work(h, S, T, N, K, r, OUT[out][0]), dtype=torch.uint8, device="cuda")
+        work = torch.empty(lib.gemm_adapters_work(h, X.data_ptr() + 2 * shift, W.data_ptr(), S, T, N, K, r, K, K if linear else N,
+                                                  OUT[out][0], flags), dtype=torch.uint8, device="cuda")
         rc = lib.gemm_run_adapters(h, X.data_ptr() + 2 * shift, W.data_ptr(), ctypes.byref(ops), None, D.data_ptr(),
                                    off.data_ptr(), S, T, N, K, K, K if linear else N, N, 0 if dt == torch.float16 else 1, flags, 1.0,
                                    0.0, 0, OUT[out][0], hidden.data_ptr(), r, work.data_ptr(),

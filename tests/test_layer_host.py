@@ -21,7 +21,7 @@ def test_argument_checks_and_rules_under_sanitizers(tmp_path):
 def test_null_handle_is_refused():
     lib = dmp.load_library()
     a, q = dmp.AdapterOperands(), dmp.Q8Operand()
-    assert lib.gemm_adapters_work(None, 1, 1, 1, 1, 1, 0) == -1
+    assert lib.gemm_adapters_work(None, 0, 0, 1, 1, 1, 1, 1, 1, 1, 0, 0) == -1
     assert lib.gemm_run_adapters(None, 0, 0, ctypes.byref(a), 0, 0, 0, 1, 1, 1, 1, 1, 1, 1, 0, 0, 1.0, 0.0, 0, 0, 0, 0, 0,
                                  0) == 1
     assert lib.gemm_wgrad8_work(None, 0, 1, 1, 1, 1, 1) == -1
