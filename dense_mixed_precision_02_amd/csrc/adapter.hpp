@@ -6,7 +6,7 @@
 // B_a: r x N, with r of 8 to a few hundred.  Two launches:
 //
 //   hidden   H[i] = s_a (X[i] A_a): r columns over a long K, bound by reading X once (and,
-//            with few rows, A_a).  A workgroup takes 16 or 64 rows of one request and up to 64
+//            with few rows, A_a).  A workgroup takes 16 or 32 rows of one request and up to 64
 //            of the columns; its eight waves split K, each streams its part of X and A_a
 //            straight into matrix-instruction operands, and their sums meet in LDS.
 //   product  [X | H] [W; B_a]: the projection's K loop runs on, over r more for each request
@@ -18,6 +18,11 @@
 // such numbers (within 2^-16 of it for bf16, 2^-22 for fp16), each multiplied by B_a.
 //
 // A tile finds its requests by scanning the offsets, 64 at a time.
+//
+// The product is bound by the matrix units on 256 x 256 tiles (8192 rows of 9 requests, 4096 x 4096, rank
+// 64, bf16: hidden 34 us, product 230 to 256, 1.1 to 1.2 PFLOP/s), by its k-tiles' turns, about 1.5 us each on
+// 128 x 128 tiles and 0.5 on 64 x 64, on smaller ones (5003 rows, 2056 x 1000, rank 24: 12 and 52 to 57).
+// Four k-tiles on their way instead of two, on 64 x 64 tiles, changed nothing (256 rows by 4096 x 4096: 33 us with two, 35 with four).
 //
 // Zeros times an infinity or a NaN are no zeros: with rows of zeros for the other requests an
 // adapter that holds one would spoil theirs.  So a 16-row block of the tile that lies in

@@ -13,6 +13,11 @@
 //
 // Rows are split where the gradients' tiles alone would leave CUs idle (wgrad8_plan);
 // each part's sums go to memory in 32 bits, and wgrad8_join adds them in their order.
+//
+// Large gradients are bound by the matrix units and, beside them, LDS (4096 x 4096 of 8192 rows, bf16: 250
+// us of a long loop, 1.1 PFLOP/s, a library product of 16-bit operands 1.2; 45 % of the matrix units'
+// cycles after a pause, 293 us); many small ones by memory (24 of 520 x 1032, 3001 rows, fp16 with C and D in 32
+// bits: 111 MB in 30 us).
 #pragma once
 #include "ragged_staged.hpp"
 #include "wgrad8_plan.hpp"

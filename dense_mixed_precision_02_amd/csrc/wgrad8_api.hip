@@ -47,7 +47,8 @@ int launch_wgrad8(gemm_handle_t h, int edge, const Wgrad8Args &a, hipStream_t s)
 extern "C" {
 
 int64_t gemm_wgrad8_work(gemm_handle_t h, const void *Y, int64_t groups, int64_t M, int64_t N, int64_t K, int64_t ldy) {
-    if (!h || !wgrad8_sizes_ok(groups, M, N, K)) return -1;
+    if (!h || !wgrad8_sizes_ok(groups, M, N, K) || (K > 0 && N > WGRAD8_LD_MAX)) return -1;
+    if (groups > 0 && M > 0 && N > 0 && !extent_ok(groups, M, N, N)) return -1;
     return wgrad8_work(h->num_cus, Y, groups, M, N, K, ldy);
 }
 

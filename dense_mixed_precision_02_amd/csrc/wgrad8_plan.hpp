@@ -15,11 +15,15 @@ inline Wgrad8Plan wgrad8_plan(int num_cus, int64_t groups, int64_t M, int64_t N,
     if (groups == 0 || M == 0 || N == 0) return {64, 1};
     const int64_t rows = K / groups, t256 = groups * cdiv(M, 256) * cdiv(N, 256);
     const bool inside = (double)M * (double)N >= 0.75 * 65536.0 * (double)(cdiv(M, 256) * cdiv(N, 256));
+    // In us with the join, 256 x 256 / 128 x 128 / 64 x 128 tiles, bf16, the parts as below.
     // 256 x 256 tiles where, with parts of 1024 rows at least, they fill most of the device and lie mostly
-    // inside the gradients, and their rows are worth a large tile's start and end
+    // inside the gradients, and their rows are worth a large tile's start and end (4096 x 4096 of 2048 rows:
+    // 80 / 111 / 123, of 512: 33 / 37 / 41; 2048 x 2048 of 8192: 94 / 113 / 126; 2000 x 3000 of 4096: 91 / 100 / 123;
+    // 16 of 1024 x 1024, 1024 rows each: 51 / 60 / 72; 8 of 2048 x 2048, 512 rows each: 64 / 67 / 78)
     const int64_t large = t256 >= num_cus ? 1 : std::max<int64_t>(1, std::min(num_cus / t256, rows / 1024));
     if (inside && rows >= 512 && 4 * t256 * large >= 3 * num_cus) return {256, (int)large};
-    // smaller ones, two to a CU, in parts of 256 rows at least
+    // smaller ones, two to a CU, in parts of 512 and 256 rows at least (128 x 128 / 64 x 128: 1504 x 1504 of 4096
+    // rows: 48 / 62; 1024 x 1024 of 8192: 39 / 41; 24 of 520 x 1032, 512 rows each: 43 / 42)
     const int64_t t128 = groups * cdiv(M, 128) * cdiv(N, 128), tiles = groups * cdiv(M, 64) * cdiv(N, 128);
     const int64_t s128 = std::max<int64_t>(1, std::min<int64_t>({2 * (int64_t)num_cus / t128, rows / 512, 16}));
     if (rows >= 512 && 4 * t128 * s128 >= 3 * num_cus) return {128, (int)s128};

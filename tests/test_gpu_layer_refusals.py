@@ -94,6 +94,7 @@ def test_scratch_is_asked_for(dmp):
     assert h.wgrad8_work(0, 1, 64, 128, 8192, 128) > 0 and h.wgrad8_work(0, 1, -1, 128, 8192, 128) == -1
     assert h.wgrad8_work(2, 1, 64, 128, 100, 128) == 100 * 128 * 2 and h.wgrad8_work(0, 1, 64, 128, 100, 128) == 0
     assert h.adapters_work(0, 0, 4, 4, 64, 64, 8, 64, 64, dmp.GEMM_OUT_BF16) > 0
+    assert h.wgrad8_work(0, 1, 1 << 30, 1 << 30, 8, 1 << 30) == -1 and h.wgrad8_work(0, 1 << 16, 1 << 22, 1 << 22, 8, 1 << 22) == -1
     assert h.adapters_work(0, 0, 4, 4, 64, 64, 0, 64, 64, 0) == -1 and h.adapters_work(0, 0, 4, 4, 1 << 22, 64, 8, 64, 1 << 22, 0) == -1
     assert h.route_work(100, 8) > 0 and h.route_work(100, 1025) == -1
     x = dmp.quant8(torch.zeros(8192, 64, device="cuda"), pow2=True)
