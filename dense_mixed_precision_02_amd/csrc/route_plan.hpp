@@ -8,11 +8,13 @@ namespace plan {
 
 constexpr int ROUTE_E_MAX = 1024, ROUTE_K_MAX = 64;
 
-// Tokens to a workgroup and workgroups.  Up to 64 tokens, four turns of its 16 waves,
-// one workgroup does everything in one launch; beyond, as many workgroups as CUs.
+// Tokens to a workgroup and workgroups.  Up to 32 tokens, two turns of its 16 waves,
+// one workgroup does everything in one launch; beyond, as many workgroups as CUs.  (Kernel
+// time of one / two launches, the second costing 1 to 4 us beside it, bf16, 8 of 64 experts and 6 of
+// 160: 32 tokens 11.6 / 9.8 and 13.7 / 10.6 us, 64 tokens 15.2 / 10.3 and 19.2 / 11.6.)
 inline void route_split(int64_t T, int num_cus, int &rows, int &blocks) {
-    if (T <= 64) {
-        rows = 64;
+    if (T <= 32) {
+        rows = 32;
         blocks = 1;
         return;
     }

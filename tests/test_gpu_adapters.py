@@ -270,6 +270,28 @@ def test_strided_operands(dmp):
         assert got is C and torch.equal(C, both)
 
 
+@pytest.mark.parametrize("T", [100, 300])
+def test_operands_that_begin_anywhere(dmp, T):
+    """Views that start at odd elements, rows of odd lengths apart, NaN around them, one operand and all of
+    them: the bits of the same numbers side by side."""
+    off = torch.tensor([0, 30, 100, T], device="cuda")
+    for linear in (True, False):
+        ops = [to_gpu(v) for v in operands(4, T, 69, 131, 13, 3, torch.bfloat16, linear)]
+
+        def odd(x):
+            t = x.transpose(-1, -2) if x.stride(-1) != 1 else x
+            n = t.shape[-1] + 5
+            flat = torch.full((t[..., 0].numel() * n + 3,), float("nan"), dtype=t.dtype, device="cuda")
+            v = flat[3:].view(*t.shape[:-1], n)[..., :t.shape[-1]]
+            v.copy_(t)
+            return v.transpose(-1, -2) if x.stride(-1) != 1 else v
+
+        want = dmp.gemm_adapters(*ops, off, out_dtype=torch.bfloat16)
+        for which in ((0,), (1,), (2,), (3,), (0, 1, 2, 3)):
+            got = dmp.gemm_adapters(*(odd(v) if i in which else v for i, v in enumerate(ops)), off, out_dtype=torch.bfloat16)
+            assert torch.equal(got, want), which
+
+
 @pytest.mark.parametrize("linear", [True, False])
 def test_gradients(dmp, linear):
     """The documented composition against the formulas in 64 bits; padding rows in front and behind."""
@@ -329,12 +351,13 @@ def test_formulas_against_differences():
             assert abs((v[0] - v[1]) / (2 * eps) - flat[i]) < 1e-7
 
 
-def test_streams_and_captured_graphs(dmp):
+@pytest.mark.parametrize("T", [120, 300])
+def test_streams_and_captured_graphs(dmp, T):
     """Each call has scratch of its own, on two streams and in two graphs replayed in turn; a graph
     follows the offsets and adapters that are there at replay."""
-    off = torch.tensor([0, 30, 100, 300], device="cuda")
+    off = torch.tensor([0, 30, 100, T], device="cuda")
     ids = torch.tensor([1, 0, -1], dtype=torch.int32, device="cuda")
-    sets = [[to_gpu(v) for v in operands(40 + i, 300, 264, 136, 16, 2, torch.bfloat16, i == 0)] for i in range(2)]
+    sets = [[to_gpu(v) for v in operands(40 + i, T, 264, 136, 16, 2, torch.bfloat16, i == 0)] for i in range(2)]
     want = [dmp.gemm_adapters(*s, off, ids) for s in sets]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in range(2)]
@@ -350,8 +373,8 @@ def test_streams_and_captured_graphs(dmp):
         with torch.cuda.graph(graph):
             outs.append(dmp.gemm_adapters(*sets[i], off, ids))
         graphs.append(graph)
-    for i, (o, a) in enumerate([([0, 30, 100, 300], [1, 0, -1]), ([0, 0, 300, 300], [0, 1, 1]), ([0, 1, 2, 300], [1, 1, 0]),
-                                ([0, 299, 299, 300], [-1, 1, 0])]):
+    for i, (o, a) in enumerate([([0, 30, 100, T], [1, 0, -1]), ([0, 0, T, T], [0, 1, 1]), ([0, 1, 2, T], [1, 1, 0]),
+                                ([0, T - 1, T - 1, T], [-1, 1, 0])]):
         off.copy_(torch.tensor(o))
         ids.copy_(torch.tensor(a, dtype=torch.int32))
         for j in range(2):
