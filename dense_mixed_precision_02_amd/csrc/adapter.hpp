@@ -15,7 +15,8 @@
 //
 // H is rounded to the inputs' type, as an input of the matrix instructions; its error
 // relative to H B_a is that of rounding X.  Where D has 32 bits H is kept as the sum of two
-// such numbers (within 2^-16 of it for bf16, 2^-22 for fp16), each multiplied by B_a.
+// such numbers for fp16 (within 2^-22 of it), of three for bf16 (2^-24; two, 2^-16, would leave
+// an error of several times fp32's), each multiplied by B_a.
 //
 // A tile finds its requests by scanning the offsets, 64 at a time.
 //
@@ -263,15 +264,13 @@ __device__ static inline void hidden_store(const AdapterArgs &p, int a, float s,
             for (int w = 1; w < HIDDEN_WAVES; ++w) v += lds[w * SZ + e];
             v *= s;
         }
-        const uint16_t hi = encode16(v, f16);
-        const int64_t at = (row0 + r) * p.rp + c0 + c;
-        ((uint16_t *)p.H)[at] = hi;
-        if (p.parts > 1) {
-            // (an infinity's rest would be no number)
-            const float left = v - decode16(hi, f16);
-            ((uint16_t *)p.H)[p.r.M * p.rp + at] = encode16(__builtin_isfinite(left) ? left : 0.0f, f16);
+        if (p.hidden && c0 + c < p.rank) ((uint16_t *)p.hidden)[(row0 + r) * p.ld_hidden + c0 + c] = encode16(v, f16);
+        for (int part = 0; part < p.parts; ++part) {
+            const uint16_t hi = encode16(v, f16);
+            ((uint16_t *)p.H)[(part * p.r.M + row0 + r) * p.rp + c0 + c] = hi;
+            v -= decode16(hi, f16);
+            v = __builtin_isfinite(v) ? v : 0.0f;  // (an infinity's rest would be no number)
         }
-        if (p.hidden && c0 + c < p.rank) ((uint16_t *)p.hidden)[(row0 + r) * p.ld_hidden + c0 + c] = hi;
     }
 }
 

@@ -67,7 +67,8 @@ int launch_few(const AdapterFewArgs &f, int parts, hipStream_t s) {
                    : ALIGNED && f.per <= 8 ? launch(adapter_few<DT, BM, ALIGNED ? 8 : 4, KC, ALIGNED>, grid, 256, s, f)
                                            : launch(adapter_few<DT, BM, 16, KC, ALIGNED>, grid, 256, s, f);
     if (rc != GEMM_OK) return rc;
-    return parts > 1 ? launch(adapter_few_join<DT, BM, 2, KC>, join, 512, s, f) : launch(adapter_few_join<DT, BM, 1, KC>, join, 512, s, f);
+    constexpr int PARTS = std::is_same_v<DT, F16> ? 2 : 3;
+    return parts > 1 ? launch(adapter_few_join<DT, BM, PARTS, KC>, join, 512, s, f) : launch(adapter_few_join<DT, BM, 1, KC>, join, 512, s, f);
 }
 
 template <class DT, bool KC>
@@ -153,7 +154,7 @@ int gemm_run_adapters(gemm_handle_t h, const void *X, const void *W, const gemm_
     a.b_fast = adapter_b_fast(*ad, N, bc);
     a.H = (char *)work;
     a.rp = (int)adapter_rp(ad->rank);
-    a.parts = adapter_parts(d_type);
+    a.parts = adapter_parts(dtype, d_type);
     a.hidden = hidden; a.ld_hidden = ld_hidden;
     hipStream_t s = (hipStream_t)stream;
     return dtype == GEMM_F16 ? run_adapters<F16>(h->num_cus, a, *ad, ac, bc, s) : run_adapters<BF16>(h->num_cus, a, *ad, ac, bc, s);

@@ -328,15 +328,16 @@ __global__ __launch_bounds__(512, 2) void adapter_few_join(const AdapterFewArgs 
         for (int m = 0; m < HEACH; ++m) {
             const int x = tid + 512 * m, row = x / 32, c = kb * 32 + x % 32;
             if (row >= BM) continue;
-            const float v = owner[row] ? hsum[m] * scales[row] : 0.0f;
-            const uint16_t hi = encode16(v, f16);
-            hl[0][row][c] = hi;
-            if constexpr (PARTS > 1) {
-                const float left = v - decode16(hi, f16);
-                hl[1][row][c] = encode16(__builtin_isfinite(left) ? left : 0.0f, f16);
-            }
+            float v = owner[row] ? hsum[m] * scales[row] : 0.0f;
             if (p.hidden && col0 == 0 && row < rows && c < p.rank)
-                ((uint16_t *)p.hidden)[(int64_t)(first + row) * p.ld_hidden + c] = hi;
+                ((uint16_t *)p.hidden)[(int64_t)(first + row) * p.ld_hidden + c] = encode16(v, f16);
+#pragma unroll
+            for (int w = 0; w < PARTS; ++w) {  // as in hidden_store
+                const uint16_t hi = encode16(v, f16);
+                hl[w][row][c] = hi;
+                v -= decode16(hi, f16);
+                v = __builtin_isfinite(v) ? v : 0.0f;
+            }
         }
     }
     barrier_vmcnt<63>();

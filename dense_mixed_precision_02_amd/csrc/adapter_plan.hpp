@@ -11,7 +11,8 @@ constexpr int64_t ADAPTER_RANK_MAX = 1024, ADAPTER_LD_MAX = 1ll << 24;  // 31-bi
 constexpr int64_t ADAPTER_WIDTH_MAX = 1ll << 21;  // K, N: 31-bit offsets in 256 rows of X and W
 
 inline int64_t adapter_rp(int64_t rank) { return cdiv(rank, 8) * 8; }
-inline int adapter_parts(int d_type) { return d_type == GEMM_OUT_F32 ? 2 : 1; }
+// Numbers of 16 bits that a hidden value is kept in.
+inline int adapter_parts(int dtype, int d_type) { return d_type != GEMM_OUT_F32 ? 1 : dtype == GEMM_F16 ? 2 : 3; }
 
 // Few rows, 64 at a time (adapter_few.hpp): parts of K, of at most 16 k-tiles of 64 and of 2 at least,
 // as many as give every CU a workgroup of the columns' or of the hidden sums'.
@@ -46,7 +47,7 @@ inline int64_t adapter_pack(const void *X, int64_t rows, int64_t cols, int64_t l
 // Scratch: the hidden rows and X's and W's copies, or the sums of the K parts.
 inline int64_t adapter_work(int num_cus, const void *X, const void *W, int64_t requests, int64_t M, int64_t N, int64_t K,
                             int64_t rank, int64_t ldx, int64_t ldw, int d_type, bool b_col) {
-    int64_t b = cdiv(adapter_parts(d_type) * M * adapter_rp(rank) * 2, 16) * 16;
+    int64_t b = cdiv(adapter_parts(GEMM_BF16, d_type) * M * adapter_rp(rank) * 2, 16) * 16;
     if (M > 0 && N > 0 && K > 0 && requests > 0) {
         b += adapter_pack(X, M, K, ldx) + (b_col ? adapter_pack(W, N, K, ldw) : adapter_pack(W, K, N, ldw));
         if (M <= FEW_ROWS && rank <= FEW_RANK_MAX)

@@ -386,10 +386,10 @@ int gemm_run_scaled8(gemm_handle_t h, const gemm_q8_t *A, const gemm_q8_t *B, co
  * each adapter, or NULL: 1.  Rows of D that no request owns are left as they were.
  *
  * h is summed in fp32 and rounded to dtype, as an input of the matrix
- * instructions; where D is fp32 it is kept as a sum of two such values.  So
+ * instructions; where D is fp32 it is kept as a sum of two (bf16: three).  So
  * per element |D - D_exact| <= gemm_run_grouped's bound with K + rank products
  * + |alpha| * e * sum over j of |h_ij * b_jn|, e = 2^-8 (bf16) or 2^-11 (fp16),
- * for fp32 D 2^-16 (2^-22) (as long as h and its parts are normal numbers of
+ * for fp32 D 2^-24 (2^-22) (as long as h and its parts are normal numbers of
  * dtype), + the bound of h's own sum, 4 * K * 2^-24 * sum of |x_ik * a_kj|,
  * times |scale| * |b_jn|.  K == 0 gives D = cvt(beta * C).
  *

@@ -4,7 +4,7 @@
 Tolerance per element, from the arithmetic alone (u = 2^-24).  A hidden value h = s * sum x a:
 4 K u |s| S_h for the sum (S_h: of magnitudes), 2 u |h| for the waves' join and the scale, and
 its rounding to 16 bits: half a step, e |h| with e = 2^-8 (bf16) or 2^-11 (fp16), and half of
-fp16's least subnormal, 2^-25; where D is fp32 the rest of that is kept too: e^2 |h|, and again 2^-25.
+fp16's least subnormal, 2^-25; where D is fp32 the rest of that is kept too: e^2 |h| for fp16, and again 2^-25; e^3 |h| for bf16.
 The product: 4 (K + n r) u (S_w + sum |h b|), n the parts of h, and the hidden values' errors times
 |b|; then the output stage's three roundings and half a step of the output type."""
 import numpy as np
@@ -55,7 +55,7 @@ def to_gpu(x):
 def reference(X, W, A, B, off, ids, scale, alpha, beta, C, out_dtype):
     """(result, tolerance, hidden, its tolerance, owned rows) in 64 bits."""
     T, K, N, r = X.shape[0], X.shape[1], W.shape[1], A.shape[2]
-    e, parts = E16[X.dtype], 2 if out_dtype == torch.float32 else 1
+    e, parts = E16[X.dtype], 1 if out_dtype != torch.float32 else 2 if X.dtype == torch.float16 else 3
     x, w = X.double(), W.double()
     acc, size, err = x @ w, x.abs() @ w.abs(), torch.zeros(T, N, dtype=torch.float64)
     h, htol = torch.zeros(T, r, dtype=torch.float64), torch.zeros(T, r, dtype=torch.float64)
@@ -73,7 +73,7 @@ def reference(X, W, A, B, off, ids, scale, alpha, beta, C, out_dtype):
         S = abs(s) * (x[lo:hi].abs() @ Aa.abs())
         base = 4 * K * U * S + 2 * U * h[lo:hi].abs()
         htol[lo:hi] = base + e * h[lo:hi].abs() * 1.01 + least
-        used = htol[lo:hi] if parts == 1 else base + e * e * h[lo:hi].abs() * 1.01 + least
+        used = htol[lo:hi] if parts == 1 else base + e ** parts * h[lo:hi].abs() * 1.01 + least
         acc[lo:hi] += h[lo:hi] @ Ba
         size[lo:hi] += h[lo:hi].abs() @ Ba.abs()
         err[lo:hi] = used @ Ba.abs()
