@@ -439,8 +439,9 @@ int gemm_run_adapters(gemm_handle_t h, const void *X, const void *W, const gemm_
  * none needed, work may be NULL; -1: sizes that are refused), 16-byte aligned,
  * for partial sums where the rows are split to fill the device (added in a
  * fixed order), and for a copy of a Y whose rows are not whole 16-byte
- * granules (of Y's address only the alignment counts).  ldy: at most 2^23.  It must not be shared with a call that can run at the same
- * time.  Nothing is allocated.
+ * granules (of Y's address only the alignment counts).  It must not be shared
+ * with a call that can run at the same time.  Nothing is allocated.  ldy: at
+ * most 2^23.
  */
 int64_t gemm_wgrad8_work(gemm_handle_t h, const void *Y, int64_t groups, int64_t M, int64_t N, int64_t K,
                          int64_t ldy);
