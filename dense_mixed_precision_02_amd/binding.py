@@ -806,7 +806,7 @@ def gemm_adapters(X, W, A, B, offsets, ids=None, scale=None, C=None, out=None, a
     request g has adapter g;  scale: (adapters,) float32, or None (1).
     W: (K, N), A: (adapters, K, r), B: (adapters, r, N) of X's dtype, row-major or transposed
     views (of the (N, K), (adapters, r, K) and (adapters, N, r) of linear layers); W and B
-    must be laid out alike, and adapters lie one after the other.
+    must be laid out alike, and adapters lie one after the other.  r up to 1024, K and N up to 2^21.
     C, ``out`` and ``out_dtype`` (default float32) as in gemm_grouped; rows that no request
     owns are left as they are in ``out``.
 
